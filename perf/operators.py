@@ -196,10 +196,9 @@ def prepare(case, seed):
         st["u_save"] = _normal(g, (R, h), 1.0, torch.bfloat16)
         st["y_disp"] = _normal(g, (R, d), 0.5, torch.bfloat16)
         st["dy"] = _normal(g, (T, d), 1.0, torch.bfloat16)
-        u8 = dict(dtype=torch.uint8, device=DEV)
         for n, cols in (("g", h), ("u", h), ("y", d)):
-            st[n + "_q"] = torch.zeros((R, cols), **u8)
-            st[n + "_scale"] = torch.zeros((R, cols // BLOCK), **u8)
+            st[n + "_q"] = torch.zeros((R, cols), dtype=torch.int8, device=DEV)
+            st[n + "_scale"] = torch.zeros((R, cols // BLOCK), dtype=torch.uint8, device=DEV)
         # rows past the accepted ones are never written: they stay zero
         bf = dict(dtype=torch.bfloat16, device=DEV)
         st["g_out"], st["u_out"] = torch.zeros((R, h), **bf), torch.zeros((R, h), **bf)
