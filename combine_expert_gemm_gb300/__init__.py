@@ -590,3 +590,11 @@ class StreamedLayer:
         if self.backward:
             codes += [read_device_error(b.ws) for b in self.bwd]
         return max(codes)
+
+
+# The operators around the layer in a training block (include/moe_block.h).
+from .block import *  # noqa: E402,F401,F403
+from .block import _SIG as _BLOCK_SIG, __all__ as _block_all  # noqa: E402
+
+EXPORTED += tuple(_BLOCK_SIG)
+__all__ += _block_all

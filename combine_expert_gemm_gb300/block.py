@@ -1,0 +1,211 @@
+"""Python binding of the operators around the routed-expert layer in a
+pre-norm training block (``include/moe_block.h``): layer norm, the router's
+balance loss with the dense router gradient, and 8-bit activation checkpoints.
+
+Argument marshalling only, as in the package's ``__init__``; these calls also
+compare every tensor's size with the shape, because a short buffer would be
+overrun on the device.
+"""
+import ctypes
+
+import torch
+
+from . import (_P, _SP, _SZ, _bf16, _check, _f32, _i32, _lib, _stream, _u8)
+
+__all__ = ["layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_bytes",
+           "balance_loss", "balance_loss_backward", "balance_loss_workspace_bytes",
+           "router_dense_backward", "router_dense_backward_workspace_bytes",
+           "checkpoint_save", "checkpoint_restore", "combine_backward_checkpoint"]
+
+_I = ctypes.c_int32
+_SIG = {
+    "moe_layer_norm": ([_I] * 3 + [_P] * 4 + [ctypes.c_float] + [_P] * 4 + [_P], ctypes.c_int),
+    "moe_layer_norm_backward_workspace_bytes": ([_I, _I], _SZ),
+    "moe_layer_norm_backward": ([_I] * 3 + [_P, _I] + [_P] * 4 + [_I] + [_P] * 4 + [_P, _SZ, _P],
+                                ctypes.c_int),
+    "moe_balance_loss_workspace_bytes": ([_SP], _SZ),
+    "moe_balance_loss": ([_SP] + [_P] * 8 + [_P, _SZ, _P], ctypes.c_int),
+    "moe_balance_loss_backward": ([_SP] + [_P] * 9 + [_P], ctypes.c_int),
+    "moe_router_dense_backward_workspace_bytes": ([_SP], _SZ),
+    "moe_router_dense_backward": ([_SP] + [_P] * 7 + [_P, _SZ, _P], ctypes.c_int),
+    "moe_checkpoint_save": ([_SP] + [_P] * 10 + [_P], ctypes.c_int),
+    "moe_checkpoint_restore": ([_SP] + [_P] * 8 + [_P], ctypes.c_int),
+    "moe_combine_backward_checkpoint": ([_SP] + [_P] * 7 + [_P], ctypes.c_int),
+}
+for _name, (_args, _res) in _SIG.items():
+    _f = getattr(_lib, _name)
+    _f.argtypes = _args
+    _f.restype = _res
+
+_DTYPE = {torch.bfloat16: 0, torch.float32: 1}  # moe_dtype
+_i8 = torch.int8
+
+
+def _arg(t, dtype, name, n, dev):
+    """Device pointer of a contiguous CUDA tensor of n elements (None: NULL)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.numel() < n:
+        raise ValueError(f"{name}: {t.numel()} elements, {n} needed")
+    return t.data_ptr()
+
+
+def _ws(ws, dev):
+    p = _arg(ws, _u8, "ws", 0, dev)
+    return p, 0 if ws is None else ws.numel()
+
+
+def _float_type(t, name):
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPE:
+        raise TypeError(f"{name}: expected a bfloat16 or float32 tensor")
+    return t.dtype
+
+
+def _rows(x, name):
+    dt = _float_type(x, name)
+    if x.dim() != 2:
+        raise ValueError(f"{name}: expected [rows, d]")
+    return dt, x.shape[0], x.shape[1]
+
+
+# -------------------------------------------------------------- layer norm --
+
+def layer_norm(x, add, gamma, beta, eps, x_sum, y, mean, rstd, stream=None):
+    """x_sum = x + add and y = layer norm of it (include/moe_block.h).  x [rows, d]
+    bf16 or fp32; add and x_sum, gamma, beta, and mean with rstd may be None."""
+    dt, rows, d = _rows(x, "x")
+    dev, n = torch.cuda.current_device(), rows * d
+    _check(_lib.moe_layer_norm(
+        rows, d, _DTYPE[dt], _arg(x, dt, "x", n, dev), _arg(add, _bf16, "add", n, dev),
+        _arg(gamma, _f32, "gamma", d, dev), _arg(beta, _f32, "beta", d, dev), eps,
+        _arg(x_sum, dt, "x_sum", n, dev), _arg(y, _bf16, "y", n, dev),
+        _arg(mean, _f32, "mean", rows, dev), _arg(rstd, _f32, "rstd", rows, dev), _stream(stream)),
+        "moe_layer_norm")
+
+
+def layer_norm_backward_workspace_bytes(rows, d):
+    return int(_lib.moe_layer_norm_backward_workspace_bytes(rows, d))
+
+
+def layer_norm_backward(x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, ws, stream=None):
+    """dx = dres + the norm's input gradient, dgamma, dbeta (include/moe_block.h).  x and
+    dy are bf16 or fp32 each, dres and dx of one type; gamma, dres, dgamma and dbeta may
+    be None."""
+    dt, rows, d = _rows(x, "x")
+    yt, gt = _float_type(dy, "dy"), _float_type(dx, "dx")
+    dev, n = torch.cuda.current_device(), rows * d
+    wp, wn = _ws(ws, dev)
+    _check(_lib.moe_layer_norm_backward(
+        rows, d, _DTYPE[dt], _arg(x, dt, "x", n, dev), _DTYPE[yt], _arg(dy, yt, "dy", n, dev),
+        _arg(gamma, _f32, "gamma", d, dev), _arg(mean, _f32, "mean", rows, dev),
+        _arg(rstd, _f32, "rstd", rows, dev), _DTYPE[gt], _arg(dres, gt, "dres", n, dev),
+        _arg(dx, gt, "dx", n, dev), _arg(dgamma, _f32, "dgamma", d, dev),
+        _arg(dbeta, _f32, "dbeta", d, dev), wp, wn, _stream(stream)), "moe_layer_norm_backward")
+
+
+# ------------------------------------------------------------ balance loss --
+
+def balance_loss_workspace_bytes(shape):
+    return int(_lib.moe_balance_loss_workspace_bytes(ctypes.byref(shape)))
+
+
+def balance_loss(shape, logits, topk_idx, token_mask, expert_count, token_count, expert_prob, lse,
+                 losses, ws, stream=None):
+    """losses = (balance loss, z loss) with the counts, mean probabilities and log sums
+    that their gradient needs (include/moe_block.h).  token_mask [T] uint8 or None."""
+    T, N, K = shape.T, shape.N, shape.K
+    dev = torch.cuda.current_device()
+    wp, wn = _ws(ws, dev)
+    _check(_lib.moe_balance_loss(
+        ctypes.byref(shape), _arg(logits, _f32, "logits", T * N, dev),
+        _arg(topk_idx, _i32, "topk_idx", T * K, dev), _arg(token_mask, _u8, "token_mask", T, dev),
+        _arg(expert_count, _i32, "expert_count", N, dev),
+        _arg(token_count, _i32, "token_count", 1, dev),
+        _arg(expert_prob, _f32, "expert_prob", N, dev), _arg(lse, _f32, "lse", T, dev),
+        _arg(losses, _f32, "losses", 2, dev), wp, wn, _stream(stream)), "moe_balance_loss")
+
+
+def balance_loss_backward(shape, logits, topk_idx, token_mask, expert_count, token_count, lse,
+                          dlosses, dlogit, dlogits, stream=None):
+    """dlogits [T, N] of both losses, plus the gates' dlogit [T, K] (or None) at the chosen
+    experts (include/moe_block.h)."""
+    T, N, K = shape.T, shape.N, shape.K
+    dev = torch.cuda.current_device()
+    _check(_lib.moe_balance_loss_backward(
+        ctypes.byref(shape), _arg(logits, _f32, "logits", T * N, dev),
+        _arg(topk_idx, _i32, "topk_idx", T * K, dev), _arg(token_mask, _u8, "token_mask", T, dev),
+        _arg(expert_count, _i32, "expert_count", N, dev),
+        _arg(token_count, _i32, "token_count", 1, dev), _arg(lse, _f32, "lse", T, dev),
+        _arg(dlosses, _f32, "dlosses", 2, dev), _arg(dlogit, _f32, "dlogit", T * K, dev),
+        _arg(dlogits, _f32, "dlogits", T * N, dev), _stream(stream)), "moe_balance_loss_backward")
+
+
+def router_dense_backward_workspace_bytes(shape):
+    return int(_lib.moe_router_dense_backward_workspace_bytes(ctypes.byref(shape)))
+
+
+def router_dense_backward(shape, x, w_router, dlogits, dx_in, dx, dw_router, dbias, ws,
+                          stream=None):
+    """dx = dx_in + dlogits W, dw_router = dlogits^T x, dbias = column sums; dx_in may be
+    None or dx itself, and each output may be None (include/moe_block.h)."""
+    T, d, N = shape.T, shape.d, shape.N
+    dev = torch.cuda.current_device()
+    wp, wn = _ws(ws, dev)
+    _check(_lib.moe_router_dense_backward(
+        ctypes.byref(shape), _arg(x, _bf16, "x", T * d, dev),
+        _arg(w_router, _f32, "w_router", N * d, dev), _arg(dlogits, _f32, "dlogits", T * N, dev),
+        _arg(dx_in, _f32, "dx_in", T * d, dev), _arg(dx, _f32, "dx", T * d, dev),
+        _arg(dw_router, _f32, "dw_router", N * d, dev), _arg(dbias, _f32, "dbias", N, dev), wp, wn,
+        _stream(stream)), "moe_router_dense_backward")
+
+
+# ------------------------------------------------------- 8-bit checkpoints --
+
+def checkpoint_save(shape, expert_offset, g_save, u_save, y_disp, g_q, g_scale, u_q, u_scale, y_q,
+                    y_scale, stream=None):
+    """The valid rows of g_save, u_save and y_disp in MXINT8 (include/moe_block.h); a
+    source that is None is left out."""
+    h, d, R = shape.h, shape.d, shape.R
+    dev = torch.cuda.current_device()
+    _check(_lib.moe_checkpoint_save(
+        ctypes.byref(shape), _arg(expert_offset, _i32, "expert_offset", shape.N + 1, dev),
+        _arg(g_save, _bf16, "g_save", R * h, dev), _arg(u_save, _bf16, "u_save", R * h, dev),
+        _arg(y_disp, _bf16, "y_disp", R * d, dev), _arg(g_q, _i8, "g_q", R * h, dev),
+        _arg(g_scale, _u8, "g_scale", R * h // 32, dev), _arg(u_q, _i8, "u_q", R * h, dev),
+        _arg(u_scale, _u8, "u_scale", R * h // 32, dev), _arg(y_q, _i8, "y_q", R * d, dev),
+        _arg(y_scale, _u8, "y_scale", R * d // 32, dev), _stream(stream)), "moe_checkpoint_save")
+
+
+def checkpoint_restore(shape, expert_offset, g_q, g_scale, u_q, u_scale, g_save, u_save, h_act,
+                       stream=None):
+    """g_save, u_save and h_act = silu(G) U of a checkpoint (include/moe_block.h)."""
+    n, dev = shape.R * shape.h, torch.cuda.current_device()
+    _check(_lib.moe_checkpoint_restore(
+        ctypes.byref(shape), _arg(expert_offset, _i32, "expert_offset", shape.N + 1, dev),
+        _arg(g_q, _i8, "g_q", n, dev), _arg(g_scale, _u8, "g_scale", n // 32, dev),
+        _arg(u_q, _i8, "u_q", n, dev), _arg(u_scale, _u8, "u_scale", n // 32, dev),
+        _arg(g_save, _bf16, "g_save", n, dev), _arg(u_save, _bf16, "u_save", n, dev),
+        _arg(h_act, _bf16, "h_act", n, dev), _stream(stream)), "moe_checkpoint_restore")
+
+
+def combine_backward_checkpoint(shape, dy, y_q, y_scale, route_row, topk_gate, dy_disp, dgate,
+                                stream=None):
+    """combine_backward with y_disp read from its checkpoint (include/moe_block.h)."""
+    T, d, K, R = shape.T, shape.d, shape.K, shape.R
+    dev = torch.cuda.current_device()
+    _check(_lib.moe_combine_backward_checkpoint(
+        ctypes.byref(shape), _arg(dy, _bf16, "dy", T * d, dev), _arg(y_q, _i8, "y_q", R * d, dev),
+        _arg(y_scale, _u8, "y_scale", R * d // 32, dev),
+        _arg(route_row, _i32, "route_row", T * K, dev),
+        _arg(topk_gate, _f32, "topk_gate", T * K, dev), _arg(dy_disp, _bf16, "dy_disp", R * d, dev),
+        _arg(dgate, _f32, "dgate", T * K, dev), _stream(stream)), "moe_combine_backward_checkpoint")

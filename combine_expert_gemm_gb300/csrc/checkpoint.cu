@@ -1,0 +1,286 @@
+// Activation checkpoints in MXINT8 and the backward steps that read them
+// (include/moe_block.h).
+//
+// Block of 32 elements along a row: E = floor(log2 max|v|) >= -127, codes
+// c = rne(v 2^(6-E)) held to +-127, value c 2^(E-6).  v 2^(6-E) is exact in
+// fp32 (a power-of-two multiple of a bf16), so the rounding decision, and
+// with it every code, is a function of the input alone; the value has at most
+// 7 significant bits and is exact in bf16.
+//
+// A lane takes 8 elements (16 bytes of bf16), a block is four lanes.  All
+// kernels are bound by HBM.
+#include "../../include/moe_block.h"
+#include "moe_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kCkThreads = 256;
+constexpr int kCkBlock = 32;
+
+// |v| of both bf16 halves of a word, as two 16-bit integers; the larger of
+// each pair orders like the magnitudes (NaN above infinity above the rest).
+__device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
+    return __vmaxu2(a & 0x7FFF7FFFu, b & 0x7FFF7FFFu);
+}
+
+// Scale byte of the block held by this lane and its three neighbours.
+__device__ __forceinline__ uint32_t block_byte(const uint4 &v) {
+    uint32_t m = abs_max2(v.x, v.y);
+    m = __vmaxu2(m, abs_max2(v.z, v.w));
+    m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    return max(m & 0xFFFFu, m >> 16) >> 7;  // the exponent field, E + 127
+}
+
+// 2^(127 - byte), that is 2^-E, for byte <= 254.
+__device__ __forceinline__ float inv_scale(uint32_t byte) {
+    return byte == 254u ? __uint_as_float(0x00400000u) : __uint_as_float((254u - byte) << 23);
+}
+
+__device__ __forceinline__ int code_of(float v, float inv) {
+    const int c = __float2int_rn(v * inv * 64.f);
+    return max(-127, min(127, c));
+}
+
+__device__ __forceinline__ uint32_t code2(uint32_t w, float inv) {
+    return (uint32_t)(code_of(bf16_lo(w), inv) & 0xFF) |
+           ((uint32_t)(code_of(bf16_hi(w), inv) & 0xFF) << 8);
+}
+
+__device__ __forceinline__ uint2 codes8(const uint4 &v, uint32_t byte) {
+    if (byte == 255u) return make_uint2(0u, 0u);
+    const float inv = inv_scale(byte);
+    return make_uint2(code2(v.x, inv) | (code2(v.y, inv) << 16),
+                      code2(v.z, inv) | (code2(v.w, inv) << 16));
+}
+
+// 2^(byte - 133), the value of one code step; NaN for byte 255.
+__device__ __forceinline__ float code_step(uint32_t byte) {
+    if (byte == 255u) return __uint_as_float(0x7FC00000u);
+    return e8m0_value(byte) * 0.015625f;
+}
+
+__device__ __forceinline__ void values8(const uint2 &q, float step, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[i] = (float)(int8_t)(q.x >> (8 * i)) * step;
+        f[4 + i] = (float)(int8_t)(q.y >> (8 * i)) * step;
+    }
+}
+
+// silu(z) = z / (1 + exp(-z)) from exp(-|z|) <= 1, which never overflows: with
+// exp(-z) a z below -88 would give 0 where z exp(z) is still a normal number.
+__device__ __forceinline__ float silu(float z) {
+    const float t = __expf(-fabsf(z));
+    const float r = __fdividef(1.f, 1.f + t);
+    return z * (z < 0.f ? t * r : r);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+struct SaveBuf {
+    const uint4 *src;
+    uint2 *q;
+    uint8_t *scale;
+    int chunks;  // 8-element chunks per row, a multiple of 4; 0: left out
+};
+struct SaveBufs {
+    SaveBuf b[3];
+};
+
+// The valid rows of a packed buffer are one contiguous run of chunks.
+__global__ void __launch_bounds__(kCkThreads)
+checkpoint_save_rows(const int32_t *__restrict__ offset, int N, int64_t R, const SaveBufs bufs) {
+    pdl_enter();
+    const int64_t A = min((int64_t)max(offset[N], 0), R);
+    const int64_t stride = (int64_t)gridDim.x * kCkThreads;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const SaveBuf b = bufs.b[i];
+        const int64_t n = A * b.chunks;
+        // whole warps step together: the shuffles need every lane
+        for (int64_t c0 = (int64_t)blockIdx.x * kCkThreads + (threadIdx.x & ~31); c0 < n; c0 += stride) {
+            const int64_t c = c0 + (threadIdx.x & 31);
+            const uint4 v = c < n ? __ldcs(b.src + c) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t byte = block_byte(v);
+            if (c >= n) continue;
+            b.q[c] = codes8(v, byte);
+            if ((c & 3) == 0) b.scale[c >> 2] = (uint8_t)byte;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kCkThreads)
+checkpoint_restore_rows(const int32_t *__restrict__ offset, int N, int64_t R, int chunks,
+                        const uint2 *__restrict__ g_q, const uint8_t *__restrict__ g_scale,
+                        const uint2 *__restrict__ u_q, const uint8_t *__restrict__ u_scale,
+                        uint4 *__restrict__ g_save, uint4 *__restrict__ u_save,
+                        uint4 *__restrict__ h_act) {
+    pdl_enter();
+    const int64_t n = min((int64_t)max(offset[N], 0), R) * chunks;
+    const int64_t stride = (int64_t)gridDim.x * kCkThreads;
+    for (int64_t c = (int64_t)blockIdx.x * kCkThreads + threadIdx.x; c < n; c += stride) {
+        float g[8], u[8], h[8];
+        values8(g_q[c], code_step(g_scale[c >> 2]), g);
+        values8(u_q[c], code_step(u_scale[c >> 2]), u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = silu(g[i]) * u[i];
+        g_save[c] = pack8(g);
+        u_save[c] = pack8(u);
+        h_act[c] = pack8(h);
+    }
+}
+
+// One warp per token, as moe_combine_backward's kernel: for each chunk of the
+// token's dy the K route rows' codes are read at once, and the K partial dot
+// products stay in registers.
+constexpr int kTokWarps = 8;
+
+template <int MAXK>
+__global__ void __launch_bounds__(kTokWarps * 32)
+combine_bwd_checkpoint_rows(int T, int nchunk, int K, const uint4 *__restrict__ dy,
+                            const uint2 *__restrict__ y_q, const uint8_t *__restrict__ y_scale,
+                            const int32_t *__restrict__ route_row, const float *__restrict__ gate,
+                            uint4 *__restrict__ dy_disp, float *__restrict__ dgate) {
+    pdl_enter();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * kTokWarps + (threadIdx.x >> 5);
+    if (t >= T) return;
+    const int32_t my_row = lane < K ? route_row[t * K + lane] : -1;
+    const float my_g = lane < K ? gate[t * K + lane] : 0.0f;
+    int32_t rows[MAXK];
+    float gs[MAXK], part[MAXK];
+#pragma unroll
+    for (int k = 0; k < MAXK; ++k) {
+        rows[k] = __shfl_sync(0xFFFFFFFFu, my_row, k);
+        gs[k] = __shfl_sync(0xFFFFFFFFu, my_g, k);
+        part[k] = 0.0f;
+    }
+    for (int c = lane; c < nchunk; c += 32) {
+        const uint4 w = dy[t * nchunk + c];
+        const float f[8] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y),
+                            bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
+        uint2 q[MAXK];
+        uint32_t sc[MAXK];
+#pragma unroll
+        for (int k = 0; k < MAXK; ++k)
+            if (k < K && rows[k] >= 0) {
+                const int64_t at = (int64_t)rows[k] * nchunk + c;
+                q[k] = __ldcs(y_q + at);
+                sc[k] = y_scale[at >> 2];
+            }
+#pragma unroll
+        for (int k = 0; k < MAXK; ++k) {
+            if (k >= K || rows[k] < 0) continue;
+            float o[8], pr[8];
+            values8(q[k], code_step(sc[k]), o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                pr[i] = __fmul_rn(gs[k], f[i]);
+                part[k] = __fmaf_rn(f[i], o[i], part[k]);
+            }
+            dy_disp[(int64_t)rows[k] * nchunk + c] = pack8(pr);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < MAXK; ++k) {
+        if (k >= K) break;
+        float v = part[k];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+        if (lane == 0) dgate[t * K + k] = rows[k] >= 0 ? v : 0.0f;
+    }
+}
+
+inline int ck_grid(int64_t chunks) {
+    const int64_t want = (chunks + kCkThreads - 1) / kCkThreads, most = (int64_t)num_sms() * 8;
+    return (int)(want < most ? want : most);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+MOE_API moe_status moe_checkpoint_save(const moe_shape *s, const int32_t *expert_offset,
+                                       const moe_bf16 *g_save, const moe_bf16 *u_save,
+                                       const moe_bf16 *y_disp, int8_t *g_q, uint8_t *g_scale,
+                                       int8_t *u_q, uint8_t *u_scale, int8_t *y_q, uint8_t *y_scale,
+                                       cudaStream_t stream) {
+    moe_status r = check_shape(s);
+    if (r != MOE_OK) return r;
+    if (s->d % kCkBlock != 0 || s->h % kCkBlock != 0) return MOE_ERR_UNSUPPORTED;
+    const int64_t R = buffer_rows(s);
+    if (R == 0) return MOE_OK;
+    if (!expert_offset || (g_save && (!g_q || !g_scale)) || (u_save && (!u_q || !u_scale)) ||
+        (y_disp && (!y_q || !y_scale)))
+        return MOE_ERR_INVALID_ARG;
+    const void *ptrs[] = {expert_offset, g_save, u_save, y_disp, g_q, g_scale, u_q, u_scale, y_q,
+                          y_scale};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
+    const moe_bf16 *src[3] = {g_save, u_save, y_disp};
+    int8_t *q[3] = {g_q, u_q, y_q};
+    uint8_t *sc[3] = {g_scale, u_scale, y_scale};
+    SaveBufs bufs;
+    int64_t most = 0;
+    for (int i = 0; i < 3; ++i) {
+        const int chunks = src[i] ? (i < 2 ? s->h : s->d) / 8 : 0;
+        bufs.b[i] = SaveBuf{reinterpret_cast<const uint4 *>(src[i]), reinterpret_cast<uint2 *>(q[i]),
+                            sc[i], chunks};
+        if (R * chunks > most) most = R * chunks;
+    }
+    if (most == 0) return MOE_OK;
+    launch_pdl(checkpoint_save_rows, ck_grid(most), kCkThreads, 0, stream, expert_offset, s->N, R, bufs);
+    return launch_status();
+}
+
+MOE_API moe_status moe_checkpoint_restore(const moe_shape *s, const int32_t *expert_offset,
+                                          const int8_t *g_q, const uint8_t *g_scale,
+                                          const int8_t *u_q, const uint8_t *u_scale,
+                                          moe_bf16 *g_save, moe_bf16 *u_save, moe_bf16 *h_act,
+                                          cudaStream_t stream) {
+    moe_status r = check_shape(s);
+    if (r != MOE_OK) return r;
+    if (s->d % kCkBlock != 0 || s->h % kCkBlock != 0) return MOE_ERR_UNSUPPORTED;
+    const int64_t R = buffer_rows(s);
+    if (R == 0) return MOE_OK;
+    const void *ptrs[] = {expert_offset, g_q, g_scale, u_q, u_scale, g_save, u_save, h_act};
+    for (const void *p : ptrs)
+        if (!p) return MOE_ERR_INVALID_ARG;
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
+    const int chunks = s->h / 8;
+    launch_pdl(checkpoint_restore_rows, ck_grid(R * chunks), kCkThreads, 0, stream, expert_offset,
+               s->N, R, chunks, reinterpret_cast<const uint2 *>(g_q), g_scale,
+               reinterpret_cast<const uint2 *>(u_q), u_scale, reinterpret_cast<uint4 *>(g_save),
+               reinterpret_cast<uint4 *>(u_save), reinterpret_cast<uint4 *>(h_act));
+    return launch_status();
+}
+
+MOE_API moe_status moe_combine_backward_checkpoint(const moe_shape *s, const moe_bf16 *dy,
+                                                   const int8_t *y_q, const uint8_t *y_scale,
+                                                   const int32_t *route_row,
+                                                   const float *topk_gate, moe_bf16 *dy_disp,
+                                                   float *dgate, cudaStream_t stream) {
+    moe_status r = check_shape(s);
+    if (r != MOE_OK) return r;
+    if (s->d % kCkBlock != 0 || s->h % kCkBlock != 0) return MOE_ERR_UNSUPPORTED;
+    if (s->T == 0) return MOE_OK;
+    if (!dy || !route_row || !topk_gate || !dgate ||
+        (s->cap > 0 && (!y_q || !y_scale || !dy_disp)))
+        return MOE_ERR_INVALID_ARG;
+    const void *ptrs[] = {dy, y_q, y_scale, route_row, topk_gate, dy_disp, dgate};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
+    auto *kern = s->K <= 8 ? combine_bwd_checkpoint_rows<8> : combine_bwd_checkpoint_rows<16>;
+    const int grid = (int)(((int64_t)s->T + kTokWarps - 1) / kTokWarps);
+    launch_pdl(kern, grid, kTokWarps * 32, 0, stream, s->T, s->d / 8, s->K,
+               reinterpret_cast<const uint4 *>(dy), reinterpret_cast<const uint2 *>(y_q), y_scale,
+               route_row, topk_gate, reinterpret_cast<uint4 *>(dy_disp), dgate);
+    return launch_status();
+}
