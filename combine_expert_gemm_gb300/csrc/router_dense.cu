@@ -1,102 +1,705 @@
 // The router's products for a gradient of every logit (include/moe_block.h):
 //   dx = dx_in + dl W;  dW = dl^T x;  dbias = column sums of dl
 // with dl [T, N] fp32, W [N, d] fp32, x [T, d] bf16.
+//
+// Both products are skinny (N experts deep or wide against d columns), so what
+// they cannot do without is the traffic of dx_in, dx and x: 10 bytes per token
+// and column against 4 N fp32 operations.  On the fp32 pipes the operations
+// would take longer than the bytes (the simple kernel of 32 fused multiply-adds
+// per load took 1747 us where the bytes take 199: T = 32768, d = 4096, N = 32),
+// so the products run on the tensor cores, with fp32 accuracy from bf16 pieces:
+//   v = v0 + v1 + v2,  v0 = bf16(v), v1 = bf16(v - v0), v2 = bf16(v - v0 - v1)
+// holds all 24 bits of an fp32 value, the residuals are exact, and a product
+// of two bf16 values is exact in the fp32 accumulator.  dl W sums the six piece
+// products whose size is at least 2^-16 of the leading one (what is left out is
+// below 2^-24 of it); dl^T x needs three, x being bf16 already.
+//
+// Launches: router_dense_prep writes the pieces (dl's transposed, so that both
+// products read them in a layout of the tensor cores) and partial sums of
+// dbias; router_dense_dx and router_dense_dw are the products; the last adds
+// dw's and dbias' partial sums in a fixed order.
+#include <algorithm>
+
 #include "../../include/moe_block.h"
 #include "moe_common.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kRdCols = 256;    // threads per CTA, one output column each
-constexpr int kRdTok = 32;      // tokens per CTA of the dx kernel
-constexpr int kRdExp = 16;      // experts per CTA of the dW kernel
-constexpr int kRdChunk = 64;    // experts or tokens staged at a time
-constexpr int kRdSplits = 32;   // token splits of dW
+constexpr int kSms = 152;  // the machine the work is split for (results do not depend on it)
 
-__global__ void __launch_bounds__(kRdCols)
-router_dense_dx(int T, int N, int d, const float *__restrict__ dl, const float *__restrict__ w,
-                const float *dx_in, float *dx) {
-    pdl_enter();
-    __shared__ float sm[kRdTok][kRdChunk];
-    const int col = blockIdx.y * kRdCols + threadIdx.x;
-    const int64_t t0 = (int64_t)blockIdx.x * kRdTok;
-    float acc[kRdTok];
-#pragma unroll
-    for (int i = 0; i < kRdTok; ++i) acc[i] = 0.f;
-    for (int e0 = 0; e0 < N; e0 += kRdChunk) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < kRdTok * kRdChunk; i += kRdCols) {
-            const int64_t t = t0 + i / kRdChunk;
-            const int e = e0 + i % kRdChunk;
-            sm[i / kRdChunk][i % kRdChunk] = t < T && e < N ? dl[t * N + e] : 0.f;
-        }
-        __syncthreads();
-        if (col >= d) continue;
-        for (int j = 0; j < kRdChunk && e0 + j < N; ++j) {
-            const float v = w[(int64_t)(e0 + j) * d + col];
-#pragma unroll
-            for (int i = 0; i < kRdTok; ++i) acc[i] = fmaf(sm[i][j], v, acc[i]);
-        }
+// ------------------------------------------------------------------ pieces --
+
+struct Pieces {
+    uint16_t p[3];
+};
+
+// The three bf16 pieces of v.  Past the largest bf16 the first piece is cut
+// instead of rounded, so that it stays finite; a non-finite v is its own first
+// piece and the others are 0.
+__device__ __forceinline__ Pieces split3(float v) {
+    Pieces r;
+    if ((__float_as_uint(v) & 0x7F800000u) == 0x7F800000u) {
+        const __nv_bfloat16 b = __float2bfloat16_rn(v);
+        r.p[0] = *reinterpret_cast<const uint16_t *>(&b);
+        r.p[1] = r.p[2] = 0;
+        return r;
     }
-    if (col >= d) return;
 #pragma unroll
-    for (int i = 0; i < kRdTok; ++i) {
-        const int64_t t = t0 + i;
-        if (t < T) dx[t * d + col] = (dx_in ? dx_in[t * d + col] : 0.f) + acc[i];
+    for (int i = 0; i < 3; ++i) {
+        const __nv_bfloat16 b = __float2bfloat16_rn(v);
+        uint32_t w = *reinterpret_cast<const uint16_t *>(&b);
+        if ((w & 0x7F80u) == 0x7F80u) w = __float_as_uint(v) >> 16;
+        r.p[i] = (uint16_t)w;
+        v -= __uint_as_float(w << 16);
+    }
+    return r;
+}
+
+constexpr int kPrepThreads = 256;
+constexpr int kPrepTok = 64;  // tokens of a transposed block
+constexpr int kPrepExp = 32;  // experts of a transposed block
+
+// blockIdx.y < chunks: dl's pieces dlp[3][N][Tp] of 32 experts, the token
+// blocks of 64 strided over blockIdx.x, and those tokens' sums in
+// db_part[blockIdx.x][N].  blockIdx.y == chunks: W's pieces wp[3][N][dp].
+// Columns from T to Tp and from d to dp are zeros.
+__global__ void __launch_bounds__(kPrepThreads)
+router_dense_prep(int T, int64_t Tp, int N, int d, int dp, int chunks, const float *__restrict__ dl,
+                  const float *__restrict__ w, uint16_t *__restrict__ dlp,
+                  uint16_t *__restrict__ wp, float *__restrict__ db_part) {
+    pdl_enter();
+    __shared__ float tile[kPrepTok][kPrepExp + 1];
+    if ((int)blockIdx.y == chunks) {
+        const int per = dp / 8;
+        const int64_t n = (int64_t)N * per, plane = (int64_t)N * dp;
+        for (int64_t i = (int64_t)blockIdx.x * kPrepThreads + threadIdx.x; i < n;
+             i += (int64_t)gridDim.x * kPrepThreads) {
+            const int64_t e = i / per;
+            const int c = (int)(i % per) * 8;
+            float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (c < d) {
+                const float4 *src = reinterpret_cast<const float4 *>(w + e * d + c);
+                const float4 a = src[0], b = src[1];
+                f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+                f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+            }
+            uint32_t o[3][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const Pieces lo = split3(f[2 * q]), hi = split3(f[2 * q + 1]);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) o[p][q] = (uint32_t)lo.p[p] | ((uint32_t)hi.p[p] << 16);
+            }
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+                *reinterpret_cast<uint4 *>(wp + p * plane + e * dp + c) =
+                    make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
+        }
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int e0 = blockIdx.y * kPrepExp;
+    const int64_t plane = (int64_t)N * Tp;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int64_t t0 = (int64_t)blockIdx.x * kPrepTok; t0 < Tp; t0 += (int64_t)gridDim.x * kPrepTok) {
+        // warp w loads tokens w, w + 8, ..., a lane per expert
+#pragma unroll
+        for (int i = 0; i < kPrepTok / 8; ++i) {
+            const int64_t t = t0 + warp + 8 * i;
+            tile[warp + 8 * i][lane] = t < T && e0 + lane < N ? dl[t * N + e0 + lane] : 0.f;
+        }
+        __syncthreads();
+        // warp w writes experts 4 w .. 4 w + 3, a lane per pair of tokens
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = e0 + 4 * warp + i;
+            const float a = tile[2 * lane][4 * warp + i], b = tile[2 * lane + 1][4 * warp + i];
+            sum[i] += a + b;
+            if (e >= N) continue;
+            const Pieces pa = split3(a), pb = split3(b);
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+                *reinterpret_cast<uint32_t *>(dlp + p * plane + (int64_t)e * Tp + t0 + 2 * lane) =
+                    (uint32_t)pa.p[p] | ((uint32_t)pb.p[p] << 16);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v = sum[i];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+        const int e = e0 + 4 * warp + i;
+        if (lane == 0 && e < N) db_part[(int64_t)blockIdx.x * N + e] = v;
     }
 }
 
-// part[split][N][d + 1]: column d holds the sums of dl (dbias).
-__global__ void __launch_bounds__(kRdCols)
-router_dense_dw(int T, int N, int d, const float *__restrict__ dl, const uint16_t *__restrict__ x,
-                float *__restrict__ part) {
-    pdl_enter();
-    __shared__ float sm[kRdChunk][kRdExp];
-    // without x only the extra column, dbias, is summed
-    const int col = x ? blockIdx.x * kRdCols + threadIdx.x : d + threadIdx.x;
-    const int e0 = blockIdx.y * kRdExp;
-    const int64_t per = ((int64_t)T + kRdSplits - 1) / kRdSplits;
-    const int64_t t0 = blockIdx.z * per, t1 = min((int64_t)T, t0 + per);
-    float acc[kRdExp];
-#pragma unroll
-    for (int i = 0; i < kRdExp; ++i) acc[i] = 0.f;
-    for (int64_t tc = t0; tc < t1; tc += kRdChunk) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < kRdChunk * kRdExp; i += kRdCols) {
-            const int64_t t = tc + i / kRdExp;
-            const int e = e0 + i % kRdExp;
-            sm[i / kRdExp][i % kRdExp] = t < t1 && e < N ? dl[t * N + e] : 0.f;
-        }
-        __syncthreads();
-        if (col > d) continue;
-        for (int j = 0; j < kRdChunk && tc + j < t1; ++j) {
-            const float v = col < d ? bf16_lo(x[(tc + j) * d + col]) : 1.f;
-#pragma unroll
-            for (int i = 0; i < kRdExp; ++i) acc[i] = fmaf(sm[j][i], v, acc[i]);
-        }
-    }
-    if (col > d) return;
-#pragma unroll
-    for (int i = 0; i < kRdExp; ++i)
-        if (e0 + i < N) part[((int64_t)blockIdx.z * N + e0 + i) * (d + 1) + col] = acc[i];
+// ------------------------------------------------------------ TMA and MMA --
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                            int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
 }
 
-__global__ void __launch_bounds__(kRdCols)
-router_dense_sum(int N, int d, const float *__restrict__ part, float *__restrict__ dw,
-                 float *__restrict__ dbias) {
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                            int32_t x, int32_t y, int32_t z, int32_t w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
+// MN-major operand, 128-byte swizzle: K rows of 128 bytes (64 M/N elements),
+// 8-row groups 1 KB apart, 64-element M/N blocks `block` bytes apart.
+__device__ __forceinline__ uint64_t mnmajor_desc(uint32_t smem_addr, uint32_t block) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(block >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+// As idesc_bf16_f32, with each operand K-major (0) or MN-major (1).
+__host__ __device__ constexpr uint32_t idesc_major(int M, int N, int a_mn, int b_mn) {
+    return idesc_bf16_f32(M, N) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16);
+}
+
+// Pieces [3][rows][inner] (inner a multiple of 64) as [3][inner / 64][rows][64]:
+// one box of 64 x box_rows x 2 blocks x 3 pieces lands piece by piece, block by
+// block, each block box_rows swizzled 128-byte rows.  Rows past the last read
+// as zeros.
+inline bool make_map_pieces_mn(CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows,
+                               uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {64, rows, inner / 64, 3};
+    const cuuint64_t strides[3] = {inner * 2, 128, inner * rows * 2};
+    const cuuint32_t box[4] = {64, box_rows, 2, 3};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pieces [3][rows][inner] read along inner: box 64 x box_rows x 3 pieces.
+inline bool make_map_pieces_k(CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows,
+                              uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {inner, rows, 3};
+    const cuuint64_t strides[2] = {inner * 2, inner * rows * 2};
+    const cuuint32_t box[3] = {64, box_rows, 3};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Row-major [rows, inner] fp32 in boxes of 32 x 32, 128-byte swizzle.
+inline bool make_map_f32(CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {inner, rows};
+    const cuuint64_t strides[1] = {inner * 4};
+    const cuuint32_t box[2] = {32, 32};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kGemmThreads = 64 + 256;  // producer warp, MMA warp, 8 epilogue warps
+constexpr int kEpiWarps = 8;
+
+// ---------------------------------------------------------------------- dx --
+//
+// Persistent CTAs, tiles of 128 tokens x 128 columns, columns fastest.  A
+// k-block is 32 experts: the three pieces of dl (24 KB) and of W (24 KB), both
+// MN-major, by one TMA request each.  The accumulator of a tile takes 128 of
+// the 512 tensor-memory columns, so four tiles are in flight between the MMA
+// thread and the epilogue.
+//
+// The epilogue's work is the traffic: each warp owns 32 tokens x 64 columns of
+// a tile and four 4 KB blocks of shared memory through which it streams 32 x 32
+// blocks of dx_in (TMA load, three blocks ahead), adds the accumulator in
+// place and stores the block to dx (TMA store).  No warp waits for another's
+// block, and 32 blocks of 4 KB cover the latency of the loads and stores.
+constexpr int kDxStages = 2;
+constexpr int kDxPiece = 2 * 32 * 128;              // 128 columns or tokens x 32 experts: 8 KB
+constexpr int kDxStageBytes = 2 * 3 * kDxPiece;     // 48 KB
+constexpr int kDxSlots = 4;
+constexpr int kDxAhead = kDxSlots - 1;
+constexpr int kDxBlk = 32 * 32 * 4;
+constexpr int kDxAcc = 4;
+
+struct alignas(8) DxBars {
+    uint64_t full[kDxStages];
+    uint64_t empty[kDxStages];
+    uint64_t tfull[kDxAcc];
+    uint64_t tempty[kDxAcc];
+    uint64_t in[kEpiWarps][kDxSlots];
+    uint32_t tmem_base;
+    int abort;
+};
+
+constexpr size_t kDxSmem =
+    1024 + (size_t)kDxStages * kDxStageBytes + (size_t)kEpiWarps * kDxSlots * kDxBlk + sizeof(DxBars);
+
+__global__ void __launch_bounds__(kGemmThreads, 1)
+router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant__ CUtensorMap tm_w,
+                const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_out,
+                int T, int N, int d, int has_in, int *status) {
     pdl_enter();
-    const int64_t n = (int64_t)N * (d + 1);
-    const int64_t i = (int64_t)blockIdx.x * kRdCols + threadIdx.x;
-    if (i >= n) return;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *blocks = smem + (size_t)kDxStages * kDxStageBytes;
+    DxBars *bars = reinterpret_cast<DxBars *>(blocks + (size_t)kEpiWarps * kDxSlots * kDxBlk);
+    volatile int *abort = &bars->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ntc = (d + 127) / 128, nk = (N + 31) / 32;
+    const int total = (int)(((int64_t)T + 127) / 128) * ntc;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kDxStages; ++s) {
+            mbar_init(smem_u32(&bars->full[s]), 1);
+            mbar_init(smem_u32(&bars->empty[s]), 1);
+        }
+        for (int a = 0; a < kDxAcc; ++a) {
+            mbar_init(smem_u32(&bars->tfull[a]), 1);
+            mbar_init(smem_u32(&bars->tempty[a]), kEpiWarps);
+        }
+        for (int w = 0; w < kEpiWarps; ++w)
+            for (int s = 0; s < kDxSlots; ++s) mbar_init(smem_u32(&bars->in[w][s]), 1);
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = bars->tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int g = blockIdx.x; g < total && ok; g += gridDim.x) {
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!mbar_wait(smem_u32(&bars->empty[stage]), phase ^ 1, status, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = smem_u32(&bars->full[stage]);
+                    const uint32_t sa = smem_u32(smem + (size_t)stage * kDxStageBytes);
+                    mbar_arrive_expect_tx(full, kDxStageBytes);
+                    tma_load_4d(sa, &tm_dl, full, 0, kb * 32, g / ntc * 2, 0);
+                    tma_load_4d(sa + 3 * kDxPiece, &tm_w, full, 0, kb * 32, g % ntc * 2, 0);
+                    ++issued;
+                    if (++stage == kDxStages) { stage = 0; phase ^= 1; }
+                }
+            }
+            // the copies in flight land before the CTA leaves
+            for (int i = max(0, issued - kDxStages); i < issued; ++i) {
+                volatile int no_abort = 0;
+                mbar_wait(smem_u32(&bars->full[i % kDxStages]), (uint32_t)(i / kDxStages & 1), status,
+                          &no_abort);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_major(128, 128, 1, 1);
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            for (int g = blockIdx.x; g < total && ok; g += gridDim.x) {
+                if (!mbar_wait(smem_u32(&bars->tempty[acc]), acc_phase ^ 1, status, abort)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * 128);
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!mbar_wait(smem_u32(&bars->full[stage]), phase, status, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + (size_t)stage * kDxStageBytes);
+                    const uint32_t sb = sa + 3 * kDxPiece;
+                    const int steps = min(2, (N - kb * 32 + 15) / 16);
+                    bool first = kb == 0;
+                    // the smallest piece products first
+#pragma unroll
+                    for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+                        for (int pa = 0; pa <= sum; ++pa)
+                            for (int kk = 0; kk < steps; ++kk) {
+                                tc_mma_bf16(d_tmem, mnmajor_desc(sa + pa * kDxPiece + kk * 2048, 4096),
+                                            mnmajor_desc(sb + (sum - pa) * kDxPiece + kk * 2048, 4096),
+                                            idesc, first ? 0u : 1u);
+                                first = false;
+                            }
+                    tc_commit(smem_u32(&bars->empty[stage]));
+                    if (++stage == kDxStages) { stage = 0; phase ^= 1; }
+                }
+                if (!ok) break;
+                tc_commit(smem_u32(&bars->tfull[acc]));
+                if (++acc == kDxAcc) { acc = 0; acc_phase ^= 1; }
+            }
+        }
+    } else {
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        uint8_t *mine = blocks + (size_t)(warp - 2) * kDxSlots * kDxBlk;
+        uint64_t *in = bars->in[warp - 2];
+        // This warp's blocks: two per tile, those that start inside dx.  The
+        // load cursor runs kDxAhead blocks ahead of the one being added.
+        auto block_at = [&](int g, int u, int &row, int &col) {
+            row = g / ntc * 128 + quad * 32;
+            col = g % ntc * 128 + half * 64 + u * 32;
+            return row < T && col < d;
+        };
+        int lg = blockIdx.x, lu = 0, loaded = 0, used = 0;
+        auto load_next = [&] {  // lane 0
+            while (lg < total) {
+                int row, col;
+                const bool valid = block_at(lg, lu, row, col);
+                if (++lu == 2) { lu = 0; lg += gridDim.x; }
+                if (!valid) continue;
+                const int s = loaded++ % kDxSlots;
+                const uint32_t bar = smem_u32(&in[s]);
+                mbar_arrive_expect_tx(bar, kDxBlk);
+                tma_load_2d(smem_u32(mine + s * kDxBlk), &tm_in, bar, col, row);
+                return;
+            }
+        };
+        if (has_in && lane == 0)
+            for (int i = 0; i < kDxAhead; ++i) load_next();
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        for (int g = blockIdx.x; g < total && ok; g += gridDim.x) {
+            if (!mbar_wait(smem_u32(&bars->tfull[acc]), acc_phase, status, abort)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                int row, col;
+                const bool valid = block_at(g, u, row, col);  // warp-uniform
+                uint32_t r0[16], r1[16];
+                const uint32_t at =
+                    tmem_base + ((uint32_t)(quad * 32) << 16) + acc * 128 + half * 64 + u * 32;
+                tmem_ld16(at, r0);
+                tmem_ld16(at + 16, r1);
+                tmem_ld_wait();
+                reg_fence(r0);
+                reg_fence(r1);
+                if (!valid) continue;
+                const int s = used % kDxSlots;
+                uint8_t *blk = mine + s * kDxBlk;
+                if (has_in) {
+                    if (!mbar_wait(smem_u32(&in[s]), (uint32_t)(used / kDxSlots & 1), status, abort)) {
+                        ok = false;
+                        break;
+                    }
+                } else {
+                    if (lane == 0) bulk_wait_read<kDxSlots - 1>();
+                    __syncwarp();
+                }
+                ++used;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const uint32_t *a = q < 4 ? &r0[4 * q] : &r1[4 * (q - 4)];
+                    float4 *at4 = reinterpret_cast<float4 *>(blk + lane * 128 + ((q ^ (lane & 7)) * 16));
+                    float4 v = has_in ? *at4 : make_float4(0.f, 0.f, 0.f, 0.f);
+                    v.x += __uint_as_float(a[0]);
+                    v.y += __uint_as_float(a[1]);
+                    v.z += __uint_as_float(a[2]);
+                    v.w += __uint_as_float(a[3]);
+                    *at4 = v;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(&tm_out, smem_u32(blk), col, row);
+                    bulk_commit();
+                    if (has_in) {
+                        // the next load's block is the one stored before this
+                        bulk_wait_read<1>();
+                        load_next();
+                    }
+                }
+            }
+            if (!ok) break;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc]));
+            if (++acc == kDxAcc) { acc = 0; acc_phase ^= 1; }
+        }
+        if (lane == 0) {
+            for (; used < loaded; ++used) {  // after an abort: loads still in flight
+                volatile int no_abort = 0;
+                mbar_wait(smem_u32(&in[used % kDxSlots]), (uint32_t)(used / kDxSlots & 1), status,
+                          &no_abort);
+            }
+            bulk_wait<0>();  // stores complete before the CTA ends
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 512);
+    }
+}
+
+// ---------------------------------------------------------------------- dW --
+//
+// The transposed product dW^T = x^T dl: 128 columns of x as the MMA's rows
+// (MN-major boxes of 64 columns x 64 tokens), NT experts as its columns (dl's
+// pieces along the tokens), the tokens as K in blocks of 64.  x is read once
+// per NT experts.  There are few output tiles, so the tokens are split over
+// CTAs and the partial sums added by the last kernel.
+//
+// The tensor core's accumulator keeps fp32 but cuts where an fp32 addition
+// rounds, so a long sum drifts; after every kDwGroup k-blocks (256 tokens) the
+// epilogue adds the accumulator to fp32 registers while the next group runs in
+// the other half of tensor memory.
+constexpr int kDwGroup = 4;
+constexpr int kDwA = 2 * 64 * 128;  // 128 columns x 64 tokens: 16 KB
+
+template <int NT>
+struct Dw {
+    static constexpr int ctas_per_sm = NT == 32 ? 2 : 1;
+    static constexpr int stages = NT == 32 ? 3 : NT == 64 ? 5 : 3;
+    static constexpr int piece = NT * 128;
+    static constexpr int stage_bytes = kDwA + 3 * piece;
+    static constexpr int tmem_cols = 2 * NT;
+    struct alignas(8) Bars {
+        uint64_t full[stages];
+        uint64_t empty[stages];
+        uint64_t tfull[2];
+        uint64_t tempty[2];
+        uint32_t tmem_base;
+        int abort;
+    };
+    static constexpr size_t smem = 1024 + (size_t)stages * stage_bytes + sizeof(Bars);
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kGemmThreads, Dw<NT>::ctas_per_sm)
+router_dense_dw(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_dl,
+                int T, int N, int d, float *__restrict__ part, int *status) {
+    using C = Dw<NT>;
+    pdl_enter();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    typename C::Bars *bars = reinterpret_cast<typename C::Bars *>(smem + (size_t)C::stages * C::stage_bytes);
+    volatile int *abort = &bars->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c0 = blockIdx.x * 128, e0 = blockIdx.y * NT;
+    const int nc = (int)(((int64_t)T + 63) / 64);
+    const int k0 = (int)((int64_t)nc * blockIdx.z / gridDim.z);
+    const int nk = (int)((int64_t)nc * (blockIdx.z + 1) / gridDim.z) - k0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::stages; ++s) {
+            mbar_init(smem_u32(&bars->full[s]), 1);
+            mbar_init(smem_u32(&bars->empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&bars->tfull[a]), 1);
+            mbar_init(smem_u32(&bars->tempty[a]), kEpiWarps);
+        }
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), C::tmem_cols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = bars->tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            for (int kb = 0; kb < nk; ++kb) {
+                if (!mbar_wait(smem_u32(&bars->empty[stage]), phase ^ 1, status, abort)) break;
+                const uint32_t full = smem_u32(&bars->full[stage]);
+                const uint32_t sa = smem_u32(smem + (size_t)stage * C::stage_bytes);
+                const int t = (k0 + kb) * 64;
+                mbar_arrive_expect_tx(full, C::stage_bytes);
+                tma_load_2d(sa, &tm_x, full, c0, t);
+                tma_load_2d(sa + kDwA / 2, &tm_x, full, c0 + 64, t);
+                tma_load_3d(sa + kDwA, &tm_dl, full, t, e0, 0);
+                ++issued;
+                if (++stage == C::stages) { stage = 0; phase ^= 1; }
+            }
+            for (int i = max(0, issued - C::stages); i < issued; ++i) {
+                volatile int no_abort = 0;
+                mbar_wait(smem_u32(&bars->full[i % C::stages]), (uint32_t)(i / C::stages & 1), status,
+                          &no_abort);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_major(128, NT, 1, 0);
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            for (int kb0 = 0; kb0 < nk && ok; kb0 += kDwGroup) {
+                if (!mbar_wait(smem_u32(&bars->tempty[acc]), acc_phase ^ 1, status, abort)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * NT);
+                for (int kb = kb0; kb < min(nk, kb0 + kDwGroup); ++kb) {
+                    if (!mbar_wait(smem_u32(&bars->full[stage]), phase, status, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + (size_t)stage * C::stage_bytes);
+                    const uint32_t sb = sa + kDwA;
+#pragma unroll
+                    for (int p = 2; p >= 0; --p)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_bf16(d_tmem, mnmajor_desc(sa + kk * 2048, kDwA / 2),
+                                        sw128_kmajor_desc(sb + p * C::piece + kk * 32), idesc,
+                                        kb == kb0 && p == 2 && kk == 0 ? 0u : 1u);
+                    tc_commit(smem_u32(&bars->empty[stage]));
+                    if (++stage == C::stages) { stage = 0; phase ^= 1; }
+                }
+                if (!ok) break;
+                tc_commit(smem_u32(&bars->tfull[acc]));
+                if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+            }
+        }
+    } else {
+        // TMEM lane = column of x; this warp's half of the experts
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        float sum[NT / 2];
+#pragma unroll
+        for (int j = 0; j < NT / 2; ++j) sum[j] = 0.f;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int kb0 = 0; kb0 < nk; kb0 += kDwGroup) {
+            if (!mbar_wait(smem_u32(&bars->tfull[acc]), acc_phase, status, abort)) break;
+            tc_fence_after();
+            const uint32_t at =
+                tmem_base + ((uint32_t)(quad * 32) << 16) + acc * NT + half * (NT / 2);
+#pragma unroll
+            for (int j = 0; j < NT / 2; j += 16) {
+                uint32_t r[16];
+                tmem_ld16(at + j, r);
+                tmem_ld_wait();
+                reg_fence(r);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[j + i] += __uint_as_float(r[i]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc]));
+            if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+        }
+        const int col = c0 + quad * 32 + lane;
+        if (col < d) {
+            float *o = part + ((int64_t)blockIdx.z * N + e0 + half * (NT / 2)) * d + col;
+#pragma unroll
+            for (int j = 0; j < NT / 2; ++j)
+                if (e0 + half * (NT / 2) + j < N) o[(int64_t)j * d] = sum[j];
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, C::tmem_cols);
+    }
+}
+
+// ------------------------------------------------------------- last sums --
+
+constexpr int kSumThreads = 256;
+
+// dw = sum of the splits, four columns a thread; dbias = sum of the prep
+// CTAs, one warp per expert (a lane every 32nd partial sum).
+__global__ void __launch_bounds__(kSumThreads)
+router_dense_sum(int64_t n4, int splits, const float4 *__restrict__ part, float4 *__restrict__ dw,
+                 int N, int groups, const float *__restrict__ db_part, float *__restrict__ dbias,
+                 int dw_blocks) {
+    pdl_enter();
+    if ((int)blockIdx.x < dw_blocks) {
+        const int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x;
+        if (i >= n4) return;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < splits; ++s) {
+            const float4 p = part[s * n4 + i];
+            v.x += p.x;
+            v.y += p.y;
+            v.z += p.z;
+            v.w += p.w;
+        }
+        dw[i] = v;
+        return;
+    }
+    const int e = ((int)blockIdx.x - dw_blocks) * (kSumThreads / 32) + (threadIdx.x >> 5);
+    if (e >= N) return;
     float v = 0.f;
-    for (int s = 0; s < kRdSplits; ++s) v += part[s * n + i];
-    const int64_t e = i / (d + 1);
-    const int c = (int)(i % (d + 1));
-    if (c < d) {
-        if (dw) dw[e * d + c] = v;
-    } else if (dbias) {
-        dbias[e] = v;
-    }
+    for (int g = threadIdx.x & 31; g < groups; g += 32) v += db_part[(int64_t)g * N + e];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+    if ((threadIdx.x & 31) == 0) dbias[e] = v;
+}
+
+// ------------------------------------------------------------------- host --
+
+// How the work of one shape is split, and where the workspace holds what.
+struct Plan {
+    int64_t Tp;
+    int dp, chunks, groups, nt, splits;
+    size_t dlp, wp, db, part, bytes;
+};
+
+inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+Plan plan_of(const moe_shape *s) {
+    Plan p;
+    p.Tp = ((int64_t)s->T + 63) / 64 * 64;
+    p.dp = (s->d + 63) / 64 * 64;
+    p.chunks = (s->N + kPrepExp - 1) / kPrepExp;
+    p.groups = (int)std::max<int64_t>(1, std::min<int64_t>(p.Tp / kPrepTok, 4 * kSms / p.chunks));
+    p.nt = s->N <= 32 ? 32 : s->N <= 64 ? 64 : 128;
+    const int64_t tiles = (int64_t)((s->d + 127) / 128) * ((s->N + p.nt - 1) / p.nt);
+    const int64_t room = kSms * (p.nt == 32 ? 2 : 1);
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(p.Tp / 64, room / tiles));
+    p.dlp = 256;
+    p.wp = p.dlp + align256((size_t)3 * s->N * p.Tp * 2);
+    p.db = p.wp + align256((size_t)3 * s->N * p.dp * 2);
+    p.part = p.db + align256((size_t)p.groups * s->N * 4);
+    p.bytes = p.part + align256((size_t)p.splits * s->N * s->d * 4);
+    return p;
+}
+
+template <int NT>
+moe_status launch_dw(const CUtensorMap &mx, const CUtensorMap &mdl, const moe_shape *s, int splits,
+                     float *part, int *status, cudaStream_t stream) {
+    static PerDeviceOnce smem_attr;
+    if (!device_once(smem_attr, [] { return set_smem_limit(router_dense_dw<NT>, Dw<NT>::smem); }))
+        return MOE_ERR_CUDA;
+    launch_pdl(router_dense_dw<NT>,
+               dim3((s->d + 127) / 128, (s->N + NT - 1) / NT, (unsigned)splits), kGemmThreads,
+               Dw<NT>::smem, stream, mx, mdl, s->T, s->N, s->d, part, status);
+    return launch_status();
 }
 
 }  // namespace
@@ -106,7 +709,7 @@ using namespace moe;
 
 MOE_API size_t moe_router_dense_backward_workspace_bytes(const moe_shape *s) {
     if (check_shape(s) != MOE_OK) return 0;
-    return 256 + (size_t)kRdSplits * s->N * (s->d + 1) * sizeof(float);
+    return plan_of(s).bytes;
 }
 
 MOE_API moe_status moe_router_dense_backward(const moe_shape *s, const moe_bf16 *x,
@@ -121,23 +724,51 @@ MOE_API moe_status moe_router_dense_backward(const moe_shape *s, const moe_bf16 
     const void *ptrs[] = {x, w_router, dlogits, dx_in, dx, dw_router, dbias};
     for (const void *p : ptrs)
         if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
-    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) ||
-        ws_bytes < moe_router_dense_backward_workspace_bytes(s))
+    const Plan pl = plan_of(s);
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < pl.bytes)
         return MOE_ERR_WORKSPACE;
-    const int T = s->T, N = s->N, d = s->d;
     if (!dx && !dw_router && !dbias) return MOE_OK;
-    if (dx && T > 0)
-        launch_pdl(router_dense_dx, dim3((T + kRdTok - 1) / kRdTok, (d + kRdCols - 1) / kRdCols),
-                   kRdCols, 0, stream, T, N, d, dlogits, w_router, dx_in, dx);
+    const int T = s->T, N = s->N, d = s->d;
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    int *status = static_cast<int *>(ws);
+    uint16_t *dlp = reinterpret_cast<uint16_t *>(base + pl.dlp);
+    uint16_t *wp = reinterpret_cast<uint16_t *>(base + pl.wp);
+    float *db = reinterpret_cast<float *>(base + pl.db);
+    float *part = reinterpret_cast<float *>(base + pl.part);
+    if (T > 0) {
+        launch_pdl(router_dense_prep, dim3(pl.groups, pl.chunks + (dx ? 1 : 0)), kPrepThreads, 0,
+                   stream, T, pl.Tp, N, d, pl.dp, pl.chunks, dlogits, w_router, dlp, wp, db);
+        if (dx) {
+            static PerDeviceOnce smem_attr;
+            if (!device_once(smem_attr, [] { return set_smem_limit(router_dense_dx, kDxSmem); }))
+                return MOE_ERR_CUDA;
+            CUtensorMap mdl, mw, min_, mout;
+            if (!make_map_pieces_mn(&mdl, dlp, pl.Tp, N, 32) ||
+                !make_map_pieces_mn(&mw, wp, pl.dp, N, 32) ||
+                !make_map_f32(&min_, dx_in ? dx_in : dx, d, T) || !make_map_f32(&mout, dx, d, T))
+                return MOE_ERR_CUDA;
+            const int64_t tiles = ((int64_t)T + 127) / 128 * ((d + 127) / 128);
+            launch_pdl(router_dense_dx, (unsigned)std::min<int64_t>(tiles, num_sms()), kGemmThreads,
+                       kDxSmem, stream, mdl, mw, min_, mout, T, N, d, dx_in ? 1 : 0, status);
+        }
+        if (dw_router) {
+            CUtensorMap mx, mdl;
+            if (!make_map(&mx, x, d, T, 64) || !make_map_pieces_k(&mdl, dlp, pl.Tp, N, pl.nt))
+                return MOE_ERR_CUDA;
+            r = pl.nt == 32   ? launch_dw<32>(mx, mdl, s, pl.splits, part, status, stream)
+                : pl.nt == 64 ? launch_dw<64>(mx, mdl, s, pl.splits, part, status, stream)
+                              : launch_dw<128>(mx, mdl, s, pl.splits, part, status, stream);
+            if (r != MOE_OK) return r;
+        }
+    }
     if (dw_router || dbias) {
-        float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
-        launch_pdl(router_dense_dw,
-                   dim3(dw_router ? d / kRdCols + 1 : 1, (N + kRdExp - 1) / kRdExp, kRdSplits),
-                   kRdCols, 0, stream, T, N, d, dlogits,
-                   dw_router ? x : static_cast<const moe_bf16 *>(nullptr), part);
-        const int64_t n = (int64_t)N * (d + 1);
-        launch_pdl(router_dense_sum, (unsigned)((n + kRdCols - 1) / kRdCols), kRdCols, 0, stream, N,
-                   d, static_cast<const float *>(part), dw_router, dbias);
+        const int64_t n4 = (int64_t)N * d / 4;
+        const int dw_blocks = dw_router ? (int)((n4 + kSumThreads - 1) / kSumThreads) : 0;
+        const int db_blocks = dbias ? (N + kSumThreads / 32 - 1) / (kSumThreads / 32) : 0;
+        launch_pdl(router_dense_sum, dw_blocks + db_blocks, kSumThreads, 0, stream, n4,
+                   T > 0 ? pl.splits : 0, reinterpret_cast<const float4 *>(part),
+                   reinterpret_cast<float4 *>(dw_router), N, T > 0 ? pl.groups : 0,
+                   static_cast<const float *>(db), dbias, dw_blocks);
     }
     return launch_status();
 }
