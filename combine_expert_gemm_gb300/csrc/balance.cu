@@ -5,91 +5,175 @@
 //   z = sum_t lse_t^2 / Tc
 //   dlogits = p (gb N / Tc (f - sum_e p_e f_e) + gz 2 lse / Tc) + scattered dlogit
 //
-// One warp per token.  Both kernels move the [T, N] logits once and are bound
-// by HBM at length and by their launches when short.
+// A token's row of logits is held in the registers of a group of LANES lanes,
+// VPT logits each, so both kernels read the logits once and need one exponential
+// per logit.  The group is as small as the row allows (8 lanes x 4 for N <= 32)
+// up to a whole warp: short rows then fill whole 128-byte requests, four tokens
+// to a warp.  Rows of a multiple of four logits are read and written in
+// 16-byte vectors.
+#include <algorithm>
+#include <type_traits>
+
 #include "../../include/moe_block.h"
 #include "moe_common.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kBalWarps = 8;
-constexpr int kBalThreads = kBalWarps * 32;
-constexpr int kBalMaxCtas = 304;
+constexpr int kBalCtas = 152;  // partial sums of the forward: one CTA per SM
+constexpr int kBalSlots = 8;   // warps that add up side by side in shared memory
 
-// Partial sums of one CTA in the workspace, N + 2 words of each kind:
-// int32 counts [N], token count, padding; then fp32 probability sums [N],
-// sum of lse^2, padding.
-inline __host__ __device__ int64_t bal_stride(int N) { return (N + 2 + 3) / 4 * 4; }
+// Partial sums of one CTA in the workspace, rounded up to 16 bytes: int32
+// counts [N] and the tokens, then fp32 probability sums [N] and the sum of lse^2.
+inline __host__ __device__ int64_t bal_stride(int N) { return (N + 1 + 3) / 4 * 4; }
 
-__device__ __forceinline__ float warp_max(float v) {
+template <int LANES>
+__device__ __forceinline__ float group_max(float v) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
+    for (int off = LANES / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
     return v;
 }
-__device__ __forceinline__ float warp_sum(float v) {
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+    for (int off = LANES / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
     return v;
 }
 
-__global__ void __launch_bounds__(kBalThreads)
+// The experts of lane `sub` of a group: register i holds expert
+// first(sub) + step(i).
+template <int LANES, int VPT, bool VEC>
+struct Row {
+    static __device__ __forceinline__ int first(int sub) { return VEC ? 4 * sub : sub; }
+    static __device__ __forceinline__ constexpr int step(int i) {
+        return VEC ? i / 4 * 4 * LANES + i % 4 : i * LANES;
+    }
+    // a row's logits; experts past N (or all of them) read as `fill`
+    static __device__ __forceinline__ void load(const float *row, int sub, int N, bool on, float fill,
+                                                float (&v)[VPT]) {
+        const int e0 = first(sub);
+        if (VEC) {
+#pragma unroll
+            for (int i = 0; i < VPT; i += 4) {
+                float4 q = make_float4(fill, fill, fill, fill);
+                if (on && e0 + step(i) < N) q = __ldcs(reinterpret_cast<const float4 *>(row + e0 + step(i)));
+                v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) v[i] = on && e0 + step(i) < N ? __ldcs(row + e0 + step(i)) : fill;
+        }
+    }
+    static __device__ __forceinline__ void store(float *row, int sub, int N, const float (&v)[VPT]) {
+        const int e0 = first(sub);
+        if (VEC) {
+#pragma unroll
+            for (int i = 0; i < VPT; i += 4)
+                if (e0 + step(i) < N)
+                    *reinterpret_cast<float4 *>(row + e0 + step(i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (e0 + step(i) < N) row[e0 + step(i)] = v[i];
+        }
+    }
+};
+
+__host__ __device__ constexpr int bal_threads(int vpt) { return vpt >= 16 ? 512 : 1024; }
+
+template <int LANES, int VPT, bool VEC>
+__global__ void __launch_bounds__(bal_threads(VPT), 1)
 balance_partial(int T, int N, int K, const float *__restrict__ logits,
                 const int32_t *__restrict__ topk_idx, const uint8_t *__restrict__ mask,
                 float *__restrict__ lse, int32_t *__restrict__ part_i, float *__restrict__ part_f) {
     pdl_enter();
+    using R = Row<LANES, VPT, VEC>;
+    constexpr int kThreads = bal_threads(VPT), kWarps = kThreads / 32;
+    constexpr int kGroups = kThreads / LANES;
     extern __shared__ float sm[];
-    float *acc = sm;                                              // [warps][N]
-    int *cnt = reinterpret_cast<int *>(sm + kBalWarps * N);       // [N]
-    float *zs = reinterpret_cast<float *>(cnt + N);               // [warps]
-    int *ts = reinterpret_cast<int *>(zs + kBalWarps);            // [warps]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < (kBalWarps + 1) * N; i += kBalThreads) sm[i] = 0.f;
+    float *acc_s = sm;                                          // [kBalSlots][N]
+    int *cnt = reinterpret_cast<int *>(sm + kBalSlots * N);     // [N]
+    __shared__ float zs[kWarps];
+    __shared__ int ts[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = threadIdx.x % LANES;
+    for (int i = threadIdx.x; i < (kBalSlots + 1) * N; i += kThreads) sm[i] = 0.f;
     __syncthreads();
+    float acc[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) acc[i] = 0.f;
     float z = 0.f;
     int tok = 0;
-    float *my = acc + warp * N;
-    for (int64_t t = (int64_t)blockIdx.x * kBalWarps + warp; t < T; t += gridDim.x * kBalWarps) {
-        if (mask && mask[t] == 0) {
-            if (lane == 0) lse[t] = 0.f;
-            continue;
-        }
-        const float *l = logits + t * N;
-        float m = -INFINITY;
-        for (int e = lane; e < N; e += 32) m = fmaxf(m, l[e]);
-        m = warp_max(m);
+    // whole warps step together: a group past T, or at a masked token, idles
+    for (int64_t w0 = (int64_t)blockIdx.x * kGroups + warp * (32 / LANES); w0 < T;
+         w0 += (int64_t)gridDim.x * kGroups) {
+        const int64_t t = w0 + lane / LANES;
+        const bool in = t < T;
+        const bool on = in && !(mask && mask[t] == 0);
+        float v[VPT];
+        R::load(logits + t * N, sub, N, on, -INFINITY, v);
+        float m = v[0];
+#pragma unroll
+        for (int i = 1; i < VPT; ++i) m = fmaxf(m, v[i]);
+        m = group_max<LANES>(m);
         if (m == -INFINITY) m = 0.f;  // all -inf: probabilities 0; all NaN: NaN below
         float sum = 0.f;
-        for (int e = lane; e < N; e += 32) sum += expf(l[e] - m);
-        sum = warp_sum(sum);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            v[i] = expf(v[i] - m);
+            sum += v[i];
+        }
+        sum = group_sum<LANES>(sum);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        for (int e = lane; e < N; e += 32) my[e] += expf(l[e] - m) * inv;
-        const float v = m + logf(sum);
-        if (sum != 0.f) z = fmaf(v, v, z);
-        ++tok;
-        if (lane == 0) lse[t] = v;
-        if (lane < K) {
-            const int e = topk_idx[t * K + lane];
-            if (e >= 0 && e < N) atomicAdd(cnt + e, 1);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+        if (on) {
+            for (int k = sub; k < K; k += LANES) {
+                const int e = topk_idx[t * K + k];
+                if (e >= 0 && e < N) atomicAdd(cnt + e, 1);
+            }
+        }
+        if (in && sub == 0) {
+            const float l = m + logf(sum);
+            lse[t] = on ? l : 0.f;
+            if (on) {
+                ++tok;
+                if (sum != 0.f) z = fmaf(l, l, z);
+            }
         }
     }
+    // the warp's groups, then the warps, in a fixed order
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int off = LANES; off < 32; off <<= 1) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], off);
+    z = group_sum<32>(z);
+    tok = __reduce_add_sync(0xFFFFFFFFu, tok);
     if (lane == 0) {
         zs[warp] = z;
         ts[warp] = tok;
     }
-    __syncthreads();
+    for (int w = 0; w < kWarps; w += kBalSlots) {
+        if (warp >= w && warp < w + kBalSlots && lane < LANES) {
+            float *my = acc_s + (warp - w) * N + R::first(sub);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (R::first(sub) + R::step(i) < N) my[R::step(i)] += acc[i];
+        }
+        __syncthreads();
+    }
     part_i += blockIdx.x * bal_stride(N);
     part_f += blockIdx.x * bal_stride(N);
-    for (int e = threadIdx.x; e < N; e += kBalThreads) {
+    for (int e = threadIdx.x; e < N; e += kThreads) {
         float p = 0.f;
-        for (int w = 0; w < kBalWarps; ++w) p += acc[w * N + e];
+#pragma unroll
+        for (int w = 0; w < kBalSlots; ++w) p += acc_s[w * N + e];
         part_i[e] = cnt[e];
         part_f[e] = p;
     }
     if (threadIdx.x == 0) {
         float p = 0.f;
         int n = 0;
-        for (int w = 0; w < kBalWarps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             p += zs[w];
             n += ts[w];
         }
@@ -98,39 +182,51 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
     }
 }
 
-// One CTA: the partial sums over CTAs in order, and the two losses.
+// One CTA: the CTAs' partial sums and the two losses.  `slices` threads share
+// an expert, each adding every slices-th CTA's sums; the slices are then added
+// in order.
 __global__ void __launch_bounds__(1024)
-balance_finish(int N, int K, int ctas, const int32_t *__restrict__ part_i,
+balance_finish(int N, int K, int ctas, int slices, const int32_t *__restrict__ part_i,
                const float *__restrict__ part_f, int32_t *__restrict__ count,
                int32_t *__restrict__ token_count, float *__restrict__ prob,
                float *__restrict__ losses) {
     pdl_enter();
-    __shared__ float sum_f[1025];
-    __shared__ int sum_i[1025];
+    __shared__ float sf[1025];
+    __shared__ int si[1025];
     __shared__ float red[32];
+    const int cols = N + 1;
     const int64_t st = bal_stride(N);
-    for (int e = threadIdx.x; e <= N; e += blockDim.x) {
+    // slices > 1 only when slices * cols <= 1024: one pass, a column per thread
+    for (int j = threadIdx.x; j < slices * cols; j += blockDim.x) {
+        const int e = j % cols, q = j / cols;
         float p = 0.f;
         int c = 0;
-        for (int g = 0; g < ctas; ++g) {
+#pragma unroll 8
+        for (int g = q; g < ctas; g += slices) {
             p += part_f[g * st + e];
             c += part_i[g * st + e];
         }
-        sum_f[e] = p;
-        sum_i[e] = c;
+        sf[j] = p;
+        si[j] = c;
     }
     __syncthreads();
-    const int tc = sum_i[N];
+    for (int e = threadIdx.x; e < cols && slices > 1; e += blockDim.x)
+        for (int q = 1; q < slices; ++q) {
+            sf[e] += sf[q * cols + e];
+            si[e] += si[q * cols + e];
+        }
+    __syncthreads();
+    const int tc = si[N];
     const float inv = tc > 0 ? 1.f / (float)tc : 0.f;
     float dot = 0.f;
     const int e = threadIdx.x;
     if (e < N) {
-        const float p = sum_f[e] * inv;
-        count[e] = sum_i[e];
+        const float p = sf[e] * inv;
+        count[e] = si[e];
         prob[e] = p;
-        dot = (float)sum_i[e] * inv / (float)K * p;
+        dot = (float)si[e] * inv / (float)K * p;
     }
-    dot = warp_sum(dot);
+    dot = group_sum<32>(dot);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dot;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -138,63 +234,86 @@ balance_finish(int N, int K, int ctas, const int32_t *__restrict__ part_i,
         for (int w = 0; w < (int)blockDim.x / 32; ++w) b += red[w];
         token_count[0] = tc;
         losses[0] = (float)N * b;
-        losses[1] = sum_f[N] * inv;
+        losses[1] = sf[N] * inv;
     }
 }
 
-__global__ void __launch_bounds__(kBalThreads)
+constexpr int kBwdThreads = 256;
+
+template <int LANES, int VPT, bool VEC>
+__global__ void __launch_bounds__(kBwdThreads)
 balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
                  const int32_t *__restrict__ topk_idx, const uint8_t *__restrict__ mask,
                  const int32_t *__restrict__ count, const int32_t *__restrict__ token_count,
                  const float *__restrict__ lse, const float *__restrict__ dlosses,
                  const float *__restrict__ dlogit, float *__restrict__ dlogits) {
     pdl_enter();
-    extern __shared__ float sm[];
-    float *f = sm;  // [N]
+    using R = Row<LANES, VPT, VEC>;
+    constexpr int kGroups = kBwdThreads / LANES;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = threadIdx.x % LANES;
     const int tc = token_count[0];
     const float inv = tc > 0 ? 1.f / (float)tc : 0.f;
-    for (int e = threadIdx.x; e < N; e += kBalThreads) f[e] = (float)count[e] * inv / (float)K;
-    __syncthreads();
     const float cb = dlosses[0] * (float)N * inv, cz = 2.f * dlosses[1] * inv;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int64_t t = (int64_t)blockIdx.x * kBalWarps + warp; t < T; t += gridDim.x * kBalWarps) {
-        const float *l = logits + t * N;
-        float *o = dlogits + t * N;
-        const bool live = !(mask && mask[t] == 0);
-        float v = 0.f, dot = 0.f;
-        bool none = true;  // no probability: masked, or every logit -inf
-        if (live) {
-            v = lse[t];
-            none = v == -INFINITY;
-            if (!none)
-                for (int e = lane; e < N; e += 32) dot = fmaf(expf(l[e] - v), f[e], dot);
-            dot = warp_sum(dot);
+    float f[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int e = R::first(sub) + R::step(i);
+        f[i] = e < N ? (float)count[e] * inv / (float)K : 0.f;
+    }
+    for (int64_t w0 = (int64_t)blockIdx.x * kGroups + warp * (32 / LANES); w0 < T;
+         w0 += (int64_t)gridDim.x * kGroups) {
+        const int64_t t = w0 + lane / LANES;
+        const bool in = t < T;
+        bool on = in && !(mask && mask[t] == 0);
+        float v[VPT];
+        R::load(logits + t * N, sub, N, on, -INFINITY, v);
+        const float l = on ? lse[t] : 0.f;
+        on = on && l != -INFINITY;  // every logit -inf: no probability, no gradient
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            v[i] = on ? expf(v[i] - l) : 0.f;
+            dot = fmaf(v[i], f[i], dot);
         }
-        int my_e = -1;
-        float my_d = 0.f;
-        if (dlogit && lane < K) {
-            my_e = topk_idx[t * K + lane];
-            my_d = dlogit[t * K + lane];
-        }
-        for (int e0 = 0; e0 < N; e0 += 32) {
-            const int e = e0 + lane;
-            float r = 0.f;
-            if (!none && e < N) r = expf(l[e] - v) * (cb * (f[e] - dot) + cz * v);
-            if (dlogit)
-                for (int k = 0; k < K; ++k) {
-                    const int ek = __shfl_sync(0xFFFFFFFFu, my_e, k);
-                    const float dk = __shfl_sync(0xFFFFFFFFu, my_d, k);
-                    if (ek == e) r += dk;
-                }
-            if (e < N) o[e] = r;
-        }
+        dot = group_sum<LANES>(dot);
+        const float c = cz * l;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) v[i] = on ? v[i] * fmaf(cb, f[i] - dot, c) : 0.f;
+        if (dlogit && in)
+            for (int k = 0; k < K; ++k) {
+                const int at = topk_idx[t * K + k];
+                const float g = dlogit[t * K + k];
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    if (at == R::first(sub) + R::step(i)) v[i] += g;
+            }
+        if (in) R::store(dlogits + t * N, sub, N, v);
     }
 }
 
-inline int bal_ctas(int T) {
-    const int want = (T + kBalWarps - 1) / kBalWarps;
-    return want < kBalMaxCtas ? (want < 1 ? 1 : want) : kBalMaxCtas;
+// The smallest group that holds a row of N logits: calls fn with LANES, VPT
+// and whether rows are whole 16-byte vectors.
+template <int L, int V, bool VEC>
+struct Shape3 {
+    static constexpr int lanes = L, vpt = V;
+    static constexpr bool vec = VEC;
+};
+template <typename Fn>
+inline void with_row(int N, Fn &&fn) {
+    auto go = [&](auto vec) {
+        constexpr bool kVec = decltype(vec)::value;
+        if (N <= 32) fn(Shape3<8, 4, kVec>());
+        else if (N <= 64) fn(Shape3<16, 4, kVec>());
+        else if (N <= 128) fn(Shape3<32, 4, kVec>());
+        else if (N <= 256) fn(Shape3<32, 8, kVec>());
+        else if (N <= 512) fn(Shape3<32, 16, kVec>());
+        else fn(Shape3<32, 32, kVec>());
+    };
+    if (N % 4 == 0) go(std::true_type());
+    else go(std::false_type());
 }
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 inline bool ws_ok(const void *ws, size_t have, size_t need) {
     return ws && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 && have >= need;
@@ -207,7 +326,7 @@ using namespace moe;
 
 MOE_API size_t moe_balance_loss_workspace_bytes(const moe_shape *s) {
     if (check_shape(s) != MOE_OK) return 0;
-    return 256 + (size_t)kBalMaxCtas * bal_stride(s->N) * 8;
+    return 256 + (size_t)kBalCtas * bal_stride(s->N) * 8;
 }
 
 MOE_API moe_status moe_balance_loss(const moe_shape *s, const float *logits,
@@ -225,13 +344,19 @@ MOE_API moe_status moe_balance_loss(const moe_shape *s, const float *logits,
     for (const void *p : ptrs)
         if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
     if (!ws_ok(ws, ws_bytes, moe_balance_loss_workspace_bytes(s))) return MOE_ERR_WORKSPACE;
-    const int ctas = bal_ctas(s->T);
+    const int N = s->N;
     int32_t *part_i = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + 256);
-    float *part_f = reinterpret_cast<float *>(part_i + kBalMaxCtas * bal_stride(s->N));
-    const size_t smem = sizeof(float) * ((kBalWarps + 1) * s->N + 2 * kBalWarps);
-    launch_pdl(balance_partial, ctas, kBalThreads, smem, stream, s->T, s->N, s->K, logits, topk_idx,
-               token_mask, lse, part_i, part_f);
-    launch_pdl(balance_finish, 1, 1024, 0, stream, s->N, s->K, ctas,
+    float *part_f = reinterpret_cast<float *>(part_i + kBalCtas * bal_stride(N));
+    int ctas = 1;
+    with_row(N, [&](auto q) {
+        using Q = decltype(q);
+        constexpr int kThreads = bal_threads(Q::vpt);
+        ctas = (int)std::min<int64_t>(kBalCtas, std::max<int64_t>(1, ceil_div(s->T, kThreads / Q::lanes)));
+        launch_pdl(balance_partial<Q::lanes, Q::vpt, Q::vec>, ctas, kThreads,
+                   sizeof(float) * (kBalSlots + 1) * N, stream, s->T, N, s->K, logits, topk_idx,
+                   token_mask, lse, part_i, part_f);
+    });
+    launch_pdl(balance_finish, 1, 1024, 0, stream, N, s->K, ctas, std::max(1, 1024 / (N + 1)),
                static_cast<const int32_t *>(part_i), static_cast<const float *>(part_f),
                expert_count, token_count, expert_prob, losses);
     return launch_status();
@@ -253,9 +378,13 @@ MOE_API moe_status moe_balance_loss_backward(const moe_shape *s, const float *lo
                           dlogit, dlogits};
     for (const void *p : ptrs)
         if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
-    const int want = (s->T + kBalWarps - 1) / kBalWarps, most = num_sms() * 8;
-    launch_pdl(balance_bwd_rows, want < most ? want : most, kBalThreads, sizeof(float) * s->N, stream,
-               s->T, s->N, s->K, logits, topk_idx, token_mask, expert_count, token_count, lse,
-               dlosses, dlogit, dlogits);
+    with_row(s->N, [&](auto q) {
+        using Q = decltype(q);
+        const int64_t want = ceil_div(s->T, kBwdThreads / Q::lanes);
+        launch_pdl(balance_bwd_rows<Q::lanes, Q::vpt, Q::vec>,
+                   (unsigned)std::min<int64_t>(want, (int64_t)num_sms() * 8), kBwdThreads, 0, stream,
+                   s->T, s->N, s->K, logits, topk_idx, token_mask, expert_count, token_count, lse,
+                   dlosses, dlogit, dlogits);
+    });
     return launch_status();
 }
