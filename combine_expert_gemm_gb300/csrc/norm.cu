@@ -6,8 +6,27 @@
 //   dx = dres + rstd (w - sum w / d - xh sum(w xh) / d),  w = dy gamma,
 //   xh = (s - mean) rstd;  dgamma = sum_t dy xh;  dbeta = sum_t dy
 //
-// All of it is bound by HBM: a few operations per element moved.
+// Bound by HBM: a few operations per element moved, so both kernels read every
+// row once.  Persistent CTAs of up to 1024 threads, one per SM, are cut into
+// groups of whole warps; a group takes one row at a time and each of its
+// threads keeps the same columns (8, or 16 for d > 8192) from row to row.  The
+// column's gamma and beta, and in the backward its share of dgamma and dbeta,
+// therefore stay in registers, and the weight gradients cost no second pass
+// over x and dy (the two-pass version took 74 of 172 us at 8192 x 2048).
+//
+// Rows arrive through rings of cp.async copies, kStages - 1 rows ahead.  A
+// thread copies exactly the bytes that it will read itself, so a ring needs no
+// barrier and no wait but the thread's own cp.async.wait_group, and the SM
+// keeps 64 KB and more of loads in flight with few registers.
+//
+// A row's sums cross the group's warps through shared memory with one barrier
+// per row (two alternating buffers).  The forward exchanges each warp's sum and
+// its squares centred at the warp's own mean, which combine exactly into the
+// variance around the row's mean:
+//   M2 = sum_w M2_w + n_w (mean_w - mean)^2.
 #include <math.h>
+
+#include <algorithm>
 
 #include "../../include/moe_block.h"
 #include "moe_common.cuh"
@@ -16,176 +35,379 @@ namespace moe {
 namespace {
 
 constexpr int kNormMaxD = 16384;
-constexpr int kNormThreads = 256;
+constexpr int kNormMaxThreads = 1024;
+constexpr int kNormCtas = 152;        // one per SM; the order of the weight sums follows it
+constexpr size_t kNormRing = 196608;  // most shared memory the rings take
 
-// Eight consecutive elements of a row as fp32.
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, float (&f)[8]);
-template <>
-__device__ __forceinline__ void load8<uint16_t>(const uint16_t *p, float (&f)[8]) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+__device__ __forceinline__ void unpack(const uint4 &v, float *f) {
     f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x);
     f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
     f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z);
     f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
 }
-template <>
-__device__ __forceinline__ void load8<float>(const float *p, float (&f)[8]) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0];
-    const float4 b = reinterpret_cast<const float4 *>(p)[1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+__device__ __forceinline__ uint4 pack(const float *f) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
 }
-__device__ __forceinline__ void store8(uint16_t *p, const float (&f)[8]) {
-    *reinterpret_cast<uint4 *>(p) =
-        make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                   pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ void store8(uint16_t *p, const float *f) {
+    *reinterpret_cast<uint4 *>(p) = pack(f);
 }
-__device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
+__device__ __forceinline__ void store8(float *p, const float *f) {
     reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
     reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
+// The value a tensor of type T holds for v.
+__device__ __forceinline__ void round8(uint16_t, float *f) {
+    const uint4 v = pack(f);
+    unpack(v, f);
+}
+__device__ __forceinline__ void round8(float, float *) {}
 
-__device__ __forceinline__ float block_sum(float v, float *red) {
+// A thread's slot of one ring stage: 16-byte words `threads` words apart, so
+// that a warp's accesses are consecutive.  T's 8 elements take 1 or 2 words.
+template <typename T>
+constexpr __host__ __device__ int words() { return (int)sizeof(T) / 2; }
+
+template <typename T>
+__device__ __forceinline__ void ring_copy(uint4 *slot, int pitch, const T *src) {
+    const uint4 *g = reinterpret_cast<const uint4 *>(src);
+#pragma unroll
+    for (int i = 0; i < words<T>(); ++i) cp_async16(slot + i * pitch, g + i);
+}
+template <typename T>
+__device__ __forceinline__ void ring_read(const uint4 *slot, int pitch, float *f);
+template <>
+__device__ __forceinline__ void ring_read<uint16_t>(const uint4 *slot, int, float *f) {
+    unpack(*slot, f);
+}
+template <>
+__device__ __forceinline__ void ring_read<float>(const uint4 *slot, int pitch, float *f) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint4 v = slot[i * pitch];
+        f[4 * i] = __uint_as_float(v.x);
+        f[4 * i + 1] = __uint_as_float(v.y);
+        f[4 * i + 2] = __uint_as_float(v.z);
+        f[4 * i + 3] = __uint_as_float(v.w);
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.f;
-    for (int w = 0; w < kNormThreads / 32; ++w) v += red[w];
     return v;
 }
 
-// One CTA per row; three passes over the row, the last two from L1.
-template <typename XT>
-__global__ void __launch_bounds__(kNormThreads)
-norm_fwd_rows(int d, const XT *x, const uint16_t *add, const float *__restrict__ gamma,
-              const float *__restrict__ beta, float eps, XT *x_sum, uint16_t *__restrict__ y,
-              float *__restrict__ mean, float *__restrict__ rstd) {
+// Barrier among the warps of one group (ids 1..15; a group of one warp needs
+// no barrier between warps).
+__device__ __forceinline__ void group_sync(int id, int warps) {
+    if (warps == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(warps * 32) : "memory");
+}
+
+// How a row of d columns is laid over threads.
+struct NormPlan {
+    int cpt;      // chunks of 8 columns per thread: 1 or 2
+    int warps;    // warps per group
+    int groups;   // groups per CTA
+    int ctas;
+};
+
+inline NormPlan norm_plan(int rows, int d) {
+    NormPlan p;
+    const int chunks = d / 8;
+    p.cpt = chunks > kNormMaxThreads ? 2 : 1;
+    p.warps = (chunks + 32 * p.cpt - 1) / (32 * p.cpt);
+    p.groups = std::min(p.warps == 1 ? 16 : 15, kNormMaxThreads / 32 / p.warps);
+    // few rows: one group per CTA before a second one on any SM
+    p.groups = std::max(1, std::min(p.groups, rows / kNormCtas));
+    p.ctas = std::max(1, std::min(kNormCtas, (rows + p.groups - 1) / p.groups));
+    return p;
+}
+
+template <typename XT, int CPT, int STAGES>
+__global__ void __launch_bounds__(kNormMaxThreads, 1)
+norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const float *__restrict__ gamma,
+         const float *__restrict__ beta, float eps, XT *x_sum, uint16_t *__restrict__ y,
+         float *__restrict__ mean, float *__restrict__ rstd) {
     pdl_enter();
-    __shared__ float red[kNormThreads / 32];
-    const int64_t base = (int64_t)blockIdx.x * d;
-    const XT *s = add ? x_sum + base : x + base;
-    float sum = 0.f;
-    for (int c = threadIdx.x * 8; c < d; c += kNormThreads * 8) {
-        float f[8];
-        load8(x + base + c, f);
-        if (add) {
-            float a[8];
-            load8(add + base + c, a);
+    extern __shared__ uint4 ring[];
+    __shared__ float2 red[2][32];
+    constexpr int kWords = CPT * (words<XT>() + 1);  // per thread and stage
+    const int gthreads = warps * 32, group = threadIdx.x / gthreads, tid = threadIdx.x % gthreads;
+    const int groups = blockDim.x / gthreads, lane = threadIdx.x & 31, gw = tid >> 5;
+    const int pitch = blockDim.x;
+    const int chunks = d / 8;
+    float ga[CPT][8], be[CPT][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] += a[i];
-            store8(x_sum + base + c, f);
-            load8(x_sum + base + c, f);  // the rounded sum, this thread's own store
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += f[i];
-    }
-    const float mu = block_sum(sum, red) / (float)d;
-    float sq = 0.f;
-    for (int c = threadIdx.x * 8; c < d; c += kNormThreads * 8) {
-        float f[8];
-        load8(s + c, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sq = fmaf(f[i] - mu, f[i] - mu, sq);
-    }
-    const float rs = 1.f / sqrtf(block_sum(sq, red) / (float)d + eps);
-    if (mean && threadIdx.x == 0) {
-        mean[blockIdx.x] = mu;
-        rstd[blockIdx.x] = rs;
-    }
-    for (int c = threadIdx.x * 8; c < d; c += kNormThreads * 8) {
-        float f[8];
-        load8(s + c, f);
+    for (int c = 0; c < CPT; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            f[i] = (f[i] - mu) * rs;
-            if (gamma) f[i] *= gamma[c + i];
-            if (beta) f[i] += beta[c + i];
+            const int col = (tid + c * gthreads) * 8 + i;
+            ga[c][i] = gamma && col < d ? gamma[col] : 1.f;
+            be[c][i] = beta && col < d ? beta[col] : 0.f;
         }
-        store8(y + base + c, f);
+    const int64_t step = (int64_t)gridDim.x * groups;
+    const int64_t first = (int64_t)blockIdx.x * groups + group;
+    auto slot = [&](int stage, int c) {
+        return ring + ((size_t)stage * kWords + c * (words<XT>() + 1)) * pitch + threadIdx.x;
+    };
+    auto fetch = [&](int64_t t, int stage) {
+        if (t < rows) {
+#pragma unroll
+            for (int c = 0; c < CPT; ++c) {
+                const int at = tid + c * gthreads;
+                if (at >= chunks) continue;
+                ring_copy(slot(stage, c), pitch, x + t * d + at * 8);
+                if (add) ring_copy(slot(stage, c) + words<XT>() * pitch, pitch, add + t * d + at * 8);
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) fetch(first + s * step, s);
+    // columns of this warp: chunks [32 gw, 32 gw + 32) of each of the CPT parts
+    int nw = 0;
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) nw += 8 * max(0, min(32, chunks - c * gthreads - gw * 32));
+    const float inv_nw = nw > 0 ? 1.f / (float)nw : 0.f, inv_d = 1.f / (float)d;
+    int stage = 0, buf = 0;
+    for (int64_t t = first; t < rows; t += step) {
+        fetch(t + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+        cp_async_wait<STAGES - 1>();
+        float f[CPT][8];
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) {
+            const int at = tid + c * gthreads;
+            if (at < chunks) {
+                ring_read<XT>(slot(stage, c), pitch, f[c]);
+                if (add) {
+                    float a[8];
+                    ring_read<uint16_t>(slot(stage, c) + words<XT>() * pitch, pitch, a);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[c][i] += a[i];
+                    round8(XT(), f[c]);
+                    store8(x_sum + t * d + at * 8, f[c]);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum += f[c][i];
+            }
+        }
+        if (++stage == STAGES) stage = 0;
+        sum = warp_sum(sum);
+        const float mw = sum * inv_nw;
+        float m2 = 0.f;
+#pragma unroll
+        for (int c = 0; c < CPT; ++c)
+            if (tid + c * gthreads < chunks) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m2 = fmaf(f[c][i] - mw, f[c][i] - mw, m2);
+            }
+        m2 = warp_sum(m2);
+        float mu = mw, var = m2;
+        if (warps > 1) {
+            float2 *r = red[buf] + group * warps;
+            if (lane == 0) r[gw] = make_float2(sum, m2);
+            group_sync(1 + group, warps);
+            buf ^= 1;
+            float tot = 0.f;
+            for (int w = 0; w < warps; ++w) tot += r[w].x;
+            mu = tot * inv_d;
+            var = 0.f;
+            for (int w = 0; w < warps; ++w) {
+                int n = 0;
+#pragma unroll
+                for (int c = 0; c < CPT; ++c) n += 8 * max(0, min(32, chunks - c * gthreads - w * 32));
+                const float dm = n > 0 ? r[w].x / (float)n - mu : 0.f;
+                var += fmaf((float)n * dm, dm, r[w].y);
+            }
+        }
+        const float rs = 1.f / sqrtf(fmaf(var, inv_d, eps));
+        if (mean && tid == 0) {
+            mean[t] = mu;
+            rstd[t] = rs;
+        }
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) {
+            const int at = tid + c * gthreads;
+            if (at >= chunks) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[c][i] = fmaf((f[c][i] - mu) * rs, ga[c][i], be[c][i]);
+            store8(y + t * d + at * 8, f[c]);
+        }
+    }
+    cp_async_wait<0>();
+}
+
+// part[cta][2][d]: this CTA's sums of dgamma and dbeta (part may be NULL).
+template <typename XT, typename YT, typename GT, int CPT, int STAGES>
+__global__ void __launch_bounds__(kNormMaxThreads, 1)
+norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restrict__ dy,
+         const float *__restrict__ gamma, const float *__restrict__ mean,
+         const float *__restrict__ rstd, const GT *dres, GT *dx, float *__restrict__ part) {
+    pdl_enter();
+    extern __shared__ uint4 ring[];
+    __shared__ float2 red[2][32];
+    constexpr int kChunkWords = words<XT>() + words<YT>() + words<GT>();
+    constexpr int kWords = CPT * kChunkWords;
+    const int gthreads = warps * 32, group = threadIdx.x / gthreads, tid = threadIdx.x % gthreads;
+    const int groups = blockDim.x / gthreads, lane = threadIdx.x & 31, gw = tid >> 5;
+    const int pitch = blockDim.x;
+    const int chunks = d / 8;
+    float ga[CPT][8], dg[CPT][8], db[CPT][8];
+#pragma unroll
+    for (int c = 0; c < CPT; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int col = (tid + c * gthreads) * 8 + i;
+            ga[c][i] = gamma && col < d ? gamma[col] : 1.f;
+            dg[c][i] = 0.f;
+            db[c][i] = 0.f;
+        }
+    const int64_t step = (int64_t)gridDim.x * groups;
+    const int64_t first = (int64_t)blockIdx.x * groups + group;
+    auto slot = [&](int stage, int c) {
+        return ring + ((size_t)stage * kWords + c * kChunkWords) * pitch + threadIdx.x;
+    };
+    auto fetch = [&](int64_t t, int stage) {
+        if (t < rows) {
+#pragma unroll
+            for (int c = 0; c < CPT; ++c) {
+                const int at = tid + c * gthreads;
+                if (at >= chunks) continue;
+                uint4 *s = slot(stage, c);
+                ring_copy(s, pitch, x + t * d + at * 8);
+                ring_copy(s + words<XT>() * pitch, pitch, dy + t * d + at * 8);
+                if (dres) ring_copy(s + (words<XT>() + words<YT>()) * pitch, pitch, dres + t * d + at * 8);
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) fetch(first + s * step, s);
+    const float inv_d = 1.f / (float)d;
+    int stage = 0, buf = 0;
+    // the row's statistics, read one row ahead
+    float mu_n = first < rows ? mean[first] : 0.f, rs_n = first < rows ? rstd[first] : 0.f;
+    for (int64_t t = first; t < rows; t += step) {
+        fetch(t + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+        const float mu = mu_n, rs = rs_n;
+        if (t + step < rows) {
+            mu_n = mean[t + step];
+            rs_n = rstd[t + step];
+        }
+        cp_async_wait<STAGES - 1>();
+        float xh[CPT][8], w[CPT][8];
+        float sa = 0.f, sb = 0.f;
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) {
+            if (tid + c * gthreads < chunks) {
+                ring_read<XT>(slot(stage, c), pitch, xh[c]);
+                ring_read<YT>(slot(stage, c) + words<XT>() * pitch, pitch, w[c]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    xh[c][i] = (xh[c][i] - mu) * rs;
+                    dg[c][i] = fmaf(w[c][i], xh[c][i], dg[c][i]);
+                    db[c][i] += w[c][i];
+                    w[c][i] *= ga[c][i];
+                    sa += w[c][i];
+                    sb = fmaf(w[c][i], xh[c][i], sb);
+                }
+            }
+        }
+        sa = warp_sum(sa);
+        sb = warp_sum(sb);
+        if (warps > 1) {
+            float2 *r = red[buf] + group * warps;
+            if (lane == 0) r[gw] = make_float2(sa, sb);
+            group_sync(1 + group, warps);
+            buf ^= 1;
+            sa = sb = 0.f;
+            for (int q = 0; q < warps; ++q) {
+                sa += r[q].x;
+                sb += r[q].y;
+            }
+        }
+        sa *= inv_d;
+        sb *= inv_d;
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) {
+            const int at = tid + c * gthreads;
+            if (at >= chunks) continue;
+            float r[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (dres) ring_read<GT>(slot(stage, c) + (words<XT>() + words<YT>()) * pitch, pitch, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] = fmaf(rs, w[c][i] - sa - xh[c][i] * sb, r[i]);
+            store8(dx + t * d + at * 8, r);
+        }
+        if (++stage == STAGES) stage = 0;
+    }
+    cp_async_wait<0>();
+    if (!part) return;
+    // the CTA's groups, in order, through the ring's memory
+    float *acc = reinterpret_cast<float *>(ring);  // [groups][2][d]
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) {
+        const int at = tid + c * gthreads;
+        if (at >= chunks) continue;
+        store8(acc + ((size_t)group * 2) * d + at * 8, dg[c]);
+        store8(acc + ((size_t)group * 2 + 1) * d + at * 8, db[c]);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * d / 4; i += blockDim.x) {
+        float4 v = reinterpret_cast<const float4 *>(acc)[i];
+        for (int g = 1; g < groups; ++g) {
+            const float4 q = reinterpret_cast<const float4 *>(acc + (size_t)g * 2 * d)[i];
+            v.x += q.x;
+            v.y += q.y;
+            v.z += q.z;
+            v.w += q.w;
+        }
+        reinterpret_cast<float4 *>(part + (int64_t)blockIdx.x * 2 * d)[i] = v;
     }
 }
 
-template <typename XT, typename YT, typename GT>
-__global__ void __launch_bounds__(kNormThreads)
-norm_bwd_rows(int d, const XT *__restrict__ x, const YT *__restrict__ dy,
-              const float *__restrict__ gamma, const float *__restrict__ mean,
-              const float *__restrict__ rstd, const GT *dres, GT *dx) {
+// dgamma and dbeta from the CTAs' sums: 64 of the 2 d columns per CTA, 16
+// slices of the CTAs' rows side by side, added in order.
+constexpr int kSumThreads = 256;
+
+__global__ void __launch_bounds__(kSumThreads)
+norm_bwd_sum(int d, int ctas, const float *__restrict__ part, float *__restrict__ dgamma,
+             float *__restrict__ dbeta) {
     pdl_enter();
-    __shared__ float red[kNormThreads / 32];
-    const int64_t base = (int64_t)blockIdx.x * d;
-    const float mu = mean[blockIdx.x], rs = rstd[blockIdx.x];
-    float sa = 0.f, sb = 0.f;
-    for (int c = threadIdx.x * 8; c < d; c += kNormThreads * 8) {
-        float f[8], w[8];
-        load8(x + base + c, f);
-        load8(dy + base + c, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (gamma) w[i] *= gamma[c + i];
-            sa += w[i];
-            sb = fmaf(w[i], (f[i] - mu) * rs, sb);
+    __shared__ float4 sm[16][16];
+    const int q = threadIdx.x & 15, s = threadIdx.x >> 4;
+    const int i = blockIdx.x * 16 + q;  // float4 index within [2][d]
+    const int n = 2 * d / 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < n) {
+#pragma unroll 5
+        for (int g = s; g < ctas; g += 16) {
+            const float4 p = reinterpret_cast<const float4 *>(part)[(int64_t)g * n + i];
+            v.x += p.x;
+            v.y += p.y;
+            v.z += p.z;
+            v.w += p.w;
         }
     }
-    const float a = block_sum(sa, red) / (float)d, b = block_sum(sb, red) / (float)d;
-    for (int c = threadIdx.x * 8; c < d; c += kNormThreads * 8) {
-        float f[8], w[8], r[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        load8(x + base + c, f);
-        load8(dy + base + c, w);
-        if (dres) load8(dres + base + c, r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (gamma) w[i] *= gamma[c + i];
-            r[i] += rs * (w[i] - a - (f[i] - mu) * rs * b);
-        }
-        store8(dx + base + c, r);
+    sm[s][q] = v;
+    __syncthreads();
+    if (s != 0 || i >= n) return;
+    for (int k = 1; k < 16; ++k) {
+        const float4 p = sm[k][q];
+        v.x += p.x;
+        v.y += p.y;
+        v.z += p.z;
+        v.w += p.w;
     }
-}
-
-constexpr int kWgSplits = 64;  // row splits of the weight gradients' partial sums
-
-// Partial dgamma / dbeta of one row split: part[split][2][d].
-template <typename XT, typename YT>
-__global__ void __launch_bounds__(kNormThreads)
-norm_bwd_weight(int rows, int d, const XT *__restrict__ x, const YT *__restrict__ dy,
-                const float *__restrict__ mean, const float *__restrict__ rstd,
-                float *__restrict__ part) {
-    pdl_enter();
-    const int c = (blockIdx.x * kNormThreads + threadIdx.x) * 8;
-    if (c >= d) return;
-    const int64_t per = ((int64_t)rows + kWgSplits - 1) / kWgSplits;
-    const int64_t t0 = blockIdx.y * per, t1 = min((int64_t)rows, t0 + per);
-    float g[8] = {0, 0, 0, 0, 0, 0, 0, 0}, b[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int64_t t = t0; t < t1; ++t) {
-        float f[8], w[8];
-        load8(x + t * d + c, f);
-        load8(dy + t * d + c, w);
-        const float mu = mean[t], rs = rstd[t];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            g[i] = fmaf(w[i], (f[i] - mu) * rs, g[i]);
-            b[i] += w[i];
-        }
+    // d is a multiple of 8, so a vector lies in one of the two rows
+    if (i < d / 4) {
+        if (dgamma) reinterpret_cast<float4 *>(dgamma)[i] = v;
+    } else if (dbeta) {
+        reinterpret_cast<float4 *>(dbeta)[i - d / 4] = v;
     }
-    store8(part + ((int64_t)blockIdx.y * 2) * d + c, g);
-    store8(part + ((int64_t)blockIdx.y * 2 + 1) * d + c, b);
-}
-
-__global__ void __launch_bounds__(kNormThreads)
-norm_bwd_weight_sum(int d, const float *__restrict__ part, float *__restrict__ dgamma,
-                    float *__restrict__ dbeta) {
-    pdl_enter();
-    const int c = blockIdx.x * kNormThreads + threadIdx.x;
-    if (c >= d) return;
-    float g = 0.f, b = 0.f;
-    for (int s = 0; s < kWgSplits; ++s) {
-        g += part[(int64_t)(2 * s) * d + c];
-        b += part[(int64_t)(2 * s + 1) * d + c];
-    }
-    if (dgamma) dgamma[c] = g;
-    if (dbeta) dbeta[c] = b;
 }
 
 inline moe_status check_norm(int32_t rows, int32_t d) {
@@ -197,23 +419,53 @@ inline moe_status check_norm(int32_t rows, int32_t d) {
 
 inline bool dtype_ok(int32_t t) { return t == MOE_BF16 || t == MOE_FP32; }
 
-template <typename XT, typename YT, typename GT>
+// As many ring stages as fit, 4 at most: three rows ahead where the row's
+// bytes allow it, none (one stage) past 8192 columns.
+constexpr int ring_stages(int words_per_thread) {
+    const int n = (int)(kNormRing / ((size_t)words_per_thread * 16 * kNormMaxThreads));
+    return n > 4 ? 4 : n;
+}
+
+template <typename XT, int CPT>
+moe_status launch_norm_fwd(int32_t rows, int32_t d, const void *x, const moe_bf16 *add,
+                           const float *gamma, const float *beta, float eps, void *x_sum,
+                           moe_bf16 *y, float *mean, float *rstd, cudaStream_t stream) {
+    constexpr int kWords = CPT * (words<XT>() + 1), kStages = ring_stages(kWords);
+    const NormPlan p = norm_plan(rows, d);
+    const int threads = p.groups * p.warps * 32;
+    auto *kern = norm_fwd<XT, CPT, kStages>;
+    static PerDeviceOnce attr;
+    if (!device_once(attr, [&] { return set_smem_limit(kern, kNormRing); })) return MOE_ERR_CUDA;
+    launch_pdl(kern, p.ctas, threads, (size_t)kStages * kWords * 16 * threads, stream, rows, d, p.warps,
+               static_cast<const XT *>(x), add, gamma, beta, eps, static_cast<XT *>(x_sum), y, mean,
+               rstd);
+    return launch_status();
+}
+
+template <typename XT, typename YT, typename GT, int CPT>
 moe_status launch_norm_bwd(int32_t rows, int32_t d, const void *x, const void *dy,
                            const float *gamma, const float *mean, const float *rstd,
                            const void *dres, void *dx, float *dgamma, float *dbeta, void *ws,
                            cudaStream_t stream) {
-    if (rows > 0)
-        launch_pdl(norm_bwd_rows<XT, YT, GT>, rows, kNormThreads, 0, stream, d,
-                   static_cast<const XT *>(x), static_cast<const YT *>(dy), gamma, mean, rstd,
-                   static_cast<const GT *>(dres), static_cast<GT *>(dx));
-    if (dgamma || dbeta) {
-        float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
-        const unsigned cols = (unsigned)((d / 8 + kNormThreads - 1) / kNormThreads);
-        launch_pdl(norm_bwd_weight<XT, YT>, dim3(cols, kWgSplits), kNormThreads, 0, stream, rows, d,
-                   static_cast<const XT *>(x), static_cast<const YT *>(dy), mean, rstd, part);
-        launch_pdl(norm_bwd_weight_sum, (d + kNormThreads - 1) / kNormThreads, kNormThreads, 0,
-                   stream, d, static_cast<const float *>(part), dgamma, dbeta);
+    constexpr int kWords = CPT * (words<XT>() + words<YT>() + words<GT>());
+    constexpr int kStages = ring_stages(kWords);
+    const NormPlan p = norm_plan(rows, d);
+    const int threads = p.groups * p.warps * 32;
+    float *part = dgamma || dbeta ? reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256) : nullptr;
+    if (rows > 0) {
+        auto *kern = norm_bwd<XT, YT, GT, CPT, kStages>;
+        static PerDeviceOnce attr;
+        if (!device_once(attr, [&] { return set_smem_limit(kern, kNormRing); })) return MOE_ERR_CUDA;
+        // the ring also holds the groups' weight sums at the end
+        const size_t smem = std::max((size_t)kStages * kWords * 16 * threads,
+                                     (size_t)p.groups * 2 * d * sizeof(float));
+        launch_pdl(kern, p.ctas, threads, smem, stream, rows, d, p.warps, static_cast<const XT *>(x),
+                   static_cast<const YT *>(dy), gamma, mean, rstd, static_cast<const GT *>(dres),
+                   static_cast<GT *>(dx), part);
     }
+    if (part)
+        launch_pdl(norm_bwd_sum, (2 * d / 4 + 15) / 16, kSumThreads, 0, stream, d,
+                   rows > 0 ? p.ctas : 0, static_cast<const float *>(part), dgamma, dbeta);
     return launch_status();
 }
 
@@ -235,20 +487,18 @@ MOE_API moe_status moe_layer_norm(int32_t rows, int32_t d, int32_t x_dtype, cons
     const void *ptrs[] = {x, add, gamma, beta, x_sum, y, mean, rstd};
     for (const void *p : ptrs)
         if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
-    if (x_dtype == MOE_BF16)
-        launch_pdl(norm_fwd_rows<uint16_t>, rows, kNormThreads, 0, stream, d,
-                   static_cast<const uint16_t *>(x), add, gamma, beta, eps,
-                   static_cast<uint16_t *>(x_sum), y, mean, rstd);
-    else
-        launch_pdl(norm_fwd_rows<float>, rows, kNormThreads, 0, stream, d,
-                   static_cast<const float *>(x), add, gamma, beta, eps,
-                   static_cast<float *>(x_sum), y, mean, rstd);
-    return launch_status();
+    const bool two = d / 8 > kNormMaxThreads;
+    auto go = [&](auto xt) {
+        using XT = decltype(xt);
+        return two ? launch_norm_fwd<XT, 2>(rows, d, x, add, gamma, beta, eps, x_sum, y, mean, rstd, stream)
+                   : launch_norm_fwd<XT, 1>(rows, d, x, add, gamma, beta, eps, x_sum, y, mean, rstd, stream);
+    };
+    return x_dtype == MOE_BF16 ? go(uint16_t()) : go(float());
 }
 
 MOE_API size_t moe_layer_norm_backward_workspace_bytes(int32_t rows, int32_t d) {
     if (check_norm(rows, d) != MOE_OK) return 0;
-    return 256 + (size_t)kWgSplits * 2 * d * sizeof(float);
+    return 256 + (size_t)norm_plan(rows, d).ctas * 2 * d * sizeof(float);
 }
 
 MOE_API moe_status moe_layer_norm_backward(int32_t rows, int32_t d, int32_t x_dtype, const void *x,
@@ -266,9 +516,15 @@ MOE_API moe_status moe_layer_norm_backward(int32_t rows, int32_t d, int32_t x_dt
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) ||
         ws_bytes < moe_layer_norm_backward_workspace_bytes(rows, d))
         return MOE_ERR_WORKSPACE;
+    const bool two = d / 8 > kNormMaxThreads;
     auto go = [&](auto xt, auto yt, auto gt) {
-        return launch_norm_bwd<decltype(xt), decltype(yt), decltype(gt)>(
-            rows, d, x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, ws, stream);
+        using XT = decltype(xt);
+        using YT = decltype(yt);
+        using GT = decltype(gt);
+        return two ? launch_norm_bwd<XT, YT, GT, 2>(rows, d, x, dy, gamma, mean, rstd, dres, dx, dgamma,
+                                                    dbeta, ws, stream)
+                   : launch_norm_bwd<XT, YT, GT, 1>(rows, d, x, dy, gamma, mean, rstd, dres, dx, dgamma,
+                                                    dbeta, ws, stream);
     };
     auto go_g = [&](auto xt, auto yt) {
         return dx_dtype == MOE_BF16 ? go(xt, yt, uint16_t()) : go(xt, yt, float());
