@@ -45,6 +45,13 @@ def _arg(t, dtype, name, n, dev):
     """Device pointer of a contiguous CUDA tensor of n elements (None: NULL)."""
     if t is None:
         return None
+    # the calls are short: a good tensor is passed with as few steps as the
+    # checks need, and only a bad one is asked what is wrong with it
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= n:
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
@@ -55,9 +62,7 @@ def _arg(t, dtype, name, n, dev):
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if t.numel() < n:
-        raise ValueError(f"{name}: {t.numel()} elements, {n} needed")
-    return t.data_ptr()
+    raise ValueError(f"{name}: {t.numel()} elements, {n} needed")
 
 
 def _ws(ws, dev):

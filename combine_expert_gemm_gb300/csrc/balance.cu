@@ -103,14 +103,35 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
     for (int i = 0; i < VPT; ++i) acc[i] = 0.f;
     float z = 0.f;
     int tok = 0;
-    // whole warps step together: a group past T, or at a masked token, idles
-    for (int64_t w0 = (int64_t)blockIdx.x * kGroups + warp * (32 / LANES); w0 < T;
-         w0 += (int64_t)gridDim.x * kGroups) {
+    // Whole warps step together: a group past T, or at a masked token, idles.
+    // The next row is loaded before this one is worked on (for up to 8 logits a
+    // lane; beyond that the row itself is enough in flight, and registers are
+    // short): without it T = 131072, N = 250 took 47 us for this kernel.
+    constexpr bool kAhead = VPT <= 8;
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    auto counted = [&](int64_t t) { return t < T && !(mask && mask[t] == 0); };
+    int64_t w0 = (int64_t)blockIdx.x * kGroups + warp * (32 / LANES);
+    float ahead[VPT];
+    bool ahead_on = false;
+    if (kAhead) {
+        ahead_on = counted(w0 + lane / LANES);
+        R::load(logits + (w0 + lane / LANES) * N, sub, N, ahead_on, -INFINITY, ahead);
+    }
+    for (; w0 < T; w0 += step) {
         const int64_t t = w0 + lane / LANES;
         const bool in = t < T;
-        const bool on = in && !(mask && mask[t] == 0);
+        bool on;
         float v[VPT];
-        R::load(logits + t * N, sub, N, on, -INFINITY, v);
+        if (kAhead) {
+            on = ahead_on;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) v[i] = ahead[i];
+            ahead_on = counted(t + step);
+            R::load(logits + (t + step) * N, sub, N, ahead_on, -INFINITY, ahead);
+        } else {
+            on = counted(t);
+            R::load(logits + t * N, sub, N, on, -INFINITY, v);
+        }
         float m = v[0];
 #pragma unroll
         for (int i = 1; i < VPT; ++i) m = fmaxf(m, v[i]);
@@ -182,39 +203,46 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
     }
 }
 
-// One CTA: the CTAs' partial sums and the two losses.  `slices` threads share
-// an expert, each adding every slices-th CTA's sums; the slices are then added
-// in order.
+// One CTA: the CTAs' partial sums and the two losses.  Each thread takes four
+// experts (a 16-byte vector) of every slices-th CTA; the slices are then added
+// pairwise.  The loads of a thread are independent, so this is one or two
+// rounds of L2 latency: an expert per thread took 9 to 12 us here.
 __global__ void __launch_bounds__(1024)
 balance_finish(int N, int K, int ctas, int slices, const int32_t *__restrict__ part_i,
                const float *__restrict__ part_f, int32_t *__restrict__ count,
                int32_t *__restrict__ token_count, float *__restrict__ prob,
                float *__restrict__ losses) {
     pdl_enter();
-    __shared__ float sf[1025];
-    __shared__ int si[1025];
+    __shared__ float4 sf4[1024];
+    __shared__ int4 si4[1024];
     __shared__ float red[32];
-    const int cols = N + 1;
-    const int64_t st = bal_stride(N);
-    // slices > 1 only when slices * cols <= 1024: one pass, a column per thread
-    for (int j = threadIdx.x; j < slices * cols; j += blockDim.x) {
-        const int e = j % cols, q = j / cols;
-        float p = 0.f;
-        int c = 0;
+    float *sf = reinterpret_cast<float *>(sf4);
+    int *si = reinterpret_cast<int *>(si4);
+    const int st = (int)bal_stride(N), vec = st / 4;
+    // the last vector's padding holds nothing that is read back
+    if ((int)threadIdx.x < slices * vec) {
+        const int e = threadIdx.x % vec, q = threadIdx.x / vec;
+        float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+        int4 c = make_int4(0, 0, 0, 0);
 #pragma unroll 8
         for (int g = q; g < ctas; g += slices) {
-            p += part_f[g * st + e];
-            c += part_i[g * st + e];
+            const float4 a = reinterpret_cast<const float4 *>(part_f)[g * vec + e];
+            const int4 b = reinterpret_cast<const int4 *>(part_i)[g * vec + e];
+            p.x += a.x; p.y += a.y; p.z += a.z; p.w += a.w;
+            c.x += b.x; c.y += b.y; c.z += b.z; c.w += b.w;
         }
-        sf[j] = p;
-        si[j] = c;
+        sf4[threadIdx.x] = p;
+        si4[threadIdx.x] = c;
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e < cols && slices > 1; e += blockDim.x)
-        for (int q = 1; q < slices; ++q) {
-            sf[e] += sf[q * cols + e];
-            si[e] += si[q * cols + e];
+    for (int h = slices; h > 1;) {
+        const int half = (h + 1) / 2;
+        __syncthreads();
+        for (int j = threadIdx.x; j < (h - half) * st; j += blockDim.x) {
+            sf[j] += sf[j + half * st];
+            si[j] += si[j + half * st];
         }
+        h = half;
+    }
     __syncthreads();
     const int tc = si[N];
     const float inv = tc > 0 ? 1.f / (float)tc : 0.f;
@@ -356,7 +384,7 @@ MOE_API moe_status moe_balance_loss(const moe_shape *s, const float *logits,
                    sizeof(float) * (kBalSlots + 1) * N, stream, s->T, N, s->K, logits, topk_idx,
                    token_mask, lse, part_i, part_f);
     });
-    launch_pdl(balance_finish, 1, 1024, 0, stream, N, s->K, ctas, std::max(1, 1024 / (N + 1)),
+    launch_pdl(balance_finish, 1, 1024, 0, stream, N, s->K, ctas, std::min(ctas, 1024 / (int)(bal_stride(N) / 4)),
                static_cast<const int32_t *>(part_i), static_cast<const float *>(part_f),
                expert_count, token_count, expert_prob, losses);
     return launch_status();

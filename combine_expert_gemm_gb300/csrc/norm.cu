@@ -7,9 +7,9 @@
 //   xh = (s - mean) rstd;  dgamma = sum_t dy xh;  dbeta = sum_t dy
 //
 // Bound by HBM: a few operations per element moved, so both kernels read every
-// row once.  Persistent CTAs of up to 1024 threads, one per SM, are cut into
+// row once.  Persistent CTAs of up to 512 threads, one per SM, are cut into
 // groups of whole warps; a group takes one row at a time and each of its
-// threads keeps the same columns (8, or 16 for d > 8192) from row to row.  The
+// threads keeps the same columns (8 to 32 of them) from row to row.  The
 // column's gamma and beta, and in the backward its share of dgamma and dbeta,
 // therefore stay in registers, and the weight gradients cost no second pass
 // over x and dy (the two-pass version took 74 of 172 us at 8192 x 2048).
@@ -20,10 +20,14 @@
 // keeps 64 KB and more of loads in flight with few registers.
 //
 // A row's sums cross the group's warps through shared memory with one barrier
-// per row (two alternating buffers).  The forward exchanges each warp's sum and
-// its squares centred at the warp's own mean, which combine exactly into the
-// variance around the row's mean:
+// per row (two alternating buffers); every warp then adds the warps' pairs
+// with lane shuffles.  The forward exchanges each warp's sum and its squares
+// centred at the warp's own mean, which combine exactly into the variance
+// around the row's mean:
 //   M2 = sum_w M2_w + n_w (mean_w - mean)^2.
+// Issue slots are the second limit: 8 columns a thread and every thread adding
+// all the warps' pairs in a loop took 370 us for the forward of 32768 x 4096,
+// whose bytes take 158.
 #include <math.h>
 
 #include <algorithm>
@@ -35,7 +39,7 @@ namespace moe {
 namespace {
 
 constexpr int kNormMaxD = 16384;
-constexpr int kNormMaxThreads = 1024;
+constexpr int kNormMaxThreads = 512;
 constexpr int kNormCtas = 152;        // one per SM; the order of the weight sums follows it
 constexpr size_t kNormRing = 196608;  // most shared memory the rings take
 
@@ -105,18 +109,33 @@ __device__ __forceinline__ void group_sync(int id, int warps) {
     else asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(warps * 32) : "memory");
 }
 
+// Sum over the group's warps of the pairs they left in r, in every thread.
+__device__ __forceinline__ float2 pair_sum(const float2 *r, int warps) {
+    const int lane = threadIdx.x & 31;
+    float2 v = lane < warps ? r[lane] : make_float2(0.f, 0.f);
+    for (int off = warps > 8 ? 8 : warps > 4 ? 4 : warps > 2 ? 2 : 1; off > 0; off >>= 1) {
+        v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, off);
+        v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, off);
+    }
+    return make_float2(__shfl_sync(0xFFFFFFFFu, v.x, 0), __shfl_sync(0xFFFFFFFFu, v.y, 0));
+}
+
 // How a row of d columns is laid over threads.
 struct NormPlan {
-    int cpt;      // chunks of 8 columns per thread: 1 or 2
+    int cpt;      // chunks of 8 columns per thread: 1, 2 or 4
     int warps;    // warps per group
     int groups;   // groups per CTA
     int ctas;
 };
 
+// 16 columns a thread halve a row's exchange between warps against 8; more
+// than 16 only where 512 threads do not reach, the registers being short.
+inline int norm_cpt(int d) { return d <= 256 ? 1 : d <= 16 * kNormMaxThreads ? 2 : 4; }
+
 inline NormPlan norm_plan(int rows, int d) {
     NormPlan p;
     const int chunks = d / 8;
-    p.cpt = chunks > kNormMaxThreads ? 2 : 1;
+    p.cpt = norm_cpt(d);
     p.warps = (chunks + 32 * p.cpt - 1) / (32 * p.cpt);
     p.groups = std::min(p.warps == 1 ? 16 : 15, kNormMaxThreads / 32 / p.warps);
     // few rows: one group per CTA before a second one on any SM
@@ -167,10 +186,17 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) fetch(first + s * step, s);
     // columns of this warp: chunks [32 gw, 32 gw + 32) of each of the CPT parts
-    int nw = 0;
+    auto columns = [&](int w) {
+        int n = 0;
 #pragma unroll
-    for (int c = 0; c < CPT; ++c) nw += 8 * max(0, min(32, chunks - c * gthreads - gw * 32));
-    const float inv_nw = nw > 0 ? 1.f / (float)nw : 0.f, inv_d = 1.f / (float)d;
+        for (int c = 0; c < CPT; ++c) n += 8 * max(0, min(32, chunks - c * gthreads - w * 32));
+        return (float)n;
+    };
+    const float inv_nw = 1.f / columns(gw), inv_d = 1.f / (float)d;
+    // lane w stands for warp w of the group when the warps' pairs are added
+    const float lane_n = lane < warps ? columns(lane) : 0.f;
+    const float lane_inv_n = lane < warps ? 1.f / lane_n : 0.f;
+    const int half_warps = warps > 8 ? 8 : warps > 4 ? 4 : warps > 2 ? 2 : 1;
     int stage = 0, buf = 0;
     for (int64_t t = first; t < rows; t += step) {
         fetch(t + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
@@ -211,17 +237,14 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
             if (lane == 0) r[gw] = make_float2(sum, m2);
             group_sync(1 + group, warps);
             buf ^= 1;
-            float tot = 0.f;
-            for (int w = 0; w < warps; ++w) tot += r[w].x;
-            mu = tot * inv_d;
-            var = 0.f;
-            for (int w = 0; w < warps; ++w) {
-                int n = 0;
-#pragma unroll
-                for (int c = 0; c < CPT; ++c) n += 8 * max(0, min(32, chunks - c * gthreads - w * 32));
-                const float dm = n > 0 ? r[w].x / (float)n - mu : 0.f;
-                var += fmaf((float)n * dm, dm, r[w].y);
-            }
+            const float2 mine = lane < warps ? r[lane] : make_float2(0.f, 0.f);
+            float tot = mine.x;
+            for (int off = half_warps; off > 0; off >>= 1) tot += __shfl_xor_sync(0xFFFFFFFFu, tot, off);
+            mu = __shfl_sync(0xFFFFFFFFu, tot, 0) * inv_d;
+            const float dm = fmaf(mine.x, lane_inv_n, -mu);
+            var = lane < warps ? fmaf(lane_n * dm, dm, mine.y) : 0.f;
+            for (int off = half_warps; off > 0; off >>= 1) var += __shfl_xor_sync(0xFFFFFFFFu, var, off);
+            var = __shfl_sync(0xFFFFFFFFu, var, 0);
         }
         const float rs = 1.f / sqrtf(fmaf(var, inv_d, eps));
         if (mean && tid == 0) {
@@ -255,13 +278,24 @@ norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restr
     const int groups = blockDim.x / gthreads, lane = threadIdx.x & 31, gw = tid >> 5;
     const int pitch = blockDim.x;
     const int chunks = d / 8;
-    float ga[CPT][8], dg[CPT][8], db[CPT][8];
+    // past 16 columns a thread the registers hold only the weight gradients:
+    // gamma is read again for each row and the row's second use of x and dy
+    // reads the ring again
+    constexpr bool kKeep = CPT <= 2;
+    constexpr int kHeld = kKeep ? CPT : 1;
+    float ga[kHeld][8], dg[CPT][8], db[CPT][8];
+    auto gamma_of = [&](int c, float (&g)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int col = (tid + c * gthreads) * 8 + i;
+            g[i] = gamma && col < d ? gamma[col] : 1.f;
+        }
+    };
 #pragma unroll
     for (int c = 0; c < CPT; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int col = (tid + c * gthreads) * 8 + i;
-            ga[c][i] = gamma && col < d ? gamma[col] : 1.f;
+            if (kKeep && i == 0) gamma_of(c, ga[c % kHeld]);
             dg[c][i] = 0.f;
             db[c][i] = 0.f;
         }
@@ -298,22 +332,31 @@ norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restr
             rs_n = rstd[t + step];
         }
         cp_async_wait<STAGES - 1>();
-        float xh[CPT][8], w[CPT][8];
+        // xh and w = dy gamma of one chunk; first: dgamma and dbeta take their share
+        auto chunk = [&](int c, bool first, float (&xh)[8], float (&w)[8]) {
+            ring_read<XT>(slot(stage, c), pitch, xh);
+            ring_read<YT>(slot(stage, c) + words<XT>() * pitch, pitch, w);
+            if (!kKeep) gamma_of(c, ga[0]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                xh[i] = (xh[i] - mu) * rs;
+                if (first) {
+                    dg[c][i] = fmaf(w[i], xh[i], dg[c][i]);
+                    db[c][i] += w[i];
+                }
+                w[i] *= ga[c % kHeld][i];
+            }
+        };
+        float xh[kHeld][8], w[kHeld][8];
         float sa = 0.f, sb = 0.f;
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
-            if (tid + c * gthreads < chunks) {
-                ring_read<XT>(slot(stage, c), pitch, xh[c]);
-                ring_read<YT>(slot(stage, c) + words<XT>() * pitch, pitch, w[c]);
+            if (tid + c * gthreads >= chunks) continue;
+            chunk(c, true, xh[c % kHeld], w[c % kHeld]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    xh[c][i] = (xh[c][i] - mu) * rs;
-                    dg[c][i] = fmaf(w[c][i], xh[c][i], dg[c][i]);
-                    db[c][i] += w[c][i];
-                    w[c][i] *= ga[c][i];
-                    sa += w[c][i];
-                    sb = fmaf(w[c][i], xh[c][i], sb);
-                }
+            for (int i = 0; i < 8; ++i) {
+                sa += w[c % kHeld][i];
+                sb = fmaf(w[c % kHeld][i], xh[c % kHeld][i], sb);
             }
         }
         sa = warp_sum(sa);
@@ -323,11 +366,9 @@ norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restr
             if (lane == 0) r[gw] = make_float2(sa, sb);
             group_sync(1 + group, warps);
             buf ^= 1;
-            sa = sb = 0.f;
-            for (int q = 0; q < warps; ++q) {
-                sa += r[q].x;
-                sb += r[q].y;
-            }
+            const float2 v = pair_sum(r, warps);
+            sa = v.x;
+            sb = v.y;
         }
         sa *= inv_d;
         sb *= inv_d;
@@ -337,8 +378,10 @@ norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restr
             if (at >= chunks) continue;
             float r[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             if (dres) ring_read<GT>(slot(stage, c) + (words<XT>() + words<YT>()) * pitch, pitch, r);
+            if (!kKeep) chunk(c, false, xh[0], w[0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] = fmaf(rs, w[c][i] - sa - xh[c][i] * sb, r[i]);
+            for (int i = 0; i < 8; ++i)
+                r[i] = fmaf(rs, w[c % kHeld][i] - sa - xh[c % kHeld][i] * sb, r[i]);
             store8(dx + t * d + at * 8, r);
         }
         if (++stage == STAGES) stage = 0;
@@ -426,6 +469,16 @@ constexpr int ring_stages(int words_per_thread) {
     return n > 4 ? 4 : n;
 }
 
+template <int V>
+struct Cpt {
+    static constexpr int value = V;
+};
+template <typename Fn>
+inline moe_status with_cpt(int d, Fn &&fn) {
+    const int c = norm_cpt(d);
+    return c == 1 ? fn(Cpt<1>()) : c == 2 ? fn(Cpt<2>()) : fn(Cpt<4>());
+}
+
 template <typename XT, int CPT>
 moe_status launch_norm_fwd(int32_t rows, int32_t d, const void *x, const moe_bf16 *add,
                            const float *gamma, const float *beta, float eps, void *x_sum,
@@ -487,11 +540,11 @@ MOE_API moe_status moe_layer_norm(int32_t rows, int32_t d, int32_t x_dtype, cons
     const void *ptrs[] = {x, add, gamma, beta, x_sum, y, mean, rstd};
     for (const void *p : ptrs)
         if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
-    const bool two = d / 8 > kNormMaxThreads;
     auto go = [&](auto xt) {
-        using XT = decltype(xt);
-        return two ? launch_norm_fwd<XT, 2>(rows, d, x, add, gamma, beta, eps, x_sum, y, mean, rstd, stream)
-                   : launch_norm_fwd<XT, 1>(rows, d, x, add, gamma, beta, eps, x_sum, y, mean, rstd, stream);
+        return with_cpt(d, [&](auto c) {
+            return launch_norm_fwd<decltype(xt), decltype(c)::value>(rows, d, x, add, gamma, beta, eps,
+                                                                     x_sum, y, mean, rstd, stream);
+        });
     };
     return x_dtype == MOE_BF16 ? go(uint16_t()) : go(float());
 }
@@ -516,15 +569,11 @@ MOE_API moe_status moe_layer_norm_backward(int32_t rows, int32_t d, int32_t x_dt
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) ||
         ws_bytes < moe_layer_norm_backward_workspace_bytes(rows, d))
         return MOE_ERR_WORKSPACE;
-    const bool two = d / 8 > kNormMaxThreads;
     auto go = [&](auto xt, auto yt, auto gt) {
-        using XT = decltype(xt);
-        using YT = decltype(yt);
-        using GT = decltype(gt);
-        return two ? launch_norm_bwd<XT, YT, GT, 2>(rows, d, x, dy, gamma, mean, rstd, dres, dx, dgamma,
-                                                    dbeta, ws, stream)
-                   : launch_norm_bwd<XT, YT, GT, 1>(rows, d, x, dy, gamma, mean, rstd, dres, dx, dgamma,
-                                                    dbeta, ws, stream);
+        return with_cpt(d, [&](auto c) {
+            return launch_norm_bwd<decltype(xt), decltype(yt), decltype(gt), decltype(c)::value>(
+                rows, d, x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, ws, stream);
+        });
     };
     auto go_g = [&](auto xt, auto yt) {
         return dx_dtype == MOE_BF16 ? go(xt, yt, uint16_t()) : go(xt, yt, float());
