@@ -43,57 +43,107 @@ constexpr int kNormMaxThreads = 512;
 constexpr int kNormCtas = 152;        // one per SM; the order of the weight sums follows it
 constexpr size_t kNormRing = 196608;  // most shared memory the rings take
 
-__device__ __forceinline__ void unpack(const uint4 &v, float *f) {
-    f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x);
-    f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
-    f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z);
-    f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
+// Two fp32 values side by side: the packed instructions halve the issue slots
+// of the element-wise work.
+typedef unsigned long long f2;
+
+__device__ __forceinline__ f2 make2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
 }
-__device__ __forceinline__ uint4 pack(const float *f) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ f2 both(float v) { return make2(v, v); }
+__device__ __forceinline__ float2 split(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
 }
-__device__ __forceinline__ void store8(uint16_t *p, const float *f) {
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float sum_of(f2 v) {
+    const float2 s = split(v);
+    return s.x + s.y;
+}
+
+// Eight elements (a chunk) as four pairs.
+__device__ __forceinline__ void unpack(const uint4 &v, f2 (&f)[4]) {
+    f[0] = make2(bf16_lo(v.x), bf16_hi(v.x));
+    f[1] = make2(bf16_lo(v.y), bf16_hi(v.y));
+    f[2] = make2(bf16_lo(v.z), bf16_hi(v.z));
+    f[3] = make2(bf16_lo(v.w), bf16_hi(v.w));
+}
+__device__ __forceinline__ uint32_t pack2(f2 v) {
+    const float2 s = split(v);
+    return pack_bf16x2(s.x, s.y);
+}
+__device__ __forceinline__ uint4 pack(const f2 (&f)[4]) {
+    return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
+}
+__device__ __forceinline__ void store8(uint16_t *p, const f2 (&f)[4]) {
     *reinterpret_cast<uint4 *>(p) = pack(f);
 }
-__device__ __forceinline__ void store8(float *p, const float *f) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ void store8(float *p, const f2 (&f)[4]) {
+    const float2 a = split(f[0]), b = split(f[1]), c = split(f[2]), e = split(f[3]);
+    reinterpret_cast<float4 *>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(c.x, c.y, e.x, e.y);
 }
-// The value a tensor of type T holds for v.
-__device__ __forceinline__ void round8(uint16_t, float *f) {
+// Stores a chunk and replaces it by what the store holds.
+__device__ __forceinline__ void store_round8(uint16_t *p, f2 (&f)[4]) {
     const uint4 v = pack(f);
+    *reinterpret_cast<uint4 *>(p) = v;
     unpack(v, f);
 }
-__device__ __forceinline__ void round8(float, float *) {}
+__device__ __forceinline__ void store_round8(float *p, f2 (&f)[4]) { store8(p, f); }
 
-// A thread's slot of one ring stage: 16-byte words `threads` words apart, so
-// that a warp's accesses are consecutive.  T's 8 elements take 1 or 2 words.
+// A thread's slot of one ring stage: 16-byte words kNormMaxThreads words apart
+// (a constant, so that words are addressed by offsets in the instruction), a
+// warp's accesses consecutive.  T's 8 elements take 1 or 2 words.
 template <typename T>
 constexpr __host__ __device__ int words() { return (int)sizeof(T) / 2; }
 
 template <typename T>
-__device__ __forceinline__ void ring_copy(uint4 *slot, int pitch, const T *src) {
+__device__ __forceinline__ void ring_copy(uint4 *slot, const T *src) {
     const uint4 *g = reinterpret_cast<const uint4 *>(src);
 #pragma unroll
-    for (int i = 0; i < words<T>(); ++i) cp_async16(slot + i * pitch, g + i);
+    for (int i = 0; i < words<T>(); ++i) cp_async16(slot + i * kNormMaxThreads, g + i);
 }
 template <typename T>
-__device__ __forceinline__ void ring_read(const uint4 *slot, int pitch, float *f);
+__device__ __forceinline__ void ring_read(const uint4 *slot, f2 (&f)[4]);
 template <>
-__device__ __forceinline__ void ring_read<uint16_t>(const uint4 *slot, int, float *f) {
+__device__ __forceinline__ void ring_read<uint16_t>(const uint4 *slot, f2 (&f)[4]) {
     unpack(*slot, f);
 }
 template <>
-__device__ __forceinline__ void ring_read<float>(const uint4 *slot, int pitch, float *f) {
+__device__ __forceinline__ void ring_read<float>(const uint4 *slot, f2 (&f)[4]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint4 v = slot[i * pitch];
-        f[4 * i] = __uint_as_float(v.x);
-        f[4 * i + 1] = __uint_as_float(v.y);
-        f[4 * i + 2] = __uint_as_float(v.z);
-        f[4 * i + 3] = __uint_as_float(v.w);
+        const uint4 v = slot[i * kNormMaxThreads];
+        f[2 * i] = make2(__uint_as_float(v.x), __uint_as_float(v.y));
+        f[2 * i + 1] = make2(__uint_as_float(v.z), __uint_as_float(v.w));
     }
+}
+// Eight consecutive fp32 parameters, or `none` where there are none.
+__device__ __forceinline__ void load_param(const float *p, int col, int d, float none, f2 (&f)[4]) {
+    float4 a = make_float4(none, none, none, none), b = a;
+    if (p && col < d) {
+        a = __ldg(reinterpret_cast<const float4 *>(p + col));
+        b = __ldg(reinterpret_cast<const float4 *>(p + col) + 1);
+    }
+    f[0] = make2(a.x, a.y); f[1] = make2(a.z, a.w);
+    f[2] = make2(b.x, b.y); f[3] = make2(b.z, b.w);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -152,40 +202,37 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
     pdl_enter();
     extern __shared__ uint4 ring[];
     __shared__ float2 red[2][32];
-    constexpr int kWords = CPT * (words<XT>() + 1);  // per thread and stage
+    constexpr int kChunkWords = words<XT>() + 1, kStage = CPT * kChunkWords * kNormMaxThreads;
     const int gthreads = warps * 32, group = threadIdx.x / gthreads, tid = threadIdx.x % gthreads;
     const int groups = blockDim.x / gthreads, lane = threadIdx.x & 31, gw = tid >> 5;
-    const int pitch = blockDim.x;
     const int chunks = d / 8;
-    float ga[CPT][8], be[CPT][8];
+    bool on[CPT];
+    f2 ga[CPT][4], be[CPT][4];
 #pragma unroll
-    for (int c = 0; c < CPT; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int col = (tid + c * gthreads) * 8 + i;
-            ga[c][i] = gamma && col < d ? gamma[col] : 1.f;
-            be[c][i] = beta && col < d ? beta[col] : 0.f;
-        }
+    for (int c = 0; c < CPT; ++c) {
+        on[c] = tid + c * gthreads < chunks;
+        load_param(gamma, (tid + c * gthreads) * 8, d, 1.f, ga[c]);
+        load_param(beta, (tid + c * gthreads) * 8, d, 0.f, be[c]);
+    }
     const int64_t step = (int64_t)gridDim.x * groups;
     const int64_t first = (int64_t)blockIdx.x * groups + group;
-    auto slot = [&](int stage, int c) {
-        return ring + ((size_t)stage * kWords + c * (words<XT>() + 1)) * pitch + threadIdx.x;
-    };
+    uint4 *mine = ring + threadIdx.x;
     auto fetch = [&](int64_t t, int stage) {
         if (t < rows) {
+            const int64_t at = t * d + tid * 8;
 #pragma unroll
             for (int c = 0; c < CPT; ++c) {
-                const int at = tid + c * gthreads;
-                if (at >= chunks) continue;
-                ring_copy(slot(stage, c), pitch, x + t * d + at * 8);
-                if (add) ring_copy(slot(stage, c) + words<XT>() * pitch, pitch, add + t * d + at * 8);
+                if (!on[c]) continue;
+                uint4 *s = mine + stage * kStage + c * kChunkWords * kNormMaxThreads;
+                ring_copy(s, x + at + c * gthreads * 8);
+                if (add) ring_copy(s + words<XT>() * kNormMaxThreads, add + at + c * gthreads * 8);
             }
         }
         cp_async_commit();
     };
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) fetch(first + s * step, s);
-    // columns of this warp: chunks [32 gw, 32 gw + 32) of each of the CPT parts
+    // columns of warp w: chunks [32 w, 32 w + 32) of each of the CPT parts
     auto columns = [&](int w) {
         int n = 0;
 #pragma unroll
@@ -201,48 +248,50 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
     for (int64_t t = first; t < rows; t += step) {
         fetch(t + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
         cp_async_wait<STAGES - 1>();
-        float f[CPT][8];
-        float sum = 0.f;
+        const int64_t at = t * d + tid * 8;
+        const uint4 *s = mine + stage * kStage;
+        if (++stage == STAGES) stage = 0;
+        f2 f[CPT][4];
+        f2 sum2 = both(0.f);
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
-            const int at = tid + c * gthreads;
-            if (at < chunks) {
-                ring_read<XT>(slot(stage, c), pitch, f[c]);
-                if (add) {
-                    float a[8];
-                    ring_read<uint16_t>(slot(stage, c) + words<XT>() * pitch, pitch, a);
+            if (!on[c]) continue;
+            ring_read<XT>(s + c * kChunkWords * kNormMaxThreads, f[c]);
+            if (add) {
+                f2 a[4];
+                ring_read<uint16_t>(s + (c * kChunkWords + words<XT>()) * kNormMaxThreads, a);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[c][i] += a[i];
-                    round8(XT(), f[c]);
-                    store8(x_sum + t * d + at * 8, f[c]);
-                }
+                for (int i = 0; i < 4; ++i) f[c][i] = add2(f[c][i], a[i]);
+                store_round8(x_sum + at + c * gthreads * 8, f[c]);
+            }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum += f[c][i];
+            for (int i = 0; i < 4; ++i) sum2 = add2(sum2, f[c][i]);
+        }
+        const float sum = warp_sum(sum_of(sum2));
+        const float mw = sum * inv_nw;
+        f2 sq2 = both(0.f);
+        const f2 neg_mw = both(-mw);
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) {
+            if (!on[c]) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f2 v = add2(f[c][i], neg_mw);
+                sq2 = fma2(v, v, sq2);
             }
         }
-        if (++stage == STAGES) stage = 0;
-        sum = warp_sum(sum);
-        const float mw = sum * inv_nw;
-        float m2 = 0.f;
-#pragma unroll
-        for (int c = 0; c < CPT; ++c)
-            if (tid + c * gthreads < chunks) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) m2 = fmaf(f[c][i] - mw, f[c][i] - mw, m2);
-            }
-        m2 = warp_sum(m2);
-        float mu = mw, var = m2;
+        float mu = mw, var = warp_sum(sum_of(sq2));
         if (warps > 1) {
             float2 *r = red[buf] + group * warps;
-            if (lane == 0) r[gw] = make_float2(sum, m2);
+            if (lane == 0) r[gw] = make_float2(sum, var);
             group_sync(1 + group, warps);
             buf ^= 1;
-            const float2 mine = lane < warps ? r[lane] : make_float2(0.f, 0.f);
-            float tot = mine.x;
+            const float2 pair = lane < warps ? r[lane] : make_float2(0.f, 0.f);
+            float tot = pair.x;
             for (int off = half_warps; off > 0; off >>= 1) tot += __shfl_xor_sync(0xFFFFFFFFu, tot, off);
             mu = __shfl_sync(0xFFFFFFFFu, tot, 0) * inv_d;
-            const float dm = fmaf(mine.x, lane_inv_n, -mu);
-            var = lane < warps ? fmaf(lane_n * dm, dm, mine.y) : 0.f;
+            const float dm = fmaf(pair.x, lane_inv_n, -mu);
+            var = lane < warps ? fmaf(lane_n * dm, dm, pair.y) : 0.f;
             for (int off = half_warps; off > 0; off >>= 1) var += __shfl_xor_sync(0xFFFFFFFFu, var, off);
             var = __shfl_sync(0xFFFFFFFFu, var, 0);
         }
@@ -251,13 +300,14 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
             mean[t] = mu;
             rstd[t] = rs;
         }
+        const f2 neg_mu = both(-mu), rs2 = both(rs);
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
-            const int at = tid + c * gthreads;
-            if (at >= chunks) continue;
+            if (!on[c]) continue;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[c][i] = fmaf((f[c][i] - mu) * rs, ga[c][i], be[c][i]);
-            store8(y + t * d + at * 8, f[c]);
+            for (int i = 0; i < 4; ++i)
+                f[c][i] = fma2(mul2(add2(f[c][i], neg_mu), rs2), ga[c][i], be[c][i]);
+            store8(y + at + c * gthreads * 8, f[c]);
         }
     }
     cp_async_wait<0>();
@@ -272,48 +322,38 @@ norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restr
     pdl_enter();
     extern __shared__ uint4 ring[];
     __shared__ float2 red[2][32];
-    constexpr int kChunkWords = words<XT>() + words<YT>() + words<GT>();
-    constexpr int kWords = CPT * kChunkWords;
+    constexpr int kDy = words<XT>(), kRes = kDy + words<YT>(), kChunkWords = kRes + words<GT>();
+    constexpr int kStage = CPT * kChunkWords * kNormMaxThreads;
     const int gthreads = warps * 32, group = threadIdx.x / gthreads, tid = threadIdx.x % gthreads;
     const int groups = blockDim.x / gthreads, lane = threadIdx.x & 31, gw = tid >> 5;
-    const int pitch = blockDim.x;
     const int chunks = d / 8;
     // past 16 columns a thread the registers hold only the weight gradients:
     // gamma is read again for each row and the row's second use of x and dy
     // reads the ring again
     constexpr bool kKeep = CPT <= 2;
     constexpr int kHeld = kKeep ? CPT : 1;
-    float ga[kHeld][8], dg[CPT][8], db[CPT][8];
-    auto gamma_of = [&](int c, float (&g)[8]) {
+    bool on[CPT];
+    f2 ga[kHeld][4], dg[CPT][4], db[CPT][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int col = (tid + c * gthreads) * 8 + i;
-            g[i] = gamma && col < d ? gamma[col] : 1.f;
-        }
-    };
+    for (int c = 0; c < CPT; ++c) {
+        on[c] = tid + c * gthreads < chunks;
+        if (kKeep) load_param(gamma, (tid + c * gthreads) * 8, d, 1.f, ga[c % kHeld]);
 #pragma unroll
-    for (int c = 0; c < CPT; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (kKeep && i == 0) gamma_of(c, ga[c % kHeld]);
-            dg[c][i] = 0.f;
-            db[c][i] = 0.f;
-        }
+        for (int i = 0; i < 4; ++i) dg[c][i] = db[c][i] = both(0.f);
+    }
     const int64_t step = (int64_t)gridDim.x * groups;
     const int64_t first = (int64_t)blockIdx.x * groups + group;
-    auto slot = [&](int stage, int c) {
-        return ring + ((size_t)stage * kWords + c * kChunkWords) * pitch + threadIdx.x;
-    };
+    uint4 *mine = ring + threadIdx.x;
     auto fetch = [&](int64_t t, int stage) {
         if (t < rows) {
+            const int64_t at = t * d + tid * 8;
 #pragma unroll
             for (int c = 0; c < CPT; ++c) {
-                const int at = tid + c * gthreads;
-                if (at >= chunks) continue;
-                uint4 *s = slot(stage, c);
-                ring_copy(s, pitch, x + t * d + at * 8);
-                ring_copy(s + words<XT>() * pitch, pitch, dy + t * d + at * 8);
-                if (dres) ring_copy(s + (words<XT>() + words<YT>()) * pitch, pitch, dres + t * d + at * 8);
+                if (!on[c]) continue;
+                uint4 *s = mine + stage * kStage + c * kChunkWords * kNormMaxThreads;
+                ring_copy(s, x + at + c * gthreads * 8);
+                ring_copy(s + kDy * kNormMaxThreads, dy + at + c * gthreads * 8);
+                if (dres) ring_copy(s + kRes * kNormMaxThreads, dres + at + c * gthreads * 8);
             }
         }
         cp_async_commit();
@@ -332,35 +372,38 @@ norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restr
             rs_n = rstd[t + step];
         }
         cp_async_wait<STAGES - 1>();
+        const int64_t at = t * d + tid * 8;
+        const uint4 *s = mine + stage * kStage;
+        if (++stage == STAGES) stage = 0;
+        const f2 neg_mu = both(-mu), rs2 = both(rs);
         // xh and w = dy gamma of one chunk; first: dgamma and dbeta take their share
-        auto chunk = [&](int c, bool first, float (&xh)[8], float (&w)[8]) {
-            ring_read<XT>(slot(stage, c), pitch, xh);
-            ring_read<YT>(slot(stage, c) + words<XT>() * pitch, pitch, w);
-            if (!kKeep) gamma_of(c, ga[0]);
+        auto chunk = [&](int c, bool take, f2 (&xh)[4], f2 (&w)[4]) {
+            ring_read<XT>(s + c * kChunkWords * kNormMaxThreads, xh);
+            ring_read<YT>(s + (c * kChunkWords + kDy) * kNormMaxThreads, w);
+            if (!kKeep) load_param(gamma, (tid + c * gthreads) * 8, d, 1.f, ga[0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                xh[i] = (xh[i] - mu) * rs;
-                if (first) {
-                    dg[c][i] = fmaf(w[i], xh[i], dg[c][i]);
-                    db[c][i] += w[i];
+            for (int i = 0; i < 4; ++i) {
+                xh[i] = mul2(add2(xh[i], neg_mu), rs2);
+                if (take) {
+                    dg[c][i] = fma2(w[i], xh[i], dg[c][i]);
+                    db[c][i] = add2(db[c][i], w[i]);
                 }
-                w[i] *= ga[c % kHeld][i];
+                w[i] = mul2(w[i], ga[c % kHeld][i]);
             }
         };
-        float xh[kHeld][8], w[kHeld][8];
-        float sa = 0.f, sb = 0.f;
+        f2 xh[kHeld][4], w[kHeld][4];
+        f2 sa2 = both(0.f), sb2 = both(0.f);
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
-            if (tid + c * gthreads >= chunks) continue;
+            if (!on[c]) continue;
             chunk(c, true, xh[c % kHeld], w[c % kHeld]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                sa += w[c % kHeld][i];
-                sb = fmaf(w[c % kHeld][i], xh[c % kHeld][i], sb);
+            for (int i = 0; i < 4; ++i) {
+                sa2 = add2(sa2, w[c % kHeld][i]);
+                sb2 = fma2(w[c % kHeld][i], xh[c % kHeld][i], sb2);
             }
         }
-        sa = warp_sum(sa);
-        sb = warp_sum(sb);
+        float sa = warp_sum(sum_of(sa2)), sb = warp_sum(sum_of(sb2));
         if (warps > 1) {
             float2 *r = red[buf] + group * warps;
             if (lane == 0) r[gw] = make_float2(sa, sb);
@@ -370,21 +413,24 @@ norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restr
             sa = v.x;
             sb = v.y;
         }
-        sa *= inv_d;
-        sb *= inv_d;
+        // dx = dres + rs w - rs sa / d - rs sb / d xh
+        const f2 a2 = both(-sa * inv_d * rs), b2 = both(-sb * inv_d * rs);
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
-            const int at = tid + c * gthreads;
-            if (at >= chunks) continue;
-            float r[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (dres) ring_read<GT>(slot(stage, c) + (words<XT>() + words<YT>()) * pitch, pitch, r);
+            if (!on[c]) continue;
+            f2 r[4];
+            if (dres) {
+                ring_read<GT>(s + (c * kChunkWords + kRes) * kNormMaxThreads, r);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[i] = both(0.f);
+            }
             if (!kKeep) chunk(c, false, xh[0], w[0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                r[i] = fmaf(rs, w[c % kHeld][i] - sa - xh[c % kHeld][i] * sb, r[i]);
-            store8(dx + t * d + at * 8, r);
+            for (int i = 0; i < 4; ++i)
+                r[i] = add2(r[i], fma2(rs2, w[c % kHeld][i], fma2(b2, xh[c % kHeld][i], a2)));
+            store8(dx + at + c * gthreads * 8, r);
         }
-        if (++stage == STAGES) stage = 0;
     }
     cp_async_wait<0>();
     if (!part) return;
@@ -489,7 +535,7 @@ moe_status launch_norm_fwd(int32_t rows, int32_t d, const void *x, const moe_bf1
     auto *kern = norm_fwd<XT, CPT, kStages>;
     static PerDeviceOnce attr;
     if (!device_once(attr, [&] { return set_smem_limit(kern, kNormRing); })) return MOE_ERR_CUDA;
-    launch_pdl(kern, p.ctas, threads, (size_t)kStages * kWords * 16 * threads, stream, rows, d, p.warps,
+    launch_pdl(kern, p.ctas, threads, (size_t)kStages * kWords * 16 * kNormMaxThreads, stream, rows, d, p.warps,
                static_cast<const XT *>(x), add, gamma, beta, eps, static_cast<XT *>(x_sum), y, mean,
                rstd);
     return launch_status();
@@ -510,7 +556,7 @@ moe_status launch_norm_bwd(int32_t rows, int32_t d, const void *x, const void *d
         static PerDeviceOnce attr;
         if (!device_once(attr, [&] { return set_smem_limit(kern, kNormRing); })) return MOE_ERR_CUDA;
         // the ring also holds the groups' weight sums at the end
-        const size_t smem = std::max((size_t)kStages * kWords * 16 * threads,
+        const size_t smem = std::max((size_t)kStages * kWords * 16 * kNormMaxThreads,
                                      (size_t)p.groups * 2 * d * sizeof(float));
         launch_pdl(kern, p.ctas, threads, smem, stream, rows, d, p.warps, static_cast<const XT *>(x),
                    static_cast<const YT *>(dy), gamma, mean, rstd, static_cast<const GT *>(dres),
