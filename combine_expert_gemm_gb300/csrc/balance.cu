@@ -10,11 +10,12 @@
 // per logit.  The group is as small as the row allows (8 lanes x 4 for N <= 32)
 // up to a whole warp: short rows then fill whole 128-byte requests, four tokens
 // to a warp.  Rows of a multiple of four logits are read and written in
-// 16-byte vectors.  __expf: 2 + 1.17 |x| ulp, so what is off the most are the
-// smallest probabilities; expf's extra instructions took the time of a third of
-// the bytes.
+// 16-byte vectors (8 bytes for an even number).
+//
+// Each probability is a packed subtraction and product and the hardware's 2^x:
+// expf and scalar arithmetic made the forward issue-bound, 40 us at T = 131072,
+// N = 250, where its bytes take 20.
 #include <algorithm>
-#include <type_traits>
 
 #include "../../include/moe_block.h"
 #include "moe_common.cuh"
@@ -28,6 +29,14 @@ constexpr int kBalSlots = 8;   // warps that add up side by side in shared memor
 // Partial sums of one CTA in the workspace, rounded up to 16 bytes: int32
 // counts [N] and the tokens, then fp32 probability sums [N] and the sum of lse^2.
 inline __host__ __device__ int64_t bal_stride(int N) { return (N + 1 + 3) / 4 * 4; }
+
+constexpr float kLog2e = 1.44269504f;
+
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 
 template <int LANES>
 __device__ __forceinline__ float group_max(float v) {
@@ -43,53 +52,59 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 // The experts of lane `sub` of a group: register i holds expert
-// first(sub) + step(i).
-template <int LANES, int VPT, bool VEC>
+// first(sub) + step(i), in vectors of VEC logits.  HALF: the row is longer than
+// half the registers, so the vectors of the first half need no bounds check.
+template <int LANES, int VPT, int VEC, bool HALF>
 struct Row {
-    static __device__ __forceinline__ int first(int sub) { return VEC ? 4 * sub : sub; }
+    static __device__ __forceinline__ int first(int sub) { return VEC * sub; }
     static __device__ __forceinline__ constexpr int step(int i) {
-        return VEC ? i / 4 * 4 * LANES + i % 4 : i * LANES;
+        return i / VEC * VEC * LANES + i % VEC;
     }
-    // a row's logits; experts past N (or all of them) read as `fill`
-    static __device__ __forceinline__ void load(const float *row, int sub, int N, bool on, float fill,
-                                                float (&v)[VPT]) {
+    static __device__ __forceinline__ bool in_row(int e0, int i, int N) {
+        return (HALF && i < VPT / 2 && VEC <= VPT / 2) || e0 + step(i) < N;
+    }
+    // a row's logits; experts past N (or all of them) read as -inf
+    static __device__ __forceinline__ void load(const float *row, int sub, int N, bool on, float (&v)[VPT]) {
         const int e0 = first(sub);
-        if (VEC) {
 #pragma unroll
-            for (int i = 0; i < VPT; i += 4) {
-                float4 q = make_float4(fill, fill, fill, fill);
-                if (on && e0 + step(i) < N) q = __ldcs(reinterpret_cast<const float4 *>(row + e0 + step(i)));
+        for (int i = 0; i < VPT; i += VEC) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) v[i + j] = -INFINITY;
+            if (!on || !in_row(e0, i, N)) continue;
+            const float *p = row + e0 + step(i);
+            if (VEC == 4) {
+                const float4 q = __ldcs(reinterpret_cast<const float4 *>(p));
                 v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+            } else if (VEC == 2) {
+                const float2 q = __ldcs(reinterpret_cast<const float2 *>(p));
+                v[i] = q.x; v[i + 1] = q.y;
+            } else {
+                v[i] = __ldcs(p);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) v[i] = on && e0 + step(i) < N ? __ldcs(row + e0 + step(i)) : fill;
         }
     }
     static __device__ __forceinline__ void store(float *row, int sub, int N, const float (&v)[VPT]) {
         const int e0 = first(sub);
-        if (VEC) {
 #pragma unroll
-            for (int i = 0; i < VPT; i += 4)
-                if (e0 + step(i) < N)
-                    *reinterpret_cast<float4 *>(row + e0 + step(i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VPT; ++i)
-                if (e0 + step(i) < N) row[e0 + step(i)] = v[i];
+        for (int i = 0; i < VPT; i += VEC) {
+            if (!in_row(e0, i, N)) continue;
+            float *p = row + e0 + step(i);
+            if (VEC == 4) *reinterpret_cast<float4 *>(p) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            else if (VEC == 2) *reinterpret_cast<float2 *>(p) = make_float2(v[i], v[i + 1]);
+            else *p = v[i];
         }
     }
 };
 
 __host__ __device__ constexpr int bal_threads(int vpt) { return vpt >= 16 ? 512 : 1024; }
 
-template <int LANES, int VPT, bool VEC>
+template <int LANES, int VPT, int VEC, bool HALF>
 __global__ void __launch_bounds__(bal_threads(VPT), 1)
 balance_partial(int T, int N, int K, const float *__restrict__ logits,
                 const int32_t *__restrict__ topk_idx, const uint8_t *__restrict__ mask,
                 float *__restrict__ lse, int32_t *__restrict__ part_i, float *__restrict__ part_f) {
     pdl_enter();
-    using R = Row<LANES, VPT, VEC>;
+    using R = Row<LANES, VPT, VEC, HALF>;
     constexpr int kThreads = bal_threads(VPT), kWarps = kThreads / 32;
     constexpr int kGroups = kThreads / LANES;
     extern __shared__ float sm[];
@@ -101,6 +116,7 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
     for (int i = threadIdx.x; i < (kBalSlots + 1) * N; i += kThreads) sm[i] = 0.f;
     __syncthreads();
     float acc[VPT];
+    float2 *acc2 = reinterpret_cast<float2 *>(acc);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) acc[i] = 0.f;
     float z = 0.f;
@@ -117,7 +133,7 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
     bool ahead_on = false;
     if (kAhead) {
         ahead_on = counted(w0 + lane / LANES);
-        R::load(logits + (w0 + lane / LANES) * N, sub, N, ahead_on, -INFINITY, ahead);
+        R::load(logits + (w0 + lane / LANES) * N, sub, N, ahead_on, ahead);
     }
     for (; w0 < T; w0 += step) {
         const int64_t t = w0 + lane / LANES;
@@ -129,26 +145,32 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
 #pragma unroll
             for (int i = 0; i < VPT; ++i) v[i] = ahead[i];
             ahead_on = counted(t + step);
-            R::load(logits + (t + step) * N, sub, N, ahead_on, -INFINITY, ahead);
+            R::load(logits + (t + step) * N, sub, N, ahead_on, ahead);
         } else {
             on = counted(t);
-            R::load(logits + t * N, sub, N, on, -INFINITY, v);
+            R::load(logits + t * N, sub, N, on, v);
         }
         float m = v[0];
 #pragma unroll
         for (int i = 1; i < VPT; ++i) m = fmaxf(m, v[i]);
         m = group_max<LANES>(m);
         if (m == -INFINITY) m = 0.f;  // all -inf: probabilities 0; all NaN: NaN below
-        float sum = 0.f;
+        // exp(v - m) = 2^((v - m) log2 e); the difference comes first, because
+        // v log2 e overflows for the lowest values that masks are made of
+        const float2 mul = make_float2(kLog2e, kLog2e), off = make_float2(-m, -m);
+        float2 sum2 = make_float2(0.f, 0.f);
+        float2 *v2 = reinterpret_cast<float2 *>(v);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            v[i] = __expf(v[i] - m);
-            sum += v[i];
+        for (int i = 0; i < VPT / 2; ++i) {
+            const float2 a = __fmul2_rn(__fadd2_rn(v2[i], off), mul);
+            v2[i] = make_float2(ex2(a.x), ex2(a.y));
+            sum2 = __fadd2_rn(sum2, v2[i]);
         }
-        sum = group_sum<LANES>(sum);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float sum = group_sum<LANES>(sum2.x + sum2.y);
+        const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+        const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+        for (int i = 0; i < VPT / 2; ++i) acc2[i] = __ffma2_rn(v2[i], inv2, acc2[i]);
         if (on) {
             for (int k = sub; k < K; k += LANES) {
                 const int e = topk_idx[t * K + k];
@@ -156,7 +178,7 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
             }
         }
         if (in && sub == 0) {
-            const float l = m + logf(sum);
+            const float l = m + __logf(sum);
             lse[t] = on ? l : 0.f;
             if (on) {
                 ++tok;
@@ -270,7 +292,7 @@ balance_finish(int N, int K, int ctas, int slices, const int32_t *__restrict__ p
 
 constexpr int kBwdThreads = 256;
 
-template <int LANES, int VPT, bool VEC>
+template <int LANES, int VPT, int VEC, bool HALF>
 __global__ void __launch_bounds__(kBwdThreads)
 balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
                  const int32_t *__restrict__ topk_idx, const uint8_t *__restrict__ mask,
@@ -278,7 +300,7 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
                  const float *__restrict__ lse, const float *__restrict__ dlosses,
                  const float *__restrict__ dlogit, float *__restrict__ dlogits) {
     pdl_enter();
-    using R = Row<LANES, VPT, VEC>;
+    using R = Row<LANES, VPT, VEC, HALF>;
     constexpr int kGroups = kBwdThreads / LANES;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = threadIdx.x % LANES;
     const int tc = token_count[0];
@@ -296,19 +318,26 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
         const bool in = t < T;
         bool on = in && !(mask && mask[t] == 0);
         float v[VPT];
-        R::load(logits + t * N, sub, N, on, -INFINITY, v);
+        R::load(logits + t * N, sub, N, on, v);
         const float l = on ? lse[t] : 0.f;
         on = on && l != -INFINITY;  // every logit -inf: no probability, no gradient
-        float dot = 0.f;
+        const float2 mul = make_float2(kLog2e, kLog2e), off = make_float2(-l, -l);
+        float2 dot2 = make_float2(0.f, 0.f);
+        float2 *v2 = reinterpret_cast<float2 *>(v), *f2 = reinterpret_cast<float2 *>(f);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            v[i] = on ? __expf(v[i] - l) : 0.f;
-            dot = fmaf(v[i], f[i], dot);
+        for (int i = 0; i < VPT / 2; ++i) {
+            const float2 a = __fmul2_rn(__fadd2_rn(v2[i], off), mul);
+            v2[i] = make_float2(ex2(a.x), ex2(a.y));
+            dot2 = __ffma2_rn(v2[i], f2[i], dot2);
         }
-        dot = group_sum<LANES>(dot);
-        const float c = cz * l;
+        const float dot = group_sum<LANES>(dot2.x + dot2.y);
+        const float c = fmaf(-cb, dot, cz * l);
+        const float2 c2 = make_float2(c, c), cb2 = make_float2(cb, cb);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) v[i] = on ? v[i] * fmaf(cb, f[i] - dot, c) : 0.f;
+        for (int i = 0; i < VPT / 2; ++i) {
+            const float2 g = __fmul2_rn(v2[i], __ffma2_rn(cb2, f2[i], c2));
+            v2[i] = on ? g : make_float2(0.f, 0.f);
+        }
         if (dlogit && in)
             for (int k = 0; k < K; ++k) {
                 const int at = topk_idx[t * K + k];
@@ -321,26 +350,31 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
     }
 }
 
-// The smallest group that holds a row of N logits: calls fn with LANES, VPT
-// and whether rows are whole 16-byte vectors.
-template <int L, int V, bool VEC>
-struct Shape3 {
-    static constexpr int lanes = L, vpt = V;
-    static constexpr bool vec = VEC;
+// The smallest group that holds a row of N logits: calls fn with LANES, VPT,
+// the vector length that keeps rows aligned, and whether N fills half of it.
+template <int L, int V, int W, bool H>
+struct RowOf {
+    static constexpr int lanes = L, vpt = V, vec = W;
+    static constexpr bool half = H;
+};
+template <int V>
+struct Int {
+    static constexpr int value = V;
 };
 template <typename Fn>
 inline void with_row(int N, Fn &&fn) {
-    auto go = [&](auto vec) {
-        constexpr bool kVec = decltype(vec)::value;
-        if (N <= 32) fn(Shape3<8, 4, kVec>());
-        else if (N <= 64) fn(Shape3<16, 4, kVec>());
-        else if (N <= 128) fn(Shape3<32, 4, kVec>());
-        else if (N <= 256) fn(Shape3<32, 8, kVec>());
-        else if (N <= 512) fn(Shape3<32, 16, kVec>());
-        else fn(Shape3<32, 32, kVec>());
+    auto go = [&](auto w) {
+        constexpr int kVec = decltype(w)::value;
+        if (N <= 32) fn(RowOf<8, 4, kVec, false>());
+        else if (N <= 64) fn(RowOf<16, 4, kVec, true>());
+        else if (N <= 128) fn(RowOf<32, 4, kVec, true>());
+        else if (N <= 256) fn(RowOf<32, 8, kVec, true>());
+        else if (N <= 512) fn(RowOf<32, 16, kVec, true>());
+        else fn(RowOf<32, 32, kVec, true>());
     };
-    if (N % 4 == 0) go(std::true_type());
-    else go(std::false_type());
+    if (N % 4 == 0) go(Int<4>());
+    else if (N % 2 == 0) go(Int<2>());
+    else go(Int<1>());
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -382,7 +416,7 @@ MOE_API moe_status moe_balance_loss(const moe_shape *s, const float *logits,
         using Q = decltype(q);
         constexpr int kThreads = bal_threads(Q::vpt);
         ctas = (int)std::min<int64_t>(kBalCtas, std::max<int64_t>(1, ceil_div(s->T, kThreads / Q::lanes)));
-        launch_pdl(balance_partial<Q::lanes, Q::vpt, Q::vec>, ctas, kThreads,
+        launch_pdl(balance_partial<Q::lanes, Q::vpt, Q::vec, Q::half>, ctas, kThreads,
                    sizeof(float) * (kBalSlots + 1) * N, stream, s->T, N, s->K, logits, topk_idx,
                    token_mask, lse, part_i, part_f);
     });
@@ -411,7 +445,7 @@ MOE_API moe_status moe_balance_loss_backward(const moe_shape *s, const float *lo
     with_row(s->N, [&](auto q) {
         using Q = decltype(q);
         const int64_t want = ceil_div(s->T, kBwdThreads / Q::lanes);
-        launch_pdl(balance_bwd_rows<Q::lanes, Q::vpt, Q::vec>,
+        launch_pdl(balance_bwd_rows<Q::lanes, Q::vpt, Q::vec, Q::half>,
                    (unsigned)std::min<int64_t>(want, (int64_t)num_sms() * 8), kBwdThreads, 0, stream,
                    s->T, s->N, s->K, logits, topk_idx, token_mask, expert_count, token_count, lse,
                    dlosses, dlogit, dlogits);

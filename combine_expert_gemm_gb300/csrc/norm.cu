@@ -45,38 +45,14 @@ constexpr size_t kNormRing = 196608;  // most shared memory the rings take
 
 // Two fp32 values side by side: the packed instructions halve the issue slots
 // of the element-wise work.
-typedef unsigned long long f2;
+typedef float2 f2;
 
-__device__ __forceinline__ f2 make2(float lo, float hi) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ f2 both(float v) { return make2(v, v); }
-__device__ __forceinline__ float2 split(f2 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float sum_of(f2 v) {
-    const float2 s = split(v);
-    return s.x + s.y;
-}
+__device__ __forceinline__ f2 make2(float lo, float hi) { return make_float2(lo, hi); }
+__device__ __forceinline__ f2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float sum_of(f2 v) { return v.x + v.y; }
 
 // Eight elements (a chunk) as four pairs.
 __device__ __forceinline__ void unpack(const uint4 &v, f2 (&f)[4]) {
@@ -85,10 +61,7 @@ __device__ __forceinline__ void unpack(const uint4 &v, f2 (&f)[4]) {
     f[2] = make2(bf16_lo(v.z), bf16_hi(v.z));
     f[3] = make2(bf16_lo(v.w), bf16_hi(v.w));
 }
-__device__ __forceinline__ uint32_t pack2(f2 v) {
-    const float2 s = split(v);
-    return pack_bf16x2(s.x, s.y);
-}
+__device__ __forceinline__ uint32_t pack2(f2 v) { return pack_bf16x2(v.x, v.y); }
 __device__ __forceinline__ uint4 pack(const f2 (&f)[4]) {
     return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
 }
@@ -96,17 +69,18 @@ __device__ __forceinline__ void store8(uint16_t *p, const f2 (&f)[4]) {
     *reinterpret_cast<uint4 *>(p) = pack(f);
 }
 __device__ __forceinline__ void store8(float *p, const f2 (&f)[4]) {
-    const float2 a = split(f[0]), b = split(f[1]), c = split(f[2]), e = split(f[3]);
-    reinterpret_cast<float4 *>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(c.x, c.y, e.x, e.y);
+    reinterpret_cast<float4 *>(p)[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
 }
-// Stores a chunk and replaces it by what the store holds.
-__device__ __forceinline__ void store_round8(uint16_t *p, f2 (&f)[4]) {
+// Stores a chunk (if on) and replaces it by what the store holds.
+__device__ __forceinline__ void store_round8(uint16_t *p, f2 (&f)[4], bool on) {
     const uint4 v = pack(f);
-    *reinterpret_cast<uint4 *>(p) = v;
+    if (on) *reinterpret_cast<uint4 *>(p) = v;
     unpack(v, f);
 }
-__device__ __forceinline__ void store_round8(float *p, f2 (&f)[4]) { store8(p, f); }
+__device__ __forceinline__ void store_round8(float *p, f2 (&f)[4], bool on) {
+    if (on) store8(p, f);
+}
 
 // A thread's slot of one ring stage: 16-byte words kNormMaxThreads words apart
 // (a constant, so that words are addressed by offsets in the instruction), a
@@ -114,11 +88,18 @@ __device__ __forceinline__ void store_round8(float *p, f2 (&f)[4]) { store8(p, f
 template <typename T>
 constexpr __host__ __device__ int words() { return (int)sizeof(T) / 2; }
 
+// Copies 8 elements (bytes = 16), or zeros without reading src (bytes = 0): a
+// thread past the row's end, or a tensor that is not there, then needs no
+// branch where the slot is read.
 template <typename T>
-__device__ __forceinline__ void ring_copy(uint4 *slot, const T *src) {
+__device__ __forceinline__ void ring_copy(uint4 *slot, const T *src, int bytes) {
     const uint4 *g = reinterpret_cast<const uint4 *>(src);
 #pragma unroll
-    for (int i = 0; i < words<T>(); ++i) cp_async16(slot + i * kNormMaxThreads, g + i);
+    for (int i = 0; i < words<T>(); ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         smem_u32(slot + i * kNormMaxThreads)),
+                     "l"(g + i), "r"(bytes)
+                     : "memory");
 }
 template <typename T>
 __device__ __forceinline__ void ring_read(const uint4 *slot, f2 (&f)[4]);
@@ -159,15 +140,12 @@ __device__ __forceinline__ void group_sync(int id, int warps) {
     else asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(warps * 32) : "memory");
 }
 
-// Sum over the group's warps of the pairs they left in r, in every thread.
-__device__ __forceinline__ float2 pair_sum(const float2 *r, int warps) {
-    const int lane = threadIdx.x & 31;
-    float2 v = lane < warps ? r[lane] : make_float2(0.f, 0.f);
-    for (int off = warps > 8 ? 8 : warps > 4 ? 4 : warps > 2 ? 2 : 1; off > 0; off >>= 1) {
-        v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, off);
-        v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, off);
-    }
-    return make_float2(__shfl_sync(0xFFFFFFFFu, v.x, 0), __shfl_sync(0xFFFFFFFFu, v.y, 0));
+// Sum over 16 lanes (the group's warps, at most 16, one per lane of each half
+// warp), in every lane.
+__device__ __forceinline__ float half_sum(float v) {
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+    return v;
 }
 
 // How a row of d columns is laid over threads.
@@ -210,7 +188,7 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
     f2 ga[CPT][4], be[CPT][4];
 #pragma unroll
     for (int c = 0; c < CPT; ++c) {
-        on[c] = tid + c * gthreads < chunks;
+        on[c] = tid + c * gthreads < chunks;  // a thread past the row works on zeros
         load_param(gamma, (tid + c * gthreads) * 8, d, 1.f, ga[c]);
         load_param(beta, (tid + c * gthreads) * 8, d, 0.f, be[c]);
     }
@@ -222,10 +200,10 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
             const int64_t at = t * d + tid * 8;
 #pragma unroll
             for (int c = 0; c < CPT; ++c) {
-                if (!on[c]) continue;
                 uint4 *s = mine + stage * kStage + c * kChunkWords * kNormMaxThreads;
-                ring_copy(s, x + at + c * gthreads * 8);
-                if (add) ring_copy(s + words<XT>() * kNormMaxThreads, add + at + c * gthreads * 8);
+                ring_copy(s, x + at + c * gthreads * 8, on[c] ? 16 : 0);
+                if (add)
+                    ring_copy(s + words<XT>() * kNormMaxThreads, add + at + c * gthreads * 8, on[c] ? 16 : 0);
             }
         }
         cp_async_commit();
@@ -241,9 +219,9 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
     };
     const float inv_nw = 1.f / columns(gw), inv_d = 1.f / (float)d;
     // lane w stands for warp w of the group when the warps' pairs are added
-    const float lane_n = lane < warps ? columns(lane) : 0.f;
-    const float lane_inv_n = lane < warps ? 1.f / lane_n : 0.f;
-    const int half_warps = warps > 8 ? 8 : warps > 4 ? 4 : warps > 2 ? 2 : 1;
+    const int other = lane & 15;
+    const float lane_n = other < warps ? columns(other) : 0.f;
+    const float lane_inv_n = other < warps ? 1.f / lane_n : 0.f;
     int stage = 0, buf = 0;
     for (int64_t t = first; t < rows; t += step) {
         fetch(t + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
@@ -255,14 +233,13 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
         f2 sum2 = both(0.f);
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
-            if (!on[c]) continue;
             ring_read<XT>(s + c * kChunkWords * kNormMaxThreads, f[c]);
             if (add) {
                 f2 a[4];
                 ring_read<uint16_t>(s + (c * kChunkWords + words<XT>()) * kNormMaxThreads, a);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f[c][i] = add2(f[c][i], a[i]);
-                store_round8(x_sum + at + c * gthreads * 8, f[c]);
+                store_round8(x_sum + at + c * gthreads * 8, f[c], on[c]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum2 = add2(sum2, f[c][i]);
@@ -270,10 +247,9 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
         const float sum = warp_sum(sum_of(sum2));
         const float mw = sum * inv_nw;
         f2 sq2 = both(0.f);
-        const f2 neg_mw = both(-mw);
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
-            if (!on[c]) continue;
+            const f2 neg_mw = both(on[c] ? -mw : 0.f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const f2 v = add2(f[c][i], neg_mw);
@@ -286,16 +262,12 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
             if (lane == 0) r[gw] = make_float2(sum, var);
             group_sync(1 + group, warps);
             buf ^= 1;
-            const float2 pair = lane < warps ? r[lane] : make_float2(0.f, 0.f);
-            float tot = pair.x;
-            for (int off = half_warps; off > 0; off >>= 1) tot += __shfl_xor_sync(0xFFFFFFFFu, tot, off);
-            mu = __shfl_sync(0xFFFFFFFFu, tot, 0) * inv_d;
+            const float2 pair = other < warps ? r[other] : make_float2(0.f, 0.f);
+            mu = half_sum(pair.x) * inv_d;
             const float dm = fmaf(pair.x, lane_inv_n, -mu);
-            var = lane < warps ? fmaf(lane_n * dm, dm, pair.y) : 0.f;
-            for (int off = half_warps; off > 0; off >>= 1) var += __shfl_xor_sync(0xFFFFFFFFu, var, off);
-            var = __shfl_sync(0xFFFFFFFFu, var, 0);
+            var = half_sum(other < warps ? fmaf(lane_n * dm, dm, pair.y) : 0.f);
         }
-        const float rs = 1.f / sqrtf(fmaf(var, inv_d, eps));
+        const float rs = rsqrtf(fmaf(var, inv_d, eps));  // within 2 ulp
         if (mean && tid == 0) {
             mean[t] = mu;
             rstd[t] = rs;
@@ -303,11 +275,10 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
         const f2 neg_mu = both(-mu), rs2 = both(rs);
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
-            if (!on[c]) continue;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 f[c][i] = fma2(mul2(add2(f[c][i], neg_mu), rs2), ga[c][i], be[c][i]);
-            store8(y + at + c * gthreads * 8, f[c]);
+            if (on[c]) store8(y + at + c * gthreads * 8, f[c]);
         }
     }
     cp_async_wait<0>();
@@ -349,11 +320,13 @@ norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restr
             const int64_t at = t * d + tid * 8;
 #pragma unroll
             for (int c = 0; c < CPT; ++c) {
-                if (!on[c]) continue;
                 uint4 *s = mine + stage * kStage + c * kChunkWords * kNormMaxThreads;
-                ring_copy(s, x + at + c * gthreads * 8);
-                ring_copy(s + kDy * kNormMaxThreads, dy + at + c * gthreads * 8);
-                if (dres) ring_copy(s + kRes * kNormMaxThreads, dres + at + c * gthreads * 8);
+                const int bytes = on[c] ? 16 : 0;
+                ring_copy(s, x + at + c * gthreads * 8, bytes);
+                ring_copy(s + kDy * kNormMaxThreads, dy + at + c * gthreads * 8, bytes);
+                // without dres: zeros (the address is not read)
+                ring_copy(s + kRes * kNormMaxThreads, (dres ? dres : dx) + at + c * gthreads * 8,
+                          dres ? bytes : 0);
             }
         }
         cp_async_commit();
@@ -395,7 +368,6 @@ norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restr
         f2 sa2 = both(0.f), sb2 = both(0.f);
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
-            if (!on[c]) continue;
             chunk(c, true, xh[c % kHeld], w[c % kHeld]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -409,27 +381,21 @@ norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restr
             if (lane == 0) r[gw] = make_float2(sa, sb);
             group_sync(1 + group, warps);
             buf ^= 1;
-            const float2 v = pair_sum(r, warps);
-            sa = v.x;
-            sb = v.y;
+            const float2 pair = (lane & 15) < warps ? r[lane & 15] : make_float2(0.f, 0.f);
+            sa = half_sum(pair.x);
+            sb = half_sum(pair.y);
         }
         // dx = dres + rs w - rs sa / d - rs sb / d xh
         const f2 a2 = both(-sa * inv_d * rs), b2 = both(-sb * inv_d * rs);
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
-            if (!on[c]) continue;
             f2 r[4];
-            if (dres) {
-                ring_read<GT>(s + (c * kChunkWords + kRes) * kNormMaxThreads, r);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) r[i] = both(0.f);
-            }
+            ring_read<GT>(s + (c * kChunkWords + kRes) * kNormMaxThreads, r);
             if (!kKeep) chunk(c, false, xh[0], w[0]);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 r[i] = add2(r[i], fma2(rs2, w[c % kHeld][i], fma2(b2, xh[c % kHeld][i], a2)));
-            store8(dx + at + c * gthreads * 8, r);
+            if (on[c]) store8(dx + at + c * gthreads * 8, r);
         }
     }
     cp_async_wait<0>();
