@@ -122,33 +122,54 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
     float z = 0.f;
     int tok = 0;
     // Whole warps step together: a group past T, or at a masked token, idles.
-    // The next row is loaded before this one is worked on (for up to 8 logits a
-    // lane; beyond that the row itself is enough in flight, and registers are
-    // short): without it T = 131072, N = 250 took 47 us for this kernel.
+    // A row's logits and chosen experts are loaded one step ahead and its mask
+    // two, so that no load of a step waits for another one (for up to 8 logits
+    // a lane; a longer row is enough in flight by itself, and registers are
+    // short): loading them in the step took 35 instead of __US__ us at T = 131072,
+    // N = 250.
     constexpr bool kAhead = VPT <= 8;
+    constexpr int kIdx = (kMaxK + LANES - 1) / LANES;
     const int64_t step = (int64_t)gridDim.x * kGroups;
     auto counted = [&](int64_t t) { return t < T && !(mask && mask[t] == 0); };
     int64_t w0 = (int64_t)blockIdx.x * kGroups + warp * (32 / LANES);
     float ahead[VPT];
-    bool ahead_on = false;
+    int idx[kIdx];
+    bool ahead_on = false, later_on = false;
+    auto load_idx = [&](int64_t t, bool on) {
+#pragma unroll
+        for (int j = 0; j < kIdx; ++j) {
+            const int k = sub + j * LANES;
+            idx[j] = on && k < K ? topk_idx[t * K + k] : -1;
+        }
+    };
     if (kAhead) {
-        ahead_on = counted(w0 + lane / LANES);
-        R::load(logits + (w0 + lane / LANES) * N, sub, N, ahead_on, ahead);
+        const int64_t t = w0 + lane / LANES;
+        ahead_on = counted(t);
+        later_on = counted(t + step);
+        R::load(logits + t * N, sub, N, ahead_on, ahead);
+        load_idx(t, ahead_on);
     }
     for (; w0 < T; w0 += step) {
         const int64_t t = w0 + lane / LANES;
         const bool in = t < T;
         bool on;
         float v[VPT];
-        if (kAhead) {
-            on = ahead_on;
+        int mine[kIdx];
+        if (!kAhead) {
+            ahead_on = counted(t);
+            R::load(logits + t * N, sub, N, ahead_on, ahead);
+            load_idx(t, ahead_on);
+        }
+        on = ahead_on;
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) v[i] = ahead[i];
-            ahead_on = counted(t + step);
+        for (int i = 0; i < VPT; ++i) v[i] = ahead[i];
+#pragma unroll
+        for (int j = 0; j < kIdx; ++j) mine[j] = idx[j];
+        if (kAhead) {
+            ahead_on = later_on;
+            later_on = counted(t + 2 * step);
             R::load(logits + (t + step) * N, sub, N, ahead_on, ahead);
-        } else {
-            on = counted(t);
-            R::load(logits + t * N, sub, N, on, v);
+            load_idx(t + step, ahead_on);
         }
         float m = v[0];
 #pragma unroll
@@ -171,12 +192,9 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
         const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
         for (int i = 0; i < VPT / 2; ++i) acc2[i] = __ffma2_rn(v2[i], inv2, acc2[i]);
-        if (on) {
-            for (int k = sub; k < K; k += LANES) {
-                const int e = topk_idx[t * K + k];
-                if (e >= 0 && e < N) atomicAdd(cnt + e, 1);
-            }
-        }
+#pragma unroll
+        for (int j = 0; j < kIdx; ++j)
+            if (mine[j] >= 0 && mine[j] < N) atomicAdd(cnt + mine[j], 1);
         if (in && sub == 0) {
             const float l = m + __logf(sum);
             lse[t] = on ? l : 0.f;
@@ -302,6 +320,7 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
     pdl_enter();
     using R = Row<LANES, VPT, VEC, HALF>;
     constexpr int kGroups = kBwdThreads / LANES;
+    constexpr int kIdx = (kMaxK + LANES - 1) / LANES;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = threadIdx.x % LANES;
     const int tc = token_count[0];
     const float inv = tc > 0 ? 1.f / (float)tc : 0.f;
@@ -319,6 +338,16 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
         bool on = in && !(mask && mask[t] == 0);
         float v[VPT];
         R::load(logits + t * N, sub, N, on, v);
+        // lane `sub` holds the token's routes sub, sub + LANES, ...
+        int idx[kIdx];
+        float gate[kIdx];
+#pragma unroll
+        for (int j = 0; j < kIdx; ++j) {
+            const int k = sub + j * LANES;
+            const bool is = dlogit && in && k < K;
+            idx[j] = is ? topk_idx[t * K + k] : -1;
+            gate[j] = is ? dlogit[t * K + k] : 0.f;
+        }
         const float l = on ? lse[t] : 0.f;
         on = on && l != -INFINITY;  // every logit -inf: no probability, no gradient
         const float2 mul = make_float2(kLog2e, kLog2e), off = make_float2(-l, -l);
@@ -338,14 +367,17 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
             const float2 g = __fmul2_rn(v2[i], __ffma2_rn(cb2, f2[i], c2));
             v2[i] = on ? g : make_float2(0.f, 0.f);
         }
-        if (dlogit && in)
-            for (int k = 0; k < K; ++k) {
-                const int at = topk_idx[t * K + k];
-                const float g = dlogit[t * K + k];
+        if (dlogit) {
 #pragma unroll
-                for (int i = 0; i < VPT; ++i)
-                    if (at == R::first(sub) + R::step(i)) v[i] += g;
-            }
+            for (int j = 0; j < kIdx; ++j)
+                for (int k = 0; k < min(LANES, K - j * LANES); ++k) {
+                    const int at = __shfl_sync(0xFFFFFFFFu, idx[j], k, LANES);
+                    const float g = __shfl_sync(0xFFFFFFFFu, gate[j], k, LANES);
+#pragma unroll
+                    for (int i = 0; i < VPT; ++i)
+                        if (at == R::first(sub) + R::step(i)) v[i] += g;
+                }
+        }
         if (in) R::store(dlogits + t * N, sub, N, v);
     }
 }

@@ -16,8 +16,10 @@
 //
 // Launches: router_dense_prep writes the pieces (dl's transposed, so that both
 // products read them in a layout of the tensor cores) and partial sums of
-// dbias; router_dense_dx and router_dense_dw are the products; the last adds
-// dw's and dbias' partial sums in a fixed order.
+// dbias; router_dense_dw and router_dense_dx are the products.  The partial sums
+// of dw and dbias are added, in a fixed order, by router_dense_dx's epilogue
+// warps while its first tile is loaded and multiplied (a launch of its own took
+// 5 us), or by router_dense_sum when dx is not wanted.
 #include <algorithm>
 
 #include "../../include/moe_block.h"
@@ -222,6 +224,49 @@ inline bool make_map_f32(CUtensorMap *m, const void *base, uint64_t inner, uint6
 constexpr int kGemmThreads = 64 + 256;  // producer warp, MMA warp, 8 epilogue warps
 constexpr int kEpiWarps = 8;
 
+// -------------------------------------------------------------- last sums --
+
+struct Sums {
+    int64_t n4;       // N * d / 4; 0: dw is not wanted
+    int splits, N, groups;
+    const float4 *part;
+    const float *db_part;
+    float4 *dw;
+    float *dbias;     // NULL: not wanted
+};
+
+// The share of `unit` (of `units`, each of 256 threads) in dw = the sum of the
+// splits, four columns a thread, and dbias = the sum of the prep CTAs, a warp
+// per expert.
+__device__ __forceinline__ void add_partials(const Sums &q, int unit, int units, int thread) {
+    for (int64_t i = (int64_t)unit * 256 + thread; i < q.n4; i += (int64_t)units * 256) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int s = 0; s < q.splits; ++s) {
+            const float4 p = q.part[s * q.n4 + i];
+            v.x += p.x;
+            v.y += p.y;
+            v.z += p.z;
+            v.w += p.w;
+        }
+        q.dw[i] = v;
+    }
+    if (!q.dbias) return;
+    for (int e = unit * 8 + (thread >> 5); e < q.N; e += units * 8) {
+        float v = 0.f;
+#pragma unroll 4
+        for (int g = thread & 31; g < q.groups; g += 32) v += q.db_part[(int64_t)g * q.N + e];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+        if ((thread & 31) == 0) q.dbias[e] = v;
+    }
+}
+
+__global__ void __launch_bounds__(256) router_dense_sum(const Sums q) {
+    pdl_enter();
+    add_partials(q, blockIdx.x, gridDim.x, threadIdx.x);
+}
+
 // ---------------------------------------------------------------------- dx --
 //
 // Persistent CTAs, tiles of 128 tokens x 128 columns, columns fastest.  A
@@ -259,7 +304,7 @@ constexpr size_t kDxSmem =
 __global__ void __launch_bounds__(kGemmThreads, 1)
 router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant__ CUtensorMap tm_w,
                 const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_out,
-                int T, int N, int d, int has_in, int *status) {
+                int T, int N, int d, int has_in, const Sums sums, int *status) {
     pdl_enter();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -384,6 +429,8 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
         };
         if (has_in && lane == 0)
             for (int i = 0; i < kDxAhead; ++i) load_next();
+        __syncwarp();
+        add_partials(sums, blockIdx.x, gridDim.x, threadIdx.x - 64);
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
@@ -463,26 +510,29 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
 
 // ---------------------------------------------------------------------- dW --
 //
-// The transposed product dW^T = x^T dl: 128 columns of x as the MMA's rows
-// (MN-major boxes of 64 columns x 64 tokens), NT experts as its columns (dl's
-// pieces along the tokens), the tokens as K in blocks of 64.  x is read once
-// per NT experts.  There are few output tiles, so the tokens are split over
-// CTAs and the partial sums added by the last kernel.
+// The transposed product dW^T = x^T dl: 256 columns of x as the rows of two
+// MMAs (MN-major boxes of 64 columns x 64 tokens), the three pieces of NT
+// experts side by side as their 3 NT columns, the tokens as K in blocks of 64.
+// What limits a CTA is its shared memory, which the copies fill and every MMA
+// reads: three MMAs of NT columns, one per piece, would read x's tile three
+// times (61 us at T = 32768, d = 4096, N = 32 against __US__).  The epilogue adds
+// the three accumulators.  There are few output tiles, so the tokens are split
+// over CTAs and the partial sums added by the last kernel.
 //
 // The tensor core's accumulator keeps fp32 but cuts where an fp32 addition
 // rounds, so a long sum drifts; after every kDwGroup k-blocks (256 tokens) the
-// epilogue adds the accumulator to fp32 registers while the next group runs in
-// the other half of tensor memory.
+// epilogue adds the accumulator to fp32 registers (for NT = 32 while the next
+// group runs in the other half of tensor memory; 64 experts fill it).
 constexpr int kDwGroup = 4;
-constexpr int kDwA = 2 * 64 * 128;  // 128 columns x 64 tokens: 16 KB
+constexpr int kDwCols = 256;
+constexpr int kDwBlk = 64 * 128;                 // 64 columns x 64 tokens: 8 KB
+constexpr int kDwA = kDwCols / 64 * kDwBlk;      // 32 KB
 
 template <int NT>
 struct Dw {
-    static constexpr int ctas_per_sm = NT == 32 ? 2 : 1;
-    static constexpr int stages = NT == 32 ? 3 : NT == 64 ? 5 : 3;
-    static constexpr int piece = NT * 128;
-    static constexpr int stage_bytes = kDwA + 3 * piece;
-    static constexpr int tmem_cols = 2 * NT;
+    static constexpr int stages = NT == 32 ? 4 : 3;
+    static constexpr int stage_bytes = kDwA + 3 * NT * 128;
+    static constexpr int bufs = NT == 32 ? 2 : 1;    // accumulators: 2 x 3 NT columns each
     struct alignas(8) Bars {
         uint64_t full[stages];
         uint64_t empty[stages];
@@ -495,7 +545,7 @@ struct Dw {
 };
 
 template <int NT>
-__global__ void __launch_bounds__(kGemmThreads, Dw<NT>::ctas_per_sm)
+__global__ void __launch_bounds__(kGemmThreads, 1)
 router_dense_dw(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_dl,
                 int T, int N, int d, float *__restrict__ part, int *status) {
     using C = Dw<NT>;
@@ -506,7 +556,7 @@ router_dense_dw(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
     typename C::Bars *bars = reinterpret_cast<typename C::Bars *>(smem + (size_t)C::stages * C::stage_bytes);
     volatile int *abort = &bars->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c0 = blockIdx.x * 128, e0 = blockIdx.y * NT;
+    const int c0 = blockIdx.x * kDwCols, e0 = blockIdx.y * NT;
     const int nc = (int)(((int64_t)T + 63) / 64);
     const int k0 = (int)((int64_t)nc * blockIdx.z / gridDim.z);
     const int nk = (int)((int64_t)nc * (blockIdx.z + 1) / gridDim.z) - k0;
@@ -523,7 +573,7 @@ router_dense_dw(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
         bars->abort = 0;
         fence_mbar_init();
     }
-    if (warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), C::tmem_cols);
+    if (warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -539,8 +589,9 @@ router_dense_dw(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 const uint32_t sa = smem_u32(smem + (size_t)stage * C::stage_bytes);
                 const int t = (k0 + kb) * 64;
                 mbar_arrive_expect_tx(full, C::stage_bytes);
-                tma_load_2d(sa, &tm_x, full, c0, t);
-                tma_load_2d(sa + kDwA / 2, &tm_x, full, c0 + 64, t);
+#pragma unroll
+                for (int b = 0; b < kDwCols / 64; ++b)
+                    tma_load_2d(sa + b * kDwBlk, &tm_x, full, c0 + b * 64, t);
                 tma_load_3d(sa + kDwA, &tm_dl, full, t, e0, 0);
                 ++issued;
                 if (++stage == C::stages) { stage = 0; phase ^= 1; }
@@ -553,14 +604,14 @@ router_dense_dw(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            constexpr uint32_t idesc = idesc_major(128, NT, 1, 0);
+            constexpr uint32_t idesc = idesc_major(128, 3 * NT, 1, 0);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
             for (int kb0 = 0; kb0 < nk && ok; kb0 += kDwGroup) {
                 if (!mbar_wait(smem_u32(&bars->tempty[acc]), acc_phase ^ 1, status, abort)) break;
                 tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * NT);
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * 6 * NT);
                 for (int kb = kb0; kb < min(nk, kb0 + kDwGroup); ++kb) {
                     if (!mbar_wait(smem_u32(&bars->full[stage]), phase, status, abort)) {
                         ok = false;
@@ -570,95 +621,66 @@ router_dense_dw(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                     const uint32_t sa = smem_u32(smem + (size_t)stage * C::stage_bytes);
                     const uint32_t sb = sa + kDwA;
 #pragma unroll
-                    for (int p = 2; p >= 0; --p)
+                    for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc_mma_bf16(d_tmem, mnmajor_desc(sa + kk * 2048, kDwA / 2),
-                                        sw128_kmajor_desc(sb + p * C::piece + kk * 32), idesc,
-                                        kb == kb0 && p == 2 && kk == 0 ? 0u : 1u);
+                        for (int m = 0; m < 2; ++m)
+                            tc_mma_bf16(d_tmem + m * 3 * NT,
+                                        mnmajor_desc(sa + m * (kDwA / 2) + kk * 2048, kDwBlk),
+                                        sw128_kmajor_desc(sb + kk * 32), idesc,
+                                        kb == kb0 && kk == 0 ? 0u : 1u);
                     tc_commit(smem_u32(&bars->empty[stage]));
                     if (++stage == C::stages) { stage = 0; phase ^= 1; }
                 }
                 if (!ok) break;
                 tc_commit(smem_u32(&bars->tfull[acc]));
-                if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                if (++acc == C::bufs) { acc = 0; acc_phase ^= 1; }
             }
         }
     } else {
-        // TMEM lane = column of x; this warp's half of the experts
+        // TMEM lane = column of x, in this warp's MMA of the two; all NT experts
         const int quad = warp & 3, half = (warp - 2) >> 2;
-        float sum[NT / 2];
+        float sum[NT];
 #pragma unroll
-        for (int j = 0; j < NT / 2; ++j) sum[j] = 0.f;
+        for (int j = 0; j < NT; ++j) sum[j] = 0.f;
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int kb0 = 0; kb0 < nk; kb0 += kDwGroup) {
             if (!mbar_wait(smem_u32(&bars->tfull[acc]), acc_phase, status, abort)) break;
             tc_fence_after();
-            const uint32_t at =
-                tmem_base + ((uint32_t)(quad * 32) << 16) + acc * NT + half * (NT / 2);
+            const uint32_t at = tmem_base + ((uint32_t)(quad * 32) << 16) + (acc * 2 + half) * 3 * NT;
 #pragma unroll
-            for (int j = 0; j < NT / 2; j += 16) {
-                uint32_t r[16];
-                tmem_ld16(at + j, r);
+            for (int j = 0; j < NT; j += 16) {
+                uint32_t r0[16], r1[16], r2[16];
+                tmem_ld16(at + j, r0);
+                tmem_ld16(at + NT + j, r1);
+                tmem_ld16(at + 2 * NT + j, r2);
                 tmem_ld_wait();
-                reg_fence(r);
+                reg_fence(r0);
+                reg_fence(r1);
+                reg_fence(r2);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sum[j + i] += __uint_as_float(r[i]);
+                for (int i = 0; i < 16; ++i)
+                    sum[j + i] += __uint_as_float(r2[i]) + __uint_as_float(r1[i]) + __uint_as_float(r0[i]);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc]));
-            if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+            if (++acc == C::bufs) { acc = 0; acc_phase ^= 1; }
         }
-        const int col = c0 + quad * 32 + lane;
+        const int col = c0 + half * 128 + quad * 32 + lane;
         if (col < d) {
-            float *o = part + ((int64_t)blockIdx.z * N + e0 + half * (NT / 2)) * d + col;
+            float *o = part + ((int64_t)blockIdx.z * N + e0) * d + col;
 #pragma unroll
-            for (int j = 0; j < NT / 2; ++j)
-                if (e0 + half * (NT / 2) + j < N) o[(int64_t)j * d] = sum[j];
+            for (int j = 0; j < NT; ++j)
+                if (e0 + j < N) o[(int64_t)j * d] = sum[j];
         }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, C::tmem_cols);
+        tmem_dealloc(tmem_base, 512);
     }
-}
-
-// ------------------------------------------------------------- last sums --
-
-constexpr int kSumThreads = 256;
-
-// dw = sum of the splits, four columns a thread; dbias = sum of the prep
-// CTAs, one warp per expert (a lane every 32nd partial sum).
-__global__ void __launch_bounds__(kSumThreads)
-router_dense_sum(int64_t n4, int splits, const float4 *__restrict__ part, float4 *__restrict__ dw,
-                 int N, int groups, const float *__restrict__ db_part, float *__restrict__ dbias,
-                 int dw_blocks) {
-    pdl_enter();
-    if ((int)blockIdx.x < dw_blocks) {
-        const int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x;
-        if (i >= n4) return;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s = 0; s < splits; ++s) {
-            const float4 p = part[s * n4 + i];
-            v.x += p.x;
-            v.y += p.y;
-            v.z += p.z;
-            v.w += p.w;
-        }
-        dw[i] = v;
-        return;
-    }
-    const int e = ((int)blockIdx.x - dw_blocks) * (kSumThreads / 32) + (threadIdx.x >> 5);
-    if (e >= N) return;
-    float v = 0.f;
-    for (int g = threadIdx.x & 31; g < groups; g += 32) v += db_part[(int64_t)g * N + e];
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
-    if ((threadIdx.x & 31) == 0) dbias[e] = v;
 }
 
 // ------------------------------------------------------------------- host --
@@ -678,10 +700,9 @@ Plan plan_of(const moe_shape *s) {
     p.dp = (s->d + 63) / 64 * 64;
     p.chunks = (s->N + kPrepExp - 1) / kPrepExp;
     p.groups = (int)std::max<int64_t>(1, std::min<int64_t>(p.Tp / kPrepTok, 4 * kSms / p.chunks));
-    p.nt = s->N <= 32 ? 32 : s->N <= 64 ? 64 : 128;
-    const int64_t tiles = (int64_t)((s->d + 127) / 128) * ((s->N + p.nt - 1) / p.nt);
-    const int64_t room = kSms * (p.nt == 32 ? 2 : 1);
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(p.Tp / 64, room / tiles));
+    p.nt = s->N <= 32 ? 32 : 64;
+    const int64_t tiles = (int64_t)((s->d + kDwCols - 1) / kDwCols) * ((s->N + p.nt - 1) / p.nt);
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(p.Tp / 64, kSms / tiles));
     p.dlp = 256;
     p.wp = p.dlp + align256((size_t)3 * s->N * p.Tp * 2);
     p.db = p.wp + align256((size_t)3 * s->N * p.dp * 2);
@@ -697,7 +718,7 @@ moe_status launch_dw(const CUtensorMap &mx, const CUtensorMap &mdl, const moe_sh
     if (!device_once(smem_attr, [] { return set_smem_limit(router_dense_dw<NT>, Dw<NT>::smem); }))
         return MOE_ERR_CUDA;
     launch_pdl(router_dense_dw<NT>,
-               dim3((s->d + 127) / 128, (s->N + NT - 1) / NT, (unsigned)splits), kGemmThreads,
+               dim3((s->d + kDwCols - 1) / kDwCols, (s->N + NT - 1) / NT, (unsigned)splits), kGemmThreads,
                Dw<NT>::smem, stream, mx, mdl, s->T, s->N, s->d, part, status);
     return launch_status();
 }
@@ -738,37 +759,38 @@ MOE_API moe_status moe_router_dense_backward(const moe_shape *s, const moe_bf16 
     if (T > 0) {
         launch_pdl(router_dense_prep, dim3(pl.groups, pl.chunks + (dx ? 1 : 0)), kPrepThreads, 0,
                    stream, T, pl.Tp, N, d, pl.dp, pl.chunks, dlogits, w_router, dlp, wp, db);
-        if (dx) {
-            static PerDeviceOnce smem_attr;
-            if (!device_once(smem_attr, [] { return set_smem_limit(router_dense_dx, kDxSmem); }))
-                return MOE_ERR_CUDA;
-            CUtensorMap mdl, mw, min_, mout;
-            if (!make_map_pieces_mn(&mdl, dlp, pl.Tp, N, 32) ||
-                !make_map_pieces_mn(&mw, wp, pl.dp, N, 32) ||
-                !make_map_f32(&min_, dx_in ? dx_in : dx, d, T) || !make_map_f32(&mout, dx, d, T))
-                return MOE_ERR_CUDA;
-            const int64_t tiles = ((int64_t)T + 127) / 128 * ((d + 127) / 128);
-            launch_pdl(router_dense_dx, (unsigned)std::min<int64_t>(tiles, num_sms()), kGemmThreads,
-                       kDxSmem, stream, mdl, mw, min_, mout, T, N, d, dx_in ? 1 : 0, status);
-        }
         if (dw_router) {
             CUtensorMap mx, mdl;
             if (!make_map(&mx, x, d, T, 64) || !make_map_pieces_k(&mdl, dlp, pl.Tp, N, pl.nt))
                 return MOE_ERR_CUDA;
-            r = pl.nt == 32   ? launch_dw<32>(mx, mdl, s, pl.splits, part, status, stream)
-                : pl.nt == 64 ? launch_dw<64>(mx, mdl, s, pl.splits, part, status, stream)
-                              : launch_dw<128>(mx, mdl, s, pl.splits, part, status, stream);
+            r = pl.nt == 32 ? launch_dw<32>(mx, mdl, s, pl.splits, part, status, stream)
+                            : launch_dw<64>(mx, mdl, s, pl.splits, part, status, stream);
             if (r != MOE_OK) return r;
         }
     }
-    if (dw_router || dbias) {
-        const int64_t n4 = (int64_t)N * d / 4;
-        const int dw_blocks = dw_router ? (int)((n4 + kSumThreads - 1) / kSumThreads) : 0;
-        const int db_blocks = dbias ? (N + kSumThreads / 32 - 1) / (kSumThreads / 32) : 0;
-        launch_pdl(router_dense_sum, dw_blocks + db_blocks, kSumThreads, 0, stream, n4,
-                   T > 0 ? pl.splits : 0, reinterpret_cast<const float4 *>(part),
-                   reinterpret_cast<float4 *>(dw_router), N, T > 0 ? pl.groups : 0,
-                   static_cast<const float *>(db), dbias, dw_blocks);
+    Sums sums;
+    sums.n4 = dw_router ? (int64_t)N * d / 4 : 0;
+    sums.splits = T > 0 ? pl.splits : 0;
+    sums.N = N;
+    sums.groups = T > 0 ? pl.groups : 0;
+    sums.part = reinterpret_cast<const float4 *>(part);
+    sums.db_part = db;
+    sums.dw = reinterpret_cast<float4 *>(dw_router);
+    sums.dbias = dbias;
+    if (dx && T > 0) {
+        static PerDeviceOnce smem_attr;
+        if (!device_once(smem_attr, [] { return set_smem_limit(router_dense_dx, kDxSmem); }))
+            return MOE_ERR_CUDA;
+        CUtensorMap mdl, mw, min_, mout;
+        if (!make_map_pieces_mn(&mdl, dlp, pl.Tp, N, 32) || !make_map_pieces_mn(&mw, wp, pl.dp, N, 32) ||
+            !make_map_f32(&min_, dx_in ? dx_in : dx, d, T) || !make_map_f32(&mout, dx, d, T))
+            return MOE_ERR_CUDA;
+        const int64_t tiles = ((int64_t)T + 127) / 128 * ((d + 127) / 128);
+        launch_pdl(router_dense_dx, (unsigned)std::min<int64_t>(tiles, num_sms()), kGemmThreads, kDxSmem,
+                   stream, mdl, mw, min_, mout, T, N, d, dx_in ? 1 : 0, sums, status);
+    } else if (dw_router || dbias) {
+        const int64_t want = std::max<int64_t>((sums.n4 + 255) / 256, dbias ? (N + 7) / 8 : 0);
+        launch_pdl(router_dense_sum, (unsigned)std::min<int64_t>(want, 4 * kSms), 256, 0, stream, sums);
     }
     return launch_status();
 }
