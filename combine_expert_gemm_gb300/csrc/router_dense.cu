@@ -510,29 +510,31 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
 
 // ---------------------------------------------------------------------- dW --
 //
-// The transposed product dW^T = x^T dl: 256 columns of x as the rows of two
-// MMAs (MN-major boxes of 64 columns x 64 tokens), the three pieces of NT
-// experts side by side as their 3 NT columns, the tokens as K in blocks of 64.
+// The transposed product dW^T = x^T dl: 128 or 256 columns of x as the rows of
+// one or two MMAs (MN-major boxes of 64 columns x 64 tokens), the three pieces
+// of NT experts side by side as their 3 NT columns, the tokens as K in blocks
+// of 64.
 // What limits a CTA is its shared memory, which the copies fill and every MMA
 // reads: three MMAs of NT columns, one per piece, would read x's tile three
-// times (61 us at T = 32768, d = 4096, N = 32 against __US__).  The epilogue adds
-// the three accumulators.  There are few output tiles, so the tokens are split
+// times (61 us against 43 at T = 32768, d = 4096, N = 32).  The epilogue adds the
+// three accumulators.  There are few output tiles, so the tokens are split
 // over CTAs and the partial sums added by the last kernel.
 //
 // The tensor core's accumulator keeps fp32 but cuts where an fp32 addition
 // rounds, so a long sum drifts; after every kDwGroup k-blocks (256 tokens) the
-// epilogue adds the accumulator to fp32 registers (for NT = 32 while the next
-// group runs in the other half of tensor memory; 64 experts fill it).
+// epilogue adds the accumulator to fp32 registers while the next group runs in
+// the other half of tensor memory.
 constexpr int kDwGroup = 4;
-constexpr int kDwCols = 256;
 constexpr int kDwBlk = 64 * 128;                 // 64 columns x 64 tokens: 8 KB
-constexpr int kDwA = kDwCols / 64 * kDwBlk;      // 32 KB
 
 template <int NT>
 struct Dw {
-    static constexpr int stages = NT == 32 ? 4 : 3;
-    static constexpr int stage_bytes = kDwA + 3 * NT * 128;
-    static constexpr int bufs = NT == 32 ? 2 : 1;    // accumulators: 2 x 3 NT columns each
+    static constexpr int mmas = NT == 32 ? 2 : 1;    // of 128 columns of x
+    static constexpr int cols = 128 * mmas;
+    static constexpr int stages = NT == 32 ? 4 : 5;
+    static constexpr int a_bytes = cols / 64 * kDwBlk;
+    static constexpr int stage_bytes = a_bytes + 3 * NT * 128;
+    static constexpr int per_warp = NT / 2 * mmas;   // experts of an epilogue warp
     struct alignas(8) Bars {
         uint64_t full[stages];
         uint64_t empty[stages];
@@ -556,7 +558,7 @@ router_dense_dw(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
     typename C::Bars *bars = reinterpret_cast<typename C::Bars *>(smem + (size_t)C::stages * C::stage_bytes);
     volatile int *abort = &bars->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c0 = blockIdx.x * kDwCols, e0 = blockIdx.y * NT;
+    const int c0 = blockIdx.x * C::cols, e0 = blockIdx.y * NT;
     const int nc = (int)(((int64_t)T + 63) / 64);
     const int k0 = (int)((int64_t)nc * blockIdx.z / gridDim.z);
     const int nk = (int)((int64_t)nc * (blockIdx.z + 1) / gridDim.z) - k0;
@@ -590,9 +592,9 @@ router_dense_dw(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 const int t = (k0 + kb) * 64;
                 mbar_arrive_expect_tx(full, C::stage_bytes);
 #pragma unroll
-                for (int b = 0; b < kDwCols / 64; ++b)
+                for (int b = 0; b < C::cols / 64; ++b)
                     tma_load_2d(sa + b * kDwBlk, &tm_x, full, c0 + b * 64, t);
-                tma_load_3d(sa + kDwA, &tm_dl, full, t, e0, 0);
+                tma_load_3d(sa + C::a_bytes, &tm_dl, full, t, e0, 0);
                 ++issued;
                 if (++stage == C::stages) { stage = 0; phase ^= 1; }
             }
@@ -611,7 +613,7 @@ router_dense_dw(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             for (int kb0 = 0; kb0 < nk && ok; kb0 += kDwGroup) {
                 if (!mbar_wait(smem_u32(&bars->tempty[acc]), acc_phase ^ 1, status, abort)) break;
                 tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * 6 * NT);
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * C::mmas * 3 * NT);
                 for (int kb = kb0; kb < min(nk, kb0 + kDwGroup); ++kb) {
                     if (!mbar_wait(smem_u32(&bars->full[stage]), phase, status, abort)) {
                         ok = false;
@@ -619,13 +621,13 @@ router_dense_dw(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                     }
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + (size_t)stage * C::stage_bytes);
-                    const uint32_t sb = sa + kDwA;
+                    const uint32_t sb = sa + C::a_bytes;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-                        for (int m = 0; m < 2; ++m)
+                        for (int m = 0; m < C::mmas; ++m)
                             tc_mma_bf16(d_tmem + m * 3 * NT,
-                                        mnmajor_desc(sa + m * (kDwA / 2) + kk * 2048, kDwBlk),
+                                        mnmajor_desc(sa + m * 2 * kDwBlk + kk * 2048, kDwBlk),
                                         sw128_kmajor_desc(sb + kk * 32), idesc,
                                         kb == kb0 && kk == 0 ? 0u : 1u);
                     tc_commit(smem_u32(&bars->empty[stage]));
@@ -633,23 +635,26 @@ router_dense_dw(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                 }
                 if (!ok) break;
                 tc_commit(smem_u32(&bars->tfull[acc]));
-                if (++acc == C::bufs) { acc = 0; acc_phase ^= 1; }
+                if (++acc == 2) { acc = 0; acc_phase ^= 1; }
             }
         }
     } else {
-        // TMEM lane = column of x, in this warp's MMA of the two; all NT experts
+        // TMEM lane = column of x; four of the warps take the second MMA's
+        // columns, or the second half of the experts
         const int quad = warp & 3, half = (warp - 2) >> 2;
-        float sum[NT];
+        const int m = C::mmas == 2 ? half : 0, je = C::mmas == 2 ? 0 : half * C::per_warp;
+        float sum[C::per_warp];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) sum[j] = 0.f;
+        for (int j = 0; j < C::per_warp; ++j) sum[j] = 0.f;
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int kb0 = 0; kb0 < nk; kb0 += kDwGroup) {
             if (!mbar_wait(smem_u32(&bars->tfull[acc]), acc_phase, status, abort)) break;
             tc_fence_after();
-            const uint32_t at = tmem_base + ((uint32_t)(quad * 32) << 16) + (acc * 2 + half) * 3 * NT;
+            const uint32_t at = tmem_base + ((uint32_t)(quad * 32) << 16) +
+                                (acc * C::mmas + m) * 3 * NT + je;
 #pragma unroll
-            for (int j = 0; j < NT; j += 16) {
+            for (int j = 0; j < C::per_warp; j += 16) {
                 uint32_t r0[16], r1[16], r2[16];
                 tmem_ld16(at + j, r0);
                 tmem_ld16(at + NT + j, r1);
@@ -665,14 +670,14 @@ router_dense_dw(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc]));
-            if (++acc == C::bufs) { acc = 0; acc_phase ^= 1; }
+            if (++acc == 2) { acc = 0; acc_phase ^= 1; }
         }
-        const int col = c0 + half * 128 + quad * 32 + lane;
+        const int col = c0 + m * 128 + quad * 32 + lane;
         if (col < d) {
-            float *o = part + ((int64_t)blockIdx.z * N + e0) * d + col;
+            float *o = part + ((int64_t)blockIdx.z * N + e0 + je) * d + col;
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                if (e0 + j < N) o[(int64_t)j * d] = sum[j];
+            for (int j = 0; j < C::per_warp; ++j)
+                if (e0 + je + j < N) o[(int64_t)j * d] = sum[j];
         }
     }
     tc_fence_before();
@@ -701,7 +706,8 @@ Plan plan_of(const moe_shape *s) {
     p.chunks = (s->N + kPrepExp - 1) / kPrepExp;
     p.groups = (int)std::max<int64_t>(1, std::min<int64_t>(p.Tp / kPrepTok, 4 * kSms / p.chunks));
     p.nt = s->N <= 32 ? 32 : 64;
-    const int64_t tiles = (int64_t)((s->d + kDwCols - 1) / kDwCols) * ((s->N + p.nt - 1) / p.nt);
+    const int cols = p.nt == 32 ? Dw<32>::cols : Dw<64>::cols;
+    const int64_t tiles = (int64_t)((s->d + cols - 1) / cols) * ((s->N + p.nt - 1) / p.nt);
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(p.Tp / 64, kSms / tiles));
     p.dlp = 256;
     p.wp = p.dlp + align256((size_t)3 * s->N * p.Tp * 2);
@@ -718,7 +724,7 @@ moe_status launch_dw(const CUtensorMap &mx, const CUtensorMap &mdl, const moe_sh
     if (!device_once(smem_attr, [] { return set_smem_limit(router_dense_dw<NT>, Dw<NT>::smem); }))
         return MOE_ERR_CUDA;
     launch_pdl(router_dense_dw<NT>,
-               dim3((s->d + kDwCols - 1) / kDwCols, (s->N + NT - 1) / NT, (unsigned)splits), kGemmThreads,
+               dim3((s->d + Dw<NT>::cols - 1) / Dw<NT>::cols, (s->N + NT - 1) / NT, (unsigned)splits), kGemmThreads,
                Dw<NT>::smem, stream, mx, mdl, s->T, s->N, s->d, part, status);
     return launch_status();
 }
