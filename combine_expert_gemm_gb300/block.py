@@ -10,12 +10,15 @@ import ctypes
 
 import torch
 
-from . import (_P, _SP, _SZ, _bf16, _check, _f32, _i32, _lib, _stream, _u8)
+from . import (_P, _SP, _SZ, BackwardBuffers, LayerBuffers, _bf16, _check, _f32, _i32, _lib, _stream,
+               _u8, combine, dispatch, dispatch_backward, expert_ffn, expert_ffn_backward, route,
+               route_logits, route_workspace_bytes)
 
 __all__ = ["layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_bytes",
            "balance_loss", "balance_loss_backward", "balance_loss_workspace_bytes",
            "router_dense_backward", "router_dense_backward_workspace_bytes",
-           "checkpoint_save", "checkpoint_restore", "combine_backward_checkpoint"]
+           "checkpoint_save", "checkpoint_restore", "combine_backward_checkpoint", "BlockState",
+           "BlockScratch", "block_forward", "block_backward"]
 
 _I = ctypes.c_int32
 _SIG = {
@@ -30,7 +33,7 @@ _SIG = {
     "moe_router_dense_backward": ([_SP] + [_P] * 7 + [_P, _SZ, _P], ctypes.c_int),
     "moe_checkpoint_save": ([_SP] + [_P] * 10 + [_P], ctypes.c_int),
     "moe_checkpoint_restore": ([_SP] + [_P] * 8 + [_P], ctypes.c_int),
-    "moe_combine_backward_checkpoint": ([_SP] + [_P] * 7 + [_P], ctypes.c_int),
+    "moe_combine_backward_checkpoint": ([_SP] + [_P] * 8 + [_P], ctypes.c_int),
 }
 for _name, (_args, _res) in _SIG.items():
     _f = getattr(_lib, _name)
@@ -204,8 +207,9 @@ def checkpoint_restore(shape, expert_offset, g_q, g_scale, u_q, u_scale, g_save,
 
 
 def combine_backward_checkpoint(shape, dy, y_q, y_scale, route_row, topk_gate, dy_disp, dgate,
-                                stream=None):
-    """combine_backward with y_disp read from its checkpoint (include/moe_block.h)."""
+                                dlogit=None, stream=None):
+    """combine_backward with y_disp read from its checkpoint, and the chosen logits'
+    gradient into dlogit [T, K] if given (include/moe_block.h)."""
     T, d, K, R = shape.T, shape.d, shape.K, shape.R
     dev = torch.cuda.current_device()
     _check(_lib.moe_combine_backward_checkpoint(
@@ -213,4 +217,113 @@ def combine_backward_checkpoint(shape, dy, y_q, y_scale, route_row, topk_gate, d
         _arg(y_scale, _u8, "y_scale", R * d // 32, dev),
         _arg(route_row, _i32, "route_row", T * K, dev),
         _arg(topk_gate, _f32, "topk_gate", T * K, dev), _arg(dy_disp, _bf16, "dy_disp", R * d, dev),
-        _arg(dgate, _f32, "dgate", T * K, dev), _stream(stream)), "moe_combine_backward_checkpoint")
+        _arg(dgate, _f32, "dgate", T * K, dev), _arg(dlogit, _f32, "dlogit", T * K, dev),
+        _stream(stream)), "moe_combine_backward_checkpoint")
+
+
+# ------------------------------------------------------------------- block --
+
+class BlockState:
+    """What one pre-norm block keeps from its forward to its backward: the residual
+    stream, the norm's output and statistics, the routes, the router's logits and
+    log sums, and the experts' buffers in 8 bits (33/32 bytes an element of G, U and
+    y_disp).  The bf16 buffers of the experts live in a BlockScratch that every block
+    of a model shares."""
+
+    def __init__(self, shape, device="cuda"):
+        T, d, N, K, h, R = shape.T, shape.d, shape.N, shape.K, shape.h, shape.R
+        e = dict(device=device)
+        self.shape = shape
+        self.h = None                                  # the rows that were normalised
+        self.x_sum = torch.empty((T, d), dtype=_bf16, **e)
+        self.n = torch.empty((T, d), dtype=_bf16, **e)
+        self.mean, self.rstd = torch.empty(T, **e), torch.empty(T, **e)
+        self.topk_idx = torch.empty((T, K), dtype=_i32, **e)
+        self.topk_gate = torch.empty((T, K), **e)
+        self.route_row = torch.empty((T, K), dtype=_i32, **e)
+        self.expert_demand = torch.empty(N, dtype=_i32, **e)
+        self.expert_count = torch.empty(N, dtype=_i32, **e)
+        self.expert_offset = torch.empty(N + 1, dtype=_i32, **e)
+        # the logits stay in moe_route's workspace
+        self.route_ws = torch.zeros(max(route_workspace_bytes(shape), 256), dtype=_u8, **e)
+        self.routed_count = torch.empty(N, dtype=_i32, **e)
+        self.token_count = torch.empty(1, dtype=_i32, **e)
+        self.expert_prob = torch.empty(N, **e)
+        self.lse = torch.empty(T, **e)
+        self.losses = torch.empty(2, **e)              # balance loss, z loss
+        self.token_mask = None
+        self.g_q, self.u_q = (torch.empty((R, h), dtype=_i8, **e) for _ in range(2))
+        self.g_scale, self.u_scale = (torch.empty((R, h // 32), dtype=_u8, **e) for _ in range(2))
+        self.y_q = torch.empty((R, d), dtype=_i8, **e)
+        self.y_scale = torch.empty((R, d // 32), dtype=_u8, **e)
+
+
+class BlockScratch:
+    """The buffers and workspaces that every block of one shape shares: the layer's
+    forward and backward buffers (LayerBuffers, BackwardBuffers) and those of the norm,
+    the balance loss and the dense router gradient.  `bwd` and the gradients below hold
+    the last block_backward's results until the next one."""
+
+    def __init__(self, shape, device="cuda"):
+        T, d, N, K = shape.T, shape.d, shape.N, shape.K
+        w = lambda n: torch.zeros(n, dtype=_u8, device=device)
+        self.fwd = LayerBuffers(shape, device, save_for_backward=True)
+        self.bwd = BackwardBuffers(shape, device)
+        self.dgamma, self.dbeta = (torch.empty(d, device=device) for _ in range(2))
+        self.dlogits = torch.empty((T, N), device=device)
+        self.norm_ws = w(layer_norm_backward_workspace_bytes(T, d))
+        self.balance_ws = w(balance_loss_workspace_bytes(shape))
+        self.dense_ws = w(router_dense_backward_workspace_bytes(shape))
+
+
+def block_forward(st, sc, x, add, gamma, beta, w_router, bias, w_gate, w_up, w_down, eps=1e-5,
+                  token_mask=None, stream=None):
+    """One pre-norm block: h = x + add (add: the previous block's output, or None),
+    n = layer norm of h, and the routed-expert layer of n; its output is returned
+    (sc.fwd.y, which the next block takes as add).  st keeps what block_backward needs,
+    the experts' buffers in 8 bits, and st.losses the balance and z loss over the tokens
+    that token_mask [T] uint8 (or None: all) counts."""
+    s, f = st.shape, sc.fwd
+    st.h = x if add is None else st.x_sum
+    st.token_mask = token_mask
+    layer_norm(x, add, gamma, beta, eps, None if add is None else st.x_sum, st.n, st.mean, st.rstd,
+               stream)
+    route(s, st.n, w_router, bias, st.topk_idx, st.topk_gate, st.route_row, st.expert_count,
+          st.expert_offset, st.expert_demand, st.route_ws, stream)
+    balance_loss(s, route_logits(s, st.route_ws), st.topk_idx, token_mask, st.routed_count,
+                 st.token_count, st.expert_prob, st.lse, st.losses, sc.balance_ws, stream)
+    dispatch(s, st.n, st.route_row, f.x_disp, stream)
+    expert_ffn(s, f.x_disp, st.expert_count, st.expert_offset, w_gate, w_up, w_down, f.h_act,
+               f.g_save, f.u_save, f.y_disp, f.ffn_ws, stream)
+    checkpoint_save(s, st.expert_offset, f.g_save, f.u_save, f.y_disp, st.g_q, st.g_scale, st.u_q,
+                    st.u_scale, st.y_q, st.y_scale, stream)
+    combine(s, f.y_disp, st.route_row, st.topk_gate, f.y, stream)
+    return f.y
+
+
+def block_backward(st, sc, dh, dx, dlosses, gamma, beta, w_router, bias, w_gate, w_up, w_down,
+                   stream=None):
+    """The backward of block_forward.  dh [T, d] bf16 is the gradient of h + y (the next
+    block's dx): it reaches h directly and through the layer.  dx [T, d] bf16 (dh itself
+    is allowed) gets the gradient of h; dlosses [2] fp32 on the device are the gradients
+    of st.losses.  sc.bwd.dw_gate, dw_up, dw_down, dw_router (and dbias), sc.dgamma and
+    sc.dbeta hold the weights' gradients until the next call."""
+    s, f, b = st.shape, sc.fwd, sc.bwd
+    combine_backward_checkpoint(s, dh, st.y_q, st.y_scale, st.route_row, st.topk_gate, b.dy_disp,
+                                b.dgate, b.dlogit, stream)
+    dispatch(s, st.n, st.route_row, f.x_disp, stream)
+    checkpoint_restore(s, st.expert_offset, st.g_q, st.g_scale, st.u_q, st.u_scale, f.g_save,
+                       f.u_save, f.h_act, stream)
+    expert_ffn_backward(s, f.x_disp, st.expert_count, st.expert_offset, w_gate, w_up, w_down,
+                        f.g_save, f.u_save, f.h_act, b.dy_disp, b.dx_disp, b.dw_gate, b.dw_up,
+                        b.dw_down, b.ws, stream)
+    dispatch_backward(s, b.dx_disp, st.route_row, b.dx, stream)
+    balance_loss_backward(s, route_logits(s, st.route_ws), st.topk_idx, st.token_mask,
+                          st.routed_count, st.token_count, st.lse, dlosses, b.dlogit, sc.dlogits,
+                          stream)
+    router_dense_backward(s, st.n, w_router, sc.dlogits, b.dx, b.dx, b.dw_router,
+                          None if bias is None else b.dbias, sc.dense_ws, stream)
+    layer_norm_backward(st.h, b.dx, gamma, st.mean, st.rstd, dh, dx,
+                        None if gamma is None else sc.dgamma, None if beta is None else sc.dbeta,
+                        sc.norm_ws, stream)
+    return dx

@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(kTokWarps * 32)
 combine_bwd_checkpoint_rows(int T, int nchunk, int K, const uint4 *__restrict__ dy,
                             const uint2 *__restrict__ y_q, const uint8_t *__restrict__ y_scale,
                             const int32_t *__restrict__ route_row, const float *__restrict__ gate,
-                            uint4 *__restrict__ dy_disp, float *__restrict__ dgate) {
+                            uint4 *__restrict__ dy_disp, float *__restrict__ dgate,
+                            float *__restrict__ dlogit) {
     pdl_enter();
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * kTokWarps + (threadIdx.x >> 5);
@@ -233,13 +234,22 @@ combine_bwd_checkpoint_rows(int T, int nchunk, int K, const uint4 *__restrict__ 
             }
         }
     }
+    // lane k < K ends up with route k's dgate; dot is the chain over k ascending
+    // that the dispatch's router backward takes
+    float mine = 0.f, dot = 0.f;
 #pragma unroll
     for (int k = 0; k < MAXK; ++k) {
         if (k >= K) break;
         float v = part[k];
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
-        if (lane == 0) dgate[t * K + k] = rows[k] >= 0 ? v : 0.0f;
+        if (rows[k] < 0) v = 0.f;
+        if (lane == k) mine = v;
+        dot = fmaf(gs[k], v, dot);
+    }
+    if (lane < K) {
+        dgate[t * K + lane] = mine;
+        if (dlogit) dlogit[t * K + lane] = my_g * (mine - dot);
     }
 }
 
@@ -313,7 +323,8 @@ MOE_API moe_status moe_combine_backward_checkpoint(const moe_shape *s, const moe
                                                    const int8_t *y_q, const uint8_t *y_scale,
                                                    const int32_t *route_row,
                                                    const float *topk_gate, moe_bf16 *dy_disp,
-                                                   float *dgate, cudaStream_t stream) {
+                                                   float *dgate, float *dlogit,
+                                                   cudaStream_t stream) {
     moe_status r = check_shape(s);
     if (r != MOE_OK) return r;
     if (s->d % kCkBlock != 0 || s->h % kCkBlock != 0) return MOE_ERR_UNSUPPORTED;
@@ -321,13 +332,13 @@ MOE_API moe_status moe_combine_backward_checkpoint(const moe_shape *s, const moe
     if (!dy || !route_row || !topk_gate || !dgate ||
         (s->cap > 0 && (!y_q || !y_scale || !dy_disp)))
         return MOE_ERR_INVALID_ARG;
-    const void *ptrs[] = {dy, y_q, y_scale, route_row, topk_gate, dy_disp, dgate};
+    const void *ptrs[] = {dy, y_q, y_scale, route_row, topk_gate, dy_disp, dgate, dlogit};
     for (const void *p : ptrs)
         if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
     auto *kern = s->K <= 8 ? combine_bwd_checkpoint_rows<8> : combine_bwd_checkpoint_rows<16>;
     const int grid = (int)(((int64_t)s->T + kTokWarps - 1) / kTokWarps);
     launch_pdl(kern, grid, kTokWarps * 32, 0, stream, s->T, s->d / 8, s->K,
                reinterpret_cast<const uint4 *>(dy), reinterpret_cast<const uint2 *>(y_q), y_scale,
-               route_row, topk_gate, reinterpret_cast<uint4 *>(dy_disp), dgate);
+               route_row, topk_gate, reinterpret_cast<uint4 *>(dy_disp), dgate, dlogit);
     return launch_status();
 }

@@ -127,9 +127,9 @@ moe_status moe_balance_loss(const moe_shape *s, const float *logits, const int32
  *                   + sum over k with topk_idx[t, k] = j of dlogit[t, k]
  * with f[e] = expert_count[e] / (Tc * K); the first line is 0 for a token that
  * does not count.  The second line, left out when dlogit is NULL, adds the
- * gradient of the gates (moe_dispatch_router_backward's or
- * moe_router_backward's dlogit), so that dlogits is the router's whole
- * gradient; it applies to every token.
+ * gradient of the gates (moe_combine_backward_checkpoint's dlogit, or
+ * moe_router_backward's), so that dlogits is the router's whole gradient; it
+ * applies to every token.
  *   logits, topk_idx, token_mask as in the forward; expert_count, token_count
  *   and lse as it wrote them (or, for a loss over several batches, the sums of
  *   their counts); dlosses [2] fp32 on the device: the gradients of losses[0] and
@@ -215,11 +215,16 @@ moe_status moe_checkpoint_restore(const moe_shape *s, const int32_t *expert_offs
  * its checkpoint:
  *   dy_disp[route_row[t, k]] = bf16(topk_gate[t, k] * dy[t])   (fp32 product)
  *   dgate[t, k] = <dy[t], value(y_q, y_scale)[route_row[t, k]]>  (fp32; 0 if dropped)
+ * and, when dlogit is not NULL, the chosen logits' gradient through the gates'
+ * softmax, as moe_router_backward defines it:
+ *   dlogit[t, k] = topk_gate[t, k] * (dgate[t, k] - sum_k' topk_gate[t, k'] * dgate[t, k'])
+ * (moe_balance_loss_backward takes it from here).  dgate, dlogit out [T, K] fp32.
  */
 moe_status moe_combine_backward_checkpoint(const moe_shape *s, const moe_bf16 *dy,
                                            const int8_t *y_q, const uint8_t *y_scale,
                                            const int32_t *route_row, const float *topk_gate,
-                                           moe_bf16 *dy_disp, float *dgate, cudaStream_t stream);
+                                           moe_bf16 *dy_disp, float *dgate, float *dlogit,
+                                           cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -133,7 +133,7 @@ def test_checkpoint_refusals(moe):
     for kw in (dict(d=136), dict(h=264)):
         assert lib.moe_checkpoint_save(_shape(moe, **kw), *f, None) == 5
         assert lib.moe_checkpoint_restore(_shape(moe, **kw), *f[:8], None) == 5
-        assert lib.moe_combine_backward_checkpoint(_shape(moe, **kw), *f[:7], None) == 5
+        assert lib.moe_combine_backward_checkpoint(_shape(moe, **kw), *f[:8], None) == 5
     assert lib.moe_checkpoint_save(_shape(moe, cap=0), *([None] * 10), None) == 0
     assert lib.moe_checkpoint_save(s, A, *([None] * 9), None) == 0      # every source left out
     for i in range(8):
@@ -142,13 +142,13 @@ def test_checkpoint_refusals(moe):
         assert lib.moe_checkpoint_restore(s, *bad, None) == 1, i
         bad[i] = MIS
         assert lib.moe_checkpoint_restore(s, *bad, None) == 2, i
-    for i in range(7):
-        bad = [A] * 7
+    for i in range(8):                # dy .. dgate, and dlogit, which may be NULL
+        bad = [A] * 8
         bad[i] = None
-        assert lib.moe_combine_backward_checkpoint(s, *bad, None) == 1, i
+        assert i == 7 or lib.moe_combine_backward_checkpoint(s, *bad, None) == 1, i
         bad[i] = MIS
         assert lib.moe_combine_backward_checkpoint(s, *bad, None) == 2, i
-    assert lib.moe_combine_backward_checkpoint(_shape(moe, T=0), *([None] * 7), None) == 0
+    assert lib.moe_combine_backward_checkpoint(_shape(moe, T=0), *([None] * 8), None) == 0
 
 
 def test_binding_refuses_wrong_tensors(moe, monkeypatch):

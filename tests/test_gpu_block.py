@@ -484,8 +484,8 @@ def test_checkpoint_codes_values_and_backward(moe, T, d, N, K, h, cap):
     for o in out:
         assert (o[Acc:] == 7).all()
     dyd = torch.full((R, d), 7.0, dtype=BF, device=DEV)
-    dgate = torch.empty(T, K, device=DEV)
-    moe.combine_backward_checkpoint(s, dy.to(DEV), *q["y"], row.to(DEV), gate.to(DEV), dyd, dgate)
+    dgate, dlogit = torch.empty(T, K, device=DEV), torch.empty(T, K, device=DEV)
+    moe.combine_backward_checkpoint(s, dy.to(DEV), *q["y"], row.to(DEV), gate.to(DEV), dyd, dgate, dlogit)
     wdy = torch.full((R, d), 7.0, dtype=BF)
     wdg, mag = torch.zeros(T, K, dtype=D), torch.zeros(T, K, dtype=D)
     for k in range(K):
@@ -496,6 +496,14 @@ def test_checkpoint_codes_values_and_backward(moe, T, d, N, K, h, cap):
         mag[t, k] = (dy[t].double() * vals["y"][r]).abs().sum(1)
     assert torch.equal(dyd.cpu(), wdy)
     _within(dgate, wdg, (d + 8) * U * mag, "dgate")
+    # the gates' Jacobian takes the dgate that was written (K <= 16 fp32 terms)
+    dg, gg = dgate.cpu().double(), gate.double()
+    dot = (gg * dg).sum(1, keepdim=True)
+    size = gg * (dg.abs() + (gg * dg).abs().sum(1, keepdim=True))
+    _within(dlogit, gg * (dg - dot), 20 * U * size + 1e-30, "dlogit")
+    alone = torch.empty(T, K, device=DEV)
+    moe.combine_backward_checkpoint(s, dy.to(DEV), *q["y"], row.to(DEV), gate.to(DEV), dyd, alone)
+    assert torch.equal(alone, dgate)
 
 
 def test_checkpoint_every_bf16_value(moe):
