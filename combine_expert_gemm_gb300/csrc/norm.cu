@@ -10,14 +10,19 @@
 // row once.  Persistent CTAs of up to 512 threads, one per SM, are cut into
 // groups of whole warps; a group takes one row at a time and each of its
 // threads keeps the same columns (8 to 32 of them) from row to row.  The
-// column's gamma and beta, and in the backward its share of dgamma and dbeta,
+// forward's gamma and beta and the backward's share of dgamma and dbeta
 // therefore stay in registers, and the weight gradients cost no second pass
 // over x and dy (the two-pass version took 74 of 172 us at 8192 x 2048).
 //
-// Rows arrive through rings of cp.async copies, kStages - 1 rows ahead.  A
-// thread copies exactly the bytes that it will read itself, so a ring needs no
-// barrier and no wait but the thread's own cp.async.wait_group, and the SM
-// keeps 64 KB and more of loads in flight with few registers.
+// The forward's rows arrive through a ring of cp.async copies, kStages - 1 rows
+// ahead.  A thread copies exactly the bytes that it will read itself, so the
+// ring needs no barrier and no wait but the thread's own cp.async.wait_group.
+// The backward moves three tensors in, and there the copies' and the ring's own
+// instructions were what it waited for (353 a warp-row, 0.34 issued a cycle): it
+// loads the next row's x and dy straight into registers as soon as the current
+// row's are unpacked, and gamma, in shared memory, makes room for them.
+// 32768 x 4096: 246 -> 210 us, of which the reads take 174 at the rate a plain
+// read reaches.
 //
 // A row's sums cross the group's warps through shared memory with one barrier
 // per row (two alternating buffers); every warp then adds the warps' pairs
@@ -41,7 +46,7 @@ namespace {
 constexpr int kNormMaxD = 16384;
 constexpr int kNormMaxThreads = 512;
 constexpr int kNormCtas = 152;        // one per SM; the order of the weight sums follows it
-constexpr size_t kNormRing = 196608;  // most shared memory the rings take
+constexpr size_t kNormRing = 196608;  // most shared memory a kernel takes
 
 // Two fp32 values side by side: the packed instructions halve the issue slots
 // of the element-wise work.
@@ -284,8 +289,31 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
     cp_async_wait<0>();
 }
 
+// Eight elements as loaded: 16 bytes of bf16 or 32 of fp32.
+template <typename T>
+struct Raw {
+    uint4 w[words<T>()];
+    __device__ __forceinline__ void load(const T *p, bool on) {
+        const uint4 *g = reinterpret_cast<const uint4 *>(p);
+#pragma unroll
+        for (int i = 0; i < words<T>(); ++i) w[i] = on ? __ldcs(g + i) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void get(f2 (&f)[4]) const {
+        if (words<T>() == 1) {
+            unpack(w[0], f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 v = w[i % words<T>()];
+                f[2 * i] = make2(__uint_as_float(v.x), __uint_as_float(v.y));
+                f[2 * i + 1] = make2(__uint_as_float(v.z), __uint_as_float(v.w));
+            }
+        }
+    }
+};
+
 // part[cta][2][d]: this CTA's sums of dgamma and dbeta (part may be NULL).
-template <typename XT, typename YT, typename GT, int CPT, int STAGES>
+template <typename XT, typename YT, typename GT, int CPT>
 __global__ void __launch_bounds__(kNormMaxThreads, 1)
 norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restrict__ dy,
          const float *__restrict__ gamma, const float *__restrict__ mean,
@@ -293,67 +321,59 @@ norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restr
     pdl_enter();
     extern __shared__ uint4 ring[];
     __shared__ float2 red[2][32];
-    constexpr int kDy = words<XT>(), kRes = kDy + words<YT>(), kChunkWords = kRes + words<GT>();
-    constexpr int kStage = CPT * kChunkWords * kNormMaxThreads;
     const int gthreads = warps * 32, group = threadIdx.x / gthreads, tid = threadIdx.x % gthreads;
     const int groups = blockDim.x / gthreads, lane = threadIdx.x & 31, gw = tid >> 5;
     const int chunks = d / 8;
     // past 16 columns a thread the registers hold only the weight gradients:
-    // gamma is read again for each row and the row's second use of x and dy
-    // reads the ring again
+    // gamma, x and dy are read again for the row's second half
     constexpr bool kKeep = CPT <= 2;
     constexpr int kHeld = kKeep ? CPT : 1;
     bool on[CPT];
-    f2 ga[kHeld][4], dg[CPT][4], db[CPT][4];
+    f2 dg[CPT][4], db[CPT][4];
+    // gamma of this thread's columns waits in its own words of shared memory
+    uint4 *gamma_s = ring + threadIdx.x;
 #pragma unroll
     for (int c = 0; c < CPT; ++c) {
         on[c] = tid + c * gthreads < chunks;
-        if (kKeep) load_param(gamma, (tid + c * gthreads) * 8, d, 1.f, ga[c % kHeld]);
+        f2 g[4];
+        load_param(gamma, (tid + c * gthreads) * 8, d, 1.f, g);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            gamma_s[(2 * c + i) * kNormMaxThreads] =
+                make_uint4(__float_as_uint(g[2 * i].x), __float_as_uint(g[2 * i].y),
+                           __float_as_uint(g[2 * i + 1].x), __float_as_uint(g[2 * i + 1].y));
 #pragma unroll
         for (int i = 0; i < 4; ++i) dg[c][i] = db[c][i] = both(0.f);
     }
     const int64_t step = (int64_t)gridDim.x * groups;
     const int64_t first = (int64_t)blockIdx.x * groups + group;
-    uint4 *mine = ring + threadIdx.x;
-    auto fetch = [&](int64_t t, int stage) {
-        if (t < rows) {
-            const int64_t at = t * d + tid * 8;
-#pragma unroll
-            for (int c = 0; c < CPT; ++c) {
-                uint4 *s = mine + stage * kStage + c * kChunkWords * kNormMaxThreads;
-                const int bytes = on[c] ? 16 : 0;
-                ring_copy(s, x + at + c * gthreads * 8, bytes);
-                ring_copy(s + kDy * kNormMaxThreads, dy + at + c * gthreads * 8, bytes);
-                // without dres: zeros (the address is not read)
-                ring_copy(s + kRes * kNormMaxThreads, (dres ? dres : dx) + at + c * gthreads * 8,
-                          dres ? bytes : 0);
-            }
-        }
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) fetch(first + s * step, s);
     const float inv_d = 1.f / (float)d;
-    int stage = 0, buf = 0;
-    // the row's statistics, read one row ahead
-    float mu_n = first < rows ? mean[first] : 0.f, rs_n = first < rows ? rstd[first] : 0.f;
-    for (int64_t t = first; t < rows; t += step) {
-        fetch(t + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
-        const float mu = mu_n, rs = rs_n;
-        if (t + step < rows) {
-            mu_n = mean[t + step];
-            rs_n = rstd[t + step];
-        }
-        cp_async_wait<STAGES - 1>();
+    int buf = 0;
+    Raw<XT> nx[kHeld];
+    Raw<YT> ny[kHeld];
+    float mu_n = 0.f, rs_n = 0.f;
+    auto fetch = [&](int64_t t) {
         const int64_t at = t * d + tid * 8;
-        const uint4 *s = mine + stage * kStage;
-        if (++stage == STAGES) stage = 0;
+        mu_n = mean[t];
+        rs_n = rstd[t];
+#pragma unroll
+        for (int c = 0; c < (kKeep ? CPT : 0); ++c) {
+            nx[c % kHeld].load(x + at + c * gthreads * 8, on[c]);
+            ny[c % kHeld].load(dy + at + c * gthreads * 8, on[c]);
+        }
+    };
+    if (first < rows) fetch(first);
+    for (int64_t t = first; t < rows; t += step) {
+        const float mu = mu_n, rs = rs_n;
+        const int64_t at = t * d + tid * 8;
         const f2 neg_mu = both(-mu), rs2 = both(rs);
-        // xh and w = dy gamma of one chunk; first: dgamma and dbeta take their share
-        auto chunk = [&](int c, bool take, f2 (&xh)[4], f2 (&w)[4]) {
-            ring_read<XT>(s + c * kChunkWords * kNormMaxThreads, xh);
-            ring_read<YT>(s + (c * kChunkWords + kDy) * kNormMaxThreads, w);
-            if (!kKeep) load_param(gamma, (tid + c * gthreads) * 8, d, 1.f, ga[0]);
+        f2 xh[kHeld][4], w[kHeld][4];
+        // xh and w = dy gamma of one chunk; take: dgamma and dbeta get their share
+        auto chunk = [&](int c, bool take, const Raw<XT> &rx, const Raw<YT> &ry, f2 (&xh)[4], f2 (&w)[4]) {
+            rx.get(xh);
+            ry.get(w);
+            f2 ga[4];
+            ring_read<float>(gamma_s + 2 * c * kNormMaxThreads, ga);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 xh[i] = mul2(add2(xh[i], neg_mu), rs2);
@@ -361,19 +381,29 @@ norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restr
                     dg[c][i] = fma2(w[i], xh[i], dg[c][i]);
                     db[c][i] = add2(db[c][i], w[i]);
                 }
-                w[i] = mul2(w[i], ga[c % kHeld][i]);
+                w[i] = mul2(w[i], ga[i]);
             }
         };
-        f2 xh[kHeld][4], w[kHeld][4];
         f2 sa2 = both(0.f), sb2 = both(0.f);
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
-            chunk(c, true, xh[c % kHeld], w[c % kHeld]);
+            if (!kKeep) {
+                nx[0].load(x + at + c * gthreads * 8, on[c]);
+                ny[0].load(dy + at + c * gthreads * 8, on[c]);
+            }
+            chunk(c, true, nx[c % kHeld], ny[c % kHeld], xh[c % kHeld], w[c % kHeld]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 sa2 = add2(sa2, w[c % kHeld][i]);
                 sb2 = fma2(w[c % kHeld][i], xh[c % kHeld][i], sb2);
             }
+        }
+        if (t + step < rows) fetch(t + step);
+        Raw<GT> res[kHeld];
+        if (kKeep) {
+#pragma unroll
+            for (int c = 0; c < kHeld; ++c)
+                res[c].load((dres ? dres : dx) + at + c * gthreads * 8, on[c] && dres);
         }
         float sa = warp_sum(sum_of(sa2)), sb = warp_sum(sum_of(sb2));
         if (warps > 1) {
@@ -389,16 +419,22 @@ norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restr
         const f2 a2 = both(-sa * inv_d * rs), b2 = both(-sb * inv_d * rs);
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
+            if (!kKeep) {
+                Raw<XT> rx;
+                Raw<YT> ry;
+                rx.load(x + at + c * gthreads * 8, on[c]);
+                ry.load(dy + at + c * gthreads * 8, on[c]);
+                res[0].load((dres ? dres : dx) + at + c * gthreads * 8, on[c] && dres);
+                chunk(c, false, rx, ry, xh[0], w[0]);
+            }
             f2 r[4];
-            ring_read<GT>(s + (c * kChunkWords + kRes) * kNormMaxThreads, r);
-            if (!kKeep) chunk(c, false, xh[0], w[0]);
+            res[c % kHeld].get(r);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 r[i] = add2(r[i], fma2(rs2, w[c % kHeld][i], fma2(b2, xh[c % kHeld][i], a2)));
             if (on[c]) store8(dx + at + c * gthreads * 8, r);
         }
     }
-    cp_async_wait<0>();
     if (!part) return;
     // the CTA's groups, in order, through the ring's memory
     float *acc = reinterpret_cast<float *>(ring);  // [groups][2][d]
@@ -474,8 +510,7 @@ inline moe_status check_norm(int32_t rows, int32_t d) {
 
 inline bool dtype_ok(int32_t t) { return t == MOE_BF16 || t == MOE_FP32; }
 
-// As many ring stages as fit, 4 at most: three rows ahead where the row's
-// bytes allow it, none (one stage) past 8192 columns.
+// As many ring stages as fit, 4 at most.
 constexpr int ring_stages(int words_per_thread) {
     const int n = (int)(kNormRing / ((size_t)words_per_thread * 16 * kNormMaxThreads));
     return n > 4 ? 4 : n;
@@ -512,18 +547,16 @@ moe_status launch_norm_bwd(int32_t rows, int32_t d, const void *x, const void *d
                            const float *gamma, const float *mean, const float *rstd,
                            const void *dres, void *dx, float *dgamma, float *dbeta, void *ws,
                            cudaStream_t stream) {
-    constexpr int kWords = CPT * (words<XT>() + words<YT>() + words<GT>());
-    constexpr int kStages = ring_stages(kWords);
     const NormPlan p = norm_plan(rows, d);
     const int threads = p.groups * p.warps * 32;
     float *part = dgamma || dbeta ? reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256) : nullptr;
     if (rows > 0) {
-        auto *kern = norm_bwd<XT, YT, GT, CPT, kStages>;
+        auto *kern = norm_bwd<XT, YT, GT, CPT>;
         static PerDeviceOnce attr;
         if (!device_once(attr, [&] { return set_smem_limit(kern, kNormRing); })) return MOE_ERR_CUDA;
-        // the ring also holds the groups' weight sums at the end
-        const size_t smem = std::max((size_t)kStages * kWords * 16 * kNormMaxThreads,
-                                     (size_t)p.groups * 2 * d * sizeof(float));
+        // gamma, and the groups' weight sums at the end
+        const size_t smem = std::max((size_t)p.groups * 2 * d * sizeof(float),
+                                     (size_t)CPT * 2 * 16 * kNormMaxThreads);
         launch_pdl(kern, p.ctas, threads, smem, stream, rows, d, p.warps, static_cast<const XT *>(x),
                    static_cast<const YT *>(dy), gamma, mean, rstd, static_cast<const GT *>(dres),
                    static_cast<GT *>(dx), part);
