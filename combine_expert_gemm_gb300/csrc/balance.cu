@@ -24,6 +24,7 @@ namespace moe {
 namespace {
 
 constexpr int kBalCtas = 152;  // partial sums of the forward: one CTA per SM
+constexpr int kAlone = 4;      // rows a group when one CTA takes all tokens
 constexpr int kBalSlots = 8;   // warps that add up side by side in shared memory
 
 // Partial sums of one CTA in the workspace, rounded up to 16 bytes: int32
@@ -96,13 +97,34 @@ struct Row {
     }
 };
 
+// The outputs that follow from the sums over all tokens.
+struct LossOut {
+    int32_t *count, *token_count;
+    float *prob, *losses;
+
+    static __device__ __forceinline__ float inv(int tc) { return tc > 0 ? 1.f / (float)tc : 0.f; }
+    // expert e's count and mean probability; its term of the balance loss over N
+    __device__ __forceinline__ float expert(int e, int c, float sum, int tc, int K) const {
+        const float p = sum * inv(tc);
+        count[e] = c;
+        prob[e] = p;
+        return (float)c * inv(tc) / (float)K * p;
+    }
+    __device__ __forceinline__ void losses_of(float dot, float z, int tc, int N) const {
+        token_count[0] = tc;
+        losses[0] = (float)N * dot;
+        losses[1] = z * inv(tc);
+    }
+};
+
 __host__ __device__ constexpr int bal_threads(int vpt) { return vpt >= 16 ? 512 : 1024; }
 
 template <int LANES, int VPT, int VEC, bool HALF>
 __global__ void __launch_bounds__(bal_threads(VPT), 1)
 balance_partial(int T, int N, int K, const float *__restrict__ logits,
                 const int32_t *__restrict__ topk_idx, const uint8_t *__restrict__ mask,
-                float *__restrict__ lse, int32_t *__restrict__ part_i, float *__restrict__ part_f) {
+                float *__restrict__ lse, int32_t *__restrict__ part_i, float *__restrict__ part_f,
+                const LossOut out) {
     pdl_enter();
     using R = Row<LANES, VPT, VEC, HALF>;
     constexpr int kThreads = bal_threads(VPT), kWarps = kThreads / 32;
@@ -224,24 +246,42 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
         }
         __syncthreads();
     }
+    z = 0.f;
+    tok = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        z += zs[w];
+        tok += ts[w];
+    }
+    float dot = 0.f;
     part_i += blockIdx.x * bal_stride(N);
     part_f += blockIdx.x * bal_stride(N);
     for (int e = threadIdx.x; e < N; e += kThreads) {
         float p = 0.f;
 #pragma unroll
         for (int w = 0; w < kBalSlots; ++w) p += acc_s[w * N + e];
-        part_i[e] = cnt[e];
-        part_f[e] = p;
-    }
-    if (threadIdx.x == 0) {
-        float p = 0.f;
-        int n = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            p += zs[w];
-            n += ts[w];
+        if (gridDim.x == 1) {
+            dot += out.expert(e, cnt[e], p, tok, K);
+        } else {
+            part_i[e] = cnt[e];
+            part_f[e] = p;
         }
-        part_i[N] = n;
-        part_f[N] = p;
+    }
+    if (gridDim.x > 1) {
+        if (threadIdx.x == 0) {
+            part_i[N] = tok;
+            part_f[N] = z;
+        }
+        return;
+    }
+    // few tokens: this CTA has all of them, and no second launch is needed
+    __syncthreads();  // zs is read above
+    dot = group_sum<32>(dot);
+    if (lane == 0) zs[warp] = dot;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        dot = 0.f;
+        for (int w = 0; w < kWarps; ++w) dot += zs[w];
+        out.losses_of(dot, z, tok, N);
     }
 }
 
@@ -251,9 +291,7 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
 // rounds of L2 latency: an expert per thread took 9 to 12 us here.
 __global__ void __launch_bounds__(1024)
 balance_finish(int N, int K, int ctas, int slices, const int32_t *__restrict__ part_i,
-               const float *__restrict__ part_f, int32_t *__restrict__ count,
-               int32_t *__restrict__ token_count, float *__restrict__ prob,
-               float *__restrict__ losses) {
+               const float *__restrict__ part_f, const LossOut out) {
     pdl_enter();
     __shared__ float4 sf4[1024];
     __shared__ int4 si4[1024];
@@ -287,24 +325,14 @@ balance_finish(int N, int K, int ctas, int slices, const int32_t *__restrict__ p
     }
     __syncthreads();
     const int tc = si[N];
-    const float inv = tc > 0 ? 1.f / (float)tc : 0.f;
-    float dot = 0.f;
-    const int e = threadIdx.x;
-    if (e < N) {
-        const float p = sf[e] * inv;
-        count[e] = si[e];
-        prob[e] = p;
-        dot = (float)si[e] * inv / (float)K * p;
-    }
+    float dot = (int)threadIdx.x < N ? out.expert(threadIdx.x, si[threadIdx.x], sf[threadIdx.x], tc, K) : 0.f;
     dot = group_sum<32>(dot);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dot;
     __syncthreads();
     if (threadIdx.x == 0) {
-        float b = 0.f;
-        for (int w = 0; w < (int)blockDim.x / 32; ++w) b += red[w];
-        token_count[0] = tc;
-        losses[0] = (float)N * b;
-        losses[1] = sf[N] * inv;
+        dot = 0.f;
+        for (int w = 0; w < (int)blockDim.x / 32; ++w) dot += red[w];
+        out.losses_of(dot, sf[N], tc, N);
     }
 }
 
@@ -443,18 +471,21 @@ MOE_API moe_status moe_balance_loss(const moe_shape *s, const float *logits,
     const int N = s->N;
     int32_t *part_i = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + 256);
     float *part_f = reinterpret_cast<float *>(part_i + kBalCtas * bal_stride(N));
+    const LossOut out = {expert_count, token_count, expert_prob, losses};
     int ctas = 1;
     with_row(N, [&](auto q) {
         using Q = decltype(q);
-        constexpr int kThreads = bal_threads(Q::vpt);
-        ctas = (int)std::min<int64_t>(kBalCtas, std::max<int64_t>(1, ceil_div(s->T, kThreads / Q::lanes)));
+        constexpr int kThreads = bal_threads(Q::vpt), kGroups = kThreads / Q::lanes;
+        // up to kAlone rows a group one CTA takes less than a second launch
+        ctas = s->T <= kAlone * kGroups ? 1 : (int)std::min<int64_t>(kBalCtas, ceil_div(s->T, kGroups));
         launch_pdl(balance_partial<Q::lanes, Q::vpt, Q::vec, Q::half>, ctas, kThreads,
                    sizeof(float) * (kBalSlots + 1) * N, stream, s->T, N, s->K, logits, topk_idx,
-                   token_mask, lse, part_i, part_f);
+                   token_mask, lse, part_i, part_f, out);
     });
-    launch_pdl(balance_finish, 1, 1024, 0, stream, N, s->K, ctas, std::min(ctas, 1024 / (int)(bal_stride(N) / 4)),
-               static_cast<const int32_t *>(part_i), static_cast<const float *>(part_f),
-               expert_count, token_count, expert_prob, losses);
+    if (ctas > 1)
+        launch_pdl(balance_finish, 1, 1024, 0, stream, N, s->K, ctas,
+                   std::min(ctas, 1024 / (int)(bal_stride(N) / 4)),
+                   static_cast<const int32_t *>(part_i), static_cast<const float *>(part_f), out);
     return launch_status();
 }
 

@@ -9,6 +9,8 @@
 //
 // A lane takes 8 elements (16 bytes of bf16), a block is four lanes.  All
 // kernels are bound by HBM.
+#include <algorithm>
+
 #include "../../include/moe_block.h"
 #include "moe_common.cuh"
 
@@ -172,8 +174,10 @@ checkpoint_restore_rows(const int32_t *__restrict__ offset, int N, int64_t R, in
 
 // One warp per token, as moe_combine_backward's kernel: for each chunk of the
 // token's dy the K route rows' codes are read at once, and the K partial dot
-// products stay in registers.
-constexpr int kTokWarps = 8;
+// products stay in registers.  Two warps a CTA: a token's work goes by its
+// accepted routes, and with 8 warps a CTA waited for its longest (84 and 98 us
+// on the OLMoE-like and a drop-heavy layer, 76 and 86 with 2).
+constexpr int kTokWarps = 2;
 constexpr int kTokUnroll = 2;
 
 template <int MAXK>
@@ -253,9 +257,17 @@ combine_bwd_checkpoint_rows(int T, int nchunk, int K, const uint4 *__restrict__ 
     }
 }
 
-inline int ck_grid(int64_t chunks, int unroll) {
-    const int64_t per = (int64_t)kCkThreads * unroll, want = (chunks + per - 1) / per, most = (int64_t)num_sms() * 8;
-    return (int)(want < most ? want : most);
+// CTAs for `chunks`, `waves` per SM at most: several times what is resident (5
+// of 48 registers a thread), so that SMs which finish early take more, but few
+// enough that the rows past expert_offset[N], which the host does not know, cost
+// nothing.  8 per SM, 1.6 waves, took 140 us to save and 94 to restore the
+// OLMoE-like layer's buffers, 40 and 80 take 135 and 86; one CTA per 1024 chunks
+// of the whole buffer took 134 instead of 112 us to save a drop-heavy layer's.
+constexpr int kSaveWaves = 40, kRestoreWaves = 80;
+
+inline int ck_grid(int64_t chunks, int unroll, int waves) {
+    const int64_t per = (int64_t)kCkThreads * unroll, want = (chunks + per - 1) / per;
+    return (int)std::min<int64_t>(want, (int64_t)num_sms() * waves);
 }
 
 }  // namespace
@@ -292,7 +304,7 @@ MOE_API moe_status moe_checkpoint_save(const moe_shape *s, const int32_t *expert
         if (R * chunks > most) most = R * chunks;
     }
     if (most == 0) return MOE_OK;
-    launch_pdl(checkpoint_save_rows, ck_grid(most, kUnroll), kCkThreads, 0, stream, expert_offset, s->N, R, bufs);
+    launch_pdl(checkpoint_save_rows, ck_grid(most, kUnroll, kSaveWaves), kCkThreads, 0, stream, expert_offset, s->N, R, bufs);
     return launch_status();
 }
 
@@ -312,7 +324,7 @@ MOE_API moe_status moe_checkpoint_restore(const moe_shape *s, const int32_t *exp
     for (const void *p : ptrs)
         if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
     const int chunks = s->h / 8;
-    launch_pdl(checkpoint_restore_rows, ck_grid(R * chunks, kRestoreUnroll), kCkThreads, 0, stream, expert_offset,
+    launch_pdl(checkpoint_restore_rows, ck_grid(R * chunks, kRestoreUnroll, kRestoreWaves), kCkThreads, 0, stream, expert_offset,
                s->N, R, chunks, reinterpret_cast<const uint2 *>(g_q), g_scale,
                reinterpret_cast<const uint2 *>(u_q), u_scale, reinterpret_cast<uint4 *>(g_save),
                reinterpret_cast<uint4 *>(u_save), reinterpret_cast<uint4 *>(h_act));
