@@ -6,15 +6,15 @@
 //   dlogits = p (gb N / Tc (f - sum_e p_e f_e) + gz 2 lse / Tc) + scattered dlogit
 //
 // A token's row of logits is held in the registers of a group of LANES lanes,
-// VPT logits each, so both kernels read the logits once and need one exponential
-// per logit.  The group is as small as the row allows (8 lanes x 4 for N <= 32)
-// up to a whole warp: short rows then fill whole 128-byte requests, four tokens
-// to a warp.  Rows of a multiple of four logits are read and written in
-// 16-byte vectors (8 bytes for an even number).
+// VPT logits each (8 x 4 for N <= 32 up to 32 x 32), so both kernels read the
+// logits once and need one exponential per logit.  Rows of a multiple of four
+// logits are read and written in 16-byte vectors (8 bytes for an even number).
 //
-// Each probability is a packed subtraction and product and the hardware's 2^x:
-// expf and scalar arithmetic made the forward issue-bound, 40 us at T = 131072,
-// N = 250, where its bytes take 20.
+// The bytes would be the bound (131072 x 250 masked logits: 20 us forward, 36
+// backward), but issue slots come close: about 200 instructions a row forward
+// with a whole warp per row.  So each probability is a packed subtraction and
+// product and the hardware's 2^x (expf and scalar arithmetic took 40 us instead
+// of 32), and the forward takes as few lanes a row as its registers allow (27).
 #include <algorithm>
 
 #include "../../include/moe_block.h"
@@ -145,11 +145,7 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
     int tok = 0;
     // Whole warps step together: a group past T, or at a masked token, idles.
     // A row's logits and chosen experts are loaded one step ahead and its mask
-    // two, so that no load of a step waits for another one (for up to 8 logits
-    // a lane; a longer row is enough in flight by itself, and registers are
-    // short): loading them in the step took 35 us instead of 32 at T = 131072,
-    // N = 250.
-    constexpr bool kAhead = VPT <= 8;
+    // two, so that no load of a step waits for another one.
     constexpr int kIdx = (kMaxK + LANES - 1) / LANES;
     const int64_t step = (int64_t)gridDim.x * kGroups;
     auto counted = [&](int64_t t) { return t < T && !(mask && mask[t] == 0); };
@@ -164,7 +160,7 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
             idx[j] = on && k < K ? topk_idx[t * K + k] : -1;
         }
     };
-    if (kAhead) {
+    {
         const int64_t t = w0 + lane / LANES;
         ahead_on = counted(t);
         later_on = counted(t + step);
@@ -174,25 +170,17 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
     for (; w0 < T; w0 += step) {
         const int64_t t = w0 + lane / LANES;
         const bool in = t < T;
-        bool on;
+        const bool on = ahead_on;
         float v[VPT];
         int mine[kIdx];
-        if (!kAhead) {
-            ahead_on = counted(t);
-            R::load(logits + t * N, sub, N, ahead_on, ahead);
-            load_idx(t, ahead_on);
-        }
-        on = ahead_on;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) v[i] = ahead[i];
 #pragma unroll
         for (int j = 0; j < kIdx; ++j) mine[j] = idx[j];
-        if (kAhead) {
-            ahead_on = later_on;
-            later_on = counted(t + 2 * step);
-            R::load(logits + (t + step) * N, sub, N, ahead_on, ahead);
-            load_idx(t + step, ahead_on);
-        }
+        ahead_on = later_on;
+        later_on = counted(t + 2 * step);
+        R::load(logits + (t + step) * N, sub, N, ahead_on, ahead);
+        load_idx(t + step, ahead_on);
         float m = v[0];
 #pragma unroll
         for (int i = 1; i < VPT; ++i) m = fmaxf(m, v[i]);
@@ -410,8 +398,12 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
     }
 }
 
-// The smallest group that holds a row of N logits: calls fn with LANES, VPT,
-// the vector length that keeps rows aligned, and whether N fills half of it.
+// How a row of N logits is held: calls fn with LANES, VPT, the vector length
+// that keeps rows aligned, and whether N fills half of it.  The forward takes few
+// lanes, because what it does once a row (statistics, counts, sums over the
+// lanes) then serves several rows an instruction: 44 -> 39 us at T = 131072,
+// N = 250.  The backward does less a row and keeps more warps with whole warps
+// (51 us there against 65).
 template <int L, int V, int W, bool H>
 struct RowOf {
     static constexpr int lanes = L, vpt = V, vec = W;
@@ -421,15 +413,15 @@ template <int V>
 struct Int {
     static constexpr int value = V;
 };
-template <typename Fn>
+template <bool FWD, typename Fn>
 inline void with_row(int N, Fn &&fn) {
     auto go = [&](auto w) {
         constexpr int kVec = decltype(w)::value;
         if (N <= 32) fn(RowOf<8, 4, kVec, false>());
-        else if (N <= 64) fn(RowOf<16, 4, kVec, true>());
-        else if (N <= 128) fn(RowOf<32, 4, kVec, true>());
-        else if (N <= 256) fn(RowOf<32, 8, kVec, true>());
-        else if (N <= 512) fn(RowOf<32, 16, kVec, true>());
+        else if (N <= 64) fn(RowOf<FWD ? 8 : 16, FWD ? 8 : 4, kVec, true>());
+        else if (N <= 128) fn(RowOf<FWD ? 8 : 32, FWD ? 16 : 4, kVec, true>());
+        else if (N <= 256) fn(RowOf<FWD ? 8 : 32, FWD ? 32 : 8, kVec, true>());
+        else if (N <= 512) fn(RowOf<FWD ? 16 : 32, FWD ? 32 : 16, kVec, true>());
         else fn(RowOf<32, 32, kVec, true>());
     };
     if (N % 4 == 0) go(Int<4>());
@@ -473,7 +465,7 @@ MOE_API moe_status moe_balance_loss(const moe_shape *s, const float *logits,
     float *part_f = reinterpret_cast<float *>(part_i + kBalCtas * bal_stride(N));
     const LossOut out = {expert_count, token_count, expert_prob, losses};
     int ctas = 1;
-    with_row(N, [&](auto q) {
+    with_row<true>(N, [&](auto q) {
         using Q = decltype(q);
         constexpr int kThreads = bal_threads(Q::vpt), kGroups = kThreads / Q::lanes;
         // up to kAlone rows a group one CTA takes less than a second launch
@@ -505,7 +497,7 @@ MOE_API moe_status moe_balance_loss_backward(const moe_shape *s, const float *lo
                           dlogit, dlogits};
     for (const void *p : ptrs)
         if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
-    with_row(s->N, [&](auto q) {
+    with_row<false>(s->N, [&](auto q) {
         using Q = decltype(q);
         const int64_t want = ceil_div(s->T, kBwdThreads / Q::lanes);
         launch_pdl(balance_bwd_rows<Q::lanes, Q::vpt, Q::vec, Q::half>,
