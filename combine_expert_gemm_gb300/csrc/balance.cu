@@ -383,7 +383,10 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
             const float2 g = __fmul2_rn(v2[i], __ffma2_rn(cb2, f2[i], c2));
             v2[i] = on ? g : make_float2(0.f, 0.f);
         }
-        if (dlogit) {
+        if (!dlogit) {
+            if (in) R::store(dlogits + t * N, sub, N, v);
+        } else if (VPT <= 4) {
+            // short rows: every lane compares its few experts with every route
 #pragma unroll
             for (int j = 0; j < kIdx; ++j)
                 for (int k = 0; k < min(LANES, K - j * LANES); ++k) {
@@ -393,8 +396,35 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
                     for (int i = 0; i < VPT; ++i)
                         if (at == R::first(sub) + R::step(i)) v[i] += g;
                 }
+            if (in) R::store(dlogits + t * N, sub, N, v);
+        } else {
+            // long rows (a warp each): the row is stored without the gates, then
+            // the lane of each route writes its expert's element again; K times
+            // VPT comparisons would be most of the kernel
+            if (in) R::store(dlogits + t * N, sub, N, v);
+            __syncwarp();
+            const int at = idx[0];
+            const bool is = at >= 0 && at < N;
+            float g = gate[0];
+            // one expert in several routes (moe_route never does this): the first
+            // of them writes, with the gates' sum
+            const unsigned peers = __match_any_sync(0xFFFFFFFFu, is ? at : -1 - lane);
+            if (__any_sync(0xFFFFFFFFu, __popc(peers) > 1)) {
+                g = 0.f;
+                for (int k = 0; k < K; ++k) {
+                    const float gk = __shfl_sync(0xFFFFFFFFu, gate[0], k);
+                    if (peers >> k & 1) g += gk;
+                }
+            }
+            if (is && lane == __ffs(peers) - 1) {
+                float r = 0.f;
+                if (on) {
+                    const float p = ex2((logits[t * N + at] - l) * kLog2e);
+                    r = p * fmaf(cb, (float)count[at] * inv / (float)K, c);
+                }
+                dlogits[t * N + at] = r + g;
+            }
         }
-        if (in) R::store(dlogits + t * N, sub, N, v);
     }
 }
 
