@@ -14,8 +14,8 @@
 // therefore stay in registers, and the weight gradients cost no second pass
 // over x and dy (the two-pass version took 74 of 172 us at 8192 x 2048).
 //
-// The forward's rows arrive through a ring of cp.async copies, kStages - 1 rows
-// ahead.  A thread copies exactly the bytes that it will read itself, so the
+// The forward's bf16 rows arrive through a ring of cp.async copies, kStages - 1
+// rows ahead (fp32 rows in registers).  A thread copies exactly the bytes that it will read itself, so the
 // ring needs no barrier and no wait but the thread's own cp.async.wait_group.
 // The backward moves three tensors in, and there the copies' and the ring's own
 // instructions were what it waited for (353 a warp-row, 0.34 issued a cycle): it
@@ -165,10 +165,16 @@ struct NormPlan {
 // than 16 only where 512 threads do not reach, the registers being short.
 inline int norm_cpt(int d) { return d <= 256 ? 1 : d <= 16 * kNormMaxThreads ? 2 : 4; }
 
-inline NormPlan norm_plan(int rows, int d) {
+// The backward holds two rows of x and dy: with both in fp32 the registers want
+// 8 columns a thread where 512 threads reach (23872 x 2040: 118 us against 144).
+inline int bwd_cpt(int d, size_t bytes) {
+    return bytes == 8 && d <= 8 * kNormMaxThreads ? 1 : norm_cpt(d);
+}
+
+inline NormPlan norm_plan(int rows, int d, int cpt) {
     NormPlan p;
     const int chunks = d / 8;
-    p.cpt = norm_cpt(d);
+    p.cpt = cpt;
     p.warps = (chunks + 32 * p.cpt - 1) / (32 * p.cpt);
     p.groups = std::min(p.warps == 1 ? 16 : 15, kNormMaxThreads / 32 / p.warps);
     // few rows: one group per CTA before a second one on any SM
@@ -176,6 +182,29 @@ inline NormPlan norm_plan(int rows, int d) {
     p.ctas = std::max(1, std::min(kNormCtas, (rows + p.groups - 1) / p.groups));
     return p;
 }
+
+// Eight elements as loaded: 16 bytes of bf16 or 32 of fp32.
+template <typename T>
+struct Raw {
+    uint4 w[words<T>()];
+    __device__ __forceinline__ void load(const T *p, bool on) {
+        const uint4 *g = reinterpret_cast<const uint4 *>(p);
+#pragma unroll
+        for (int i = 0; i < words<T>(); ++i) w[i] = on ? __ldcs(g + i) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void get(f2 (&f)[4]) const {
+        if (words<T>() == 1) {
+            unpack(w[0], f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 v = w[i % words<T>()];
+                f[2 * i] = make2(__uint_as_float(v.x), __uint_as_float(v.y));
+                f[2 * i + 1] = make2(__uint_as_float(v.z), __uint_as_float(v.w));
+            }
+        }
+    }
+};
 
 template <typename XT, int CPT, int STAGES>
 __global__ void __launch_bounds__(kNormMaxThreads, 1)
@@ -200,21 +229,36 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
     const int64_t step = (int64_t)gridDim.x * groups;
     const int64_t first = (int64_t)blockIdx.x * groups + group;
     uint4 *mine = ring + threadIdx.x;
+    // kRing: a cp.async ring, STAGES - 1 rows ahead; otherwise the next row waits
+    // in registers
+    constexpr bool kRing = STAGES > 0;
+    Raw<XT> nx[kRing ? 1 : CPT];
+    Raw<uint16_t> na[kRing ? 1 : CPT];
     auto fetch = [&](int64_t t, int stage) {
         if (t < rows) {
             const int64_t at = t * d + tid * 8;
 #pragma unroll
             for (int c = 0; c < CPT; ++c) {
-                uint4 *s = mine + stage * kStage + c * kChunkWords * kNormMaxThreads;
-                ring_copy(s, x + at + c * gthreads * 8, on[c] ? 16 : 0);
-                if (add)
-                    ring_copy(s + words<XT>() * kNormMaxThreads, add + at + c * gthreads * 8, on[c] ? 16 : 0);
+                const XT *px = x + at + c * gthreads * 8;
+                const uint16_t *pa = add + at + c * gthreads * 8;
+                if (kRing) {
+                    uint4 *s = mine + stage * kStage + c * kChunkWords * kNormMaxThreads;
+                    ring_copy(s, px, on[c] ? 16 : 0);
+                    if (add) ring_copy(s + words<XT>() * kNormMaxThreads, pa, on[c] ? 16 : 0);
+                } else {
+                    nx[c % (kRing ? 1 : CPT)].load(px, on[c]);
+                    if (add) na[c % (kRing ? 1 : CPT)].load(pa, on[c]);
+                }
             }
         }
-        cp_async_commit();
+        if (kRing) cp_async_commit();
     };
+    if (kRing) {
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) fetch(first + s * step, s);
+        for (int s = 0; s < STAGES - 1; ++s) fetch(first + s * step, s);
+    } else {
+        fetch(first, 0);
+    }
     // columns of warp w: chunks [32 w, 32 w + 32) of each of the CPT parts
     auto columns = [&](int w) {
         int n = 0;
@@ -229,8 +273,10 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
     const float lane_inv_n = other < warps ? 1.f / lane_n : 0.f;
     int stage = 0, buf = 0;
     for (int64_t t = first; t < rows; t += step) {
-        fetch(t + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
-        cp_async_wait<STAGES - 1>();
+        if (kRing) {
+            fetch(t + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+            cp_async_wait<kRing ? STAGES - 1 : 0>();
+        }
         const int64_t at = t * d + tid * 8;
         const uint4 *s = mine + stage * kStage;
         if (++stage == STAGES) stage = 0;
@@ -238,10 +284,12 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
         f2 sum2 = both(0.f);
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
-            ring_read<XT>(s + c * kChunkWords * kNormMaxThreads, f[c]);
+            if (kRing) ring_read<XT>(s + c * kChunkWords * kNormMaxThreads, f[c]);
+            else nx[c % (kRing ? 1 : CPT)].get(f[c]);
             if (add) {
                 f2 a[4];
-                ring_read<uint16_t>(s + (c * kChunkWords + words<XT>()) * kNormMaxThreads, a);
+                if (kRing) ring_read<uint16_t>(s + (c * kChunkWords + words<XT>()) * kNormMaxThreads, a);
+                else na[c % (kRing ? 1 : CPT)].get(a);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f[c][i] = add2(f[c][i], a[i]);
                 store_round8(x_sum + at + c * gthreads * 8, f[c], on[c]);
@@ -249,6 +297,7 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum2 = add2(sum2, f[c][i]);
         }
+        if (!kRing) fetch(t + step, 0);
         const float sum = warp_sum(sum_of(sum2));
         const float mw = sum * inv_nw;
         f2 sq2 = both(0.f);
@@ -286,31 +335,8 @@ norm_fwd(int rows, int d, int warps, const XT *x, const uint16_t *add, const flo
             if (on[c]) store8(y + at + c * gthreads * 8, f[c]);
         }
     }
-    cp_async_wait<0>();
+    if (kRing) cp_async_wait<0>();
 }
-
-// Eight elements as loaded: 16 bytes of bf16 or 32 of fp32.
-template <typename T>
-struct Raw {
-    uint4 w[words<T>()];
-    __device__ __forceinline__ void load(const T *p, bool on) {
-        const uint4 *g = reinterpret_cast<const uint4 *>(p);
-#pragma unroll
-        for (int i = 0; i < words<T>(); ++i) w[i] = on ? __ldcs(g + i) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    __device__ __forceinline__ void get(f2 (&f)[4]) const {
-        if (words<T>() == 1) {
-            unpack(w[0], f);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint4 v = w[i % words<T>()];
-                f[2 * i] = make2(__uint_as_float(v.x), __uint_as_float(v.y));
-                f[2 * i + 1] = make2(__uint_as_float(v.z), __uint_as_float(v.w));
-            }
-        }
-    }
-};
 
 // part[cta][2][d]: this CTA's sums of dgamma and dbeta (part may be NULL).
 template <typename XT, typename YT, typename GT, int CPT>
@@ -521,8 +547,7 @@ struct Cpt {
     static constexpr int value = V;
 };
 template <typename Fn>
-inline moe_status with_cpt(int d, Fn &&fn) {
-    const int c = norm_cpt(d);
+inline moe_status with_cpt(int c, Fn &&fn) {
     return c == 1 ? fn(Cpt<1>()) : c == 2 ? fn(Cpt<2>()) : fn(Cpt<4>());
 }
 
@@ -530,8 +555,12 @@ template <typename XT, int CPT>
 moe_status launch_norm_fwd(int32_t rows, int32_t d, const void *x, const moe_bf16 *add,
                            const float *gamma, const float *beta, float eps, void *x_sum,
                            moe_bf16 *y, float *mean, float *rstd, cudaStream_t stream) {
-    constexpr int kWords = CPT * (words<XT>() + 1), kStages = ring_stages(kWords);
-    const NormPlan p = norm_plan(rows, d);
+    // fp32 rows through the ring took 71 us at 23872 x 2040 and 110 with add,
+    // through registers 51 and 92; bf16 rows 36 and 68 against 42 and 63 to 67,
+    // and more where a row is longer (8000 x 5120: 52 against 65)
+    constexpr int kWords = CPT * (words<XT>() + 1);
+    constexpr int kStages = sizeof(XT) == 4 && CPT <= 2 ? 0 : ring_stages(kWords);
+    const NormPlan p = norm_plan(rows, d, CPT);
     const int threads = p.groups * p.warps * 32;
     auto *kern = norm_fwd<XT, CPT, kStages>;
     static PerDeviceOnce attr;
@@ -547,7 +576,7 @@ moe_status launch_norm_bwd(int32_t rows, int32_t d, const void *x, const void *d
                            const float *gamma, const float *mean, const float *rstd,
                            const void *dres, void *dx, float *dgamma, float *dbeta, void *ws,
                            cudaStream_t stream) {
-    const NormPlan p = norm_plan(rows, d);
+    const NormPlan p = norm_plan(rows, d, CPT);
     const int threads = p.groups * p.warps * 32;
     float *part = dgamma || dbeta ? reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256) : nullptr;
     if (rows > 0) {
@@ -586,7 +615,7 @@ MOE_API moe_status moe_layer_norm(int32_t rows, int32_t d, int32_t x_dtype, cons
     for (const void *p : ptrs)
         if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
     auto go = [&](auto xt) {
-        return with_cpt(d, [&](auto c) {
+        return with_cpt(norm_cpt(d), [&](auto c) {
             return launch_norm_fwd<decltype(xt), decltype(c)::value>(rows, d, x, add, gamma, beta, eps,
                                                                      x_sum, y, mean, rstd, stream);
         });
@@ -596,7 +625,7 @@ MOE_API moe_status moe_layer_norm(int32_t rows, int32_t d, int32_t x_dtype, cons
 
 MOE_API size_t moe_layer_norm_backward_workspace_bytes(int32_t rows, int32_t d) {
     if (check_norm(rows, d) != MOE_OK) return 0;
-    return 256 + (size_t)norm_plan(rows, d).ctas * 2 * d * sizeof(float);
+    return 256 + (size_t)kNormCtas * 2 * d * sizeof(float);
 }
 
 MOE_API moe_status moe_layer_norm_backward(int32_t rows, int32_t d, int32_t x_dtype, const void *x,
@@ -615,7 +644,7 @@ MOE_API moe_status moe_layer_norm_backward(int32_t rows, int32_t d, int32_t x_dt
         ws_bytes < moe_layer_norm_backward_workspace_bytes(rows, d))
         return MOE_ERR_WORKSPACE;
     auto go = [&](auto xt, auto yt, auto gt) {
-        return with_cpt(d, [&](auto c) {
+        return with_cpt(bwd_cpt(d, sizeof(xt) + sizeof(yt)), [&](auto c) {
             return launch_norm_bwd<decltype(xt), decltype(yt), decltype(gt), decltype(c)::value>(
                 rows, d, x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, ws, stream);
         });
