@@ -10,8 +10,8 @@ import ctypes
 
 import torch
 
-from . import (_P, _SP, _SZ, BackwardBuffers, LayerBuffers, _bf16, _check, _f32, _i32, _lib, _stream,
-               _u8, combine, dispatch, dispatch_backward, expert_ffn, expert_ffn_backward, route,
+from . import (_P, _SP, _SZ, BackwardBuffers, LayerBuffers, _bf16, _check, _current_raw_stream, _f32, _i32,
+               _lib, _stream, _u8, combine, dispatch, dispatch_backward, expert_ffn, expert_ffn_backward, route,
                route_logits, route_workspace_bytes)
 
 __all__ = ["layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_bytes",
@@ -68,6 +68,13 @@ def _arg(t, dtype, name, n, dev):
     raise ValueError(f"{name}: {t.numel()} elements, {n} needed")
 
 
+def _on(stream, dev):
+    """The stream's handle; the current stream of the current device dev by default."""
+    if stream is None and _current_raw_stream is not None:
+        return _current_raw_stream(dev)
+    return _stream(stream)
+
+
 def _ws(ws, dev):
     p = _arg(ws, _u8, "ws", 0, dev)
     return p, 0 if ws is None else ws.numel()
@@ -83,7 +90,8 @@ def _rows(x, name):
     dt = _float_type(x, name)
     if x.dim() != 2:
         raise ValueError(f"{name}: expected [rows, d]")
-    return dt, x.shape[0], x.shape[1]
+    rows, d = x.shape
+    return dt, rows, d
 
 
 # -------------------------------------------------------------- layer norm --
@@ -97,7 +105,7 @@ def layer_norm(x, add, gamma, beta, eps, x_sum, y, mean, rstd, stream=None):
         rows, d, _DTYPE[dt], _arg(x, dt, "x", n, dev), _arg(add, _bf16, "add", n, dev),
         _arg(gamma, _f32, "gamma", d, dev), _arg(beta, _f32, "beta", d, dev), eps,
         _arg(x_sum, dt, "x_sum", n, dev), _arg(y, _bf16, "y", n, dev),
-        _arg(mean, _f32, "mean", rows, dev), _arg(rstd, _f32, "rstd", rows, dev), _stream(stream)),
+        _arg(mean, _f32, "mean", rows, dev), _arg(rstd, _f32, "rstd", rows, dev), _on(stream, dev)),
         "moe_layer_norm")
 
 
@@ -118,7 +126,7 @@ def layer_norm_backward(x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, ws, s
         _arg(gamma, _f32, "gamma", d, dev), _arg(mean, _f32, "mean", rows, dev),
         _arg(rstd, _f32, "rstd", rows, dev), _DTYPE[gt], _arg(dres, gt, "dres", n, dev),
         _arg(dx, gt, "dx", n, dev), _arg(dgamma, _f32, "dgamma", d, dev),
-        _arg(dbeta, _f32, "dbeta", d, dev), wp, wn, _stream(stream)), "moe_layer_norm_backward")
+        _arg(dbeta, _f32, "dbeta", d, dev), wp, wn, _on(stream, dev)), "moe_layer_norm_backward")
 
 
 # ------------------------------------------------------------ balance loss --
@@ -140,7 +148,7 @@ def balance_loss(shape, logits, topk_idx, token_mask, expert_count, token_count,
         _arg(expert_count, _i32, "expert_count", N, dev),
         _arg(token_count, _i32, "token_count", 1, dev),
         _arg(expert_prob, _f32, "expert_prob", N, dev), _arg(lse, _f32, "lse", T, dev),
-        _arg(losses, _f32, "losses", 2, dev), wp, wn, _stream(stream)), "moe_balance_loss")
+        _arg(losses, _f32, "losses", 2, dev), wp, wn, _on(stream, dev)), "moe_balance_loss")
 
 
 def balance_loss_backward(shape, logits, topk_idx, token_mask, expert_count, token_count, lse,
@@ -155,7 +163,7 @@ def balance_loss_backward(shape, logits, topk_idx, token_mask, expert_count, tok
         _arg(expert_count, _i32, "expert_count", N, dev),
         _arg(token_count, _i32, "token_count", 1, dev), _arg(lse, _f32, "lse", T, dev),
         _arg(dlosses, _f32, "dlosses", 2, dev), _arg(dlogit, _f32, "dlogit", T * K, dev),
-        _arg(dlogits, _f32, "dlogits", T * N, dev), _stream(stream)), "moe_balance_loss_backward")
+        _arg(dlogits, _f32, "dlogits", T * N, dev), _on(stream, dev)), "moe_balance_loss_backward")
 
 
 def router_dense_backward_workspace_bytes(shape):
@@ -174,7 +182,7 @@ def router_dense_backward(shape, x, w_router, dlogits, dx_in, dx, dw_router, dbi
         _arg(w_router, _f32, "w_router", N * d, dev), _arg(dlogits, _f32, "dlogits", T * N, dev),
         _arg(dx_in, _f32, "dx_in", T * d, dev), _arg(dx, _f32, "dx", T * d, dev),
         _arg(dw_router, _f32, "dw_router", N * d, dev), _arg(dbias, _f32, "dbias", N, dev), wp, wn,
-        _stream(stream)), "moe_router_dense_backward")
+        _on(stream, dev)), "moe_router_dense_backward")
 
 
 # ------------------------------------------------------- 8-bit checkpoints --
@@ -191,7 +199,7 @@ def checkpoint_save(shape, expert_offset, g_save, u_save, y_disp, g_q, g_scale, 
         _arg(y_disp, _bf16, "y_disp", R * d, dev), _arg(g_q, _i8, "g_q", R * h, dev),
         _arg(g_scale, _u8, "g_scale", R * h // 32, dev), _arg(u_q, _i8, "u_q", R * h, dev),
         _arg(u_scale, _u8, "u_scale", R * h // 32, dev), _arg(y_q, _i8, "y_q", R * d, dev),
-        _arg(y_scale, _u8, "y_scale", R * d // 32, dev), _stream(stream)), "moe_checkpoint_save")
+        _arg(y_scale, _u8, "y_scale", R * d // 32, dev), _on(stream, dev)), "moe_checkpoint_save")
 
 
 def checkpoint_restore(shape, expert_offset, g_q, g_scale, u_q, u_scale, g_save, u_save, h_act,
@@ -203,7 +211,7 @@ def checkpoint_restore(shape, expert_offset, g_q, g_scale, u_q, u_scale, g_save,
         _arg(g_q, _i8, "g_q", n, dev), _arg(g_scale, _u8, "g_scale", n // 32, dev),
         _arg(u_q, _i8, "u_q", n, dev), _arg(u_scale, _u8, "u_scale", n // 32, dev),
         _arg(g_save, _bf16, "g_save", n, dev), _arg(u_save, _bf16, "u_save", n, dev),
-        _arg(h_act, _bf16, "h_act", n, dev), _stream(stream)), "moe_checkpoint_restore")
+        _arg(h_act, _bf16, "h_act", n, dev), _on(stream, dev)), "moe_checkpoint_restore")
 
 
 def combine_backward_checkpoint(shape, dy, y_q, y_scale, route_row, topk_gate, dy_disp, dgate,
@@ -218,7 +226,7 @@ def combine_backward_checkpoint(shape, dy, y_q, y_scale, route_row, topk_gate, d
         _arg(route_row, _i32, "route_row", T * K, dev),
         _arg(topk_gate, _f32, "topk_gate", T * K, dev), _arg(dy_disp, _bf16, "dy_disp", R * d, dev),
         _arg(dgate, _f32, "dgate", T * K, dev), _arg(dlogit, _f32, "dlogit", T * K, dev),
-        _stream(stream)), "moe_combine_backward_checkpoint")
+        _on(stream, dev)), "moe_combine_backward_checkpoint")
 
 
 # ------------------------------------------------------------------- block --
