@@ -335,6 +335,7 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
                  const float *__restrict__ dlogit, float *__restrict__ dlogits) {
     pdl_enter();
     using R = Row<LANES, VPT, VEC, HALF>;
+    static_assert(VPT <= 4 || LANES == 32, "long rows have a warp of their own");
     constexpr int kGroups = kBwdThreads / LANES;
     constexpr int kIdx = (kMaxK + LANES - 1) / LANES;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = threadIdx.x % LANES;

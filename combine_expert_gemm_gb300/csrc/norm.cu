@@ -462,7 +462,7 @@ norm_bwd(int rows, int d, int warps, const XT *__restrict__ x, const YT *__restr
         }
     }
     if (!part) return;
-    // the CTA's groups, in order, through the ring's memory
+    // the CTA's groups, in order, through the shared memory that held gamma
     float *acc = reinterpret_cast<float *>(ring);  // [groups][2][d]
     __syncthreads();
 #pragma unroll

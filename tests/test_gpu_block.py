@@ -679,3 +679,28 @@ def test_offsets_past_32_bits(moe):
     lse = torch.logsumexp(logits[-k:].double(), 1, keepdim=True)
     want = p * (N / T * (f - (p @ f)[:, None]) + 2 / T * lse)
     assert (out["dlogits"][-k:].double() - want).norm() <= 1e-4 * want.norm()
+
+
+def test_router_dense_offsets_past_32_bits(moe):
+    """More than 2^31 elements in x, dx_in and dx: the last tokens' dx equals the
+    same tokens' in a call of their own, and dw_router is theirs alone when every
+    other token is zero."""
+    k, d, N = 200, 8192, 6
+    T = (1 << 31) // d + 72
+    g = _gen(33)
+    x, dl = torch.zeros(T, d, dtype=BF, device=DEV), torch.zeros(T, N, device=DEV)
+    x[-k:] = torch.randn(k, d, generator=g).to(BF).to(DEV)
+    dl[-k:] = torch.randn(k, N, generator=g).to(DEV)
+    w = torch.randn(N, d, generator=g).to(DEV)
+    dx = torch.zeros(T, d, device=DEV)
+    dx[-k:] = torch.randn(k, d, generator=g).to(DEV)
+    base = dx[-k:].clone()
+    s = moe.Shape(T, d, N, 1, 8, 1)
+    dw, db = torch.empty(N, d, device=DEV), torch.empty(N, device=DEV)
+    ws = torch.zeros(moe.router_dense_backward_workspace_bytes(s), dtype=torch.uint8, device=DEV)
+    moe.router_dense_backward(s, x, w, dl, dx, dx, dw, db, ws)
+    assert moe.read_device_error(ws) == 0
+    sdx, sdw, sdb = _run_dense(moe, x[-k:].clone(), w, dl[-k:].clone(), base)
+    _last_rows_equal(dx, sdx, k)
+    assert not dx[: 1 << 12].any() and not dx[(1 << 31) // d - 4096:-k].any()
+    assert torch.allclose(dw, sdw, rtol=1e-5, atol=1e-4) and torch.allclose(db, sdb, rtol=1e-5, atol=1e-4)
