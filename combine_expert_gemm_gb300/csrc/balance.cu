@@ -335,7 +335,9 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
                  const float *__restrict__ dlogit, float *__restrict__ dlogits) {
     pdl_enter();
     using R = Row<LANES, VPT, VEC, HALF>;
-    static_assert(VPT <= 4 || LANES == 32, "long rows have a warp of their own");
+    // a lane per route is there to write a gate's element unless few lanes hold
+    // the row; for 4 logits a lane comparing is cheaper
+    constexpr bool kCompare = VPT <= 4 || LANES < kMaxK;
     constexpr int kGroups = kBwdThreads / LANES;
     constexpr int kIdx = (kMaxK + LANES - 1) / LANES;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = threadIdx.x % LANES;
@@ -386,7 +388,7 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
         }
         if (!dlogit) {
             if (in) R::store(dlogits + t * N, sub, N, v);
-        } else if (VPT <= 4) {
+        } else if (kCompare) {
             // short rows: every lane compares its few experts with every route
 #pragma unroll
             for (int j = 0; j < kIdx; ++j)
@@ -399,9 +401,9 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
                 }
             if (in) R::store(dlogits + t * N, sub, N, v);
         } else {
-            // long rows (a warp each): the row is stored without the gates, then
-            // the lane of each route writes its expert's element again; K times
-            // VPT comparisons would be most of the kernel
+            // long rows: the row is stored without the gates, then the lane of
+            // each route writes its expert's element again; K times VPT
+            // comparisons would be most of the kernel
             if (in) R::store(dlogits + t * N, sub, N, v);
             __syncwarp();
             const int at = idx[0];
@@ -409,12 +411,13 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
             float g = gate[0];
             // one expert in several routes (moe_route never does this): the first
             // of them writes, with the gates' sum
-            const unsigned peers = __match_any_sync(0xFFFFFFFFu, is ? at : -1 - lane);
+            const int lane0 = lane - sub;  // of this token's lanes
+            const unsigned peers = __match_any_sync(0xFFFFFFFFu, is ? at + lane0 * kMaxN : -1 - lane);
             if (__any_sync(0xFFFFFFFFu, __popc(peers) > 1)) {
                 g = 0.f;
                 for (int k = 0; k < K; ++k) {
-                    const float gk = __shfl_sync(0xFFFFFFFFu, gate[0], k);
-                    if (peers >> k & 1) g += gk;
+                    const float gk = __shfl_sync(0xFFFFFFFFu, gate[0], k, LANES);
+                    if (peers >> (lane0 + k) & 1) g += gk;
                 }
             }
             if (is && lane == __ffs(peers) - 1) {
@@ -430,11 +433,12 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
 }
 
 // How a row of N logits is held: calls fn with LANES, VPT, the vector length
-// that keeps rows aligned, and whether N fills half of it.  The forward takes few
-// lanes, because what it does once a row (statistics, counts, sums over the
-// lanes) then serves several rows an instruction: 44 -> 39 us at T = 131072,
-// N = 250.  The backward does less a row and keeps more warps with whole warps
-// (51 us there against 65).
+// that keeps rows aligned, and whether N fills half of it.  Few lanes, because
+// what a kernel does once a row (statistics, counts, sums over the lanes) then
+// serves several rows an instruction, as long as the registers leave enough
+// warps: the forward at T = 131072, N = 250 takes 39 us with 8 lanes, 45 with
+// 16, 44 with 32; the backward, which holds the counts beside the row, 65, 49
+// and 53, and at N = 64 the pair takes 36 with 8 against 39 with 16.
 template <int L, int V, int W, bool H>
 struct RowOf {
     static constexpr int lanes = L, vpt = V, vec = W;
@@ -449,9 +453,9 @@ inline void with_row(int N, Fn &&fn) {
     auto go = [&](auto w) {
         constexpr int kVec = decltype(w)::value;
         if (N <= 32) fn(RowOf<8, 4, kVec, false>());
-        else if (N <= 64) fn(RowOf<FWD ? 8 : 16, FWD ? 8 : 4, kVec, true>());
+        else if (N <= 64) fn(RowOf<8, 8, kVec, true>());
         else if (N <= 128) fn(RowOf<FWD ? 8 : 32, FWD ? 16 : 4, kVec, true>());
-        else if (N <= 256) fn(RowOf<FWD ? 8 : 32, FWD ? 32 : 8, kVec, true>());
+        else if (N <= 256) fn(RowOf<FWD ? 8 : 16, FWD ? 32 : 16, kVec, true>());
         else if (N <= 512) fn(RowOf<FWD ? 16 : 32, FWD ? 32 : 16, kVec, true>());
         else fn(RowOf<32, 32, kVec, true>());
     };
