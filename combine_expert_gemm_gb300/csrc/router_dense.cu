@@ -762,15 +762,24 @@ MOE_API moe_status moe_router_dense_backward(const moe_shape *s, const moe_bf16 
     uint16_t *wp = reinterpret_cast<uint16_t *>(base + pl.wp);
     float *db = reinterpret_cast<float *>(base + pl.db);
     float *part = reinterpret_cast<float *>(base + pl.part);
+    // whatever can fail comes before the first launch
+    CUtensorMap mx, mdl_k, mdl, mw, min_, mout;
+    if (T > 0 && dw_router &&
+        (!make_map(&mx, x, d, T, 64) || !make_map_pieces_k(&mdl_k, dlp, pl.Tp, N, pl.nt)))
+        return MOE_ERR_CUDA;
+    if (T > 0 && dx) {
+        static PerDeviceOnce smem_attr;
+        if (!device_once(smem_attr, [] { return set_smem_limit(router_dense_dx, kDxSmem); }) ||
+            !make_map_pieces_mn(&mdl, dlp, pl.Tp, N, 32) || !make_map_pieces_mn(&mw, wp, pl.dp, N, 32) ||
+            !make_map_f32(&min_, dx_in ? dx_in : dx, d, T) || !make_map_f32(&mout, dx, d, T))
+            return MOE_ERR_CUDA;
+    }
     if (T > 0) {
         launch_pdl(router_dense_prep, dim3(pl.groups, pl.chunks + (dx ? 1 : 0)), kPrepThreads, 0,
                    stream, T, pl.Tp, N, d, pl.dp, pl.chunks, dlogits, w_router, dlp, wp, db);
         if (dw_router) {
-            CUtensorMap mx, mdl;
-            if (!make_map(&mx, x, d, T, 64) || !make_map_pieces_k(&mdl, dlp, pl.Tp, N, pl.nt))
-                return MOE_ERR_CUDA;
-            r = pl.nt == 32 ? launch_dw<32>(mx, mdl, s, pl.splits, part, status, stream)
-                            : launch_dw<64>(mx, mdl, s, pl.splits, part, status, stream);
+            r = pl.nt == 32 ? launch_dw<32>(mx, mdl_k, s, pl.splits, part, status, stream)
+                            : launch_dw<64>(mx, mdl_k, s, pl.splits, part, status, stream);
             if (r != MOE_OK) return r;
         }
     }
@@ -784,13 +793,6 @@ MOE_API moe_status moe_router_dense_backward(const moe_shape *s, const moe_bf16 
     sums.dw = reinterpret_cast<float4 *>(dw_router);
     sums.dbias = dbias;
     if (dx && T > 0) {
-        static PerDeviceOnce smem_attr;
-        if (!device_once(smem_attr, [] { return set_smem_limit(router_dense_dx, kDxSmem); }))
-            return MOE_ERR_CUDA;
-        CUtensorMap mdl, mw, min_, mout;
-        if (!make_map_pieces_mn(&mdl, dlp, pl.Tp, N, 32) || !make_map_pieces_mn(&mw, wp, pl.dp, N, 32) ||
-            !make_map_f32(&min_, dx_in ? dx_in : dx, d, T) || !make_map_f32(&mout, dx, d, T))
-            return MOE_ERR_CUDA;
         const int64_t tiles = ((int64_t)T + 127) / 128 * ((d + 127) / 128);
         launch_pdl(router_dense_dx, (unsigned)std::min<int64_t>(tiles, num_sms()), kGemmThreads, kDxSmem,
                    stream, mdl, mw, min_, mout, T, N, d, dx_in ? 1 : 0, sums, status);
