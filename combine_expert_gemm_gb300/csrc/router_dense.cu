@@ -276,31 +276,40 @@ __global__ void __launch_bounds__(256) router_dense_sum(const Sums q) {
 // thread and the epilogue.
 //
 // The epilogue's work is the traffic: each warp owns 32 tokens x 64 columns of
-// a tile and four 4 KB blocks of shared memory through which it streams 32 x 32
-// blocks of dx_in (TMA load, three blocks ahead), adds the accumulator in
+// a tile and SLOTS blocks of 4 KB in shared memory, through which it streams
+// 32 x 32 blocks of dx_in (TMA load, SLOTS - 1 ahead), adds the accumulator in
 // place and stores the block to dx (TMA store).  No warp waits for another's
-// block, and 32 blocks of 4 KB cover the latency of the loads and stores.
-constexpr int kDxStages = 2;
+// block, and 24 or 32 blocks of 4 KB cover the latency of the loads and stores.
+//
+// One k-block a tile (N <= 32) needs one operand stage and leaves room for four
+// slots; more k-blocks take two stages, with three slots.  The whole call, us:
+//                                       <1, 4>   <2, 3>   <2, 4>
+//   T = 32768, d = 4096, N = 32           219      220      231
+//   T = 32768, d = 2048, N = 16           113      117      119
+//   T =  8192, d = 2048, N = 64            50       41       42
+// <2, 4> takes 225 KB; alone it is 4% slower than <1, 4> (169 against 163 us in
+// the first shape), the rest is lost where the launches before and after meet it.
 constexpr int kDxPiece = 2 * 32 * 128;              // 128 columns or tokens x 32 experts: 8 KB
 constexpr int kDxStageBytes = 2 * 3 * kDxPiece;     // 48 KB
-constexpr int kDxSlots = 4;
-constexpr int kDxAhead = kDxSlots - 1;
 constexpr int kDxBlk = 32 * 32 * 4;
 constexpr int kDxAcc = 4;
 
-struct alignas(8) DxBars {
-    uint64_t full[kDxStages];
-    uint64_t empty[kDxStages];
-    uint64_t tfull[kDxAcc];
-    uint64_t tempty[kDxAcc];
-    uint64_t in[kEpiWarps][kDxSlots];
-    uint32_t tmem_base;
-    int abort;
+template <int STAGES, int SLOTS>
+struct Dx {
+    struct alignas(8) Bars {
+        uint64_t full[STAGES];
+        uint64_t empty[STAGES];
+        uint64_t tfull[kDxAcc];
+        uint64_t tempty[kDxAcc];
+        uint64_t in[kEpiWarps][SLOTS];
+        uint32_t tmem_base;
+        int abort;
+    };
+    static constexpr size_t smem =
+        1024 + (size_t)STAGES * kDxStageBytes + (size_t)kEpiWarps * SLOTS * kDxBlk + sizeof(Bars);
 };
 
-constexpr size_t kDxSmem =
-    1024 + (size_t)kDxStages * kDxStageBytes + (size_t)kEpiWarps * kDxSlots * kDxBlk + sizeof(DxBars);
-
+template <int STAGES, int SLOTS>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant__ CUtensorMap tm_w,
                 const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_out,
@@ -309,15 +318,16 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t *blocks = smem + (size_t)kDxStages * kDxStageBytes;
-    DxBars *bars = reinterpret_cast<DxBars *>(blocks + (size_t)kEpiWarps * kDxSlots * kDxBlk);
+    uint8_t *blocks = smem + (size_t)STAGES * kDxStageBytes;
+    using Bars = typename Dx<STAGES, SLOTS>::Bars;
+    Bars *bars = reinterpret_cast<Bars *>(blocks + (size_t)kEpiWarps * SLOTS * kDxBlk);
     volatile int *abort = &bars->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ntc = (d + 127) / 128, nk = (N + 31) / 32;
     const int total = (int)(((int64_t)T + 127) / 128) * ntc;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kDxStages; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&bars->full[s]), 1);
             mbar_init(smem_u32(&bars->empty[s]), 1);
         }
@@ -326,7 +336,7 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
             mbar_init(smem_u32(&bars->tempty[a]), kEpiWarps);
         }
         for (int w = 0; w < kEpiWarps; ++w)
-            for (int s = 0; s < kDxSlots; ++s) mbar_init(smem_u32(&bars->in[w][s]), 1);
+            for (int s = 0; s < SLOTS; ++s) mbar_init(smem_u32(&bars->in[w][s]), 1);
         bars->abort = 0;
         fence_mbar_init();
     }
@@ -353,13 +363,13 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
                     tma_load_4d(sa, &tm_dl, full, 0, kb * 32, g / ntc * 2, 0);
                     tma_load_4d(sa + 3 * kDxPiece, &tm_w, full, 0, kb * 32, g % ntc * 2, 0);
                     ++issued;
-                    if (++stage == kDxStages) { stage = 0; phase ^= 1; }
+                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
             }
             // the copies in flight land before the CTA leaves
-            for (int i = max(0, issued - kDxStages); i < issued; ++i) {
+            for (int i = max(0, issued - STAGES); i < issued; ++i) {
                 volatile int no_abort = 0;
-                mbar_wait(smem_u32(&bars->full[i % kDxStages]), (uint32_t)(i / kDxStages & 1), status,
+                mbar_wait(smem_u32(&bars->full[i % STAGES]), (uint32_t)(i / STAGES & 1), status,
                           &no_abort);
             }
         }
@@ -395,7 +405,7 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
                                 first = false;
                             }
                     tc_commit(smem_u32(&bars->empty[stage]));
-                    if (++stage == kDxStages) { stage = 0; phase ^= 1; }
+                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
                 if (!ok) break;
                 tc_commit(smem_u32(&bars->tfull[acc]));
@@ -404,10 +414,10 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
         }
     } else {
         const int quad = warp & 3, half = (warp - 2) >> 2;
-        uint8_t *mine = blocks + (size_t)(warp - 2) * kDxSlots * kDxBlk;
+        uint8_t *mine = blocks + (size_t)(warp - 2) * SLOTS * kDxBlk;
         uint64_t *in = bars->in[warp - 2];
         // This warp's blocks: two per tile, those that start inside dx.  The
-        // load cursor runs kDxAhead blocks ahead of the one being added.
+        // load cursor runs SLOTS - 1 blocks ahead of the one being added.
         auto block_at = [&](int g, int u, int &row, int &col) {
             row = g / ntc * 128 + quad * 32;
             col = g % ntc * 128 + half * 64 + u * 32;
@@ -420,7 +430,7 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
                 const bool valid = block_at(lg, lu, row, col);
                 if (++lu == 2) { lu = 0; lg += gridDim.x; }
                 if (!valid) continue;
-                const int s = loaded++ % kDxSlots;
+                const int s = loaded++ % SLOTS;
                 const uint32_t bar = smem_u32(&in[s]);
                 mbar_arrive_expect_tx(bar, kDxBlk);
                 tma_load_2d(smem_u32(mine + s * kDxBlk), &tm_in, bar, col, row);
@@ -428,7 +438,7 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
             }
         };
         if (has_in && lane == 0)
-            for (int i = 0; i < kDxAhead; ++i) load_next();
+            for (int i = 0; i < SLOTS - 1; ++i) load_next();
         __syncwarp();
         add_partials(sums, blockIdx.x, gridDim.x, threadIdx.x - 64);
         int acc = 0;
@@ -450,15 +460,15 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
                 reg_fence(r0);
                 reg_fence(r1);
                 if (!valid) continue;
-                const int s = used % kDxSlots;
+                const int s = used % SLOTS;
                 uint8_t *blk = mine + s * kDxBlk;
                 if (has_in) {
-                    if (!mbar_wait(smem_u32(&in[s]), (uint32_t)(used / kDxSlots & 1), status, abort)) {
+                    if (!mbar_wait(smem_u32(&in[s]), (uint32_t)(used / SLOTS & 1), status, abort)) {
                         ok = false;
                         break;
                     }
                 } else {
-                    if (lane == 0) bulk_wait_read<kDxSlots - 1>();
+                    if (lane == 0) bulk_wait_read<SLOTS - 1>();
                     __syncwarp();
                 }
                 ++used;
@@ -494,7 +504,7 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
         if (lane == 0) {
             for (; used < loaded; ++used) {  // after an abort: loads still in flight
                 volatile int no_abort = 0;
-                mbar_wait(smem_u32(&in[used % kDxSlots]), (uint32_t)(used / kDxSlots & 1), status,
+                mbar_wait(smem_u32(&in[used % SLOTS]), (uint32_t)(used / SLOTS & 1), status,
                           &no_abort);
             }
             bulk_wait<0>();  // stores complete before the CTA ends
@@ -717,6 +727,14 @@ Plan plan_of(const moe_shape *s) {
     return p;
 }
 
+template <int STAGES, int SLOTS>
+bool dx_attr() {
+    static PerDeviceOnce smem_attr;
+    return device_once(smem_attr, [] {
+        return set_smem_limit(router_dense_dx<STAGES, SLOTS>, Dx<STAGES, SLOTS>::smem);
+    });
+}
+
 template <int NT>
 moe_status launch_dw(const CUtensorMap &mx, const CUtensorMap &mdl, const moe_shape *s, int splits,
                      float *part, int *status, cudaStream_t stream) {
@@ -763,14 +781,13 @@ MOE_API moe_status moe_router_dense_backward(const moe_shape *s, const moe_bf16 
     float *db = reinterpret_cast<float *>(base + pl.db);
     float *part = reinterpret_cast<float *>(base + pl.part);
     // whatever can fail comes before the first launch
+    const bool one = N <= 32;  // one k-block of dx
     CUtensorMap mx, mdl_k, mdl, mw, min_, mout;
     if (T > 0 && dw_router &&
         (!make_map(&mx, x, d, T, 64) || !make_map_pieces_k(&mdl_k, dlp, pl.Tp, N, pl.nt)))
         return MOE_ERR_CUDA;
     if (T > 0 && dx) {
-        static PerDeviceOnce smem_attr;
-        if (!device_once(smem_attr, [] { return set_smem_limit(router_dense_dx, kDxSmem); }) ||
-            !make_map_pieces_mn(&mdl, dlp, pl.Tp, N, 32) || !make_map_pieces_mn(&mw, wp, pl.dp, N, 32) ||
+        if (!(one ? dx_attr<1, 4>() : dx_attr<2, 3>()) || !make_map_pieces_mn(&mdl, dlp, pl.Tp, N, 32) || !make_map_pieces_mn(&mw, wp, pl.dp, N, 32) ||
             !make_map_f32(&min_, dx_in ? dx_in : dx, d, T) || !make_map_f32(&mout, dx, d, T))
             return MOE_ERR_CUDA;
     }
@@ -794,8 +811,10 @@ MOE_API moe_status moe_router_dense_backward(const moe_shape *s, const moe_bf16 
     sums.dbias = dbias;
     if (dx && T > 0) {
         const int64_t tiles = ((int64_t)T + 127) / 128 * ((d + 127) / 128);
-        launch_pdl(router_dense_dx, (unsigned)std::min<int64_t>(tiles, num_sms()), kGemmThreads, kDxSmem,
-                   stream, mdl, mw, min_, mout, T, N, d, dx_in ? 1 : 0, sums, status);
+        launch_pdl(one ? router_dense_dx<1, 4> : router_dense_dx<2, 3>,
+                   (unsigned)std::min<int64_t>(tiles, num_sms()), kGemmThreads,
+                   one ? Dx<1, 4>::smem : Dx<2, 3>::smem, stream, mdl, mw, min_, mout, T, N, d,
+                   dx_in ? 1 : 0, sums, status);
     } else if (dw_router || dbias) {
         const int64_t want = std::max<int64_t>((sums.n4 + 255) / 256, dbias ? (N + 7) / 8 : 0);
         launch_pdl(router_dense_sum, (unsigned)std::min<int64_t>(want, 4 * kSms), 256, 0, stream, sums);
