@@ -21,6 +21,7 @@
 // warps while its first tile is loaded and multiplied (a launch of its own took
 // 5 us), or by router_dense_sum when dx is not wanted.
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/moe_block.h"
 #include "moe_common.cuh"
@@ -64,19 +65,20 @@ constexpr int kPrepExp = 32;  // experts of a transposed block
 
 // blockIdx.y < chunks: dl's pieces dlp[3][N][Tp] of 32 experts, the token
 // blocks of 64 strided over blockIdx.x, and those tokens' sums in
-// db_part[blockIdx.x][N].  blockIdx.y == chunks: W's pieces wp[3][N][dp].
+// db_part[blockIdx.x][N].  The CTAs from there on: W's pieces wp[3][N][dp].
 // Columns from T to Tp and from d to dp are zeros.
 __global__ void __launch_bounds__(kPrepThreads)
-router_dense_prep(int T, int64_t Tp, int N, int d, int dp, int chunks, const float *__restrict__ dl,
-                  const float *__restrict__ w, uint16_t *__restrict__ dlp,
+router_dense_prep(int T, int64_t Tp, int N, int d, int dp, int chunks,
+                  const float *__restrict__ dl, const float *__restrict__ w, uint16_t *__restrict__ dlp,
                   uint16_t *__restrict__ wp, float *__restrict__ db_part) {
     pdl_enter();
     __shared__ float tile[kPrepTok][kPrepExp + 1];
-    if ((int)blockIdx.y == chunks) {
+    if ((int)blockIdx.y >= chunks) {
+        const int64_t cta = (int64_t)(blockIdx.y - chunks) * gridDim.x + blockIdx.x;
+        const int64_t ctas = (int64_t)(gridDim.y - chunks) * gridDim.x;
         const int per = dp / 8;
         const int64_t n = (int64_t)N * per, plane = (int64_t)N * dp;
-        for (int64_t i = (int64_t)blockIdx.x * kPrepThreads + threadIdx.x; i < n;
-             i += (int64_t)gridDim.x * kPrepThreads) {
+        for (int64_t i = cta * kPrepThreads + threadIdx.x; i < n; i += ctas * kPrepThreads) {
             const int64_t e = i / per;
             const int c = (int)(i % per) * 8;
             float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -391,19 +393,23 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + (size_t)stage * kDxStageBytes);
                     const uint32_t sb = sa + 3 * kDxPiece;
-                    const int steps = min(2, (N - kb * 32 + 15) / 16);
-                    bool first = kb == 0;
+                    const uint64_t da = mnmajor_desc(sa, 4096), db = mnmajor_desc(sb, 4096);
                     // the smallest piece products first
+                    auto products = [&](auto steps) {
 #pragma unroll
-                    for (int sum = 2; sum >= 0; --sum)
+                        for (int sum = 2; sum >= 0; --sum)
 #pragma unroll
-                        for (int pa = 0; pa <= sum; ++pa)
-                            for (int kk = 0; kk < steps; ++kk) {
-                                tc_mma_bf16(d_tmem, mnmajor_desc(sa + pa * kDxPiece + kk * 2048, 4096),
-                                            mnmajor_desc(sb + (sum - pa) * kDxPiece + kk * 2048, 4096),
-                                            idesc, first ? 0u : 1u);
-                                first = false;
-                            }
+                            for (int pa = 0; pa <= sum; ++pa)
+#pragma unroll
+                                for (int kk = 0; kk < decltype(steps)::value; ++kk)
+                                    tc_mma_bf16(d_tmem, da + ((pa * kDxPiece + kk * 2048) >> 4),
+                                                db + (((sum - pa) * kDxPiece + kk * 2048) >> 4), idesc,
+                                                sum < 2 || pa > 0 || kk > 0 || kb > 0);
+                    };
+                    if (N - kb * 32 > 16)
+                        products(std::integral_constant<int, 2>());
+                    else
+                        products(std::integral_constant<int, 1>());
                     tc_commit(smem_u32(&bars->empty[stage]));
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
@@ -631,15 +637,14 @@ router_dense_dw(const __grid_constant__ CUtensorMap tm_x, const __grid_constant_
                     }
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + (size_t)stage * C::stage_bytes);
-                    const uint32_t sb = sa + C::a_bytes;
+                    const uint64_t da = mnmajor_desc(sa, kDwBlk);
+                    const uint64_t db = sw128_kmajor_desc(sa + C::a_bytes);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                         for (int m = 0; m < C::mmas; ++m)
-                            tc_mma_bf16(d_tmem + m * 3 * NT,
-                                        mnmajor_desc(sa + m * 2 * kDwBlk + kk * 2048, kDwBlk),
-                                        sw128_kmajor_desc(sb + kk * 32), idesc,
-                                        kb == kb0 && kk == 0 ? 0u : 1u);
+                            tc_mma_bf16(d_tmem + m * 3 * NT, da + ((m * 2 * kDwBlk + kk * 2048) >> 4),
+                                        db + ((kk * 32) >> 4), idesc, kk > 0 || kb > kb0);
                     tc_commit(smem_u32(&bars->empty[stage]));
                     if (++stage == C::stages) { stage = 0; phase ^= 1; }
                 }
@@ -787,13 +792,18 @@ MOE_API moe_status moe_router_dense_backward(const moe_shape *s, const moe_bf16 
         (!make_map(&mx, x, d, T, 64) || !make_map_pieces_k(&mdl_k, dlp, pl.Tp, N, pl.nt)))
         return MOE_ERR_CUDA;
     if (T > 0 && dx) {
-        if (!(one ? dx_attr<1, 4>() : dx_attr<2, 3>()) || !make_map_pieces_mn(&mdl, dlp, pl.Tp, N, 32) || !make_map_pieces_mn(&mw, wp, pl.dp, N, 32) ||
+        if (!(one ? dx_attr<1, 4>() : dx_attr<2, 3>()) ||
+            !make_map_pieces_mn(&mdl, dlp, pl.Tp, N, 32) || !make_map_pieces_mn(&mw, wp, pl.dp, N, 32) ||
             !make_map_f32(&min_, dx_in ? dx_in : dx, d, T) || !make_map_f32(&mout, dx, d, T))
             return MOE_ERR_CUDA;
     }
     if (T > 0) {
-        launch_pdl(router_dense_prep, dim3(pl.groups, pl.chunks + (dx ? 1 : 0)), kPrepThreads, 0,
-                   stream, T, pl.Tp, N, d, pl.dp, pl.chunks, dlogits, w_router, dlp, wp, db);
+        // W's CTAs: eight columns a thread, or four CTAs an SM
+        const int64_t wctas =
+            std::min<int64_t>(((int64_t)N * pl.dp / 8 + kPrepThreads - 1) / kPrepThreads, 4 * kSms);
+        const int rows = dx ? (int)((wctas + pl.groups - 1) / pl.groups) : 0;
+        launch_pdl(router_dense_prep, dim3(pl.groups, pl.chunks + rows), kPrepThreads, 0, stream, T,
+                   pl.Tp, N, d, pl.dp, pl.chunks, dlogits, w_router, dlp, wp, db);
         if (dw_router) {
             r = pl.nt == 32 ? launch_dw<32>(mx, mdl_k, s, pl.splits, part, status, stream)
                             : launch_dw<64>(mx, mdl_k, s, pl.splits, part, status, stream);
