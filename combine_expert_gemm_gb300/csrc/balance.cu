@@ -273,10 +273,25 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
     }
 }
 
-// One CTA: the CTAs' partial sums and the two losses.  Each thread takes four
-// experts (a 16-byte vector) of every slices-th CTA; the slices are then added
-// pairwise.  The loads of a thread are independent, so this is one or two
-// rounds of L2 latency: an expert per thread took 9 to 12 us here.
+constexpr int kFinishCtas = 8;
+
+// The CTAs' partial sums and the two losses.  Each thread takes four experts (a
+// 16-byte vector) of every slices-th CTA; the slices are then added pairwise.
+// The loads of a thread are independent, so this is one or two rounds of L2
+// latency: an expert per thread took 9 to 12 us here.
+// One cluster of CTAs: what one SM can read in time bounds many experts' sums
+// (588 KB for 152 CTAs of 481 experts), so each CTA adds its share of the rows
+// and the first one adds the others' sums from their shared memory.
+__device__ __forceinline__ float4 peer_f4(const float4 *p, uint32_t rank) {
+    float4 v;
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n"
+                 " ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(smem_u32(p)), "r"(rank)
+                 : "memory");
+    return v;
+}
+
 __global__ void __launch_bounds__(1024)
 balance_finish(int N, int K, int ctas, int slices, const int32_t *__restrict__ part_i,
                const float *__restrict__ part_f, const LossOut out) {
@@ -288,12 +303,13 @@ balance_finish(int N, int K, int ctas, int slices, const int32_t *__restrict__ p
     int *si = reinterpret_cast<int *>(si4);
     const int st = (int)bal_stride(N), vec = st / 4;
     // the last vector's padding holds nothing that is read back
+    const int rank = (int)cluster_rank(), peers = (int)gridDim.x;
     if ((int)threadIdx.x < slices * vec) {
         const int e = threadIdx.x % vec, q = threadIdx.x / vec;
         float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
         int4 c = make_int4(0, 0, 0, 0);
 #pragma unroll 8
-        for (int g = q; g < ctas; g += slices) {
+        for (int g = rank * slices + q; g < ctas; g += peers * slices) {
             const float4 a = reinterpret_cast<const float4 *>(part_f)[g * vec + e];
             const int4 b = reinterpret_cast<const int4 *>(part_i)[g * vec + e];
             p.x += a.x; p.y += a.y; p.z += a.z; p.w += a.w;
@@ -310,6 +326,25 @@ balance_finish(int N, int K, int ctas, int slices, const int32_t *__restrict__ p
             si[j] += si[j + half * st];
         }
         h = half;
+    }
+    if (peers > 1) {
+        cluster_sync_all();
+        if (rank == 0 && (int)threadIdx.x < vec) {
+            float4 p = sf4[threadIdx.x];
+            int4 c = si4[threadIdx.x];
+#pragma unroll
+            for (int r = 1; r < kFinishCtas; ++r) {
+                const float4 a = peer_f4(&sf4[threadIdx.x], r);
+                const float4 b = peer_f4(reinterpret_cast<float4 *>(&si4[threadIdx.x]), r);
+                p.x += a.x; p.y += a.y; p.z += a.z; p.w += a.w;
+                c.x += __float_as_int(b.x); c.y += __float_as_int(b.y);
+                c.z += __float_as_int(b.z); c.w += __float_as_int(b.w);
+            }
+            sf4[threadIdx.x] = p;
+            si4[threadIdx.x] = c;
+        }
+        cluster_sync_all();  // the others' shared memory stays until it is read
+        if (rank != 0) return;
     }
     __syncthreads();
     const int tc = si[N];
@@ -344,11 +379,14 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
     const int tc = token_count[0];
     const float inv = tc > 0 ? 1.f / (float)tc : 0.f;
     const float cb = dlosses[0] * (float)N * inv, cz = 2.f * dlosses[1] * inv;
+    // one division: sixteen a thread were two thirds of the instructions of a
+    // launch with one row a warp
+    const float share = inv / (float)K;
     float f[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int e = R::first(sub) + R::step(i);
-        f[i] = e < N ? (float)count[e] * inv / (float)K : 0.f;
+        f[i] = e < N ? (float)count[e] * share : 0.f;
     }
     for (int64_t w0 = (int64_t)blockIdx.x * kGroups + warp * (32 / LANES); w0 < T;
          w0 += (int64_t)gridDim.x * kGroups) {
@@ -424,7 +462,7 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
                 float r = 0.f;
                 if (on) {
                     const float p = ex2((logits[t * N + at] - l) * kLog2e);
-                    r = p * fmaf(cb, (float)count[at] * inv / (float)K, c);
+                    r = p * fmaf(cb, (float)count[at] * share, c);
                 }
                 dlogits[t * N + at] = r + g;
             }
@@ -438,7 +476,9 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
 // serves several rows an instruction, as long as the registers leave enough
 // warps: the forward at T = 131072, N = 250 takes 39 us with 8 lanes, 45 with
 // 16, 44 with 32; the backward, which holds the counts beside the row, 65, 49
-// and 53, and at N = 64 the pair takes 36 with 8 against 39 with 16.
+// and 53; at N = 64 the pair takes 36 with 8 against 39 with 16, at T = 72396,
+// N = 71 the backward's 16 against 32 gain 7 us of 41 with K = 14 and lose 2 of
+// 31 with K = 2.
 template <int L, int V, int W, bool H>
 struct RowOf {
     static constexpr int lanes = L, vpt = V, vec = W;
@@ -454,7 +494,7 @@ inline void with_row(int N, Fn &&fn) {
         constexpr int kVec = decltype(w)::value;
         if (N <= 32) fn(RowOf<8, 4, kVec, false>());
         else if (N <= 64) fn(RowOf<8, 8, kVec, true>());
-        else if (N <= 128) fn(RowOf<FWD ? 8 : 32, FWD ? 16 : 4, kVec, true>());
+        else if (N <= 128) fn(RowOf<FWD ? 8 : 16, FWD ? 16 : 8, kVec, true>());
         else if (N <= 256) fn(RowOf<FWD ? 8 : 16, FWD ? 32 : 16, kVec, true>());
         else if (N <= 512) fn(RowOf<FWD ? 16 : 32, FWD ? 32 : 16, kVec, true>());
         else fn(RowOf<32, 32, kVec, true>());
@@ -509,10 +549,29 @@ MOE_API moe_status moe_balance_loss(const moe_shape *s, const float *logits,
                    sizeof(float) * (kBalSlots + 1) * N, stream, s->T, N, s->K, logits, topk_idx,
                    token_mask, lse, part_i, part_f, out);
     });
-    if (ctas > 1)
-        launch_pdl(balance_finish, 1, 1024, 0, stream, N, s->K, ctas,
-                   std::min(ctas, 1024 / (int)(bal_stride(N) / 4)),
-                   static_cast<const int32_t *>(part_i), static_cast<const float *>(part_f), out);
+    if (ctas > 1) {
+        // one CTA up to 128 KB of sums: 152 x 71 experts took 31.5 us with eight and
+        // 30.7 with one, 152 x 128 the same, 152 x 250 85.7 and 88.3, 152 x 1000 85
+        // and 99 (both calls)
+        const unsigned peers = ctas * bal_stride(N) > 16384 ? kFinishCtas : 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(peers);
+        cfg.blockDim = dim3(1024);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        set_pdl_attr(attr[0]);
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = peers;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        if (cudaLaunchKernelEx(&cfg, balance_finish, N, s->K, ctas,
+                               std::min(ctas, 1024 / (int)(bal_stride(N) / 4)),
+                               static_cast<const int32_t *>(part_i), static_cast<const float *>(part_f),
+                               out) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    }
     return launch_status();
 }
 

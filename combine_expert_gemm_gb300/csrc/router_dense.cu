@@ -230,7 +230,7 @@ constexpr int kEpiWarps = 8;
 
 struct Sums {
     int64_t n4;       // N * d / 4; 0: dw is not wanted
-    int splits, N, groups;
+    int splits, lanes, N, groups;
     const float4 *part;
     const float *db_part;
     float4 *dw;
@@ -239,19 +239,33 @@ struct Sums {
 
 // The share of `unit` (of `units`, each of 256 threads) in dw = the sum of the
 // splits, four columns a thread, and dbias = the sum of the prep CTAs, a warp
-// per expert.
+// per expert.  q.lanes (1, 2, 4 or 8) threads of a warp share a sum where there
+// are fewer sums than threads: one thread for the 152 splits of 24 x 128 took
+// 9 us longer than eight.
 __device__ __forceinline__ void add_partials(const Sums &q, int unit, int units, int thread) {
-    for (int64_t i = (int64_t)unit * 256 + thread; i < q.n4; i += (int64_t)units * 256) {
+    const int per = 32 / q.lanes, lane = thread & 31;
+    const int64_t step = (int64_t)units * 8 * per;
+    // all lanes of a warp take the same rounds
+    for (int64_t w = ((int64_t)unit * 8 + (thread >> 5)) * per; w < q.n4; w += step) {
+        const int64_t i = w + lane % per;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < q.n4) {
 #pragma unroll 4
-        for (int s = 0; s < q.splits; ++s) {
-            const float4 p = q.part[s * q.n4 + i];
-            v.x += p.x;
-            v.y += p.y;
-            v.z += p.z;
-            v.w += p.w;
+            for (int s = lane / per; s < q.splits; s += q.lanes) {
+                const float4 p = q.part[s * q.n4 + i];
+                v.x += p.x;
+                v.y += p.y;
+                v.z += p.z;
+                v.w += p.w;
+            }
         }
-        q.dw[i] = v;
+        for (int off = per; off < 32; off <<= 1) {
+            v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, off);
+            v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, off);
+            v.z += __shfl_xor_sync(0xFFFFFFFFu, v.z, off);
+            v.w += __shfl_xor_sync(0xFFFFFFFFu, v.w, off);
+        }
+        if (lane < per && i < q.n4) q.dw[i] = v;
     }
     if (!q.dbias) return;
     for (int e = unit * 8 + (thread >> 5); e < q.N; e += units * 8) {
@@ -819,15 +833,20 @@ MOE_API moe_status moe_router_dense_backward(const moe_shape *s, const moe_bf16 
     sums.db_part = db;
     sums.dw = reinterpret_cast<float4 *>(dw_router);
     sums.dbias = dbias;
+    sums.lanes = 1;  // by the shape alone, so that every call adds in the same order
+    while (sums.lanes < 8 && 2 * sums.lanes <= sums.splits && 2 * sums.lanes * sums.n4 <= kSms * 256)
+        sums.lanes *= 2;
+    const int64_t adds =
+        std::max<int64_t>((sums.n4 * sums.lanes + 255) / 256, dbias ? (N + 7) / 8 : 0);
     if (dx && T > 0) {
+        // CTAs without a tile add partial sums
         const int64_t tiles = ((int64_t)T + 127) / 128 * ((d + 127) / 128);
         launch_pdl(one ? router_dense_dx<1, 4> : router_dense_dx<2, 3>,
-                   (unsigned)std::min<int64_t>(tiles, num_sms()), kGemmThreads,
+                   (unsigned)std::min<int64_t>(std::max(tiles, adds), num_sms()), kGemmThreads,
                    one ? Dx<1, 4>::smem : Dx<2, 3>::smem, stream, mdl, mw, min_, mout, T, N, d,
                    dx_in ? 1 : 0, sums, status);
     } else if (dw_router || dbias) {
-        const int64_t want = std::max<int64_t>((sums.n4 + 255) / 256, dbias ? (N + 7) / 8 : 0);
-        launch_pdl(router_dense_sum, (unsigned)std::min<int64_t>(want, 4 * kSms), 256, 0, stream, sums);
+        launch_pdl(router_dense_sum, (unsigned)std::min<int64_t>(adds, 4 * kSms), 256, 0, stream, sums);
     }
     return launch_status();
 }

@@ -400,6 +400,21 @@ def test_router_dense_backward_left_out_and_in_place(moe):
     assert not dw0.any() and not db0.any()
 
 
+@pytest.mark.parametrize("T,d,N", [(9000, 64, 5), (2500, 128, 24), (85, 328, 381), (40, 4096, 64)])
+def test_router_dense_weight_gradients_do_not_depend_on_dx(moe, T, d, N):
+    """Many partial sums of few weights and few of many, with more and fewer
+    tiles of dx than CTAs that add them: the same bits with and without dx."""
+    g = _gen(T + d + N)
+    n = lambda *q: torch.randn(*q, generator=g).to(DEV)
+    x, w, dl, base = n(T, d).to(BF), n(N, d), n(T, N), n(T, d)
+    s = moe.Shape(T, d, N, 1, 8, 1)
+    _, dw, db = _run_dense(moe, x, w, dl, base)
+    ws = torch.zeros(moe.router_dense_backward_workspace_bytes(s), dtype=torch.uint8, device=DEV)
+    o, ob = torch.full_like(dw, float("nan")), torch.full_like(db, float("nan"))
+    moe.router_dense_backward(s, x, None, dl, None, None, o, ob, ws)
+    assert torch.equal(o, dw) and torch.equal(ob, db)
+
+
 def test_router_dense_backward_non_finite(moe):
     """A broken token's gradient does not reach other tokens' dx; it reaches
     dw_router's rows of its broken logits only where x is finite."""
