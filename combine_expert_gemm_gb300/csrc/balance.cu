@@ -476,9 +476,10 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
 // serves several rows an instruction, as long as the registers leave enough
 // warps: the forward at T = 131072, N = 250 takes 39 us with 8 lanes, 45 with
 // 16, 44 with 32; the backward, which holds the counts beside the row, 65, 49
-// and 53; at N = 64 the pair takes 36 with 8 against 39 with 16, at T = 72396,
-// N = 71 the backward's 16 against 32 gain 7 us of 41 with K = 14 and lose 2 of
-// 31 with K = 2.
+// and 53.  Both calls: N = 64, T = 131072, 36 with 8 against 39 with 16; N = 71,
+// T = 72396 with 16 lanes in the backward against 32, 31.7 against 40.5 with K =
+// 14 and 31.0 against 29.9 with K = 2; N = 481, T = 7886 with 32 lanes in the
+// forward against 16, 18.5 against 19.6.
 template <int L, int V, int W, bool H>
 struct RowOf {
     static constexpr int lanes = L, vpt = V, vec = W;
@@ -496,7 +497,7 @@ inline void with_row(int N, Fn &&fn) {
         else if (N <= 64) fn(RowOf<8, 8, kVec, true>());
         else if (N <= 128) fn(RowOf<FWD ? 8 : 16, FWD ? 16 : 8, kVec, true>());
         else if (N <= 256) fn(RowOf<FWD ? 8 : 16, FWD ? 32 : 16, kVec, true>());
-        else if (N <= 512) fn(RowOf<FWD ? 16 : 32, FWD ? 32 : 16, kVec, true>());
+        else if (N <= 512) fn(RowOf<32, 16, kVec, true>());
         else fn(RowOf<32, 32, kVec, true>());
     };
     if (N % 4 == 0) go(Int<4>());

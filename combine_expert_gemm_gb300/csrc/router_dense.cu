@@ -298,13 +298,14 @@ __global__ void __launch_bounds__(256) router_dense_sum(const Sums q) {
 // block, and 24 or 32 blocks of 4 KB cover the latency of the loads and stores.
 //
 // One k-block a tile (N <= 32) needs one operand stage and leaves room for four
-// slots; more k-blocks take two stages, with three slots.  The whole call, us:
-//                                       <1, 4>   <2, 3>   <2, 4>
-//   T = 32768, d = 4096, N = 32           219      220      231
-//   T = 32768, d = 2048, N = 16           113      117      119
-//   T =  8192, d = 2048, N = 64            50       41       42
-// <2, 4> takes 225 KB; alone it is 4% slower than <1, 4> (169 against 163 us in
-// the first shape), the rest is lost where the launches before and after meet it.
+// slots.  Up to four k-blocks the epilogue's traffic weighs more and takes three
+// slots, beyond them the operands' latency does and takes three stages.  The
+// whole call, us, with STAGES, SLOTS:
+//                                     <1, 4>   <2, 3>   <3, 2>   <2, 4>
+//   T = 32768, d = 4096, N = 32         213      221      266      232
+//   T =  8192, d = 2048, N = 64          45       41       49       41
+//   T = 16384, d = 2048, N = 128        130       96       99       97
+//   T =  4096, d = 4096, N = 256        115       82       76       82
 constexpr int kDxPiece = 2 * 32 * 128;              // 128 columns or tokens x 32 experts: 8 KB
 constexpr int kDxStageBytes = 2 * 3 * kDxPiece;     // 48 KB
 constexpr int kDxBlk = 32 * 32 * 4;
@@ -407,6 +408,9 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + (size_t)stage * kDxStageBytes);
                     const uint32_t sb = sa + 3 * kDxPiece;
+                    // One thread issues twelve MMAs of 64 cycles: with a descriptor
+                    // built anew for each, the issue took longer than the MMAs
+                    // (T = 4096, d = 4096, N = 256: 102 us against 90).
                     const uint64_t da = mnmajor_desc(sa, 4096), db = mnmajor_desc(sb, 4096);
                     // the smallest piece products first
                     auto products = [&](auto steps) {
@@ -800,13 +804,13 @@ MOE_API moe_status moe_router_dense_backward(const moe_shape *s, const moe_bf16 
     float *db = reinterpret_cast<float *>(base + pl.db);
     float *part = reinterpret_cast<float *>(base + pl.part);
     // whatever can fail comes before the first launch
-    const bool one = N <= 32;  // one k-block of dx
+    const int blocks = (N + 31) / 32;  // k-blocks of a tile of dx
     CUtensorMap mx, mdl_k, mdl, mw, min_, mout;
     if (T > 0 && dw_router &&
         (!make_map(&mx, x, d, T, 64) || !make_map_pieces_k(&mdl_k, dlp, pl.Tp, N, pl.nt)))
         return MOE_ERR_CUDA;
     if (T > 0 && dx) {
-        if (!(one ? dx_attr<1, 4>() : dx_attr<2, 3>()) ||
+        if (!(blocks == 1 ? dx_attr<1, 4>() : blocks <= 4 ? dx_attr<2, 3>() : dx_attr<3, 2>()) ||
             !make_map_pieces_mn(&mdl, dlp, pl.Tp, N, 32) || !make_map_pieces_mn(&mw, wp, pl.dp, N, 32) ||
             !make_map_f32(&min_, dx_in ? dx_in : dx, d, T) || !make_map_f32(&mout, dx, d, T))
             return MOE_ERR_CUDA;
@@ -841,10 +845,14 @@ MOE_API moe_status moe_router_dense_backward(const moe_shape *s, const moe_bf16 
     if (dx && T > 0) {
         // CTAs without a tile add partial sums
         const int64_t tiles = ((int64_t)T + 127) / 128 * ((d + 127) / 128);
-        launch_pdl(one ? router_dense_dx<1, 4> : router_dense_dx<2, 3>,
-                   (unsigned)std::min<int64_t>(std::max(tiles, adds), num_sms()), kGemmThreads,
-                   one ? Dx<1, 4>::smem : Dx<2, 3>::smem, stream, mdl, mw, min_, mout, T, N, d,
-                   dx_in ? 1 : 0, sums, status);
+        const unsigned grid = (unsigned)std::min<int64_t>(std::max(tiles, adds), num_sms());
+        auto go = [&](auto *kern, size_t smem) {
+            launch_pdl(kern, grid, kGemmThreads, smem, stream, mdl, mw, min_, mout, T, N, d,
+                       dx_in ? 1 : 0, sums, status);
+        };
+        if (blocks == 1) go(router_dense_dx<1, 4>, Dx<1, 4>::smem);
+        else if (blocks <= 4) go(router_dense_dx<2, 3>, Dx<2, 3>::smem);
+        else go(router_dense_dx<3, 2>, Dx<3, 2>::smem);
     } else if (dw_router || dbias) {
         launch_pdl(router_dense_sum, (unsigned)std::min<int64_t>(adds, 4 * kSms), 256, 0, stream, sums);
     }
