@@ -474,12 +474,13 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
 // that keeps rows aligned, and whether N fills half of it.  Few lanes, because
 // what a kernel does once a row (statistics, counts, sums over the lanes) then
 // serves several rows an instruction, as long as the registers leave enough
-// warps: the forward at T = 131072, N = 250 takes 39 us with 8 lanes, 45 with
-// 16, 44 with 32; the backward, which holds the counts beside the row, 65, 49
-// and 53.  Both calls: N = 64, T = 131072, 36 with 8 against 39 with 16; N = 71,
-// T = 72396 with 16 lanes in the backward against 32, 31.7 against 40.5 with K =
-// 14 and 31.0 against 29.9 with K = 2; N = 481, T = 7886 with 32 lanes in the
-// forward against 16, 18.5 against 19.6.
+// warps.  Both calls, us, with these lanes (forward, backward) and with others:
+//   T = 131072, N = 250, K = 10   (8, 16)   82   (16, 16) 89   (32, 16) 87
+//                                                (8, 8)   87   (8, 32)  92
+//   T = 131072, N = 60,  K = 4    (8, 8)    34   (16, 16) 41
+//   T = 72396,  N = 71,  K = 14   (8, 16)   32   (8, 32)  40
+//   T = 72396,  N = 71,  K = 2    (8, 16)   31   (8, 32)  30
+//   T = 18976,  N = 435, K = 10   (32, 32)  31   (16, 32) 32
 template <int L, int V, int W, bool H>
 struct RowOf {
     static constexpr int lanes = L, vpt = V, vec = W;

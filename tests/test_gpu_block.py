@@ -255,6 +255,23 @@ def test_balance_loss_and_gradient(moe, T, N, K, masked):
     _check_balance(moe, logits, idx, mask, dlogit)
 
 
+@pytest.mark.parametrize("T,N,K", [(300, 1000, 16), (6000, 128, 8), (5000, 301, 4), (7886, 481, 1),
+                                   (4000, 75, 14)])
+def test_balance_many_partial_sums(moe, T, N, K):
+    """Enough CTAs and experts that a cluster adds the partial sums, with fewer
+    and more of them than its threads take at once; every call gives the same
+    bits."""
+    g = _gen(T + N)
+    logits = 2 * torch.randn(T, N, generator=g)
+    idx = torch.topk(logits + torch.randn(T, N, generator=g), K, 1).indices.int()
+    dlogit = torch.randn(T, K, generator=g) / T
+    got = _check_balance(moe, logits, idx, None, dlogit)
+    again = _run_balance(moe, logits.to(DEV), idx.to(DEV), None, N, K, torch.tensor((0.7, 0.3)).to(DEV),
+                         dlogit.to(DEV))
+    for k in got:
+        assert torch.equal(got[k], again[k]), k
+
+
 def test_balance_even_and_collapsed_routers(moe):
     """Even routing gives a loss of 1; a router that sends everything to one
     expert gives N (the extremes of the definition)."""
