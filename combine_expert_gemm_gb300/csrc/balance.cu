@@ -53,8 +53,9 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 // The experts of lane `sub` of a group: register i holds expert
-// first(sub) + step(i), in vectors of VEC logits.  HALF: the row is longer than
-// half the registers, so the vectors of the first half need no bounds check.
+// first(sub) + step(i), in vectors of VEC logits.  HALF: the row fills every
+// vector that starts in the first half of the registers (of 12 registers in
+// vectors of 4, the first 8), and these need no bounds check.
 template <int LANES, int VPT, int VEC, bool HALF>
 struct Row {
     static __device__ __forceinline__ int first(int sub) { return VEC * sub; }
@@ -371,8 +372,8 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
     pdl_enter();
     using R = Row<LANES, VPT, VEC, HALF>;
     // a lane per route is there to write a gate's element unless few lanes hold
-    // the row; for 4 logits a lane comparing is cheaper
-    constexpr bool kCompare = VPT <= 4 || LANES < kMaxK;
+    // the row
+    constexpr bool kCompare = LANES < kMaxK;
     constexpr int kGroups = kBwdThreads / LANES;
     constexpr int kIdx = (kMaxK + LANES - 1) / LANES;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = threadIdx.x % LANES;
@@ -471,16 +472,23 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
 }
 
 // How a row of N logits is held: calls fn with LANES, VPT, the vector length
-// that keeps rows aligned, and whether N fills half of it.  Few lanes, because
+// that keeps rows aligned, and whether N fills half of it (each type's N begins
+// where the type before it ends).  Few lanes, because
 // what a kernel does once a row (statistics, counts, sums over the lanes) then
 // serves several rows an instruction, as long as the registers leave enough
 // warps.  Both calls, us, with these lanes (forward, backward) and with others:
+//   T = 131072, N = 60,  K = 4    (8, 8)    34   (16, 16) 41
+//   T = 72396,  N = 71,  K = 14   (8, 8)    30   (8, 16)  31   (8, 32)  40
+//   T = 131072, N = 96,  K = 8    (8, 8)    41   (8, 16)  49
+//   T = 131072, N = 128, K = 8    (8, 8)    52   (8, 16)  57
+//   T = 65536,  N = 128, K = 16   (8, 8)    36   (8, 16)  35
+//   T = 65536,  N = 160, K = 6    (8, 16)   38   (8, 8)   42
 //   T = 131072, N = 250, K = 10   (8, 16)   82   (16, 16) 89   (32, 16) 87
 //                                                (8, 8)   87   (8, 32)  92
-//   T = 131072, N = 60,  K = 4    (8, 8)    34   (16, 16) 41
-//   T = 72396,  N = 71,  K = 14   (8, 16)   32   (8, 32)  40
-//   T = 72396,  N = 71,  K = 2    (8, 16)   31   (8, 32)  30
+//   T = 61814,  N = 259, K = 14   (32, 32)  57   (32, 16) 61
 //   T = 18976,  N = 435, K = 10   (32, 32)  31   (16, 32) 32
+// Room for 96, 192 and 384 experts beside the powers of two: N = 96 in a row of
+// 128 takes 52 to 56 us, N = 160 in one of 256 41, N = 259 in one of 512 64.
 template <int L, int V, int W, bool H>
 struct RowOf {
     static constexpr int lanes = L, vpt = V, vec = W;
@@ -496,8 +504,11 @@ inline void with_row(int N, Fn &&fn) {
         constexpr int kVec = decltype(w)::value;
         if (N <= 32) fn(RowOf<8, 4, kVec, false>());
         else if (N <= 64) fn(RowOf<8, 8, kVec, true>());
-        else if (N <= 128) fn(RowOf<FWD ? 8 : 16, FWD ? 16 : 8, kVec, true>());
+        else if (N <= 96) fn(RowOf<8, 12, kVec, true>());
+        else if (N <= 128) fn(RowOf<8, 16, kVec, true>());
+        else if (N <= 192) fn(RowOf<FWD ? 8 : 16, FWD ? 24 : 12, kVec, true>());
         else if (N <= 256) fn(RowOf<FWD ? 8 : 16, FWD ? 32 : 16, kVec, true>());
+        else if (N <= 384) fn(RowOf<32, 12, kVec, true>());
         else if (N <= 512) fn(RowOf<32, 16, kVec, true>());
         else fn(RowOf<32, 32, kVec, true>());
     };

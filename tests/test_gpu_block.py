@@ -272,6 +272,21 @@ def test_balance_many_partial_sums(moe, T, N, K):
         assert torch.equal(got[k], again[k]), k
 
 
+@pytest.mark.parametrize("N", [1, 32, 34, 63, 64, 65, 66, 68, 95, 96, 97, 98, 100, 127, 129, 130, 132,
+                               191, 192, 193, 194, 196, 257, 258, 260, 383, 384, 385, 386, 388,
+                               511, 513, 514, 516])
+def test_balance_row_widths(moe, N):
+    """Either side of every width at which a row is held another way, for rows
+    aligned to 4, 8 and 16 bytes; one row in the middle has a forbidden tail."""
+    g = _gen(N)
+    T, K = 67, min(N, 11)
+    logits = 2 * torch.randn(T, N, generator=g)
+    logits[40, N // 2 + 1:] = -float("inf")
+    idx = torch.topk(logits + torch.randn(T, N, generator=g), K, 1).indices.int()
+    _check_balance(moe, logits, idx, None, torch.randn(T, K, generator=g) / T)
+    _check_balance(moe, logits, idx, None, None)
+
+
 def test_balance_even_and_collapsed_routers(moe):
     """Even routing gives a loss of 1; a router that sends everything to one
     expert gives N (the extremes of the definition)."""
