@@ -59,6 +59,25 @@ __device__ __forceinline__ Pieces split3(float v) {
     return r;
 }
 
+// The pieces of a (low half) and b.  Up to the largest bf16 both are split at
+// once and nothing can overflow: one by one, with the checks, router_dense_prep
+// took 2 us longer at 31595 x 272 x 73 (40 us for the whole call) and 0.5 at
+// 8192 x 2048 x 64.
+__device__ __forceinline__ void split3x2(float a, float b, uint32_t (&o)[3]) {
+    if (fabsf(a) <= 0x1.fep127f && fabsf(b) <= 0x1.fep127f) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            o[i] = pack_bf16x2(a, b);
+            a -= __uint_as_float(o[i] << 16);
+            b -= __uint_as_float(o[i] & 0xFFFF0000u);
+        }
+        return;
+    }
+    const Pieces pa = split3(a), pb = split3(b);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) o[i] = (uint32_t)pa.p[i] | ((uint32_t)pb.p[i] << 16);
+}
+
 constexpr int kPrepThreads = 256;
 constexpr int kPrepTok = 64;  // tokens of a transposed block
 constexpr int kPrepExp = 32;  // experts of a transposed block
@@ -91,9 +110,10 @@ router_dense_prep(int T, int64_t Tp, int N, int d, int dp, int chunks,
             uint32_t o[3][4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const Pieces lo = split3(f[2 * q]), hi = split3(f[2 * q + 1]);
+                uint32_t w3[3];
+                split3x2(f[2 * q], f[2 * q + 1], w3);
 #pragma unroll
-                for (int p = 0; p < 3; ++p) o[p][q] = (uint32_t)lo.p[p] | ((uint32_t)hi.p[p] << 16);
+                for (int p = 0; p < 3; ++p) o[p][q] = w3[p];
             }
 #pragma unroll
             for (int p = 0; p < 3; ++p)
@@ -121,11 +141,11 @@ router_dense_prep(int T, int64_t Tp, int N, int d, int dp, int chunks,
             const float a = tile[2 * lane][4 * warp + i], b = tile[2 * lane + 1][4 * warp + i];
             sum[i] += a + b;
             if (e >= N) continue;
-            const Pieces pa = split3(a), pb = split3(b);
+            uint32_t w3[3];
+            split3x2(a, b, w3);
 #pragma unroll
             for (int p = 0; p < 3; ++p)
-                *reinterpret_cast<uint32_t *>(dlp + p * plane + (int64_t)e * Tp + t0 + 2 * lane) =
-                    (uint32_t)pa.p[p] | ((uint32_t)pb.p[p] << 16);
+                *reinterpret_cast<uint32_t *>(dlp + p * plane + (int64_t)e * Tp + t0 + 2 * lane) = w3[p];
         }
         __syncthreads();
     }
