@@ -85,6 +85,24 @@ struct Row {
             }
         }
     }
+    // adds a row in shared memory, aligned as the vectors want it
+    static __device__ __forceinline__ void add(const float *row, int sub, int N, float (&v)[VPT]) {
+        const int e0 = first(sub);
+#pragma unroll
+        for (int i = 0; i < VPT; i += VEC) {
+            if (!in_row(e0, i, N)) continue;
+            const float *p = row + e0 + step(i);
+            if (VEC == 4) {
+                const float4 q = *reinterpret_cast<const float4 *>(p);
+                v[i] += q.x; v[i + 1] += q.y; v[i + 2] += q.z; v[i + 3] += q.w;
+            } else if (VEC == 2) {
+                const float2 q = *reinterpret_cast<const float2 *>(p);
+                v[i] += q.x; v[i + 1] += q.y;
+            } else {
+                v[i] += *p;
+            }
+        }
+    }
     static __device__ __forceinline__ void store(float *row, int sub, int N, const float (&v)[VPT]) {
         const int e0 = first(sub);
 #pragma unroll
@@ -362,6 +380,8 @@ balance_finish(int N, int K, int ctas, int slices, const int32_t *__restrict__ p
 
 constexpr int kBwdThreads = 256;
 
+inline __host__ __device__ int bal_gate_stride(int N) { return (N + 3) / 4 * 4; }
+
 template <int LANES, int VPT, int VEC, bool HALF>
 __global__ void __launch_bounds__(kBwdThreads)
 balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
@@ -371,12 +391,17 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
                  const float *__restrict__ dlogit, float *__restrict__ dlogits) {
     pdl_enter();
     using R = Row<LANES, VPT, VEC, HALF>;
-    // a lane per route is there to write a gate's element unless few lanes hold
-    // the row
-    constexpr bool kCompare = LANES < kMaxK;
     constexpr int kGroups = kBwdThreads / LANES;
     constexpr int kIdx = (kMaxK + LANES - 1) / LANES;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = threadIdx.x % LANES;
+    // this token's gates by expert, zero between rows
+    extern __shared__ float gate_s[];
+    const int stride = bal_gate_stride(N);
+    float *gates = gate_s + threadIdx.x / LANES * stride;
+    if (dlogit) {
+        for (int e = sub; e < stride; e += LANES) gates[e] = 0.f;
+        __syncwarp();
+    }
     const int tc = token_count[0];
     const float inv = tc > 0 ? 1.f / (float)tc : 0.f;
     const float cb = dlosses[0] * (float)N * inv, cz = 2.f * dlosses[1] * inv;
@@ -425,49 +450,43 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
             const float2 g = __fmul2_rn(v2[i], __ffma2_rn(cb2, f2[i], c2));
             v2[i] = on ? g : make_float2(0.f, 0.f);
         }
-        if (!dlogit) {
-            if (in) R::store(dlogits + t * N, sub, N, v);
-        } else if (kCompare) {
-            // short rows: every lane compares its few experts with every route
+        if (dlogit) {
+            // The lane of each route puts its gate where the lane that holds the
+            // expert finds it.  Comparing every expert with every route took 36
+            // us instead of 31 (both calls) at T = 65536, N = 128, K = 16, and a
+            // second write of the routes' elements 82 instead of 75 at T =
+            // 131072, N = 250, K = 10; with K = 1 or 2 comparing would gain 3%.
+            int *tag = reinterpret_cast<int *>(gates);
+            bool is[kIdx], dup = false;
+#pragma unroll
+            for (int j = 0; j < kIdx; ++j) {
+                is[j] = idx[j] >= 0 && idx[j] < N;
+                if (is[j]) tag[idx[j]] = sub + j * LANES;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < kIdx; ++j) dup |= is[j] && tag[idx[j]] != sub + j * LANES;
+            const bool any = __any_sync(0xFFFFFFFFu, dup);
 #pragma unroll
             for (int j = 0; j < kIdx; ++j)
-                for (int k = 0; k < min(LANES, K - j * LANES); ++k) {
-                    const int at = __shfl_sync(0xFFFFFFFFu, idx[j], k, LANES);
-                    const float g = __shfl_sync(0xFFFFFFFFu, gate[j], k, LANES);
-#pragma unroll
-                    for (int i = 0; i < VPT; ++i)
-                        if (at == R::first(sub) + R::step(i)) v[i] += g;
-                }
-            if (in) R::store(dlogits + t * N, sub, N, v);
-        } else {
-            // long rows: the row is stored without the gates, then the lane of
-            // each route writes its expert's element again; K times VPT
-            // comparisons would be most of the kernel
-            if (in) R::store(dlogits + t * N, sub, N, v);
+                if (is[j]) gates[idx[j]] = any ? 0.f : gate[j];
             __syncwarp();
-            const int at = idx[0];
-            const bool is = at >= 0 && at < N;
-            float g = gate[0];
-            // one expert in several routes (moe_route never does this): the first
-            // of them writes, with the gates' sum
-            const int lane0 = lane - sub;  // of this token's lanes
-            const unsigned peers = __match_any_sync(0xFFFFFFFFu, is ? at + lane0 * kMaxN : -1 - lane);
-            if (__any_sync(0xFFFFFFFFu, __popc(peers) > 1)) {
-                g = 0.f;
-                for (int k = 0; k < K; ++k) {
-                    const float gk = __shfl_sync(0xFFFFFFFFu, gate[0], k, LANES);
-                    if (peers >> (lane0 + k) & 1) g += gk;
-                }
+            // one expert in several routes (moe_route never does this): their
+            // gates are added one after the other
+            for (int k = 0; any && k < K; ++k) {
+#pragma unroll
+                for (int j = 0; j < kIdx; ++j)
+                    if (is[j] && sub + j * LANES == k) gates[idx[j]] += gate[j];
+                __syncwarp();
             }
-            if (is && lane == __ffs(peers) - 1) {
-                float r = 0.f;
-                if (on) {
-                    const float p = ex2((logits[t * N + at] - l) * kLog2e);
-                    r = p * fmaf(cb, (float)count[at] * share, c);
-                }
-                dlogits[t * N + at] = r + g;
-            }
+            R::add(gates, sub, N, v);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < kIdx; ++j)
+                if (is[j]) gates[idx[j]] = 0.f;
+            __syncwarp();
         }
+        if (in) R::store(dlogits + t * N, sub, N, v);
     }
 }
 
@@ -477,18 +496,16 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
 // what a kernel does once a row (statistics, counts, sums over the lanes) then
 // serves several rows an instruction, as long as the registers leave enough
 // warps.  Both calls, us, with these lanes (forward, backward) and with others:
-//   T = 131072, N = 60,  K = 4    (8, 8)    34   (16, 16) 41
-//   T = 72396,  N = 71,  K = 14   (8, 8)    30   (8, 16)  31   (8, 32)  40
-//   T = 131072, N = 96,  K = 8    (8, 8)    41   (8, 16)  49
-//   T = 131072, N = 128, K = 8    (8, 8)    52   (8, 16)  57
-//   T = 65536,  N = 128, K = 16   (8, 8)    36   (8, 16)  35
-//   T = 65536,  N = 160, K = 6    (8, 16)   38   (8, 8)   42
-//   T = 131072, N = 250, K = 10   (8, 16)   82   (16, 16) 89   (32, 16) 87
-//                                                (8, 8)   87   (8, 32)  92
-//   T = 61814,  N = 259, K = 14   (32, 32)  57   (32, 16) 61
-//   T = 18976,  N = 435, K = 10   (32, 32)  31   (16, 32) 32
+//   T = 131072, N = 64,  K = 8    (8, 16)  33   (8, 8)   35   (16, 16) 37
+//   T = 131072, N = 96,  K = 8    (8, 8)   40   (8, 16)  43
+//   T = 131072, N = 128, K = 8    (8, 8)   48   (8, 16)  50   (16, 8)  48
+//   T = 65536,  N = 160, K = 6    (8, 16)  36   (8, 8)   40   (8, 32)  41
+//   T = 131072, N = 250, K = 10   (8, 16)  75   (8, 8)   83   (8, 32)  82   (16, 16) 80
+//   T = 61814,  N = 259, K = 14   (32, 32) 52   (32, 16) 54   (16, 32) 52
+//   T = 7886,   N = 481, K = 1    (32, 32) 18   (32, 16) 21   (16, 32) 19
+//   T = 30000,  N = 512, K = 8    (32, 32) 46   (32, 16) 53   (16, 32) 44
 // Room for 96, 192 and 384 experts beside the powers of two: N = 96 in a row of
-// 128 takes 52 to 56 us, N = 160 in one of 256 41, N = 259 in one of 512 64.
+// 128 takes 44 us, N = 160 in one of 256 39, N = 259 in one of 512 59.
 template <int L, int V, int W, bool H>
 struct RowOf {
     static constexpr int lanes = L, vpt = V, vec = W;
@@ -503,7 +520,7 @@ inline void with_row(int N, Fn &&fn) {
     auto go = [&](auto w) {
         constexpr int kVec = decltype(w)::value;
         if (N <= 32) fn(RowOf<8, 4, kVec, false>());
-        else if (N <= 64) fn(RowOf<8, 8, kVec, true>());
+        else if (N <= 64) fn(RowOf<FWD ? 8 : 16, FWD ? 8 : 4, kVec, true>());
         else if (N <= 96) fn(RowOf<8, 12, kVec, true>());
         else if (N <= 128) fn(RowOf<8, 16, kVec, true>());
         else if (N <= 192) fn(RowOf<FWD ? 8 : 16, FWD ? 24 : 12, kVec, true>());
@@ -608,7 +625,8 @@ MOE_API moe_status moe_balance_loss_backward(const moe_shape *s, const float *lo
         using Q = decltype(q);
         const int64_t want = ceil_div(s->T, kBwdThreads / Q::lanes);
         launch_pdl(balance_bwd_rows<Q::lanes, Q::vpt, Q::vec, Q::half>,
-                   (unsigned)std::min<int64_t>(want, (int64_t)num_sms() * 8), kBwdThreads, 0, stream,
+                   (unsigned)std::min<int64_t>(want, (int64_t)num_sms() * 8), kBwdThreads,
+                   dlogit ? sizeof(float) * (kBwdThreads / Q::lanes) * bal_gate_stride(s->N) : 0, stream,
                    s->T, s->N, s->K, logits, topk_idx, token_mask, expert_count, token_count, lse,
                    dlosses, dlogit, dlogits);
     });
