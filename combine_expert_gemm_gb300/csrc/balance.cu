@@ -433,21 +433,34 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
         }
         const float l = on ? lse[t] : 0.f;
         on = on && l != -INFINITY;  // every logit -inf: no probability, no gradient
+        // e_j = exp(v_j - lse) holds the error of a log sum rounded at the row's
+        // size (at 1e9 it equals every logit, and each e_j is 1), so it is only a
+        // shifted exponential: p_j = e_j / sum e.  lse is at most half an ulp off, 4
+        // where an ulp is 8, and equals the largest logit where it is more: the
+        // largest e_j is between e^-4 / N and e^4.
         const float2 mul = make_float2(kLog2e, kLog2e), off = make_float2(-l, -l);
-        float2 dot2 = make_float2(0.f, 0.f);
+        float2 dot2 = make_float2(0.f, 0.f), sum2 = make_float2(0.f, 0.f);
         float2 *v2 = reinterpret_cast<float2 *>(v), *f2 = reinterpret_cast<float2 *>(f);
 #pragma unroll
         for (int i = 0; i < VPT / 2; ++i) {
             const float2 a = __fmul2_rn(__fadd2_rn(v2[i], off), mul);
             v2[i] = make_float2(ex2(a.x), ex2(a.y));
+            sum2 = __fadd2_rn(sum2, v2[i]);
             dot2 = __ffma2_rn(v2[i], f2[i], dot2);
         }
-        const float dot = group_sum<LANES>(dot2.x + dot2.y);
-        const float c = fmaf(-cb, dot, cz * l);
-        const float2 c2 = make_float2(c, c), cb2 = make_float2(cb, cb);
+        float sum = sum2.x + sum2.y, dot = dot2.x + dot2.y;
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) {
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+        }
+        // p_j (cb (f_j - sum_e p_e f_e) + cz lse), the two divisions in the factors
+        const float scale = __frcp_rn(sum);
+        const float cs = cb * scale, c = fmaf(-cb, dot * scale, cz * l) * scale;
+        const float2 c2 = make_float2(c, c), cs2 = make_float2(cs, cs);
 #pragma unroll
         for (int i = 0; i < VPT / 2; ++i) {
-            const float2 g = __fmul2_rn(v2[i], __ffma2_rn(cb2, f2[i], c2));
+            const float2 g = __fmul2_rn(v2[i], __ffma2_rn(cs2, f2[i], c2));
             v2[i] = on ? g : make_float2(0.f, 0.f);
         }
         if (dlogit) {
@@ -496,7 +509,8 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
 // what a kernel does once a row (statistics, counts, sums over the lanes) then
 // serves several rows an instruction, as long as the registers leave enough
 // warps.  Both calls, us, with these lanes (forward, backward) and with others:
-//   T = 131072, N = 64,  K = 8    (8, 16)  33   (8, 8)   35   (16, 16) 37
+//   T = 131072, N = 64,  K = 8    (8, 8)   34   (8, 16)  37
+//   T = 131072, N = 33,  K = 4    (8, 8)   28   (8, 16)  30
 //   T = 131072, N = 96,  K = 8    (8, 8)   40   (8, 16)  43
 //   T = 131072, N = 128, K = 8    (8, 8)   48   (8, 16)  50   (16, 8)  48
 //   T = 65536,  N = 160, K = 6    (8, 16)  36   (8, 8)   40   (8, 32)  41
@@ -520,7 +534,7 @@ inline void with_row(int N, Fn &&fn) {
     auto go = [&](auto w) {
         constexpr int kVec = decltype(w)::value;
         if (N <= 32) fn(RowOf<8, 4, kVec, false>());
-        else if (N <= 64) fn(RowOf<FWD ? 8 : 16, FWD ? 8 : 4, kVec, true>());
+        else if (N <= 64) fn(RowOf<8, 8, kVec, true>());
         else if (N <= 96) fn(RowOf<8, 12, kVec, true>());
         else if (N <= 128) fn(RowOf<8, 16, kVec, true>());
         else if (N <= 192) fn(RowOf<FWD ? 8 : 16, FWD ? 24 : 12, kVec, true>());
