@@ -156,7 +156,7 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = threadIdx.x % LANES;
     for (int i = threadIdx.x; i < (kBalSlots + 1) * N; i += kThreads) sm[i] = 0.f;
     __syncthreads();
-    float acc[VPT];
+    alignas(float2) float acc[VPT];  // read in pairs, should it ever leave the registers
     float2 *acc2 = reinterpret_cast<float2 *>(acc);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) acc[i] = 0.f;
@@ -190,7 +190,7 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
         const int64_t t = w0 + lane / LANES;
         const bool in = t < T;
         const bool on = ahead_on;
-        float v[VPT];
+        alignas(float2) float v[VPT];
         int mine[kIdx];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) v[i] = ahead[i];
@@ -408,7 +408,7 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
     // one division: sixteen a thread were two thirds of the instructions of a
     // launch with one row a warp
     const float share = inv / (float)K;
-    float f[VPT];
+    alignas(float2) float f[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int e = R::first(sub) + R::step(i);
@@ -419,7 +419,7 @@ balance_bwd_rows(int T, int N, int K, const float *__restrict__ logits,
         const int64_t t = w0 + lane / LANES;
         const bool in = t < T;
         bool on = in && !(mask && mask[t] == 0);
-        float v[VPT];
+        alignas(float2) float v[VPT];
         R::load(logits + t * N, sub, N, on, v);
         // lane `sub` holds the token's routes sub, sub + LANES, ...
         int idx[kIdx];

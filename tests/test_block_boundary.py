@@ -275,3 +275,18 @@ def test_mxint8_error_bound():
     step = torch.exp2(s.double() - 133).repeat_interleave(32, 1)
     err = (ref.mxint8_value(q, s) - v.double()).abs()
     assert torch.all(err <= step * torch.where(q.abs() == 127, 1.0, 0.5))
+
+
+def test_local_arrays_read_as_pairs_are_aligned_for_them():
+    """A float array of a kernel that is read as float2 has float2's alignment:
+    without it the access is misaligned if the array ever lands in memory."""
+    import os
+    import re
+    src = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       "combine_expert_gemm_gb300", "csrc", "balance.cu")
+    text = open(src).read()
+    names = set(re.findall(r"reinterpret_cast<float2 \*>\((\w+)\)", text)) - {"p"}   # p: global rows
+    assert names == {"acc", "v", "f"}
+    for n in names:
+        decl = re.findall(r"^ *(.*float %s\[VPT\];)" % n, text, re.M)
+        assert decl and all(d.startswith("alignas(float2)") for d in decl), n
