@@ -21,7 +21,6 @@
 // warps while its first tile is loaded and multiplied (a launch of its own took
 // 5 us), or by router_dense_sum when dx is not wanted.
 #include <algorithm>
-#include <type_traits>
 
 #include "../../include/moe_block.h"
 #include "moe_common.cuh"
@@ -307,9 +306,29 @@ __global__ void __launch_bounds__(256) router_dense_sum(const Sums q) {
 //
 // Persistent CTAs, tiles of 128 tokens x 128 columns, columns fastest.  A
 // k-block is 32 experts: the three pieces of dl (24 KB) and of W (24 KB), both
-// MN-major, by one TMA request each.  The accumulator of a tile takes 128 of
-// the 512 tensor-memory columns, so four tiles are in flight between the MMA
-// thread and the epilogue.
+// MN-major, by one TMA request each.  An accumulator takes 128 of the 512
+// tensor-memory columns, so four are in flight between the MMA thread and the
+// epilogue.
+//
+// The tensor core cuts where an fp32 addition rounds, always towards zero, and
+// each of the twelve MMAs of a k-block does: one accumulator for a whole tile
+// was 5, 27 and 115 u (u = 2^-24) off in the 2-norm at 64, 256 and 1024
+// experts, where an fp32 sum of the same length is 2.4, 4.8 and 9.6 u off.  A
+// cut costs an ulp of the sum it is added to.  So
+//   up to four k-blocks, each k-block has an accumulator of its own, the
+//   smallest piece products first, and the epilogue adds the k-blocks in fp32
+//   registers: 1.1 u at 64 experts, 1.2 at 128;
+//   beyond them, all of a tile's small piece products (2^-8 of the sum and less)
+//   go to one accumulator and the leading ones of every four k-blocks to
+//   another, which leaves eight k-blocks in flight instead of four and a third
+//   of the reads: 2 to 3 u from 256 to 1024.
+// The whole call, us, with one accumulator a tile, with one a k-block and with
+// the small products apart:
+//   T =  8192, d = 2048, N = 64          40.8     41.5     41.9
+//   T = 16384, d = 2048, N = 128         95       96       96.5
+//   T =  9998, d = 2768, N = 152         96      103       95.5
+//   T =  4096, d = 4096, N = 256         75       86       78
+//   T =  4096, d = 2048, N = 512         78.5     87       81
 //
 // The epilogue's work is the traffic: each warp owns 32 tokens x 64 columns of
 // a tile and SLOTS blocks of 4 KB in shared memory, through which it streams
@@ -320,7 +339,7 @@ __global__ void __launch_bounds__(256) router_dense_sum(const Sums q) {
 // One k-block a tile (N <= 32) needs one operand stage and leaves room for four
 // slots.  Up to four k-blocks the epilogue's traffic weighs more and takes three
 // slots, beyond them the operands' latency does and takes three stages.  The
-// whole call, us, with STAGES, SLOTS:
+// whole call, us, with STAGES, SLOTS, while a tile had one accumulator:
 //                                     <1, 4>   <2, 3>   <3, 2>   <2, 4>
 //   T = 32768, d = 4096, N = 32         213      221      266      232
 //   T =  8192, d = 2048, N = 64          45       41       49       41
@@ -330,9 +349,16 @@ constexpr int kDxPiece = 2 * 32 * 128;              // 128 columns or tokens x 3
 constexpr int kDxStageBytes = 2 * 3 * kDxPiece;     // 48 KB
 constexpr int kDxBlk = 32 * 32 * 4;
 constexpr int kDxAcc = 4;
+constexpr int kDxGroup = 4;  // k-blocks of leading products in an accumulator
 
 template <int STAGES, int SLOTS>
 struct Dx {
+    // accumulators 0 and 1: the small products of two tiles; 2 and 3: the leading
+    // ones.  Otherwise all four go from k-block to k-block.
+    static constexpr bool small_apart = STAGES == 3;
+    static constexpr int ring = small_apart ? 2 : kDxAcc;
+    static constexpr int ring0 = small_apart ? 2 : 0;
+    static constexpr int group = small_apart ? kDxGroup : 1;  // k-blocks of an accumulator of the ring
     struct alignas(8) Bars {
         uint64_t full[STAGES];
         uint64_t empty[STAGES];
@@ -356,7 +382,8 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t *blocks = smem + (size_t)STAGES * kDxStageBytes;
-    using Bars = typename Dx<STAGES, SLOTS>::Bars;
+    using C = Dx<STAGES, SLOTS>;
+    using Bars = typename C::Bars;
     Bars *bars = reinterpret_cast<Bars *>(blocks + (size_t)kEpiWarps * SLOTS * kDxBlk);
     volatile int *abort = &bars->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -413,47 +440,59 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
     } else if (warp == 1) {
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_major(128, 128, 1, 1);
-            int stage = 0, acc = 0;
+            // One k-block's piece products, the smallest first.  One thread issues
+            // twelve MMAs of 64 cycles: with a descriptor built anew for each, the
+            // issue took longer than the MMAs (T = 4096, d = 4096, N = 256: 102 us
+            // against 90).  `two`: more than 16 experts; fresh: the accumulator's
+            // first products.
+            auto products = [&](uint32_t small, bool fresh_small, uint32_t lead, bool fresh_lead, int s,
+                                bool two) {
+                const uint32_t sa = smem_u32(smem + (size_t)s * kDxStageBytes);
+                const uint64_t da = mnmajor_desc(sa, 4096), db = mnmajor_desc(sa + 3 * kDxPiece, 4096);
+#pragma unroll
+                for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+                    for (int pa = 0; pa <= sum; ++pa)
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk) {
+                            const bool fresh = kk == 0 && ((sum == 2 && pa == 0 && fresh_small) ||
+                                                           (sum == 0 && fresh_lead));
+                            if (kk == 0 || two)
+                                tc_mma_bf16(sum > 0 ? small : lead, da + ((pa * kDxPiece + kk * 2048) >> 4),
+                                            db + (((sum - pa) * kDxPiece + kk * 2048) >> 4), idesc, !fresh);
+                        }
+            };
+            int stage = 0, acc = 0, tile = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            for (int g = blockIdx.x; g < total && ok; g += gridDim.x) {
-                if (!mbar_wait(smem_u32(&bars->tempty[acc]), acc_phase ^ 1, status, abort)) break;
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * 128);
+            for (int g = blockIdx.x; g < total && ok; g += gridDim.x, ++tile) {
+                const int sa = tile & 1;  // this tile's accumulator of small products
+                if (C::small_apart &&
+                    !mbar_wait(smem_u32(&bars->tempty[sa]), (uint32_t)(tile >> 1 & 1) ^ 1, status, abort))
+                    break;
                 for (int kb = 0; kb < nk; ++kb) {
-                    if (!mbar_wait(smem_u32(&bars->full[stage]), phase, status, abort)) {
+                    const int at = C::ring0 + acc, in_group = kb % C::group;
+                    if ((in_group == 0 &&
+                         !mbar_wait(smem_u32(&bars->tempty[at]), acc_phase ^ 1, status, abort)) ||
+                        !mbar_wait(smem_u32(&bars->full[stage]), phase, status, abort)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + (size_t)stage * kDxStageBytes);
-                    const uint32_t sb = sa + 3 * kDxPiece;
-                    // One thread issues twelve MMAs of 64 cycles: with a descriptor
-                    // built anew for each, the issue took longer than the MMAs
-                    // (T = 4096, d = 4096, N = 256: 102 us against 90).
-                    const uint64_t da = mnmajor_desc(sa, 4096), db = mnmajor_desc(sb, 4096);
-                    // the smallest piece products first
-                    auto products = [&](auto steps) {
-#pragma unroll
-                        for (int sum = 2; sum >= 0; --sum)
-#pragma unroll
-                            for (int pa = 0; pa <= sum; ++pa)
-#pragma unroll
-                                for (int kk = 0; kk < decltype(steps)::value; ++kk)
-                                    tc_mma_bf16(d_tmem, da + ((pa * kDxPiece + kk * 2048) >> 4),
-                                                db + (((sum - pa) * kDxPiece + kk * 2048) >> 4), idesc,
-                                                sum < 2 || pa > 0 || kk > 0 || kb > 0);
-                    };
-                    if (N - kb * 32 > 16)
-                        products(std::integral_constant<int, 2>());
+                    const uint32_t lead = tmem_base + (uint32_t)(at * 128);
+                    if (C::small_apart)
+                        products(tmem_base + (uint32_t)(sa * 128), kb == 0, lead, in_group == 0, stage,
+                                 N - kb * 32 > 16);
                     else
-                        products(std::integral_constant<int, 1>());
+                        products(lead, true, lead, false, stage, N - kb * 32 > 16);
                     tc_commit(smem_u32(&bars->empty[stage]));
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                    if (in_group == C::group - 1 || kb == nk - 1) {
+                        tc_commit(smem_u32(&bars->tfull[at]));
+                        if (++acc == C::ring) { acc = 0; acc_phase ^= 1; }
+                    }
                 }
-                if (!ok) break;
-                tc_commit(smem_u32(&bars->tfull[acc]));
-                if (++acc == kDxAcc) { acc = 0; acc_phase ^= 1; }
+                if (C::small_apart && ok) tc_commit(smem_u32(&bars->tfull[sa]));
             }
         }
     } else {
@@ -485,24 +524,62 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
             for (int i = 0; i < SLOTS - 1; ++i) load_next();
         __syncwarp();
         add_partials(sums, blockIdx.x, gridDim.x, threadIdx.x - 64);
-        int acc = 0;
+        const uint32_t tmem = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * 64);
+        auto release = [&](int a) {  // this warp has read accumulator a
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[a]));
+        };
+        // 32 columns of accumulator a
+        auto columns = [&](int a, int c, uint32_t (&r)[2][16]) {
+            tmem_ld16(tmem + (uint32_t)(a * 128 + c), r[0]);
+            tmem_ld16(tmem + (uint32_t)(a * 128 + c + 16), r[1]);
+            tmem_ld_wait();
+            reg_fence(r[0]);
+            reg_fence(r[1]);
+        };
+        auto pair = [](const uint32_t (&r)[2][16], int i) {
+            return make_float2(__uint_as_float(r[i / 8][i % 8 * 2]), __uint_as_float(r[i / 8][i % 8 * 2 + 1]));
+        };
+        int acc = 0, tile = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
-        for (int g = blockIdx.x; g < total && ok; g += gridDim.x) {
-            if (!mbar_wait(smem_u32(&bars->tfull[acc]), acc_phase, status, abort)) break;
+        for (int g = blockIdx.x; g < total && ok; g += gridDim.x, ++tile) {
+            // the sum of all accumulators of this tile but the last, in order
+            float2 v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = make_float2(0.f, 0.f);
+            for (int kb = C::small_apart ? 0 : 1; kb < nk; kb += C::group) {
+                const int a = C::ring0 + acc;
+                if (!mbar_wait(smem_u32(&bars->tfull[a]), acc_phase, status, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    uint32_t r[2][16];
+                    columns(a, c, r);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[c / 2 + i] = __fadd2_rn(v[c / 2 + i], pair(r, i));
+                }
+                release(a);
+                if (++acc == C::ring) { acc = 0; acc_phase ^= 1; }
+            }
+            if (!ok) break;
+            const int last = C::small_apart ? tile & 1 : acc;
+            if (!mbar_wait(smem_u32(&bars->tfull[last]),
+                           C::small_apart ? (uint32_t)(tile >> 1 & 1) : acc_phase, status, abort))
+                break;
+            if (!C::small_apart && ++acc == C::ring) { acc = 0; acc_phase ^= 1; }
             tc_fence_after();
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 int row, col;
                 const bool valid = block_at(g, u, row, col);  // warp-uniform
-                uint32_t r0[16], r1[16];
-                const uint32_t at =
-                    tmem_base + ((uint32_t)(quad * 32) << 16) + acc * 128 + half * 64 + u * 32;
-                tmem_ld16(at, r0);
-                tmem_ld16(at + 16, r1);
-                tmem_ld_wait();
-                reg_fence(r0);
-                reg_fence(r1);
+                uint32_t r[2][16];
+                columns(last, u * 32, r);
+                if (u == 1) release(last);
                 if (!valid) continue;
                 const int s = used % SLOTS;
                 uint8_t *blk = mine + s * kDxBlk;
@@ -518,14 +595,14 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
                 ++used;
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    const uint32_t *a = q < 4 ? &r0[4 * q] : &r1[4 * (q - 4)];
                     float4 *at4 = reinterpret_cast<float4 *>(blk + lane * 128 + ((q ^ (lane & 7)) * 16));
-                    float4 v = has_in ? *at4 : make_float4(0.f, 0.f, 0.f, 0.f);
-                    v.x += __uint_as_float(a[0]);
-                    v.y += __uint_as_float(a[1]);
-                    v.z += __uint_as_float(a[2]);
-                    v.w += __uint_as_float(a[3]);
-                    *at4 = v;
+                    float2 lo = pair(r, 2 * q), hi = pair(r, 2 * q + 1);
+                    if (STAGES > 1) {
+                        lo = __fadd2_rn(v[16 * u + 2 * q], lo);
+                        hi = __fadd2_rn(v[16 * u + 2 * q + 1], hi);
+                    }
+                    const float4 o = has_in ? *at4 : make_float4(0.f, 0.f, 0.f, 0.f);
+                    *at4 = make_float4(o.x + lo.x, o.y + lo.y, o.z + hi.x, o.w + hi.y);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -540,10 +617,6 @@ router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant
                 }
             }
             if (!ok) break;
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc]));
-            if (++acc == kDxAcc) { acc = 0; acc_phase ^= 1; }
         }
         if (lane == 0) {
             for (; used < loaded; ++used) {  // after an abort: loads still in flight

@@ -59,3 +59,67 @@ def test_balance_gradient_does_not_depend_on_a_common_value(moe, N, K, offset):
     mag = p * (0.7 * N / T) * (f + (p @ f)[:, None])
     block._within(got["dlogits"], want, (6 * size + 160) * U * mag + 1e-30, "dlogits")
     block._within(got["expert_prob"], p.mean(0), (3 * size + 160 + T) * U * p.mean(0) + 1e-30, "expert_prob")
+
+
+# ----------------------------------------------------- dense router gradient --
+
+def _chain(a, b):
+    """a @ b as fp32 products are summed: one fused multiply-add after the other."""
+    out = torch.zeros(a.shape[0], b.shape[1], device=a.device)
+    for k in range(a.shape[1]):
+        # the product is exact in 64 bits, the sum is rounded once more there
+        out = (out.double() + a[:, k, None].double() * b[k, None].double()).float()
+    return out
+
+
+def _as_good_as_fp32(got, a, b, what):
+    """Within twice the chain's error and 5 u in the 2-norm.  The second term
+    is for sums so short that the chain hardly rounds: a k-block's partial sum
+    is cut, not rounded, and loses at most one unit in the last place, 2 u, in
+    each of its last two steps, and the pieces hold each operand to u / 2.  The
+    factor covers that the order of the sum is another one."""
+    want = a.double() @ b.double()
+    err = lambda t: ((t.double() - want).norm() / want.norm()).item()
+    mine, chain = err(got), err(_chain(a, b))
+    assert mine <= 2 * chain + 5 * U, f"{what}: {mine:.3g}, an fp32 chain {chain:.3g}"
+
+
+@pytest.mark.parametrize("sign", ["mixed", "same"])
+@pytest.mark.parametrize("T,d,N", [(300, 264, 8), (300, 264, 32), (333, 264, 48), (333, 264, 64), (400, 264, 100),
+                                   (500, 520, 128), (257, 1032, 250), (700, 264, 256), (300, 520, 512),
+                                   (150, 1544, 1000), (200, 264, 1024), (64, 2048, 300), (2100, 136, 64)])
+def test_router_dense_keeps_fp32_accuracy(moe, T, d, N, sign):
+    """Every expert count from one k-block of dx to 32 of them: the error of an
+    fp32 product of the same length, without dx_in to hide it.  Operands of one
+    sign show a sum that drifts, of both signs one that loses pieces."""
+    g = torch.Generator().manual_seed(T + N)
+    n = lambda *s: torch.randn(*s, generator=g)
+    x, w, dl = n(T, d).to(BF).float(), n(N, d), n(T, N)
+    if sign == "same":
+        x, w, dl = x.abs(), w.abs(), dl.abs()
+    x, w, dl = x.to(DEV), w.to(DEV), dl.to(DEV)
+    dx, dw, db = block._run_dense(moe, x.to(BF), w, dl, None)
+    _as_good_as_fp32(dx, dl, w, "dx")
+    _as_good_as_fp32(dw, dl.t().contiguous(), x, "dw_router")
+    _as_good_as_fp32(db[:, None], dl.t().contiguous(), torch.ones(T, 1, device=DEV), "dbias")
+
+
+@pytest.mark.parametrize("N", [8, 40, 200, 600])
+def test_router_dense_products_of_single_entries(moe, N):
+    """One token for each expert and full 24-bit values: each element is one
+    product.  dw_router's is exact but for one cut (2 u); dx's leaves out piece
+    products below 2^-24, 2^-24 and 2^-32 of it and is cut at most four times;
+    dbias is the value itself."""
+    g = torch.Generator().manual_seed(N)
+    d = 72
+    n = lambda *s: torch.randn(*s, generator=g)
+    x = n(N, d).to(BF)
+    for scale_dl, scale_w in ((1.0, 1.0), (1e-30, 1e6), (1e30, 1e-30), (1e-18, 1e18), (1e36, 1e-3)):
+        v, w = n(N) * scale_dl, n(N, d) * scale_w
+        dl = torch.diag(v)
+        dx, dw, db = block._run_dense(moe, x.to(DEV), w.to(DEV), dl.to(DEV), None)
+        assert torch.equal(db.cpu(), v)
+        want = v.double()[:, None] * x.double()
+        block._within(dw, want, 4 * U * want.abs() + 1e-37, f"dw at {scale_dl}")
+        want = v.double()[:, None] * w.double()
+        block._within(dx, want, 12 * U * want.abs() + 1e-37, f"dx at {scale_dl}")
