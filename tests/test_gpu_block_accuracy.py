@@ -123,3 +123,33 @@ def test_router_dense_products_of_single_entries(moe, N):
         block._within(dw, want, 4 * U * want.abs() + 1e-37, f"dw at {scale_dl}")
         want = v.double()[:, None] * w.double()
         block._within(dx, want, 12 * U * want.abs() + 1e-37, f"dx at {scale_dl}")
+
+
+@pytest.mark.parametrize("T,d,N", [(8192, 2048, 64), (9001, 4104, 31), (5000, 3080, 100), (6000, 2568, 200),
+                                   (4097, 1992, 1000), (40000, 264, 5)])
+@pytest.mark.parametrize("with_in", [True, False])
+def test_router_dense_later_rounds(moe, T, d, N, with_in):
+    """Enough tiles and k-blocks that every ring, accumulator and slot of a CTA
+    is used several times over, and every CTA that splits dlogits has more than
+    one block of tokens in the cases that can: dense data, so that a block
+    taken twice, left out or stale would show.  The bounds are those of
+    sums of n terms (2 n u), and the chain's in the 2-norm."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    tiles, k_blocks = -(-T // 128) * -(-d // 128), -(-N // 32)
+    assert tiles >= 6 * sms or tiles * k_blocks >= 48 * sms or T >= 38912   # rounds of dx, or of the split
+    g = torch.Generator(device=DEV).manual_seed(T + N)
+    n = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    x, w, dl = n(T, d).to(BF), 0.02 * n(N, d), n(T, N)
+    dx_in = n(T, d) if with_in else None
+    dx, dw, db = block._run_dense(moe, x, w, dl, dx_in)
+    a, b, c = dl.double(), w.double(), x.double()
+    base = dx_in.double() if with_in else torch.zeros_like(c)
+    for got, want, size, k, what in ((dx, base + a @ b, base.abs() + a.abs() @ b.abs(), N, "dx"),
+                                     (dw, a.t() @ c, a.abs().t() @ c.abs(), T, "dw_router"),
+                                     (db, a.sum(0), a.abs().sum(0), T, "dbias")):
+        off = (got.double() - want).abs() - (2 * k + 64) * U * size
+        assert not (off > 0).any(), what
+    if not with_in:
+        _as_good_as_fp32(dx, dl, w, "dx")
+        rows = slice(0, 5)                     # the chain over T on a few experts
+        _as_good_as_fp32(dw[rows], dl[:, rows].t().contiguous(), x.float(), "dw_router")
