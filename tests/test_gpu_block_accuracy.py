@@ -153,3 +153,20 @@ def test_router_dense_later_rounds(moe, T, d, N, with_in):
         _as_good_as_fp32(dx, dl, w, "dx")
         rows = slice(0, 5)                     # the chain over T on a few experts
         _as_good_as_fp32(dw[rows], dl[:, rows].t().contiguous(), x.float(), "dw_router")
+
+
+# -------------------------------------------------------------- layer norm --
+
+@pytest.mark.parametrize("T,d,xt,yt,gt", [
+    (30001, 64, BF, FP, BF), (26001, 256, FP, BF, FP), (8195, 2048, BF, FP, BF), (3300, 4096, FP, BF, BF),
+    (8000, 1032, FP, FP, FP), (1700, 8192, BF, BF, BF), (1601, 8200, FP, FP, BF), (1700, 16376, BF, FP, FP),
+])
+@pytest.mark.parametrize("kind", ["full", "bare"])
+def test_layer_norm_many_rows_a_group(moe, T, d, xt, yt, gt, kind):
+    """At least ten rows for each group of warps, so that the copies' ring, the
+    alternating buffers of the row sums and the weight gradients' registers are
+    used over and over, with the bounds of the short cases."""
+    warps = -(-d // 512)                       # of a group, at 16 columns a thread
+    groups = max(1, 16 // warps) * torch.cuda.get_device_properties(0).multi_processor_count
+    assert T >= 10 * groups
+    block.test_layer_norm_and_backward(moe, T, d, xt, yt, gt, kind)
