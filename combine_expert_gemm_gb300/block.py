@@ -242,8 +242,9 @@ class BlockState:
         T, d, N, K, h, R = shape.T, shape.d, shape.N, shape.K, shape.h, shape.R
         e = dict(device=device)
         self.shape = shape
-        self.h = None                                  # the rows that were normalised
+        self.h = None                                  # the rows that were normalised: x_sum or x_fp32
         self.x_sum = torch.empty((T, d), dtype=_bf16, **e)
+        self.x_fp32 = None                             # allocated by the first fp32 x
         self.n = torch.empty((T, d), dtype=_bf16, **e)
         self.mean, self.rstd = torch.empty(T, **e), torch.empty(T, **e)
         self.topk_idx = torch.empty((T, K), dtype=_i32, **e)
@@ -259,7 +260,8 @@ class BlockState:
         self.expert_prob = torch.empty(N, **e)
         self.lse = torch.empty(T, **e)
         self.losses = torch.empty(2, **e)              # balance loss, z loss
-        self.token_mask = None
+        self.token_mask = None                         # mask, or None if every token counts
+        self.mask = torch.empty(T, dtype=_u8, **e)
         self.g_q, self.u_q = (torch.empty((R, h), dtype=_i8, **e) for _ in range(2))
         self.g_scale, self.u_scale = (torch.empty((R, h // 32), dtype=_u8, **e) for _ in range(2))
         self.y_q = torch.empty((R, d), dtype=_i8, **e)
@@ -284,22 +286,41 @@ class BlockScratch:
         self.dense_ws = w(router_dense_backward_workspace_bytes(shape))
 
 
+def _keep(dst, src, stream):
+    """Copies src into the state's dst on the calls' stream."""
+    if stream is None:
+        dst.copy_(src)
+    else:
+        with torch.cuda.stream(stream):
+            dst.copy_(src)
+
+
 def block_forward(st, sc, x, add, gamma, beta, w_router, bias, w_gate, w_up, w_down, eps=1e-5,
                   token_mask=None, stream=None):
     """One pre-norm block: h = x + add (add: the previous block's output, or None),
     n = layer norm of h, and the routed-expert layer of n; its output is returned
     (sc.fwd.y, which the next block takes as add).  st keeps what block_backward needs,
     the experts' buffers in 8 bits, and st.losses the balance and z loss over the tokens
-    that token_mask [T] uint8 (or None: all) counts."""
+    that token_mask [T] uint8 (or None: all) counts.  x, add and token_mask are copied
+    where the backward needs them and may be overwritten once these calls have run."""
     s, f = st.shape, sc.fwd
-    st.h = x if add is None else st.x_sum
-    st.token_mask = token_mask
     layer_norm(x, add, gamma, beta, eps, None if add is None else st.x_sum, st.n, st.mean, st.rstd,
                stream)
+    st.h = st.x_sum
+    if add is None:
+        if x.dtype is _f32:
+            if st.x_fp32 is None:
+                st.x_fp32 = torch.empty_like(x)
+            st.h = st.x_fp32
+        _keep(st.h, x, stream)
     route(s, st.n, w_router, bias, st.topk_idx, st.topk_gate, st.route_row, st.expert_count,
           st.expert_offset, st.expert_demand, st.route_ws, stream)
     balance_loss(s, route_logits(s, st.route_ws), st.topk_idx, token_mask, st.routed_count,
                  st.token_count, st.expert_prob, st.lse, st.losses, sc.balance_ws, stream)
+    st.token_mask = None
+    if token_mask is not None:
+        _keep(st.mask, token_mask.view(-1)[:s.T], stream)
+        st.token_mask = st.mask
     dispatch(s, st.n, st.route_row, f.x_disp, stream)
     expert_ffn(s, f.x_disp, st.expert_count, st.expert_offset, w_gate, w_up, w_down, f.h_act,
                f.g_save, f.u_save, f.y_disp, f.ffn_ws, stream)

@@ -125,3 +125,37 @@ def test_train_example_learns_and_balances(moe):
     st = blocks[0].state
     held = sum(t.numel() for t in (st.g_q, st.g_scale, st.u_q, st.u_scale, st.y_q, st.y_scale))
     assert held * 3 < bf16
+
+
+@pytest.mark.parametrize("xt", [BF, torch.float32])
+@pytest.mark.parametrize("side", [False, True])
+def test_caller_may_reuse_its_input_and_mask_after_the_forward(moe, xt, side):
+    """What the backward needs of the first block's input and of the mask is
+    the state's own: a caller who fills the same buffers with the next batch
+    before the backward gets the same gradients, bit for bit."""
+    T, d, N, K, h = 200, 128, 8, 2, 64
+    s = moe.Shape(T, d, N, K, h, 80)
+    g = torch.Generator().manual_seed(9)
+    r = lambda *q, std=1.0: (torch.randn(*q, generator=g) * std).to(DEV)
+    p = [1 + r(d, std=0.1), r(d, std=0.1), r(N, d, std=0.1), r(N, std=0.2)]
+    p += [r(N, h, d, std=0.1).to(BF), r(N, h, d, std=0.1).to(BF), r(N, d, h, std=0.1).to(BF)]
+    x, dh, dlosses = r(T, d).to(xt), r(T, d).to(BF), torch.tensor([40.0, 5.0], device=DEV)
+    mask = (torch.rand(T, generator=g) < 0.7).to(torch.uint8).to(DEV)
+    stream = torch.cuda.Stream() if side else None
+    runs = []
+    for reuse in (False, True):
+        st, sc = moe.BlockState(s, DEV), moe.BlockScratch(s, DEV)
+        xin, m, dx = x.clone(), mask.clone(), torch.empty(T, d, dtype=BF, device=DEV)
+        torch.cuda.synchronize()
+        moe.block_forward(st, sc, xin, None, *p, token_mask=m, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(st.h, x)
+        if reuse:
+            xin.fill_(3.0)
+            m.fill_(1)
+            torch.cuda.synchronize()
+        moe.block_backward(st, sc, dh, dx, dlosses, *p, stream=stream)
+        torch.cuda.synchronize()
+        runs.append([t.clone() for t in (dx, sc.dgamma, sc.dbeta, sc.dlogits, sc.bwd.dw_router, sc.bwd.dw_up)])
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
