@@ -304,6 +304,9 @@ def block_forward(st, sc, x, add, gamma, beta, w_router, bias, w_gate, w_up, w_d
     that token_mask [T] uint8 (or None: all) counts.  x, add and token_mask are copied
     where the backward needs them and may be overwritten once these calls have run."""
     s, f = st.shape, sc.fwd
+    _, rows, d = _rows(x, "x")
+    if (rows, d) != (s.T, s.d):
+        raise ValueError(f"x: expected [{s.T}, {s.d}], got [{rows}, {d}]")
     layer_norm(x, add, gamma, beta, eps, None if add is None else st.x_sum, st.n, st.mean, st.rstd,
                stream)
     st.h = st.x_sum

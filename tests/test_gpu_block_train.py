@@ -159,3 +159,14 @@ def test_caller_may_reuse_its_input_and_mask_after_the_forward(moe, xt, side):
         runs.append([t.clone() for t in (dx, sc.dgamma, sc.dbeta, sc.dlogits, sc.bwd.dw_router, sc.bwd.dw_up)])
     for a, b in zip(*runs):
         assert torch.equal(a, b)
+
+
+def test_block_refuses_an_input_of_another_shape(moe):
+    """Fewer rows would leave the rest of the state's rows those of an earlier call."""
+    s = moe.Shape(64, 128, 4, 2, 64, 40)
+    st, sc = moe.BlockState(s, DEV), moe.BlockScratch(s, DEV)
+    w = [torch.ones(128, device=DEV), None, torch.zeros(4, 128, device=DEV), None]
+    w += [torch.zeros(*q, dtype=BF, device=DEV) for q in ((4, 64, 128), (4, 64, 128), (4, 128, 64))]
+    for q in ((63, 128), (1, 128), (128, 64)):
+        with pytest.raises(ValueError):
+            moe.block_forward(st, sc, torch.zeros(*q, dtype=BF, device=DEV), None, *w)
