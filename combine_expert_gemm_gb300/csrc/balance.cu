@@ -217,7 +217,7 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
             sum2 = __fadd2_rn(sum2, v2[i]);
         }
         const float sum = group_sum<LANES>(sum2.x + sum2.y);
-        const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+        const float inv = sum == 0.f ? 0.f : __frcp_rn(sum);
         const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
         for (int i = 0; i < VPT / 2; ++i) acc2[i] = __ffma2_rn(v2[i], inv2, acc2[i]);
@@ -225,7 +225,7 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
         for (int j = 0; j < kIdx; ++j)
             if (mine[j] >= 0 && mine[j] < N) atomicAdd(cnt + mine[j], 1);
         if (in && sub == 0) {
-            const float l = m + __logf(sum);
+            const float l = m + logf(sum);
             lse[t] = on ? l : 0.f;
             if (on) {
                 ++tok;

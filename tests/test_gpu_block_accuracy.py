@@ -61,6 +61,23 @@ def test_balance_gradient_does_not_depend_on_a_common_value(moe, N, K, offset):
     block._within(got["expert_prob"], p.mean(0), (3 * size + 160 + T) * U * p.mean(0) + 1e-30, "expert_prob")
 
 
+@pytest.mark.parametrize("m", [0.0, 0.02, -0.02])
+def test_balance_log_sum_of_nearly_certain_rows(moe, m):
+    """log sum e of rows with one expert far ahead, whose log of the sum 1 +
+    e^-d is itself near 0: no absolute error of a short logarithm hides there.
+    The sum is rounded by u, its second term by (3 d + 4) u of itself, the
+    logarithm by 2 u of itself and the result by u of itself."""
+    T, N = 20000, 2
+    g = torch.Generator().manual_seed(3)
+    d = 3 + 9 * torch.rand(T, generator=g)
+    logits = torch.stack([torch.full((T,), m), m - d], 1)
+    idx = torch.zeros(T, 1, dtype=torch.int32)
+    got = block._run_balance(moe, logits.to(DEV), idx.to(DEV), None, N, 1, torch.tensor([1.0, 1.0], device=DEV), None)
+    want = torch.logsumexp(logits.to(D), 1)
+    d = (logits[:, 0].to(D) - logits[:, 1].to(D))
+    block._within(got["lse"], want, U * (1.1 + (3 * d + 6) * torch.exp(-d) + want.abs()), "lse")
+
+
 # ----------------------------------------------------- dense router gradient --
 
 def _chain(a, b):
