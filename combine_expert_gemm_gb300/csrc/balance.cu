@@ -253,12 +253,10 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
         }
         __syncthreads();
     }
-    z = 0.f;
-    tok = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        z += zs[w];
-        tok += ts[w];
-    }
+    // the warps' sums as a tree: one after the other, 32 of them could each lose
+    // half an ulp of the whole
+    z = group_sum<32>(lane < kWarps ? zs[lane] : 0.f);
+    tok = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? ts[lane] : 0);
     float dot = 0.f;
     part_i += blockIdx.x * bal_stride(N);
     part_f += blockIdx.x * bal_stride(N);
@@ -285,11 +283,9 @@ balance_partial(int T, int N, int K, const float *__restrict__ logits,
     dot = group_sum<32>(dot);
     if (lane == 0) zs[warp] = dot;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        dot = 0.f;
-        for (int w = 0; w < kWarps; ++w) dot += zs[w];
-        out.losses_of(dot, z, tok, N);
-    }
+    if (warp > 0) return;
+    dot = group_sum<32>(lane < kWarps ? zs[lane] : 0.f);
+    if (lane == 0) out.losses_of(dot, z, tok, N);
 }
 
 constexpr int kFinishCtas = 8;
@@ -371,11 +367,9 @@ balance_finish(int N, int K, int ctas, int slices, const int32_t *__restrict__ p
     dot = group_sum<32>(dot);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dot;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        dot = 0.f;
-        for (int w = 0; w < (int)blockDim.x / 32; ++w) dot += red[w];
-        out.losses_of(dot, sf[N], tc, N);
-    }
+    if (threadIdx.x >= 32) return;
+    dot = group_sum<32>(red[threadIdx.x]);  // 1024 threads
+    if (threadIdx.x == 0) out.losses_of(dot, sf[N], tc, N);
 }
 
 constexpr int kBwdThreads = 256;

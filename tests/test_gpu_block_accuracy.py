@@ -78,6 +78,21 @@ def test_balance_log_sum_of_nearly_certain_rows(moe, m):
     block._within(got["lse"], want, U * (1.1 + (3 * d + 6) * torch.exp(-d) + want.abs()), "lse")
 
 
+def test_balance_sums_over_warps_are_trees(moe):
+    """One token's square of 1 and 31 of 2^-25, each in a warp of its own: added
+    one after the other to the 1 they all vanish (15 u).  A tree over lanes and
+    warps rounds once a level, at most 5 + 5 + 2 u."""
+    T = 128                                    # four tokens of one expert a warp, 32 warps
+    logits = torch.zeros(T, 1)
+    logits[::4] = 2.0 ** -12.5
+    logits[0] = 1.0
+    got = block._run_balance(moe, logits.to(DEV), torch.zeros(T, 1, dtype=torch.int32, device=DEV), None, 1, 1,
+                             torch.tensor([1.0, 1.0], device=DEV), None)
+    want = (logits.to(D) ** 2).sum() / T
+    assert abs(got["losses"][1].double().item() - want.item()) <= 12 * U * want.item()
+    assert got["losses"][0].item() == 1.0
+
+
 # ----------------------------------------------------- dense router gradient --
 
 def _chain(a, b):
