@@ -45,8 +45,8 @@ typedef enum {
  *   mean[t] = sum_j s[t, j] / d
  *   rstd[t] = 1 / sqrt(sum_j (s[t, j] - mean[t])^2 / d + eps)
  *   y[t, j] = bf16((s[t, j] - mean[t]) * rstd[t] * gamma[j] + beta[j])
- * in fp32, the variance from the centred values (a row with a large mean
- * loses nothing).  The norm is taken of the rounded sum, which is what the
+ * in fp32, the variance from the centred values (a large mean does not cancel
+ * in it).  The norm is taken of the rounded sum, which is what the
  * backward reads.
  *   x [rows, d] of x_dtype; add [rows, d] bf16 or NULL; gamma, beta [d] fp32,
  *   each may be NULL (1 and 0); x_sum out [rows, d] of x_dtype, required with
@@ -157,9 +157,10 @@ size_t moe_router_dense_backward_workspace_bytes(const moe_shape *s);
  *   be dx_in itself, NULL to leave it out; dw_router out [N, d] fp32 or NULL;
  *   dbias out [N] fp32 or NULL; ws of moe_router_dense_backward_workspace_bytes
  *   bytes, 256-byte aligned, word 0 the device status word.
- * Products and sums keep fp32 accuracy (the error of an fp32 product of the
- * same length).  A non-finite dlogit or weight makes what it reaches
- * non-finite, inf or NaN.  Uses T, d and N of the shape.
+ * Products and sums keep fp32 accuracy: in the 2-norm about the error of a chain
+ * of fp32 multiply-adds of the same length, or less.  A non-finite dlogit or
+ * weight makes what it reaches non-finite, inf or NaN.  Uses T, d and N of the
+ * shape.
  */
 moe_status moe_router_dense_backward(const moe_shape *s, const moe_bf16 *x, const float *w_router,
                                      const float *dlogits, const float *dx_in, float *dx,
