@@ -349,6 +349,12 @@ constexpr int kDxPiece = 2 * 32 * 128;              // 128 columns or tokens x 3
 constexpr int kDxStageBytes = 2 * 3 * kDxPiece;     // 48 KB
 constexpr int kDxBlk = 32 * 32 * 4;
 constexpr int kDxAcc = 4;
+// Declared for more threads than it has, which holds it to 128 registers: with
+// the 166 that it would take, no CTA of the stream's next kernel finds registers
+// beside one of these before it ends.  Calls in a row, us: T = 82, d = 624, N =
+// 269 15.6 (16.9 with 166), 25 x 1064 x 418 18.3 (19.4), 64 x 4096 x 256 16.2
+// (17.1), 31595 x 272 x 73 38.1 (38.6), larger ones within 1% either way.
+constexpr int kDxBound = 512;
 constexpr int kDxGroup = 4;  // k-blocks of leading products in an accumulator
 
 template <int STAGES, int SLOTS>
@@ -373,7 +379,7 @@ struct Dx {
 };
 
 template <int STAGES, int SLOTS>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(kDxBound, 1)
 router_dense_dx(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant__ CUtensorMap tm_w,
                 const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_out,
                 int T, int N, int d, int has_in, const Sums sums, int *status) {
