@@ -6,6 +6,7 @@ Argument marshalling only, as in the package's ``__init__``; these calls also
 compare every tensor's size with the shape, because a short buffer would be
 overrun on the device.
 """
+import contextlib
 import ctypes
 
 import torch
@@ -287,12 +288,12 @@ class BlockScratch:
 
 
 def _keep(dst, src, stream):
-    """Copies src into the state's dst on the calls' stream."""
-    if stream is None:
-        dst.copy_(src)
-    else:
-        with torch.cuda.stream(stream):
-            dst.copy_(src)
+    """dst, or where it is None a new tensor of the calls' stream (on another one its
+    memory could still be in use), with a copy of src made on that stream."""
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        if dst is None:
+            dst = torch.empty_like(src)
+        return dst.copy_(src)
 
 
 def block_forward(st, sc, x, add, gamma, beta, w_router, bias, w_gate, w_up, w_down, eps=1e-5,
@@ -309,21 +310,19 @@ def block_forward(st, sc, x, add, gamma, beta, w_router, bias, w_gate, w_up, w_d
         raise ValueError(f"x: expected [{s.T}, {s.d}], got [{rows}, {d}]")
     layer_norm(x, add, gamma, beta, eps, None if add is None else st.x_sum, st.n, st.mean, st.rstd,
                stream)
-    st.h = st.x_sum
-    if add is None:
-        if x.dtype is _f32:
-            if st.x_fp32 is None:
-                st.x_fp32 = torch.empty_like(x)
-            st.h = st.x_fp32
-        _keep(st.h, x, stream)
+    if add is not None:
+        st.h = st.x_sum
+    elif x.dtype is _f32:
+        st.h = st.x_fp32 = _keep(st.x_fp32, x, stream)
+    else:
+        st.h = _keep(st.x_sum, x, stream)
     route(s, st.n, w_router, bias, st.topk_idx, st.topk_gate, st.route_row, st.expert_count,
           st.expert_offset, st.expert_demand, st.route_ws, stream)
     balance_loss(s, route_logits(s, st.route_ws), st.topk_idx, token_mask, st.routed_count,
                  st.token_count, st.expert_prob, st.lse, st.losses, sc.balance_ws, stream)
     st.token_mask = None
     if token_mask is not None:
-        _keep(st.mask, token_mask.view(-1)[:s.T], stream)
-        st.token_mask = st.mask
+        st.token_mask = _keep(st.mask, token_mask.view(-1)[:s.T], stream)
     dispatch(s, st.n, st.route_row, f.x_disp, stream)
     expert_ffn(s, f.x_disp, st.expert_count, st.expert_offset, w_gate, w_up, w_down, f.h_act,
                f.g_save, f.u_save, f.y_disp, f.ffn_ws, stream)
