@@ -606,3 +606,10 @@ from .block import _SIG as _BLOCK_SIG, __all__ as _block_all  # noqa: E402
 
 EXPORTED += tuple(_BLOCK_SIG)
 __all__ += _block_all
+
+# The dense operators beside the routed experts (include/moe_dense.h).
+from .dense import *  # noqa: E402,F401,F403
+from .dense import _SIG as _DENSE_SIG, __all__ as _dense_all  # noqa: E402
+
+EXPORTED += tuple(_DENSE_SIG)
+__all__ += _dense_all

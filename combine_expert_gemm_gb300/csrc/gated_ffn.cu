@@ -1,0 +1,242 @@
+// The dense gated feed-forward block (include/moe_dense.h): a shared expert that
+// every token passes.
+//
+//   G = x Wg^T, U = x Wu^T;  H = act(G) U;  y = add + s (H Wd^T)
+//
+// Two products.  The first computes G and U of the same 128 hidden units in one
+// 256-column tile (the pair's leader holds the gate rows, its peer the up rows)
+// and leaves H and, for the backward, P = act(G) and Q = U act'(G): with these
+// dU = dH P and dG = dH Q, so the backward takes no exponential and does
+// not depend on the activation, at the memory that G and U would take.  The second
+// adds and scales in its epilogue.  Widths are multiples of 8 only: what a tile
+// reaches past T, d or h is read as zeros and never stored.
+#include "ffn_common.cuh"
+
+namespace moe {
+namespace {
+
+using namespace pair;
+
+struct HiddenArgs {
+    CUtensorMap x, wg, wu, o, p, q;
+    int T, d, h, mt, nt;
+    int *status;
+};
+
+// act(g) and act'(g).  silu and gelu are both g sigmoid(z): z = g, or
+// 2 sqrt(2 / pi) (g + 0.044715 g^3).
+template <int ACT>
+__device__ __forceinline__ void activate(float g, float &a, float &da) {
+    if (ACT == MOE_ACT_RELU) {
+        // not fmaxf, which would drop a NaN
+        a = g < 0.0f ? 0.0f : g;
+        da = g > 0.0f ? 1.0f : 0.0f;
+        return;
+    }
+    float z = g, dz = 1.0f;
+    if (ACT == MOE_ACT_GELU) {
+        constexpr float k = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+        const float g2 = g * g;
+        z = k * g * fmaf(0.044715f, g2, 1.0f);
+        dz = k * fmaf(3.0f * 0.044715f, g2, 1.0f);
+    }
+    // 1 + e^-z past 2^126 gives 0, which is what s is then to fp32
+    const float s = __fdividef(1.0f, 1.0f + __expf(-z));
+    a = g * s;
+    const float gz = ACT == MOE_ACT_GELU ? g * dz : g;
+    // far from 0 the slope is s itself, also where g dz overflows
+    da = s == 0.0f || s == 1.0f ? s : fmaf(gz * s, 1.0f - s, s);
+}
+
+template <int ACT, bool SAVE>
+struct Hidden {
+    using Args = HiddenArgs;
+    struct Regs {};
+    static constexpr int kStages = 6;
+    static constexpr int kStageBytes = 2 * OPERAND;
+    static constexpr int kGroup = 0;
+    static __device__ __forceinline__ int tiles(const Args &p) { return p.mt * p.nt; }
+    static __device__ __forceinline__ Tile tile(const Args &p, int g) {
+        int m, n;
+        band_tile(g, p.mt, p.nt, m, n);
+        return Tile{0, m * PM, n * (BN / 2)};
+    }
+    static __device__ __forceinline__ int k_blocks(const Args &p, const Tile &) { return (p.d + BK - 1) / BK; }
+    static __device__ __forceinline__ void load(const Args &p, const Tile &t, int kb, uint32_t s, uint32_t bar,
+                                                int rank) {
+        load_k(s, &p.x, bar, kb * BK, t.m + rank * BM, 0);
+        load_k(s + OPERAND, rank ? &p.wu : &p.wg, bar, kb * BK, t.n, 0);
+    }
+    static __device__ __forceinline__ void mma(const Args &, const Tile &, uint32_t d, uint32_t s, bool first) {
+        mma_block<1, false, false>(d, s, s + OPERAND, first);
+    }
+    static __device__ __forceinline__ void before(const Args &, const Tile &, const Epi &, int, Regs &) {}
+    static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, const Epi &e, int wrow, Regs &) {
+        const int row0 = t.m + wrow;
+        if (row0 >= p.T) return;
+        // G in columns 0-127 of the tile, U in 128-255: this warp's 64 hidden units
+        const int unit = e.col / 2;
+        const uint32_t gat = e.taddr - (uint32_t)(e.col - unit);
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 32) {
+            const int col = t.n + unit + c;
+            if (col >= p.h) break;
+            float g[32], u[32];
+            read32(gat + c, g);
+            read32(gat + BN / 2 + c, u);
+            uint32_t hw[16], pw[16], qw[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float a0, a1, d0, d1;
+                activate<ACT>(g[2 * i], a0, d0);
+                activate<ACT>(g[2 * i + 1], a1, d1);
+                hw[i] = pack_bf16x2(a0 * u[2 * i], a1 * u[2 * i + 1]);
+                if (SAVE) {
+                    pw[i] = pack_bf16x2(a0, a1);
+                    qw[i] = pack_bf16x2(u[2 * i] * d0, u[2 * i + 1] * d1);
+                }
+            }
+            store_block16(e.blk, hw, &p.o, col, row0, 0, e.lane);
+            if (SAVE) {
+                store_block16(e.blk, pw, &p.p, col, row0, 0, e.lane);
+                store_block16(e.blk, qw, &p.q, col, row0, 0, e.lane);
+            }
+        }
+    }
+};
+
+struct OutArgs {
+    CUtensorMap hact, wd, o;
+    int T, d, h, mt, nt;
+    const uint16_t *add;
+    const float *scale;
+    int *status;
+};
+
+struct Out {
+    using Args = OutArgs;
+    struct Regs {
+        uint4 add[16];  // this lane's 128 columns of add
+        float s;
+    };
+    static constexpr int kStages = 6;
+    static constexpr int kStageBytes = 2 * OPERAND;
+    static constexpr int kGroup = 0;
+    static __device__ __forceinline__ int tiles(const Args &p) { return p.mt * p.nt; }
+    static __device__ __forceinline__ Tile tile(const Args &p, int g) {
+        int m, n;
+        band_tile(g, p.mt, p.nt, m, n);
+        return Tile{0, m * PM, n * BN};
+    }
+    static __device__ __forceinline__ int k_blocks(const Args &p, const Tile &) { return (p.h + BK - 1) / BK; }
+    static __device__ __forceinline__ void load(const Args &p, const Tile &t, int kb, uint32_t s, uint32_t bar,
+                                                int rank) {
+        load_k(s, &p.hact, bar, kb * BK, t.m + rank * BM, 0);
+        load_k(s + OPERAND, &p.wd, bar, kb * BK, t.n + rank * BM, 0);
+    }
+    static __device__ __forceinline__ void mma(const Args &, const Tile &, uint32_t d, uint32_t s, bool first) {
+        mma_block<1, false, false>(d, s, s + OPERAND, first);
+    }
+    static __device__ __forceinline__ void before(const Args &p, const Tile &t, const Epi &e, int wrow, Regs &r) {
+        const int row = t.m + wrow + e.lane;
+        r.s = p.scale && row < p.T ? p.scale[row] : 1.0f;
+        if (p.add) {
+            const int col = t.n + e.col;
+            const uint16_t *src = p.add + (int64_t)row * p.d + col;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                r.add[i] = row < p.T && col + 8 * i < p.d ? __ldcs(reinterpret_cast<const uint4 *>(src) + i)
+                                                          : make_uint4(0, 0, 0, 0);
+        }
+    }
+    static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, const Epi &e, int wrow, Regs &r) {
+        const int row0 = t.m + wrow;
+        if (row0 >= p.T) return;
+#pragma unroll
+        for (int c = 0; c < BN / 2; c += 32) {
+            const int col = t.n + e.col + c;
+            if (col >= p.d) break;
+            float v[32];
+            read32(e.taddr + c, v);
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float a = v[2 * i], b = v[2 * i + 1];
+                if (p.add) {
+                    const uint4 &q = r.add[c / 8 + i / 4];
+                    const uint32_t z = i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
+                    a = fmaf(r.s, a, bf16_lo(z));
+                    b = fmaf(r.s, b, bf16_hi(z));
+                } else if (p.scale) {
+                    a *= r.s;
+                    b *= r.s;
+                }
+                w[i] = pack_bf16x2(a, b);
+            }
+            store_block16(e.blk, w, &p.o, col, row0, 0, e.lane);
+        }
+    }
+};
+
+template <int ACT>
+moe_status launch_hidden(const HiddenArgs &a, bool save, cudaStream_t st) {
+    const int64_t tiles = (int64_t)a.mt * a.nt;
+    return save ? launch<Hidden<ACT, true>>(a, tiles, st) : launch<Hidden<ACT, false>>(a, tiles, st);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+MOE_API size_t moe_gated_ffn_workspace_bytes(int32_t T, int32_t d, int32_t h) {
+    if (check_ffn(T, d, h) != MOE_OK) return 0;
+    return 256;
+}
+
+MOE_API moe_status moe_gated_ffn(int32_t T, int32_t d, int32_t h, int32_t act, const moe_bf16 *x,
+                                 const moe_bf16 *w_gate, const moe_bf16 *w_up,
+                                 const moe_bf16 *w_down, const moe_bf16 *add,
+                                 const float *token_scale, moe_bf16 *y, moe_bf16 *h_act,
+                                 moe_bf16 *p_save, moe_bf16 *q_save, void *ws, size_t ws_bytes,
+                                 cudaStream_t stream) {
+    moe_status r = check_ffn(T, d, h);
+    if (r != MOE_OK) return r;
+    if (act < MOE_ACT_SILU || act > MOE_ACT_RELU) return MOE_ERR_INVALID_ARG;
+    if (!p_save != !q_save) return MOE_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < moe_gated_ffn_workspace_bytes(T, d, h) || (reinterpret_cast<uintptr_t>(ws) & 255u))
+        return MOE_ERR_WORKSPACE;
+    if (T == 0) return MOE_OK;
+    if (!x || !w_gate || !w_up || !w_down || !y || !h_act || x == y) return MOE_ERR_INVALID_ARG;
+    const void *ptrs[] = {x, w_gate, w_up, w_down, add, token_scale, y, h_act, p_save, q_save};
+    for (const void *q : ptrs)
+        if (!aligned16(q)) return MOE_ERR_ALIGNMENT;
+
+    HiddenArgs a{};
+    a.T = T;
+    a.d = d;
+    a.h = h;
+    a.mt = (T + PM - 1) / PM;
+    a.nt = (h + BN / 2 - 1) / (BN / 2);
+    a.status = static_cast<int *>(ws);
+    OutArgs o{};
+    o.T = T;
+    o.d = d;
+    o.h = h;
+    o.mt = a.mt;
+    o.nt = (d + BN - 1) / BN;
+    o.add = reinterpret_cast<const uint16_t *>(add);
+    o.scale = token_scale;
+    o.status = a.status;
+    if (!map_k(&a.x, x, d, T) || !map_k(&a.wg, w_gate, d, h) || !map_k(&a.wu, w_up, d, h) ||
+        !map_store(&a.o, h_act, h, T) || !map_store(&a.p, p_save ? p_save : h_act, h, T) ||
+        !map_store(&a.q, q_save ? q_save : h_act, h, T) || !map_k(&o.hact, h_act, h, T) ||
+        !map_k(&o.wd, w_down, h, d) || !map_store(&o.o, y, d, T))
+        return MOE_ERR_CUDA;
+    const bool save = p_save != nullptr;
+    r = act == MOE_ACT_SILU   ? launch_hidden<MOE_ACT_SILU>(a, save, stream)
+        : act == MOE_ACT_GELU ? launch_hidden<MOE_ACT_GELU>(a, save, stream)
+                              : launch_hidden<MOE_ACT_RELU>(a, save, stream);
+    if (r != MOE_OK) return r;
+    return launch<Out>(o, (int64_t)o.mt * o.nt, stream);
+}

@@ -1,0 +1,524 @@
+// Newton-Schulz orthogonalisation of batches of matrices and the Muon step built
+// on it (include/moe_dense.h).  With X [m, n], m <= n (the matrix or its
+// transpose), |X|_F = 1 at first, a step is
+//
+//   S = X X^T;  C = a I + b S + c S S;  X <- C X
+//
+// Three products a step, 2 m^2 n, 2 m^3 and 2 m^2 n operations; S and C are
+// symmetric, so of their tiles only those on and above the diagonal are computed
+// and each is stored twice.  a sits on C's diagonal, so the third product needs no
+// epilogue of its own: its result is the next X.
+//
+// Precision.  A step multiplies a small singular value by a (3.4445), so a
+// rounding error of the first step reaches the last one up to 485 times larger
+// where M's singular values are small; 8 bits of mantissa would leave percents.
+// The iterates are held as two fp16 pieces, v 2^10 = hi + lo, hi = fp16(v 2^10),
+// lo = fp16(v 2^10 - hi): the difference is exact, |v| < 60 stays finite and lo
+// loses nothing to fp16's smallest step (2^-24, or 2^-34 of 1) that matters
+// beside hi's 2^-22.  A product takes three MMAs a k-step, lo hi, hi lo, hi hi
+// (lo lo is 2^-22 of the product and random); a stage holds the four pieces, so
+// the third MMA loads nothing.  The accumulators hold kGroup k-blocks and
+// are added in fp32 registers (pair_gemm.cuh says why).
+//
+// Launches: one or two passes over the matrices (momentum and sums of squares;
+// scaling, splitting and transposing), three products a step; the last
+// product's epilogue writes the result or updates the weights.
+#include <cmath>
+
+#include "../../include/moe_dense.h"
+#include "pair_gemm.cuh"
+
+namespace moe {
+namespace {
+
+using namespace pair;
+
+constexpr float kScale = 1024.0f;     // pieces hold 2^10 times the value
+constexpr float kUnscale = 1.0f / kScale;
+constexpr int kParts = 128;           // partial sums of squares of a matrix, at most
+constexpr int kNormThreads = 256;
+
+// Pieces of two values, each packed as a pair (a in the low half).
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+__device__ __forceinline__ float2 join2(uint32_t hi, uint32_t lo) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    return make_float2(a.x + b.x, a.y + b.y);
+}
+
+__device__ __forceinline__ float load_elem(const float *p, int64_t i) { return p[i]; }
+__device__ __forceinline__ float load_elem(const uint16_t *p, int64_t i) {
+    return __uint_as_float((uint32_t)p[i] << 16);
+}
+
+// ---------------------------------------------------------- first passes --
+
+// Sums of squares of matrix blockIdx.y: part[y][x] over a strided share of it.
+// With MUON the values are the update direction and the momentum is advanced.
+template <bool MUON, typename TIN>
+__global__ void __launch_bounds__(kNormThreads)
+ns_norm(int64_t elems, const TIN *__restrict__ x, float *__restrict__ momentum, float mu, int nesterov,
+        float *__restrict__ part) {
+    pdl_enter();
+    const int64_t base = (int64_t)blockIdx.y * elems;
+    float s = 0.0f;
+    for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < elems;
+         i += (int64_t)gridDim.x * kNormThreads) {
+        float v = load_elem(x, base + i);
+        if (MUON) {
+            const float m = fmaf(mu, momentum[base + i], v);
+            momentum[base + i] = m;
+            v = nesterov ? fmaf(mu, m, v) : m;
+        }
+        s = fmaf(v, v, s);
+    }
+    __shared__ float red[kNormThreads / 32];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float t = 0.0f;
+        for (int i = 0; i < kNormThreads / 32; ++i) t += red[i];
+        part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = t;
+    }
+}
+
+constexpr int kSplitTile = 64;
+
+// The pieces of X_0 = M / (|M| + eps), or of its transpose: a 64 x 64 tile of
+// M a CTA.  hi [B][m][ld], lo [B][m][ld] one plane group after the other.
+template <bool MUON, typename TIN>
+__global__ void __launch_bounds__(256)
+ns_split(int rows, int cols, int tall, int64_t ld, const TIN *__restrict__ x, const float *__restrict__ momentum,
+         float mu, int nesterov, float eps, const float *__restrict__ part, int parts, uint16_t *__restrict__ hi,
+         uint16_t *__restrict__ lo) {
+    pdl_enter();
+    __shared__ float tile[kSplitTile][kSplitTile + 1];
+    __shared__ float inv_s;
+    const int64_t b = blockIdx.z;
+    if (threadIdx.x < 32) {
+        double s = 0.0;
+        for (int i = threadIdx.x; i < parts; i += 32) s += part[b * parts + i];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        if (threadIdx.x == 0) inv_s = 1.0f / ((float)sqrt(s) + eps);
+    }
+    __syncthreads();
+    const float inv = inv_s;
+    const int r0 = blockIdx.y * kSplitTile, c0 = blockIdx.x * kSplitTile;
+    const int64_t base = b * rows * cols;
+    const int64_t out = b * (tall ? cols : rows) * ld;
+    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+    for (int r = ty; r < kSplitTile; r += 4) {
+        float v = 0.0f;
+        if (r0 + r < rows && c0 + tx < cols) {
+            const int64_t i = base + (int64_t)(r0 + r) * cols + c0 + tx;
+            v = load_elem(x, i);
+            if (MUON) v = nesterov ? fmaf(mu, momentum[i], v) : momentum[i];
+            v = v * inv * kScale;
+        }
+        tile[r][tx] = v;
+    }
+    __syncthreads();
+    // rows of the iterate: of M, or its columns
+    const int orow0 = tall ? c0 : r0, ocol0 = tall ? r0 : c0;
+    const int orows = tall ? cols : rows;
+    for (int i = threadIdx.x; i < kSplitTile * (kSplitTile / 2); i += 256) {
+        const int r = i / (kSplitTile / 2), c = 2 * (i % (kSplitTile / 2));
+        if (orow0 + r >= orows || ocol0 + c >= ld) continue;
+        uint32_t h, l;
+        split2(tall ? tile[c][r] : tile[r][c], tall ? tile[c + 1][r] : tile[r][c + 1], h, l);
+        const int64_t at = out + (int64_t)(orow0 + r) * ld + ocol0 + c;
+        *reinterpret_cast<uint32_t *>(hi + at) = h;
+        *reinterpret_cast<uint32_t *>(lo + at) = l;
+    }
+}
+
+// ------------------------------------------------------------- products --
+
+enum { NS_GRAM = 0, NS_POLY = 1, NS_APPLY = 2, NS_LAST = 3 };
+
+struct NsArgs {
+    CUtensorMap a, b;    // operands: planes [0, B) are hi, [B, 2 B) lo
+    CUtensorMap o;       // pieces of the result
+    int B, m, n, k;      // result [m, n], reduction k
+    int mt, nt;
+    float ca, cb, cc;    // NS_POLY
+    const uint16_t *s;   // NS_POLY: the pieces of S, rows lds apart
+    int64_t lds;
+    // NS_LAST: out [B, rows, cols] or the weights' update
+    int rows, cols, tall, out_f32;
+    void *out;
+    float *w;
+    uint16_t *w_copy;
+    const float *lr;
+    float decay, factor;
+    int *status;
+};
+
+// A warp's 32 x 32 block of pieces, transposed: lane r holds row r, element (c, r)
+// of the block goes to row c.
+__device__ __forceinline__ void store_block16_t(uint8_t *blk, const uint32_t (&w)[16], const CUtensorMap *map,
+                                                int x, int y, int z, int lane) {
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        *reinterpret_cast<uint16_t *>(blk + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) * 16) + (lane & 7) * 2) =
+            (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_3d(map, smem_u32(blk), x, y, z);
+        bulk_commit();
+    }
+}
+
+template <int MODE>
+struct Ns {
+    using Args = NsArgs;
+    struct Regs {};
+    static constexpr int kStages = 3;
+    static constexpr int kStageBytes = 4 * OPERAND;  // hi and lo of A, hi and lo of B
+    static constexpr int kGroup = 4;
+    static constexpr int COLS = BN / 2;
+    static constexpr bool kSym = MODE == NS_GRAM || MODE == NS_POLY;
+    static __device__ __forceinline__ int per_matrix(const Args &p) {
+        return kSym ? p.mt * (p.mt + 1) / 2 : p.mt * p.nt;
+    }
+    static __device__ __forceinline__ int tiles(const Args &p) { return p.B * per_matrix(p); }
+    static __device__ __forceinline__ Tile tile(const Args &p, int g) {
+        const int per = per_matrix(p), z = g / per;
+        int r = g - z * per, m = 0, n;
+        if (kSym) {  // row m of the upper triangle has mt - m tiles
+            while (r >= p.mt - m) r -= p.mt - m++;
+            n = m + r;
+        } else {
+            band_tile(r, p.mt, p.nt, m, n);
+        }
+        return Tile{z, m * PM, n * BN};
+    }
+    static __device__ __forceinline__ int k_blocks(const Args &p, const Tile &) { return (p.k + BK - 1) / BK; }
+    static __device__ __forceinline__ void load(const Args &p, const Tile &t, int kb, uint32_t s, uint32_t bar,
+                                                int rank) {
+        const int k = kb * BK, row = t.m + rank * BM, col = t.n + rank * BM;
+        load_k(s, &p.a, bar, k, row, t.z);
+        load_k(s + OPERAND, &p.a, bar, k, row, t.z + p.B);
+        if (kSym) {
+            load_k(s + 2 * OPERAND, &p.b, bar, k, col, t.z);
+            load_k(s + 3 * OPERAND, &p.b, bar, k, col, t.z + p.B);
+        } else {
+            load_mn(s + 2 * OPERAND, &p.b, bar, col, k, t.z);
+            load_mn(s + 3 * OPERAND, &p.b, bar, col, k, t.z + p.B);
+        }
+    }
+    static __device__ __forceinline__ void mma(const Args &, const Tile &, uint32_t d, uint32_t s, bool first) {
+        // the small products first: what they leave is cut least
+        mma_block<0, false, !kSym>(d, s + OPERAND, s + 2 * OPERAND, first);
+        mma_block<0, false, !kSym>(d, s, s + 3 * OPERAND, false);
+        mma_block<0, false, !kSym>(d, s, s + 2 * OPERAND, false);
+    }
+    static __device__ __forceinline__ void finish(const Args &p, const Tile &t, const Epi &e, int wrow,
+                                                  const float (&sum)[COLS]) {
+        const int row0 = t.m + wrow;
+        if (row0 >= p.m) return;
+        const int col0 = t.n + e.col;
+#pragma unroll
+        for (int c = 0; c < COLS; c += 32) {
+            const int col = col0 + c;
+            if (col >= p.n) break;
+            if constexpr (MODE == NS_LAST) {
+                last(p, t, e, row0, col, &sum[c]);
+            } else {
+                uint32_t hi[16], lo[16];
+                if constexpr (MODE == NS_POLY) {
+                    const int row = row0 + e.lane;
+                    const uint16_t *sh = p.s + ((int64_t)t.z * p.m + row) * p.lds + col;
+                    const uint16_t *sl = sh + (int64_t)p.B * p.m * p.lds;
+                    uint4 h4[4], l4[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool in = row < p.m && col + 8 * i < p.lds;
+                        h4[i] = in ? reinterpret_cast<const uint4 *>(sh)[i] : make_uint4(0, 0, 0, 0);
+                        l4[i] = in ? reinterpret_cast<const uint4 *>(sl)[i] : make_uint4(0, 0, 0, 0);
+                    }
+                    const uint32_t *hw = reinterpret_cast<const uint32_t *>(h4);
+                    const uint32_t *lw = reinterpret_cast<const uint32_t *>(l4);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 s = join2(hw[i], lw[i]);
+                        float v0 = fmaf(p.cb, s.x, p.cc * (sum[c + 2 * i] * kUnscale));
+                        float v1 = fmaf(p.cb, s.y, p.cc * (sum[c + 2 * i + 1] * kUnscale));
+                        if (row == col + 2 * i) v0 += p.ca * kScale;
+                        if (row == col + 2 * i + 1) v1 += p.ca * kScale;
+                        split2(v0, v1, hi[i], lo[i]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        split2(sum[c + 2 * i] * kUnscale, sum[c + 2 * i + 1] * kUnscale, hi[i], lo[i]);
+                }
+                store_block16(e.blk, hi, &p.o, col, row0, t.z, e.lane);
+                store_block16(e.blk + 2048, lo, &p.o, col, row0, t.z + p.B, e.lane);
+                if (kSym && t.m != t.n) {
+                    store_block16_t(e.blk, hi, &p.o, row0, col, t.z, e.lane);
+                    store_block16_t(e.blk + 2048, lo, &p.o, row0, col, t.z + p.B, e.lane);
+                }
+            }
+        }
+    }
+    // 32 x 32 values of the last iterate (row0.., col..) to M's own layout, whatever
+    // its alignment is: the lanes run along M's rows, which are the block's columns
+    // where M is tall and, through shared memory, its rows where it is not.
+    static __device__ __forceinline__ void last(const Args &p, const Tile &t, const Epi &e, int row0, int col,
+                                                const float *v) {
+        float *blk = reinterpret_cast<float *>(e.blk);  // [32][32], each row rotated by its index
+        const int64_t base = (int64_t)t.z * p.rows * p.cols;
+        float lr = 0.0f, keep = 0.0f;
+        if (p.w) {
+            lr = *p.lr;
+            keep = 1.0f - lr * p.decay;
+            lr *= p.factor;
+        }
+        auto put = [&](int r, int c, float o) {
+            if (r >= p.rows || c >= p.cols) return;
+            o *= kUnscale * kUnscale;
+            const int64_t at = base + (int64_t)r * p.cols + c;
+            if (p.w) {
+                const float w = fmaf(keep, p.w[at], -lr * o);
+                p.w[at] = w;
+                if (p.w_copy) reinterpret_cast<__nv_bfloat16 *>(p.w_copy)[at] = __float2bfloat16_rn(w);
+            } else if (p.out_f32) {
+                static_cast<float *>(p.out)[at] = o;
+            } else {
+                static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(o);
+            }
+        };
+        if (p.tall) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) put(col + i, row0 + e.lane, v[i]);
+            return;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) blk[e.lane * 32 + ((i + e.lane) & 31)] = v[i];
+        __syncwarp();
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) put(row0 + i, col + e.lane, blk[i * 32 + ((e.lane + i) & 31)]);
+    }
+};
+
+// -------------------------------------------------------------- host side --
+
+inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+struct Layout {
+    int m, n;
+    int64_t ldx, lds;  // rows of the iterates and of S, C
+    size_t part, x[2], s, c, bytes;
+    Layout(int64_t B, int rows, int cols) {
+        m = std::min(rows, cols);
+        n = std::max(rows, cols);
+        ldx = (n + 7) / 8 * 8;
+        lds = (m + 7) / 8 * 8;
+        const size_t xb = align256((size_t)(2 * B * m * ldx * 2)), sb = align256((size_t)(2 * B * m * lds * 2));
+        part = 256;
+        x[0] = part + align256((size_t)(B * kParts * 4));
+        x[1] = x[0] + xb;
+        s = x[1] + xb;
+        c = s + sb;
+        bytes = c + sb;
+    }
+};
+
+inline moe_status check_ns(int32_t B, int32_t rows, int32_t cols) {
+    if (B < 0 || rows <= 0 || cols <= 0) return MOE_ERR_INVALID_ARG;
+    if (rows > 65536 || cols > 65536 || B > 65535) return MOE_ERR_UNSUPPORTED;
+    const int64_t mt = (rows + PM - 1) / PM, nt = (cols + PM - 1) / PM;
+    if (B * mt * nt >= (int64_t)1 << 30) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+// Whether every iterate stays inside the pieces' range: the interval that holds
+// X's singular values, [0, 1] at first, through each step's polynomial, sampled
+// (the polynomials are of degree 5; 2% and 1e-3 cover what lies between samples).
+inline bool bounded(int steps, const float *coef) {
+    double r = 1.001;
+    for (int k = 0; k < steps; ++k) {
+        const double a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2];
+        double most = 0.0, factor = 0.0;
+        for (int i = 0; i <= 1024; ++i) {
+            const double s = r * i / 1024, t = s * s, f = a + t * (b + c * t);
+            factor = std::max(factor, std::fabs(f));
+            most = std::max(most, std::fabs(s * f));
+        }
+        if (factor > 60.0 || most > 7.5) return false;
+        r = most * 1.02 + 1e-3;
+    }
+    return true;
+}
+
+constexpr float kDefault[3] = {3.4445f, -4.7750f, 2.0315f};
+
+struct Update {  // NS_LAST
+    void *out = nullptr;
+    int out_f32 = 0;
+    float *w = nullptr;
+    uint16_t *w_copy = nullptr;
+    const float *lr = nullptr;
+    float decay = 0.0f, factor = 0.0f;
+};
+
+// Checks what both calls share; coef gets steps x 3 coefficients.
+moe_status check_steps(int steps, const float *coefficients, float eps, float (&coef)[3 * MOE_NS_MAX_STEPS]) {
+    if (steps < 1 || steps > MOE_NS_MAX_STEPS) return MOE_ERR_INVALID_ARG;
+    if (!std::isfinite(eps) || eps < 1e-30f) return MOE_ERR_INVALID_ARG;
+    for (int i = 0; i < 3 * steps; ++i) {
+        coef[i] = coefficients ? coefficients[i] : kDefault[i % 3];
+        if (!std::isfinite(coef[i])) return MOE_ERR_INVALID_ARG;
+    }
+    return bounded(steps, coef) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+template <bool MUON, typename TIN>
+moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float mu, int nesterov, int steps,
+               const float *coef, float eps, const Update &up, char *ws, cudaStream_t st) {
+    const Layout at(B, rows, cols);
+    const int m = at.m, n = at.n;
+    const int tall = rows > cols;
+    uint16_t *xs[2] = {reinterpret_cast<uint16_t *>(ws + at.x[0]), reinterpret_cast<uint16_t *>(ws + at.x[1])};
+    uint16_t *s = reinterpret_cast<uint16_t *>(ws + at.s), *c = reinterpret_cast<uint16_t *>(ws + at.c);
+    NsArgs gram{}, poly{}, apply[2] = {};
+    gram.B = B;
+    gram.status = reinterpret_cast<int *>(ws);
+    gram.m = gram.n = m;
+    gram.k = n;
+    gram.mt = gram.nt = (m + PM - 1) / PM;
+    poly = gram;
+    poly.k = m;
+    poly.s = s;
+    poly.lds = at.lds;
+    apply[0] = gram;
+    apply[0].n = n;
+    apply[0].k = m;
+    apply[0].nt = (n + BN - 1) / BN;
+    apply[0].rows = rows;
+    apply[0].cols = cols;
+    apply[0].tall = tall;
+    apply[0].out = up.out;
+    apply[0].out_f32 = up.out_f32;
+    apply[0].w = up.w;
+    apply[0].w_copy = up.w_copy;
+    apply[0].lr = up.lr;
+    apply[0].decay = up.decay;
+    apply[0].factor = up.factor;
+    apply[1] = apply[0];
+    const uint64_t planes = 2 * (uint64_t)B;
+    CUtensorMap xk[2];
+    for (int i = 0; i < 2; ++i)
+        if (!map_k(&xk[i], xs[i], n, m, planes, at.ldx) || !map_mn(&apply[i].b, xs[i], n, m, planes, at.ldx) ||
+            !map_store(&apply[i].o, xs[1 - i], n, m, planes, at.ldx) || !map_k(&apply[i].a, c, m, m, planes, at.lds))
+            return MOE_ERR_CUDA;
+    if (!map_store(&gram.o, s, m, m, planes, at.lds) || !map_k(&poly.a, s, m, m, planes, at.lds) ||
+        !map_store(&poly.o, c, m, m, planes, at.lds))
+        return MOE_ERR_CUDA;
+    poly.b = poly.a;
+
+    const int64_t elems = (int64_t)rows * cols;
+    const int want = std::max(1, 8 * num_sms() / B);
+    const int parts = (int)std::min<int64_t>(std::min(want, kParts), (elems + kNormThreads * 8 - 1) / (kNormThreads * 8));
+    float *part = reinterpret_cast<float *>(ws + at.part);
+    launch_pdl(ns_norm<MUON, TIN>, dim3(parts, B), kNormThreads, 0, st, elems, x, momentum, mu, nesterov, part);
+    moe_status r = launch_status();
+    if (r != MOE_OK) return r;
+    launch_pdl(ns_split<MUON, TIN>,
+               dim3((cols + kSplitTile - 1) / kSplitTile, (rows + kSplitTile - 1) / kSplitTile, B), 256, 0, st, rows,
+               cols, tall, at.ldx, x, momentum, mu, nesterov, eps, part, parts, xs[0],
+               xs[0] + (int64_t)B * m * at.ldx);
+    if ((r = launch_status()) != MOE_OK) return r;
+    const int64_t tri = (int64_t)B * gram.mt * (gram.mt + 1) / 2, full = (int64_t)B * apply[0].mt * apply[0].nt;
+    for (int k = 0; k < steps; ++k) {
+        const int cur = k & 1;
+        gram.a = gram.b = xk[cur];
+        poly.ca = coef[3 * k];
+        poly.cb = coef[3 * k + 1];
+        poly.cc = coef[3 * k + 2];
+        if ((r = launch<Ns<NS_GRAM>>(gram, tri, st)) != MOE_OK) return r;
+        if ((r = launch<Ns<NS_POLY>>(poly, tri, st)) != MOE_OK) return r;
+        r = k + 1 < steps ? launch<Ns<NS_APPLY>>(apply[cur], full, st) : launch<Ns<NS_LAST>>(apply[cur], full, st);
+        if (r != MOE_OK) return r;
+    }
+    return MOE_OK;
+}
+
+inline bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+MOE_API size_t moe_newton_schulz_workspace_bytes(int32_t B, int32_t rows, int32_t cols) {
+    if (check_ns(B, rows, cols) != MOE_OK) return 0;
+    return Layout(B, rows, cols).bytes;
+}
+
+MOE_API moe_status moe_newton_schulz(int32_t B, int32_t rows, int32_t cols, int32_t x_dtype, const void *x,
+                                     int32_t out_dtype, void *out, int32_t steps, const float *coefficients,
+                                     float eps, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    moe_status r = check_ns(B, rows, cols);
+    if (r != MOE_OK) return r;
+    if ((x_dtype != MOE_BF16 && x_dtype != MOE_FP32) || (out_dtype != MOE_BF16 && out_dtype != MOE_FP32))
+        return MOE_ERR_INVALID_ARG;
+    float coef[3 * MOE_NS_MAX_STEPS];
+    if ((r = check_steps(steps, coefficients, eps, coef)) != MOE_OK) return r;
+    if (!ws || ws_bytes < Layout(B, rows, cols).bytes || !aligned(ws, 256)) return MOE_ERR_WORKSPACE;
+    if (B == 0) return MOE_OK;
+    if (!x || !out || (x == out && x_dtype != out_dtype)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(x, x_dtype == MOE_FP32 ? 4 : 2) || !aligned(out, out_dtype == MOE_FP32 ? 4 : 2))
+        return MOE_ERR_ALIGNMENT;
+    Update up;
+    up.out = out;
+    up.out_f32 = out_dtype == MOE_FP32;
+    if (x_dtype == MOE_FP32)
+        return run<false>(B, rows, cols, static_cast<const float *>(x), nullptr, 0.0f, 0, steps, coef, eps, up,
+                          static_cast<char *>(ws), stream);
+    return run<false>(B, rows, cols, static_cast<const uint16_t *>(x), nullptr, 0.0f, 0, steps, coef, eps, up,
+                      static_cast<char *>(ws), stream);
+}
+
+MOE_API moe_status moe_muon_step(int32_t B, int32_t rows, int32_t cols, float *w, moe_bf16 *w_copy,
+                                 float *momentum, const float *grad, const float *lr, float mu,
+                                 float weight_decay, float scale, int32_t nesterov, int32_t steps,
+                                 const float *coefficients, float eps, void *ws, size_t ws_bytes,
+                                 cudaStream_t stream) {
+    moe_status r = check_ns(B, rows, cols);
+    if (r != MOE_OK) return r;
+    if (!std::isfinite(mu) || !std::isfinite(weight_decay) || !std::isfinite(scale)) return MOE_ERR_INVALID_ARG;
+    float coef[3 * MOE_NS_MAX_STEPS];
+    if ((r = check_steps(steps, coefficients, eps, coef)) != MOE_OK) return r;
+    if (!ws || ws_bytes < Layout(B, rows, cols).bytes || !aligned(ws, 256)) return MOE_ERR_WORKSPACE;
+    if (B == 0) return MOE_OK;
+    if (!w || !momentum || !grad || !lr) return MOE_ERR_INVALID_ARG;
+    if (w == momentum || w == grad || momentum == grad || lr == w || lr == momentum ||
+        (const void *)w_copy == (const void *)w || (const void *)w_copy == (const void *)momentum ||
+        (const void *)w_copy == (const void *)grad)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(w, 4) || !aligned(momentum, 4) || !aligned(grad, 4) || !aligned(lr, 4) || !aligned(w_copy, 2))
+        return MOE_ERR_ALIGNMENT;
+    Update up;
+    up.w = w;
+    up.w_copy = reinterpret_cast<uint16_t *>(w_copy);
+    up.lr = lr;
+    up.decay = weight_decay;
+    up.factor = scale;
+    return run<true>(B, rows, cols, grad, momentum, mu, nesterov != 0, steps, coef, eps, up, static_cast<char *>(ws),
+                     stream);
+}

@@ -1,0 +1,149 @@
+"""Python binding of the dense operators beside the routed experts
+(``include/moe_dense.h``): the gated feed-forward block of a shared expert, and
+the Newton-Schulz orthogonalisation with the Muon step that updates weight
+matrices.
+
+Argument marshalling only, as in the package's ``__init__``; like the operators of
+a training block these calls compare every tensor's size with the shape.
+"""
+import ctypes
+
+import torch
+
+from . import _P, _SZ, _bf16, _check, _f32, _lib
+from .block import _DTYPE, _arg, _float_type, _on, _ws
+
+__all__ = ["gated_ffn", "gated_ffn_workspace_bytes", "gated_ffn_backward",
+           "gated_ffn_backward_workspace_bytes", "newton_schulz", "newton_schulz_workspace_bytes",
+           "muon_step"]
+
+_I, _F = ctypes.c_int32, ctypes.c_float
+_SIG = {
+    "moe_gated_ffn_workspace_bytes": ([_I] * 3, _SZ),
+    "moe_gated_ffn_backward_workspace_bytes": ([_I] * 3, _SZ),
+    "moe_gated_ffn": ([_I] * 4 + [_P] * 10 + [_P, _SZ, _P], ctypes.c_int),
+    "moe_gated_ffn_backward": ([_I] * 3 + [_P] * 9 + [_I] + [_P] * 2 + [_I] + [_P] * 4 + [_P, _SZ, _P],
+                               ctypes.c_int),
+    "moe_newton_schulz_workspace_bytes": ([_I] * 3, _SZ),
+    "moe_newton_schulz": ([_I] * 4 + [_P, _I, _P, _I, _P, _F, _P, _SZ, _P], ctypes.c_int),
+    "moe_muon_step": ([_I] * 3 + [_P] * 5 + [_F] * 3 + [_I, _I, _P, _F, _P, _SZ, _P], ctypes.c_int),
+}
+for _name, (_args, _res) in _SIG.items():
+    _f = getattr(_lib, _name)
+    _f.argtypes = _args
+    _f.restype = _res
+
+_ACT = {"silu": 0, "gelu": 1, "relu": 2}  # moe_act
+
+
+# ------------------------------------------------------------ gated FFN --
+
+def gated_ffn_workspace_bytes(T, d, h):
+    return int(_lib.moe_gated_ffn_workspace_bytes(T, d, h))
+
+
+def gated_ffn_backward_workspace_bytes(T, d, h):
+    return int(_lib.moe_gated_ffn_backward_workspace_bytes(T, d, h))
+
+
+def _ffn_sizes(x, w_gate):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x: expected [T, d]")
+    if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
+        raise ValueError("w_gate: expected [h, d]")
+    (T, d), (h, d2) = x.shape, w_gate.shape
+    if d != d2:
+        raise ValueError(f"w_gate: expected [h, {d}], got [{h}, {d2}]")
+    return T, d, h
+
+
+def gated_ffn(x, w_gate, w_up, w_down, add, token_scale, y, h_act, p_save, q_save, ws, act="silu",
+              stream=None):
+    """y = add + token_scale * (act(x Wg^T) * (x Wu^T)) Wd^T (include/moe_dense.h).  x [T, d],
+    w_gate, w_up [h, d], w_down [d, h]; add, token_scale, and p_save with q_save may be None;
+    act is "silu", "gelu" (the tanh form) or "relu"."""
+    T, d, h = _ffn_sizes(x, w_gate)
+    if act not in _ACT:
+        raise ValueError(f"act: expected one of {', '.join(_ACT)}, got {act!r}")
+    dev, n, nh, nw = torch.cuda.current_device(), T * d, T * h, d * h
+    wp, wn = _ws(ws, dev)
+    _check(_lib.moe_gated_ffn(
+        T, d, h, _ACT[act], _arg(x, _bf16, "x", n, dev), _arg(w_gate, _bf16, "w_gate", nw, dev),
+        _arg(w_up, _bf16, "w_up", nw, dev), _arg(w_down, _bf16, "w_down", nw, dev),
+        _arg(add, _bf16, "add", n, dev), _arg(token_scale, _f32, "token_scale", T, dev),
+        _arg(y, _bf16, "y", n, dev), _arg(h_act, _bf16, "h_act", nh, dev),
+        _arg(p_save, _bf16, "p_save", nh, dev), _arg(q_save, _bf16, "q_save", nh, dev), wp, wn,
+        _on(stream, dev)), "moe_gated_ffn")
+
+
+def gated_ffn_backward(x, w_gate, w_up, w_down, token_scale, h_act, p_save, q_save, dy, dx_in, dx,
+                       dw_gate, dw_up, dw_down, dtoken_scale, ws, stream=None):
+    """The backward of gated_ffn (include/moe_dense.h): dx = dx_in + the block's input gradient
+    (bf16 or fp32, dx_in of dx's type or None), the weights' gradients and dtoken_scale (or
+    None), all four bf16 or fp32."""
+    T, d, h = _ffn_sizes(x, w_gate)
+    xt, wt = _float_type(dx, "dx"), _float_type(dw_gate, "dw_gate")
+    dev, n, nh, nw = torch.cuda.current_device(), T * d, T * h, d * h
+    wp, wn = _ws(ws, dev)
+    _check(_lib.moe_gated_ffn_backward(
+        T, d, h, _arg(x, _bf16, "x", n, dev), _arg(w_gate, _bf16, "w_gate", nw, dev),
+        _arg(w_up, _bf16, "w_up", nw, dev), _arg(w_down, _bf16, "w_down", nw, dev),
+        _arg(token_scale, _f32, "token_scale", T, dev), _arg(h_act, _bf16, "h_act", nh, dev),
+        _arg(p_save, _bf16, "p_save", nh, dev), _arg(q_save, _bf16, "q_save", nh, dev),
+        _arg(dy, _bf16, "dy", n, dev), _DTYPE[xt], _arg(dx_in, xt, "dx_in", n, dev),
+        _arg(dx, xt, "dx", n, dev), _DTYPE[wt], _arg(dw_gate, wt, "dw_gate", nw, dev),
+        _arg(dw_up, wt, "dw_up", nw, dev), _arg(dw_down, wt, "dw_down", nw, dev),
+        _arg(dtoken_scale, wt, "dtoken_scale", T, dev), wp, wn, _on(stream, dev)),
+        "moe_gated_ffn_backward")
+
+
+# ------------------------------------------------------------ Newton-Schulz --
+
+def newton_schulz_workspace_bytes(B, rows, cols):
+    return int(_lib.moe_newton_schulz_workspace_bytes(B, rows, cols))
+
+
+def _matrices(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() not in (2, 3):
+        raise ValueError(f"{name}: expected [B, rows, cols] or [rows, cols]")
+    return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
+
+
+def _coefficients(c, steps):
+    """A float array of one (a, b, c) a step, or None: c is one triple for all steps, or one
+    for each."""
+    if c is None:
+        return None
+    c = [float(v) for v in c] if not hasattr(c[0], "__len__") else [float(v) for t in c for v in t]
+    if len(c) == 3:
+        c = c * steps
+    if len(c) != 3 * steps:
+        raise ValueError(f"coefficients: {len(c)} numbers, 3 or {3 * steps} expected")
+    return (ctypes.c_float * len(c))(*c)
+
+
+def newton_schulz(x, out, ws, steps=5, coefficients=None, eps=1e-7, stream=None):
+    """out = x's matrices with their singular values taken to about 1 (include/moe_dense.h).
+    x [B, rows, cols] or [rows, cols], bf16 or fp32, out of its shape (and x itself where the
+    types are one); coefficients: one (a, b, c) for all steps, one for each, or None."""
+    B, rows, cols = _matrices(x, "x")
+    xt, ot = _float_type(x, "x"), _float_type(out, "out")
+    dev, n = torch.cuda.current_device(), B * rows * cols
+    wp, wn = _ws(ws, dev)
+    _check(_lib.moe_newton_schulz(B, rows, cols, _DTYPE[xt], _arg(x, xt, "x", n, dev), _DTYPE[ot],
+                                  _arg(out, ot, "out", n, dev), steps, _coefficients(coefficients, steps),
+                                  eps, wp, wn, _on(stream, dev)), "moe_newton_schulz")
+
+
+def muon_step(w, w_copy, momentum, grad, lr, mu, weight_decay, scale, ws, nesterov=True, steps=5,
+              coefficients=None, eps=1e-7, stream=None):
+    """One Muon step of w [B, rows, cols] or [rows, cols] (include/moe_dense.h): momentum and w
+    fp32 in place, w_copy (or None) its bf16 copy, lr a [1] fp32 tensor on the device."""
+    B, rows, cols = _matrices(w, "w")
+    dev, n = torch.cuda.current_device(), B * rows * cols
+    wp, wn = _ws(ws, dev)
+    _check(_lib.moe_muon_step(
+        B, rows, cols, _arg(w, _f32, "w", n, dev), _arg(w_copy, _bf16, "w_copy", n, dev),
+        _arg(momentum, _f32, "momentum", n, dev), _arg(grad, _f32, "grad", n, dev),
+        _arg(lr, _f32, "lr", 1, dev), mu, weight_decay, scale, 1 if nesterov else 0, steps,
+        _coefficients(coefficients, steps), eps, wp, wn, _on(stream, dev)), "moe_muon_step")
