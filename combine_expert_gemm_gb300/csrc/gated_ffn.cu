@@ -71,7 +71,7 @@ struct Hidden {
         mma_block<1, false, false>(d, s, s + OPERAND, first);
     }
     static __device__ __forceinline__ void before(const Args &, const Tile &, const Epi &, int, Regs &) {}
-    static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, const Epi &e, int wrow, Regs &) {
+    static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, Epi &e, int wrow, Regs &) {
         const int row0 = t.m + wrow;
         if (row0 >= p.T) return;
         // G in columns 0-127 of the tile, U in 128-255: this warp's 64 hidden units
@@ -96,10 +96,10 @@ struct Hidden {
                     qw[i] = pack_bf16x2(u[2 * i] * d0, u[2 * i + 1] * d1);
                 }
             }
-            store_block16(e.blk, hw, &p.o, col, row0, 0, e.lane);
+            store_block16(e, hw, &p.o, col, row0, 0);
             if (SAVE) {
-                store_block16(e.blk, pw, &p.p, col, row0, 0, e.lane);
-                store_block16(e.blk, qw, &p.q, col, row0, 0, e.lane);
+                store_block16(e, pw, &p.p, col, row0, 0);
+                store_block16(e, qw, &p.q, col, row0, 0);
             }
         }
     }
@@ -137,7 +137,7 @@ struct Out {
     static __device__ __forceinline__ void mma(const Args &, const Tile &, uint32_t d, uint32_t s, bool first) {
         mma_block<1, false, false>(d, s, s + OPERAND, first);
     }
-    static __device__ __forceinline__ void before(const Args &p, const Tile &t, const Epi &e, int wrow, Regs &r) {
+    static __device__ __forceinline__ void before(const Args &p, const Tile &t, Epi &e, int wrow, Regs &r) {
         const int row = t.m + wrow + e.lane;
         r.s = p.scale && row < p.T ? p.scale[row] : 1.0f;
         if (p.add) {
@@ -149,7 +149,7 @@ struct Out {
                                                           : make_uint4(0, 0, 0, 0);
         }
     }
-    static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, const Epi &e, int wrow, Regs &r) {
+    static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, Epi &e, int wrow, Regs &r) {
         const int row0 = t.m + wrow;
         if (row0 >= p.T) return;
 #pragma unroll
@@ -173,7 +173,7 @@ struct Out {
                 }
                 w[i] = pack_bf16x2(a, b);
             }
-            store_block16(e.blk, w, &p.o, col, row0, 0, e.lane);
+            store_block16(e, w, &p.o, col, row0, 0);
         }
     }
 };

@@ -32,6 +32,7 @@ struct Factor {
     using Args = FactorArgs;
     struct Regs {
         float s;
+        uint4 p[4], q[4], h[4];  // the factors of the 32 columns to come
     };
     static constexpr int kStages = 6;
     static constexpr int kStageBytes = 2 * OPERAND;
@@ -51,16 +52,23 @@ struct Factor {
     static __device__ __forceinline__ void mma(const Args &, const Tile &, uint32_t d, uint32_t s, bool first) {
         mma_block<1, false, true>(d, s, s + OPERAND, first);
     }
-    static __device__ __forceinline__ void before(const Args &p, const Tile &t, const Epi &e, int wrow, Regs &r) {
+    static __device__ __forceinline__ void before(const Args &p, const Tile &t, Epi &e, int wrow, Regs &r) {
         const int row = t.m + wrow + e.lane;
         if (SCALE) r.s = row < p.T ? p.scale[row] : 0.0f;
+        factors(p, row, t.n + e.col, r);
     }
     static __device__ __forceinline__ void fetch(const uint16_t *src, bool row_ok, int col, int h, uint4 (&v)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             v[i] = row_ok && col + 8 * i < h ? __ldcs(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0, 0, 0, 0);
     }
-    static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, const Epi &e, int wrow, Regs &r) {
+    static __device__ __forceinline__ void factors(const Args &p, int row, int col, Regs &r) {
+        const int64_t at = (int64_t)row * p.h + col;
+        fetch(p.p + at, row < p.T, col, p.h, r.p);
+        fetch(p.q + at, row < p.T, col, p.h, r.q);
+        if (SCALE) fetch(p.hact + at, row < p.T, col, p.h, r.h);
+    }
+    static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, Epi &e, int wrow, Regs &r) {
         const int row0 = t.m + wrow, row = row0 + e.lane;
         if (row0 >= p.T) return;
         float ds = 0.0f;
@@ -69,16 +77,11 @@ struct Factor {
         for (int c = 0; c < BN / 2; c += 32) {
             const int col = colh + c;
             if (col >= p.h) break;
-            const int64_t at = (int64_t)row * p.h + col;
-            uint4 pv[4], qv[4], hv[4];
-            fetch(p.p + at, row < p.T, col, p.h, pv);
-            fetch(p.q + at, row < p.T, col, p.h, qv);
-            if (SCALE) fetch(p.hact + at, row < p.T, col, p.h, hv);
             float v[32];
             read32(e.taddr + c, v);
-            const uint32_t *pw = reinterpret_cast<const uint32_t *>(pv);
-            const uint32_t *qw = reinterpret_cast<const uint32_t *>(qv);
-            const uint32_t *hw = reinterpret_cast<const uint32_t *>(hv);
+            const uint32_t *pw = reinterpret_cast<const uint32_t *>(r.p);
+            const uint32_t *qw = reinterpret_cast<const uint32_t *>(r.q);
+            const uint32_t *hw = reinterpret_cast<const uint32_t *>(r.h);
             uint32_t du[16], dg[16], hs[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -95,9 +98,10 @@ struct Factor {
                 du[i] = pack_bf16x2(a * bf16_lo(pw[i]), b * bf16_hi(pw[i]));
                 dg[i] = pack_bf16x2(a * bf16_lo(qw[i]), b * bf16_hi(qw[i]));
             }
-            store_block16(e.blk, du, &p.odu, col, row0, 0, e.lane);
-            store_block16(e.blk, dg, &p.odg, col, row0, 0, e.lane);
-            if (SCALE) store_block16(e.blk, hs, &p.ohs, col, row0, 0, e.lane);
+            if (c + 32 < BN / 2) factors(p, row, col + 32, r);
+            store_block16(e, du, &p.odu, col, row0, 0);
+            store_block16(e, dg, &p.odg, col, row0, 0);
+            if (SCALE) store_block16(e, hs, &p.ohs, col, row0, 0);
         }
         if (SCALE && p.part && row < p.T) p.part[(int64_t)(colh / (BN / 2)) * p.T + row] = ds;
     }
@@ -136,7 +140,7 @@ struct Dx {
         mma_block<1, false, true>(d, s, s + OPERAND, first);
     }
     static __device__ __forceinline__ void before(const Args &, const Tile &, const Epi &, int, Regs &) {}
-    static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, const Epi &e, int wrow, Regs &) {
+    static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, Epi &e, int wrow, Regs &) {
         const int row0 = t.m + wrow, row = row0 + e.lane;
         if (row0 >= p.T) return;
 #pragma unroll 1
@@ -176,7 +180,7 @@ struct Dx {
                 for (int i = 0; i < 16; ++i)
                     w[i] = p.dx_in ? pack_bf16x2(v[2 * i] + bf16_lo(iw[i]), v[2 * i + 1] + bf16_hi(iw[i]))
                                    : pack_bf16x2(v[2 * i], v[2 * i + 1]);
-                store_block16(e.blk, w, &p.o, col, row0, 0, e.lane);
+                store_block16(e, w, &p.o, col, row0, 0);
             }
         }
     }
@@ -218,7 +222,7 @@ struct Weight {
         mma_block<1, true, true>(d, s, s + OPERAND, first);
     }
     static __device__ __forceinline__ void before(const Args &, const Tile &, const Epi &, int, Regs &) {}
-    static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, const Epi &e, int wrow, Regs &) {
+    static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, Epi &e, int wrow, Regs &) {
         const int row0 = t.m + wrow, rows = t.z ? p.h : p.d, cols = t.z ? p.d : p.h;
         if (row0 >= rows) return;
         const CUtensorMap *map = &p.o[t.z];
@@ -245,7 +249,7 @@ struct Weight {
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-                store_block16(e.blk, w, map, col, row0, 0, e.lane);
+                store_block16(e, w, map, col, row0, 0);
             }
         }
     }

@@ -152,6 +152,7 @@ struct NsArgs {
     int mt, nt;
     float ca, cb, cc;    // NS_POLY
     const uint16_t *s;   // NS_POLY: the pieces of S, rows lds apart
+    uint16_t *mirror;    // NS_GRAM, NS_POLY: the result's pieces, rows lds apart
     int64_t lds;
     // NS_LAST: out [B, rows, cols] or the weights' update
     int rows, cols, tall, out_f32;
@@ -163,31 +164,13 @@ struct NsArgs {
     int *status;
 };
 
-// A warp's 32 x 32 block of pieces, transposed: lane r holds row r, element (c, r)
-// of the block goes to row c.
-__device__ __forceinline__ void store_block16_t(uint8_t *blk, const uint32_t (&w)[16], const CUtensorMap *map,
-                                                int x, int y, int z, int lane) {
-    if (lane == 0) bulk_wait_read<0>();
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        *reinterpret_cast<uint16_t *>(blk + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) * 16) + (lane & 7) * 2) =
-            (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) {
-        tma_store_3d(map, smem_u32(blk), x, y, z);
-        bulk_commit();
-    }
-}
-
 template <int MODE>
 struct Ns {
     using Args = NsArgs;
     struct Regs {};
     static constexpr int kStages = 3;
     static constexpr int kStageBytes = 4 * OPERAND;  // hi and lo of A, hi and lo of B
-    static constexpr int kGroup = 4;
+    static constexpr int kGroup = 2;
     static constexpr int COLS = BN / 2;
     static constexpr bool kSym = MODE == NS_GRAM || MODE == NS_POLY;
     static __device__ __forceinline__ int per_matrix(const Args &p) {
@@ -225,93 +208,127 @@ struct Ns {
         mma_block<0, false, !kSym>(d, s, s + 3 * OPERAND, false);
         mma_block<0, false, !kSym>(d, s, s + 2 * OPERAND, false);
     }
-    static __device__ __forceinline__ void finish(const Args &p, const Tile &t, const Epi &e, int wrow,
+    static __device__ __forceinline__ void finish(const Args &p, const Tile &t, Epi &e, int wrow,
                                                   const float (&sum)[COLS]) {
         const int row0 = t.m + wrow;
         if (row0 >= p.m) return;
         const int col0 = t.n + e.col;
+        if constexpr (MODE == NS_LAST) {
+            last(p, t, e, row0, col0, sum);
+        } else {
+            const int row = row0 + e.lane;
+            uint4 s4[8];  // S's pieces of the 32 columns to come
+            if constexpr (MODE == NS_POLY) fetch_s(p, t.z, row, col0, s4);
 #pragma unroll
-        for (int c = 0; c < COLS; c += 32) {
-            const int col = col0 + c;
-            if (col >= p.n) break;
-            if constexpr (MODE == NS_LAST) {
-                last(p, t, e, row0, col, &sum[c]);
-            } else {
+            for (int c = 0; c < COLS; c += 32) {
+                const int col = col0 + c;
+                if (col >= p.n) break;
                 uint32_t hi[16], lo[16];
                 if constexpr (MODE == NS_POLY) {
-                    const int row = row0 + e.lane;
-                    const uint16_t *sh = p.s + ((int64_t)t.z * p.m + row) * p.lds + col;
-                    const uint16_t *sl = sh + (int64_t)p.B * p.m * p.lds;
-                    uint4 h4[4], l4[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool in = row < p.m && col + 8 * i < p.lds;
-                        h4[i] = in ? reinterpret_cast<const uint4 *>(sh)[i] : make_uint4(0, 0, 0, 0);
-                        l4[i] = in ? reinterpret_cast<const uint4 *>(sl)[i] : make_uint4(0, 0, 0, 0);
-                    }
-                    const uint32_t *hw = reinterpret_cast<const uint32_t *>(h4);
-                    const uint32_t *lw = reinterpret_cast<const uint32_t *>(l4);
+                    const uint32_t *sw = reinterpret_cast<const uint32_t *>(s4);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float2 s = join2(hw[i], lw[i]);
+                        const float2 s = join2(sw[i], sw[16 + i]);
                         float v0 = fmaf(p.cb, s.x, p.cc * (sum[c + 2 * i] * kUnscale));
                         float v1 = fmaf(p.cb, s.y, p.cc * (sum[c + 2 * i + 1] * kUnscale));
                         if (row == col + 2 * i) v0 += p.ca * kScale;
                         if (row == col + 2 * i + 1) v1 += p.ca * kScale;
                         split2(v0, v1, hi[i], lo[i]);
                     }
+                    if (c + 32 < COLS) fetch_s(p, t.z, row, col + 32, s4);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         split2(sum[c + 2 * i] * kUnscale, sum[c + 2 * i + 1] * kUnscale, hi[i], lo[i]);
                 }
-                store_block16(e.blk, hi, &p.o, col, row0, t.z, e.lane);
-                store_block16(e.blk + 2048, lo, &p.o, col, row0, t.z + p.B, e.lane);
-                if (kSym && t.m != t.n) {
-                    store_block16_t(e.blk, hi, &p.o, row0, col, t.z, e.lane);
-                    store_block16_t(e.blk + 2048, lo, &p.o, row0, col, t.z + p.B, e.lane);
+                store_block16(e, hi, &p.o, col, row0, t.z);
+                store_block16(e, lo, &p.o, col, row0, t.z + p.B);
+                if (kSym && t.m != t.n && row < p.m) {
+                    // the mirrored block: 32 lanes write 64 bytes of one of its rows
+                    uint16_t *mh = p.mirror + ((int64_t)t.z * p.m + col) * p.lds + row;
+                    uint16_t *ml = mh + (int64_t)p.B * p.m * p.lds;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (col + i >= p.m) break;
+                        mh[i * p.lds] = (uint16_t)(i & 1 ? hi[i / 2] >> 16 : hi[i / 2]);
+                        ml[i * p.lds] = (uint16_t)(i & 1 ? lo[i / 2] >> 16 : lo[i / 2]);
+                    }
                 }
             }
         }
     }
-    // 32 x 32 values of the last iterate (row0.., col..) to M's own layout, whatever
-    // its alignment is: the lanes run along M's rows, which are the block's columns
-    // where M is tall and, through shared memory, its rows where it is not.
-    static __device__ __forceinline__ void last(const Args &p, const Tile &t, const Epi &e, int row0, int col,
-                                                const float *v) {
+    // 32 columns of row `row` of S: hi in v[0..3], lo in v[4..7].
+    static __device__ __forceinline__ void fetch_s(const Args &p, int z, int row, int col, uint4 (&v)[8]) {
+        const uint16_t *sh = p.s + ((int64_t)z * p.m + row) * p.lds + col;
+        const uint16_t *sl = sh + (int64_t)p.B * p.m * p.lds;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool in = row < p.m && col + 8 * i < p.lds;
+            v[i] = in ? reinterpret_cast<const uint4 *>(sh)[i] : make_uint4(0, 0, 0, 0);
+            v[4 + i] = in ? reinterpret_cast<const uint4 *>(sl)[i] : make_uint4(0, 0, 0, 0);
+        }
+    }
+    // The last iterate (this warp's rows row0.., columns col0..) to M's own layout,
+    // whatever its alignment is: the lanes run along M's rows, which are the
+    // iterate's columns where M is tall and, through shared memory, its rows where it is
+    // not.  The weights of the next 32 columns are on their way while 32 are
+    // updated (one by one, the last product took 2.2 ms where the others take 0.44).
+    static __device__ __forceinline__ void last(const Args &p, const Tile &t, Epi &e, int row0, int col0,
+                                                const float (&sum)[COLS]) {
         float *blk = reinterpret_cast<float *>(e.blk);  // [32][32], each row rotated by its index
         const int64_t base = (int64_t)t.z * p.rows * p.cols;
+        const int limit = p.rows, cols = p.cols;
         float lr = 0.0f, keep = 0.0f;
         if (p.w) {
             lr = *p.lr;
             keep = 1.0f - lr * p.decay;
             lr *= p.factor;
         }
-        auto put = [&](int r, int c, float o) {
-            if (r >= p.rows || c >= p.cols) return;
-            o *= kUnscale * kUnscale;
-            const int64_t at = base + (int64_t)r * p.cols + c;
-            if (p.w) {
-                const float w = fmaf(keep, p.w[at], -lr * o);
-                p.w[at] = w;
-                if (p.w_copy) reinterpret_cast<__nv_bfloat16 *>(p.w_copy)[at] = __float2bfloat16_rn(w);
-            } else if (p.out_f32) {
-                static_cast<float *>(p.out)[at] = o;
-            } else {
-                static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(o);
-            }
+        float w[32];
+        auto fetch = [&](int c) {
+            const int r = p.tall ? col0 + c : row0, j = p.tall ? row0 + e.lane : col0 + c + e.lane;
+            const float *src = p.w + base + (int64_t)r * cols + j;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = r + i < limit && j < cols ? __ldcs(src + (int64_t)i * cols) : 0.0f;
         };
-        if (p.tall) {
+        if (p.w) fetch(0);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) put(col + i, row0 + e.lane, v[i]);
-            return;
+        for (int c = 0; c < COLS; c += 32) {
+            if (col0 + c >= p.n) break;
+            float o[32];
+            if (p.tall) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = sum[c + i] * (kUnscale * kUnscale);
+            } else {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) blk[e.lane * 32 + ((i + e.lane) & 31)] = sum[c + i] * (kUnscale * kUnscale);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = blk[i * 32 + ((e.lane + i) & 31)];
+            }
+            const int r = p.tall ? col0 + c : row0, j = p.tall ? row0 + e.lane : col0 + c + e.lane;
+            const int64_t at = base + (int64_t)r * cols + j;
+            if (p.w) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = fmaf(keep, w[i], -lr * o[i]);
+                if (c + 32 < COLS) fetch(c + 32);
+            }
+            if (j >= cols) continue;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (r + i >= limit) break;
+                const int64_t to = at + (int64_t)i * cols;
+                if (p.w) {
+                    __stcs(p.w + to, o[i]);
+                    if (p.w_copy) reinterpret_cast<__nv_bfloat16 *>(p.w_copy)[to] = __float2bfloat16_rn(o[i]);
+                } else if (p.out_f32) {
+                    static_cast<float *>(p.out)[to] = o[i];
+                } else {
+                    static_cast<__nv_bfloat16 *>(p.out)[to] = __float2bfloat16_rn(o[i]);
+                }
+            }
         }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) blk[e.lane * 32 + ((i + e.lane) & 31)] = v[i];
-        __syncwarp();
-#pragma unroll 8
-        for (int i = 0; i < 32; ++i) put(row0 + i, col + e.lane, blk[i * 32 + ((e.lane + i) & 31)]);
     }
 };
 
@@ -401,10 +418,12 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
     gram.m = gram.n = m;
     gram.k = n;
     gram.mt = gram.nt = (m + PM - 1) / PM;
+    gram.mirror = s;
+    gram.lds = at.lds;
     poly = gram;
     poly.k = m;
     poly.s = s;
-    poly.lds = at.lds;
+    poly.mirror = c;
     apply[0] = gram;
     apply[0].n = n;
     apply[0].k = m;
