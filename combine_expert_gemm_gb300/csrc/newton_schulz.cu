@@ -7,7 +7,12 @@
 // Three products a step, 2 m^2 n, 2 m^3 and 2 m^2 n operations; S and C are
 // symmetric, so of their tiles only those on and above the diagonal are computed
 // and each is stored twice.  a sits on C's diagonal, so the third product needs no
-// epilogue of its own: its result is the next X.
+// epilogue of its own: its result is the next X.  Nor does the second one:
+//   C = c (S + b / (2 c) I)^2 + (a - b^2 / (4 c)) I,
+// so the first product's epilogue shifts S's diagonal and the second's reads nothing.
+// (With S read for b S the second product of 64 matrices 1024 x 2048 took 259 us,
+// its multiplications 147.)  A step with c = 0 takes C from the first product and has
+// no second; only a c that is small beside b leaves S as it is and reads it.
 //
 // Precision.  A step multiplies a small singular value by a (3.4445), so a
 // rounding error of the first step reaches the last one up to 485 times larger
@@ -143,16 +148,17 @@ ns_split(int rows, int cols, int tall, int64_t ld, const TIN *__restrict__ x, co
 
 // ------------------------------------------------------------- products --
 
-enum { NS_GRAM = 0, NS_POLY = 1, NS_APPLY = 2, NS_LAST = 3 };
+// NS_GRAM: r I + q X X^T.  NS_SQUARE: r I + q S S.  NS_POLY: r I + q S S + b S, for
+// steps whose square cannot be completed.  NS_APPLY: C X.  NS_LAST: its last.
+enum { NS_GRAM, NS_SQUARE, NS_POLY, NS_APPLY, NS_LAST };
 
 struct NsArgs {
     CUtensorMap a, b;    // operands: planes [0, B) are hi, [B, 2 B) lo
     CUtensorMap o;       // pieces of the result
     int B, m, n, k;      // result [m, n], reduction k
     int mt, nt;
-    float ca, cb, cc;    // NS_POLY
+    float r, q, lin;     // of the symmetric products: diagonal, product, S
     const uint16_t *s;   // NS_POLY: the pieces of S, rows lds apart
-    uint16_t *mirror;    // NS_GRAM, NS_POLY: the result's pieces, rows lds apart
     int64_t lds;
     // NS_LAST: out [B, rows, cols] or the weights' update
     int rows, cols, tall, out_f32;
@@ -164,6 +170,27 @@ struct NsArgs {
     int *status;
 };
 
+// As store_block16, transposed: element (row lane, column i) of the block goes to
+// row i of (x, y, z).
+__device__ __forceinline__ void store_mirrored(Epi &e, const uint32_t (&w)[16], const CUtensorMap *map, int x,
+                                               int y, int z) {
+    uint8_t *blk = e.blk + (e.turn ^= 2048);
+    if (e.lane == 0) bulk_wait_read<1>();
+    __syncwarp();
+    // row i at 64 i, its 16-byte chunk lane / 8 swizzled by (i / 2) % 4
+    uint8_t *at = blk + (e.lane & 7) * 2;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        *reinterpret_cast<uint16_t *>(at + i * 64 + (((e.lane >> 3) ^ ((i >> 1) & 3)) * 16)) =
+            (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (e.lane == 0) {
+        tma_store_3d(map, smem_u32(blk), x, y, z);
+        bulk_commit();
+    }
+}
+
 template <int MODE>
 struct Ns {
     using Args = NsArgs;
@@ -172,7 +199,7 @@ struct Ns {
     static constexpr int kStageBytes = 4 * OPERAND;  // hi and lo of A, hi and lo of B
     static constexpr int kGroup = 2;
     static constexpr int COLS = BN / 2;
-    static constexpr bool kSym = MODE == NS_GRAM || MODE == NS_POLY;
+    static constexpr bool kSym = MODE < NS_APPLY;
     static __device__ __forceinline__ int per_matrix(const Args &p) {
         return kSym ? p.mt * (p.mt + 1) / 2 : p.mt * p.nt;
     }
@@ -202,58 +229,79 @@ struct Ns {
             load_mn(s + 3 * OPERAND, &p.b, bar, col, k, t.z + p.B);
         }
     }
+    // The weights that this warp will update, on their way to L2 while the tile is
+    // multiplied.
+    static __device__ __forceinline__ void begin(const Args &p, const Tile &t, const Epi &e, int wrow) {
+        if constexpr (MODE == NS_LAST) {
+            if (!p.w) return;
+            const int row0 = t.m + wrow, col0 = t.n + e.col;
+            const float *base = p.w + (int64_t)t.z * p.rows * p.cols;
+            // M's rows [r, r + nr) and columns [c, c + nc) of this warp
+            const int r = p.tall ? col0 : row0, nr = p.tall ? COLS : 32;
+            const int c = p.tall ? row0 : col0, nc = p.tall ? 32 : COLS;
+            for (int i = e.lane; i < nr && r + i < p.rows; i += 32)
+                for (int j = 0; j < nc && c + j < p.cols; j += 32)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(base + (int64_t)(r + i) * p.cols + c + j));
+        }
+    }
     static __device__ __forceinline__ void mma(const Args &, const Tile &, uint32_t d, uint32_t s, bool first) {
         // the small products first: what they leave is cut least
         mma_block<0, false, !kSym>(d, s + OPERAND, s + 2 * OPERAND, first);
         mma_block<0, false, !kSym>(d, s, s + 3 * OPERAND, false);
         mma_block<0, false, !kSym>(d, s, s + 2 * OPERAND, false);
     }
+    // The chunks of 32 columns one after the other in a loop, which picks its sums by
+    // selections, as registers have no index: unrolled over the four chunks, the
+    // epilogue's code comes through the instruction cache too slowly (the last
+    // product of 64 matrices 1024 x 2048 took 1.4 ms where the others take 0.47; of
+    // three matrices 1001 x 717, 42 us instead of 27).
     static __device__ __forceinline__ void finish(const Args &p, const Tile &t, Epi &e, int wrow,
                                                   const float (&sum)[COLS]) {
         const int row0 = t.m + wrow;
         if (row0 >= p.m) return;
-        const int col0 = t.n + e.col;
-        if constexpr (MODE == NS_LAST) {
-            last(p, t, e, row0, col0, sum);
-        } else {
-            const int row = row0 + e.lane;
-            uint4 s4[8];  // S's pieces of the 32 columns to come
-            if constexpr (MODE == NS_POLY) fetch_s(p, t.z, row, col0, s4);
+        const int col0 = t.n + e.col, row = row0 + e.lane;
+        uint4 s4[8];  // NS_POLY: S's pieces of the 32 columns to come
+        if constexpr (MODE == NS_POLY) fetch_s(p, t.z, row, col0, s4);
+#pragma unroll 1
+        for (int c = 0; c < COLS / 32; ++c) {
+            const int col = col0 + 32 * c;
+            if (col >= p.n) break;
+            float v[32];
 #pragma unroll
-            for (int c = 0; c < COLS; c += 32) {
-                const int col = col0 + c;
-                if (col >= p.n) break;
-                uint32_t hi[16], lo[16];
+            for (int i = 0; i < 32; ++i) {
+                const float a = c & 1 ? sum[32 + i] : sum[i], b = c & 1 ? sum[96 + i] : sum[64 + i];
+                v[i] = c & 2 ? b : a;
+            }
+            if constexpr (MODE == NS_LAST) {
+                last(p, t, e, row0, col, v);
+                continue;
+            }
+            uint32_t hi[16], lo[16];
+            if constexpr (kSym) {
+                const float q = p.q * kUnscale, r = p.r * kScale;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = fmaf(q, v[i], row == col + i ? r : 0.0f);
                 if constexpr (MODE == NS_POLY) {
                     const uint32_t *sw = reinterpret_cast<const uint32_t *>(s4);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float2 s = join2(sw[i], sw[16 + i]);
-                        float v0 = fmaf(p.cb, s.x, p.cc * (sum[c + 2 * i] * kUnscale));
-                        float v1 = fmaf(p.cb, s.y, p.cc * (sum[c + 2 * i + 1] * kUnscale));
-                        if (row == col + 2 * i) v0 += p.ca * kScale;
-                        if (row == col + 2 * i + 1) v1 += p.ca * kScale;
-                        split2(v0, v1, hi[i], lo[i]);
+                        v[2 * i] = fmaf(p.lin, s.x, v[2 * i]);
+                        v[2 * i + 1] = fmaf(p.lin, s.y, v[2 * i + 1]);
                     }
-                    if (c + 32 < COLS) fetch_s(p, t.z, row, col + 32, s4);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        split2(sum[c + 2 * i] * kUnscale, sum[c + 2 * i + 1] * kUnscale, hi[i], lo[i]);
+                    if (c + 1 < COLS / 32) fetch_s(p, t.z, row, col + 32, s4);
                 }
-                store_block16(e, hi, &p.o, col, row0, t.z);
-                store_block16(e, lo, &p.o, col, row0, t.z + p.B);
-                if (kSym && t.m != t.n && row < p.m) {
-                    // the mirrored block: 32 lanes write 64 bytes of one of its rows
-                    uint16_t *mh = p.mirror + ((int64_t)t.z * p.m + col) * p.lds + row;
-                    uint16_t *ml = mh + (int64_t)p.B * p.m * p.lds;
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (col + i >= p.m) break;
-                        mh[i * p.lds] = (uint16_t)(i & 1 ? hi[i / 2] >> 16 : hi[i / 2]);
-                        ml[i * p.lds] = (uint16_t)(i & 1 ? lo[i / 2] >> 16 : lo[i / 2]);
-                    }
-                }
+                for (int i = 0; i < 32; ++i) v[i] *= kUnscale;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) split2(v[2 * i], v[2 * i + 1], hi[i], lo[i]);
+            store_block16(e, hi, &p.o, col, row0, t.z);
+            store_block16(e, lo, &p.o, col, row0, t.z + p.B);
+            if (kSym && t.m != t.n) {
+                store_mirrored(e, hi, &p.o, row0, col, t.z);
+                store_mirrored(e, lo, &p.o, row0, col, t.z + p.B);
             }
         }
     }
@@ -268,66 +316,53 @@ struct Ns {
             v[4 + i] = in ? reinterpret_cast<const uint4 *>(sl)[i] : make_uint4(0, 0, 0, 0);
         }
     }
-    // The last iterate (this warp's rows row0.., columns col0..) to M's own layout,
-    // whatever its alignment is: the lanes run along M's rows, which are the
-    // iterate's columns where M is tall and, through shared memory, its rows where it is
-    // not.  The weights of the next 32 columns are on their way while 32 are
-    // updated (one by one, the last product took 2.2 ms where the others take 0.44).
-    static __device__ __forceinline__ void last(const Args &p, const Tile &t, Epi &e, int row0, int col0,
-                                                const float (&sum)[COLS]) {
-        float *blk = reinterpret_cast<float *>(e.blk);  // [32][32], each row rotated by its index
-        const int64_t base = (int64_t)t.z * p.rows * p.cols;
-        const int limit = p.rows, cols = p.cols;
-        float lr = 0.0f, keep = 0.0f;
-        if (p.w) {
-            lr = *p.lr;
-            keep = 1.0f - lr * p.decay;
-            lr *= p.factor;
-        }
+    // 32 x 32 values of the last iterate (rows row0.., columns col..) to M's own
+    // layout, whatever its alignment is: the lanes run along M's rows, which are the
+    // iterate's columns where M is tall and, through shared memory, its rows where it
+    // is not.  All 32 weights of a lane are on their way before the first is updated.
+    static __device__ __forceinline__ void last(const Args &p, const Tile &t, Epi &e, int row0, int col,
+                                                float (&v)[32]) {
+        // element i of this lane: (r + i, j) of M
+        const int r = p.tall ? col : row0, j = p.tall ? row0 + e.lane : col + e.lane;
+        const int n = min(32, p.rows - r);
+        const bool in = j < p.cols;
+        const int64_t at = ((int64_t)t.z * p.rows + r) * p.cols + j;
         float w[32];
-        auto fetch = [&](int c) {
-            const int r = p.tall ? col0 + c : row0, j = p.tall ? row0 + e.lane : col0 + c + e.lane;
-            const float *src = p.w + base + (int64_t)r * cols + j;
+        if (p.w) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = r + i < limit && j < cols ? __ldcs(src + (int64_t)i * cols) : 0.0f;
-        };
-        if (p.w) fetch(0);
+            for (int i = 0; i < 32; ++i) w[i] = in && i < n ? p.w[at + (int64_t)i * p.cols] : 0.0f;
+        }
+        if (!p.tall) {
+            float *blk = reinterpret_cast<float *>(e.blk);  // [32][32], each row rotated by its index
+            __syncwarp();
 #pragma unroll
-        for (int c = 0; c < COLS; c += 32) {
-            if (col0 + c >= p.n) break;
-            float o[32];
-            if (p.tall) {
+            for (int i = 0; i < 32; ++i) blk[e.lane * 32 + ((i + e.lane) & 31)] = v[i];
+            __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = sum[c + i] * (kUnscale * kUnscale);
-            } else {
-                __syncwarp();
+            for (int i = 0; i < 32; ++i) v[i] = blk[i * 32 + ((e.lane + i) & 31)];
+        }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) blk[e.lane * 32 + ((i + e.lane) & 31)] = sum[c + i] * (kUnscale * kUnscale);
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = blk[i * 32 + ((e.lane + i) & 31)];
-            }
-            const int r = p.tall ? col0 + c : row0, j = p.tall ? row0 + e.lane : col0 + c + e.lane;
-            const int64_t at = base + (int64_t)r * cols + j;
-            if (p.w) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = fmaf(keep, w[i], -lr * o[i]);
-                if (c + 32 < COLS) fetch(c + 32);
-            }
-            if (j >= cols) continue;
+        for (int i = 0; i < 32; ++i) v[i] *= kUnscale * kUnscale;
+        if (!in) return;
+        if (p.w) {
+            const float lr = *p.lr, keep = 1.0f - lr * p.decay, step = lr * p.factor;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                if (r + i >= limit) break;
-                const int64_t to = at + (int64_t)i * cols;
-                if (p.w) {
-                    __stcs(p.w + to, o[i]);
-                    if (p.w_copy) reinterpret_cast<__nv_bfloat16 *>(p.w_copy)[to] = __float2bfloat16_rn(o[i]);
-                } else if (p.out_f32) {
-                    static_cast<float *>(p.out)[to] = o[i];
-                } else {
-                    static_cast<__nv_bfloat16 *>(p.out)[to] = __float2bfloat16_rn(o[i]);
+                if (i < n) {
+                    const int64_t to = at + (int64_t)i * p.cols;
+                    const float u = fmaf(keep, w[i], -step * v[i]);
+                    p.w[to] = u;
+                    if (p.w_copy) reinterpret_cast<__nv_bfloat16 *>(p.w_copy)[to] = __float2bfloat16_rn(u);
                 }
             }
+        } else if (p.out_f32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i < n) static_cast<float *>(p.out)[at + (int64_t)i * p.cols] = v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i < n) static_cast<__nv_bfloat16 *>(p.out)[at + (int64_t)i * p.cols] = __float2bfloat16_rn(v[i]);
         }
     }
 };
@@ -363,22 +398,24 @@ inline moe_status check_ns(int32_t B, int32_t rows, int32_t cols) {
     return MOE_OK;
 }
 
-// Whether every iterate stays inside the pieces' range: the interval that holds
-// X's singular values, [0, 1] at first, through each step's polynomial, sampled
-// (the polynomials are of degree 5; 2% and 1e-3 cover what lies between samples).
+// One step's polynomial on singular values in [0, r]: the largest result, a little
+// enlarged (1024 samples of a polynomial of degree 5; 2% and 1e-3 cover what lies
+// between them), and whether it and the factor stay inside the pieces' range.
+inline bool step_bound(double r, double a, double b, double c, double &next) {
+    double most = 0.0, factor = 0.0;
+    for (int i = 0; i <= 1024; ++i) {
+        const double s = r * i / 1024, t = s * s, f = a + t * (b + c * t);
+        factor = std::max(factor, std::fabs(f));
+        most = std::max(most, std::fabs(s * f));
+    }
+    next = most * 1.02 + 1e-3;
+    return factor <= 60.0 && most <= 7.5;
+}
+
 inline bool bounded(int steps, const float *coef) {
     double r = 1.001;
-    for (int k = 0; k < steps; ++k) {
-        const double a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2];
-        double most = 0.0, factor = 0.0;
-        for (int i = 0; i <= 1024; ++i) {
-            const double s = r * i / 1024, t = s * s, f = a + t * (b + c * t);
-            factor = std::max(factor, std::fabs(f));
-            most = std::max(most, std::fabs(s * f));
-        }
-        if (factor > 60.0 || most > 7.5) return false;
-        r = most * 1.02 + 1e-3;
-    }
+    for (int k = 0; k < steps; ++k)
+        if (!step_bound(r, coef[3 * k], coef[3 * k + 1], coef[3 * k + 2], r)) return false;
     return true;
 }
 
@@ -418,12 +455,10 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
     gram.m = gram.n = m;
     gram.k = n;
     gram.mt = gram.nt = (m + PM - 1) / PM;
-    gram.mirror = s;
     gram.lds = at.lds;
     poly = gram;
     poly.k = m;
     poly.s = s;
-    poly.mirror = c;
     apply[0] = gram;
     apply[0].n = n;
     apply[0].k = m;
@@ -463,16 +498,35 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
                xs[0] + (int64_t)B * m * at.ldx);
     if ((r = launch_status()) != MOE_OK) return r;
     const int64_t tri = (int64_t)B * gram.mt * (gram.mt + 1) / 2, full = (int64_t)B * apply[0].mt * apply[0].nt;
+    const CUtensorMap gram_to_s = gram.o;
+    double most = 1.001;  // of X's singular values
     for (int k = 0; k < steps; ++k) {
         const int cur = k & 1;
+        const double ca = coef[3 * k], cb = coef[3 * k + 1], cc = coef[3 * k + 2];
         gram.a = gram.b = xk[cur];
-        poly.ca = coef[3 * k];
-        poly.cb = coef[3 * k + 1];
-        poly.cc = coef[3 * k + 2];
-        if ((r = launch<Ns<NS_GRAM>>(gram, tri, st)) != MOE_OK) return r;
-        if ((r = launch<Ns<NS_POLY>>(poly, tri, st)) != MOE_OK) return r;
+        if (cc == 0.0) {
+            gram.o = poly.o;
+            gram.r = (float)ca;
+            gram.q = (float)cb;
+            r = launch<Ns<NS_GRAM>>(gram, tri, st);
+        } else {
+            const double shift = cb / (2 * cc);
+            const bool square = std::fabs(shift) <= 8.0 && most * most + std::fabs(shift) < 60.0;
+            gram.o = gram_to_s;
+                    gram.r = square ? (float)shift : 0.0f;
+            gram.q = 1.0f;
+            if ((r = launch<Ns<NS_GRAM>>(gram, tri, st)) != MOE_OK) return r;
+            poly.q = (float)cc;
+            poly.r = (float)(square ? ca - cb * cb / (4 * cc) : ca);
+            poly.lin = (float)cb;
+            r = square ? launch<Ns<NS_SQUARE>>(poly, tri, st) : launch<Ns<NS_POLY>>(poly, tri, st);
+        }
+        if (r != MOE_OK) return r;
         r = k + 1 < steps ? launch<Ns<NS_APPLY>>(apply[cur], full, st) : launch<Ns<NS_LAST>>(apply[cur], full, st);
         if (r != MOE_OK) return r;
+        double next = 0.0;
+        step_bound(most, ca, cb, cc, next);
+        most = next;
     }
     return MOE_OK;
 }

@@ -347,9 +347,10 @@ def test_newton_schulz_transposes(moe):
 def test_newton_schulz_coefficients_in_place_and_unaligned(moe, B, rows, cols):
     m = _mats(B, rows, cols)
     cubic = (1.5, -0.5, 0.0)
-    coef = [ref.COEF, ref.COEF, (2.0, -1.5, 0.5), cubic, cubic, cubic, cubic]
+    # c = 0 and a c that is small beside b among them
+    coef = [ref.COEF, ref.COEF, (2.0, -1.5, 0.5), cubic, (1.5, -0.5, 1e-3), cubic, cubic]
     want, norms = ref.newton_schulz(m, 7, coef)
-    # the slopes of the third step and of the cubic are below the default's
+    # the slopes of the third step and of the cubics are below the default's
     _check_ns(_ns(moe, m, steps=7, coefficients=coef), want, _ns_bound(norms, 7), "per step")
     want, norms = ref.newton_schulz(m, 4, [cubic] * 4)
     _check_ns(_ns(moe, m, steps=4, coefficients=cubic), want, _ns_bound(norms, 4), "one triple")
