@@ -229,21 +229,6 @@ struct Ns {
             load_mn(s + 3 * OPERAND, &p.b, bar, col, k, t.z + p.B);
         }
     }
-    // The weights that this warp will update, on their way to L2 while the tile is
-    // multiplied.
-    static __device__ __forceinline__ void begin(const Args &p, const Tile &t, const Epi &e, int wrow) {
-        if constexpr (MODE == NS_LAST) {
-            if (!p.w) return;
-            const int row0 = t.m + wrow, col0 = t.n + e.col;
-            const float *base = p.w + (int64_t)t.z * p.rows * p.cols;
-            // M's rows [r, r + nr) and columns [c, c + nc) of this warp
-            const int r = p.tall ? col0 : row0, nr = p.tall ? COLS : 32;
-            const int c = p.tall ? row0 : col0, nc = p.tall ? 32 : COLS;
-            for (int i = e.lane; i < nr && r + i < p.rows; i += 32)
-                for (int j = 0; j < nc && c + j < p.cols; j += 32)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(base + (int64_t)(r + i) * p.cols + c + j));
-        }
-    }
     static __device__ __forceinline__ void mma(const Args &, const Tile &, uint32_t d, uint32_t s, bool first) {
         // the small products first: what they leave is cut least
         mma_block<0, false, !kSym>(d, s + OPERAND, s + 2 * OPERAND, first);
@@ -317,52 +302,69 @@ struct Ns {
         }
     }
     // 32 x 32 values of the last iterate (rows row0.., columns col..) to M's own
-    // layout, whatever its alignment is: the lanes run along M's rows, which are the
-    // iterate's columns where M is tall and, through shared memory, its rows where it
-    // is not.  All 32 weights of a lane are on their way before the first is updated.
+    // layout, whatever its alignment is: through shared memory, so that the lanes run
+    // along M's rows (the iterate's columns where M is tall) and the loop over M's rows is
+    // short.  kRows rows of a lane are on their way at once.
     static __device__ __forceinline__ void last(const Args &p, const Tile &t, Epi &e, int row0, int col,
-                                                float (&v)[32]) {
-        // element i of this lane: (r + i, j) of M
-        const int r = p.tall ? col : row0, j = p.tall ? row0 + e.lane : col + e.lane;
-        const int n = min(32, p.rows - r);
-        const bool in = j < p.cols;
-        const int64_t at = ((int64_t)t.z * p.rows + r) * p.cols + j;
-        float w[32];
-        if (p.w) {
+                                                const float (&v)[32]) {
+        constexpr int kRows = 16;
+        float *blk = reinterpret_cast<float *>(e.blk);  // row i of M: 32 columns, rotated by i
+        __syncwarp();
+        if (p.tall) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = in && i < n ? p.w[at + (int64_t)i * p.cols] : 0.0f;
-        }
-        if (!p.tall) {
-            float *blk = reinterpret_cast<float *>(e.blk);  // [32][32], each row rotated by its index
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) blk[e.lane * 32 + ((i + e.lane) & 31)] = v[i];
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = blk[i * 32 + ((e.lane + i) & 31)];
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= kUnscale * kUnscale;
-        if (!in) return;
-        if (p.w) {
-            const float lr = *p.lr, keep = 1.0f - lr * p.decay, step = lr * p.factor;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                if (i < n) {
-                    const int64_t to = at + (int64_t)i * p.cols;
-                    const float u = fmaf(keep, w[i], -step * v[i]);
-                    p.w[to] = u;
-                    if (p.w_copy) reinterpret_cast<__nv_bfloat16 *>(p.w_copy)[to] = __float2bfloat16_rn(u);
-                }
-            }
-        } else if (p.out_f32) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < n) static_cast<float *>(p.out)[at + (int64_t)i * p.cols] = v[i];
+            for (int i = 0; i < 32; ++i) blk[i * 32 + ((e.lane + i) & 31)] = v[i];
         } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < n) static_cast<__nv_bfloat16 *>(p.out)[at + (int64_t)i * p.cols] = __float2bfloat16_rn(v[i]);
+            for (int i = 0; i < 32; ++i) blk[e.lane * 32 + ((i + e.lane) & 31)] = v[i];
+        }
+        __syncwarp();
+        const int r = p.tall ? col : row0, j = (p.tall ? row0 : col) + e.lane;
+        const int rows = min(32, p.rows - r);
+        const bool in = j < p.cols;
+        const int64_t step = p.cols;
+        int64_t at = ((int64_t)t.z * p.rows + r) * p.cols + j;
+        const float lr = p.w ? *p.lr : 0.0f, keep = 1.0f - lr * p.decay;
+        const float f = p.w ? -lr * p.factor * (kUnscale * kUnscale) : kUnscale * kUnscale;
+        uint16_t *const o16 = p.w ? p.w_copy : p.out_f32 ? nullptr : static_cast<uint16_t *>(p.out);
+        float *const o32 = p.w ? p.w : p.out_f32 ? static_cast<float *>(p.out) : nullptr;
+        // pairs of columns a lane, of every other row, where they are 4-byte aligned
+        const bool pairs = (p.cols & 1) == 0 && (reinterpret_cast<uintptr_t>(o16) & 3) == 0;
+#pragma unroll 1
+        for (int i0 = 0; i0 < rows; i0 += kRows, at += kRows * step) {
+            const int n = in ? rows - i0 : 0;
+            float u[kRows];
+            if (p.w) {
+                const float *src = p.w + at;
+#pragma unroll
+                for (int i = 0; i < kRows; ++i, src += step) u[i] = i < n ? *src : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const float o = f * blk[(i0 + i) * 32 + ((e.lane + i0 + i) & 31)];
+                u[i] = p.w ? fmaf(keep, u[i], o) : o;
+            }
+            if (o32) {
+                float *dst = o32 + at;
+#pragma unroll
+                for (int i = 0; i < kRows; ++i, dst += step)
+                    if (i < n) *dst = u[i];
+            }
+            if (!o16) continue;
+            uint16_t *dst = o16 + at;
+            if (pairs) {
+                const int odd = e.lane & 1;
+                if (odd) dst += step - 1;
+#pragma unroll
+                for (int i = 0; i < kRows; i += 2, dst += 2 * step) {
+                    const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? u[i] : u[i + 1], 1);
+                    const uint32_t w = odd ? pack_bf16x2(other, u[i + 1]) : pack_bf16x2(u[i], other);
+                    if (i + odd < n) *reinterpret_cast<uint32_t *>(dst) = w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kRows; ++i, dst += step)
+                    if (i < n) *reinterpret_cast<__nv_bfloat16 *>(dst) = __float2bfloat16_rn(u[i]);
+            }
         }
     }
 };

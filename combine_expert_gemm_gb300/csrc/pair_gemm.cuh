@@ -19,8 +19,7 @@
 // P::kGroup > 0: an accumulator holds kGroup k-blocks.  The tensor core cuts
 // where an fp32 addition rounds, always towards zero, so a long sum in one
 // accumulator drifts by up to 2^-23 of its size per MMA; the epilogue warps
-// add the groups in fp32 registers instead, and P::finish gets the sums; P::begin
-// runs before the first group.
+// add the groups in fp32 registers instead, and P::finish gets the sums.
 //
 // Every store of the epilogues goes through maps or guards that end at the
 // matrix's extent, every load of a tile past it reads zeros.
@@ -368,7 +367,6 @@ __global__ void __launch_bounds__(threads<P>(), 1) pair_gemm(const __grid_consta
             } else {
                 float sum[COLS];
                 const int nk = P::k_blocks(p, t);
-                P::begin(p, t, e, wrow);
                 for (int k0 = 0; k0 < nk; k0 += P::kGroup) {
                     if (!mbar_wait(smem_u32(&bars->tfull[acc]), acc_phase, status, abort)) {
                         ok = false;
