@@ -55,10 +55,12 @@ struct Hidden {
     static constexpr int kStages = 6;
     static constexpr int kStageBytes = 2 * OPERAND;
     static constexpr int kGroup = 0;
-    static __device__ __forceinline__ int tiles(const Args &p) { return p.mt * p.nt; }
-    static __device__ __forceinline__ Tile tile(const Args &p, int g) {
+    static __device__ __forceinline__ int count(const Args &p, int unit, int units) {
+        return strided_count(p.mt * p.nt, unit, units);
+    }
+    static __device__ __forceinline__ Tile tile(const Args &p, int unit, int units, int i) {
         int m, n;
-        band_tile(g, p.mt, p.nt, m, n);
+        band_tile(unit + i * units, p.mt, p.nt, m, n);
         return Tile{0, m * PM, n * (BN / 2)};
     }
     static __device__ __forceinline__ int k_blocks(const Args &p, const Tile &) { return (p.d + BK - 1) / BK; }
@@ -122,10 +124,12 @@ struct Out {
     static constexpr int kStages = 6;
     static constexpr int kStageBytes = 2 * OPERAND;
     static constexpr int kGroup = 0;
-    static __device__ __forceinline__ int tiles(const Args &p) { return p.mt * p.nt; }
-    static __device__ __forceinline__ Tile tile(const Args &p, int g) {
+    static __device__ __forceinline__ int count(const Args &p, int unit, int units) {
+        return strided_count(p.mt * p.nt, unit, units);
+    }
+    static __device__ __forceinline__ Tile tile(const Args &p, int unit, int units, int i) {
         int m, n;
-        band_tile(g, p.mt, p.nt, m, n);
+        band_tile(unit + i * units, p.mt, p.nt, m, n);
         return Tile{0, m * PM, n * BN};
     }
     static __device__ __forceinline__ int k_blocks(const Args &p, const Tile &) { return (p.h + BK - 1) / BK; }

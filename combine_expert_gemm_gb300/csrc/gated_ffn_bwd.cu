@@ -4,11 +4,10 @@
 //   R = dy Wd;  dU = s R P,  dG = s R Q,  Hs = s H,  ds = row sums of R H
 //   dx = dx_in + dG Wg + dU Wu;  dWg = dG^T x, dWu = dU^T x, dWd = dy^T Hs
 //
-// Three products of CTA pairs (pair_gemm.cuh): R with the factors in its
-// epilogue; dx over the 2 h columns of dG and dU; and the three weight gradients
-// in one launch.  Operands that are transposed against their storage (weights in
-// the first two, activations in the third) are read MN-major, so nothing is
-// transposed in memory.  dG and dU are rounded to bf16 between the products, as
+// Two launches of CTA pairs (pair_gemm.cuh): R with the factors in its epilogue,
+// then dx and the three weight gradients together.  Operands that are transposed
+// against their storage (weights in R and dx, activations in the weight gradients)
+// are read MN-major, so nothing is transposed in memory.  dG and dU are rounded to bf16 between the products, as
 // the tensor core's operands have to be; all sums are fp32.
 #include "ffn_common.cuh"
 
@@ -37,10 +36,12 @@ struct Factor {
     static constexpr int kStages = 6;
     static constexpr int kStageBytes = 2 * OPERAND;
     static constexpr int kGroup = 0;
-    static __device__ __forceinline__ int tiles(const Args &p) { return p.mt * p.nt; }
-    static __device__ __forceinline__ Tile tile(const Args &p, int g) {
+    static __device__ __forceinline__ int count(const Args &p, int unit, int units) {
+        return strided_count(p.mt * p.nt, unit, units);
+    }
+    static __device__ __forceinline__ Tile tile(const Args &p, int unit, int units, int i) {
         int m, n;
-        band_tile(g, p.mt, p.nt, m, n);
+        band_tile(unit + i * units, p.mt, p.nt, m, n);
         return Tile{0, m * PM, n * BN};
     }
     static __device__ __forceinline__ int k_blocks(const Args &p, const Tile &) { return (p.d + BK - 1) / BK; }
@@ -107,144 +108,103 @@ struct Factor {
     }
 };
 
-struct DxArgs {
-    CUtensorMap dg, du, wg, wu, o;
-    int T, d, h, mt, nt, hb;
-    const void *dx_in;
-    float *dx32;
-    int *status;
-};
-
-template <bool F32>
-struct Dx {
-    using Args = DxArgs;
-    struct Regs {};
-    static constexpr int kStages = 6;
-    static constexpr int kStageBytes = 2 * OPERAND;
-    static constexpr int kGroup = 0;
-    static __device__ __forceinline__ int tiles(const Args &p) { return p.mt * p.nt; }
-    static __device__ __forceinline__ Tile tile(const Args &p, int g) {
-        int m, n;
-        band_tile(g, p.mt, p.nt, m, n);
-        return Tile{0, m * PM, n * BN};
-    }
-    static __device__ __forceinline__ int k_blocks(const Args &p, const Tile &) { return 2 * p.hb; }
-    static __device__ __forceinline__ void load(const Args &p, const Tile &t, int kb, uint32_t s, uint32_t bar,
-                                                int rank) {
-        const bool up = kb >= p.hb;
-        const int k = (up ? kb - p.hb : kb) * BK;
-        load_k(s, up ? &p.du : &p.dg, bar, k, t.m + rank * BM, 0);
-        load_mn(s + OPERAND, up ? &p.wu : &p.wg, bar, t.n + rank * BM, k, 0);
-    }
-    static __device__ __forceinline__ void mma(const Args &, const Tile &, uint32_t d, uint32_t s, bool first) {
-        mma_block<1, false, true>(d, s, s + OPERAND, first);
-    }
-    static __device__ __forceinline__ void before(const Args &, const Tile &, const Epi &, int, Regs &) {}
-    static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, Epi &e, int wrow, Regs &) {
-        const int row0 = t.m + wrow, row = row0 + e.lane;
-        if (row0 >= p.T) return;
-#pragma unroll 1
-        for (int c = 0; c < BN / 2; c += 32) {
-            const int col = t.n + e.col + c;
-            if (col >= p.d) break;
-            const int64_t at = (int64_t)row * p.d + col;
-            float v[32];
-            if (F32) {
-                const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.dx_in) + at);
-                float4 in[8];
-                if (p.dx_in) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        in[i] = row < p.T && col + 4 * i < p.d ? __ldcs(src + i) : make_float4(0, 0, 0, 0);
-                }
-                read32(e.taddr + c, v);
-                float4 *dst = reinterpret_cast<float4 *>(p.dx32 + at);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float4 o = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    if (p.dx_in) o = make_float4(o.x + in[i].x, o.y + in[i].y, o.z + in[i].z, o.w + in[i].w);
-                    if (row < p.T && col + 4 * i < p.d) __stcs(dst + i, o);
-                }
-            } else {
-                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.dx_in) + at);
-                uint4 in[4];
-                if (p.dx_in) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        in[i] = row < p.T && col + 8 * i < p.d ? __ldcs(src + i) : make_uint4(0, 0, 0, 0);
-                }
-                read32(e.taddr + c, v);
-                const uint32_t *iw = reinterpret_cast<const uint32_t *>(in);
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    w[i] = p.dx_in ? pack_bf16x2(v[2 * i] + bf16_lo(iw[i]), v[2 * i + 1] + bf16_hi(iw[i]))
-                                   : pack_bf16x2(v[2 * i], v[2 * i + 1]);
-                store_block16(e, w, &p.o, col, row0, 0);
-            }
-        }
-    }
-};
-
-// The three weight gradients: their tiles one after the other, dWd first.  The
-// reduction runs over the tokens.
-struct WeightArgs {
-    CUtensorMap a[3];  // dy, dG, dU: rows of the gradient
-    CUtensorMap b[2];  // Hs, x: its columns
-    CUtensorMap o[3];
+// dx and the three weight gradients in one launch: z = 0..2 are tiles of dWd
+// [d, h], dWg and dWu [h, d], reduced over the tokens, z = 3 tiles of dx, reduced over
+// the 2 h columns of dG and dU.  Alone, 96 weight tiles of an 8192-token step on 76
+// pairs take two rounds and 256 tiles of dx four, 127 us where the products take 90;
+// together the pairs get equal shares: first the kind with the longer tiles, in
+// turn, then of the other kind as many as even the shares out (Share).
+struct GradArgs {
+    CUtensorMap wa[3];     // dy, dG, dU: rows of a weight gradient
+    CUtensorMap wb[2];     // Hs, x: its columns
+    CUtensorMap wo[3];
+    CUtensorMap xa[2];     // dG, dU
+    CUtensorMap xb[2];     // Wg, Wu
+    CUtensorMap xo;
     int T, d, h;
-    int md, nd;        // 256-tiles of d and h
+    int mt, md, nd;        // 256-tiles of T, d and h
+    int hb, tb;            // k-blocks of h and T
+    const void *dx_in;
+    int long_x;            // the longer tiles are dx's
+    // `r` units have q + 1 long tiles, the others q; of the short ones they get sa each, and
+    // the others sb each, the first `se` of them one more
+    int q, r, sa, sb, se;
     int *status;
 };
 
-template <bool F32>
-struct Weight {
-    using Args = WeightArgs;
+template <bool DX32, bool DW32>
+struct Grad {
+    using Args = GradArgs;
     struct Regs {};
     static constexpr int kStages = 6;
     static constexpr int kStageBytes = 2 * OPERAND;
     static constexpr int kGroup = 0;
-    static __device__ __forceinline__ int tiles(const Args &p) { return 3 * p.md * p.nd; }
-    // z: which weight.  dWd [d, h], dWg and dWu [h, d]
-    static __device__ __forceinline__ Tile tile(const Args &p, int g) {
-        const int per = p.md * p.nd, z = g / per;
+    static __device__ __forceinline__ int longs(const Args &p, int unit) { return p.q + (unit < p.r ? 1 : 0); }
+    static __device__ __forceinline__ int count(const Args &p, int unit, int) {
+        const int v = unit - p.r;
+        return longs(p, unit) + (v < 0 ? p.sa : p.sb + (v < p.se ? 1 : 0));
+    }
+    static __device__ __forceinline__ Tile tile(const Args &p, int unit, int units, int i) {
+        const int nl = longs(p, unit);
+        bool x = p.long_x;
+        int g = unit + i * units;
+        if (i >= nl) {
+            x = !x;
+            // the short tiles: first those of the units from r on, then of the others
+            const int v = unit - p.r, rest = units - p.r;
+            g = (v >= 0 ? v * p.sb + min(v, p.se) : rest * p.sb + p.se + unit * p.sa) + i - nl;
+        }
         int m, n;
+        if (x) {
+            band_tile(g, p.mt, p.md, m, n);
+            return Tile{3, m * PM, n * BN};
+        }
+        const int per = p.md * p.nd, z = g / per;
         band_tile(g - z * per, z ? p.nd : p.md, z ? p.md : p.nd, m, n);
         return Tile{z, m * PM, n * BN};
     }
-    static __device__ __forceinline__ int k_blocks(const Args &p, const Tile &) { return (p.T + BK - 1) / BK; }
+    static __device__ __forceinline__ int k_blocks(const Args &p, const Tile &t) { return t.z == 3 ? 2 * p.hb : p.tb; }
     static __device__ __forceinline__ void load(const Args &p, const Tile &t, int kb, uint32_t s, uint32_t bar,
                                                 int rank) {
-        load_mn(s, &p.a[t.z], bar, t.m + rank * BM, kb * BK, 0);
-        load_mn(s + OPERAND, &p.b[t.z ? 1 : 0], bar, t.n + rank * BM, kb * BK, 0);
+        if (t.z == 3) {
+            const int up = kb >= p.hb, k = (kb - up * p.hb) * BK;
+            load_k(s, &p.xa[up], bar, k, t.m + rank * BM, 0);
+            load_mn(s + OPERAND, &p.xb[up], bar, t.n + rank * BM, k, 0);
+        } else {
+            load_mn(s, &p.wa[t.z], bar, t.m + rank * BM, kb * BK, 0);
+            load_mn(s + OPERAND, &p.wb[t.z ? 1 : 0], bar, t.n + rank * BM, kb * BK, 0);
+        }
     }
-    static __device__ __forceinline__ void mma(const Args &, const Tile &, uint32_t d, uint32_t s, bool first) {
-        mma_block<1, true, true>(d, s, s + OPERAND, first);
+    static __device__ __forceinline__ void mma(const Args &, const Tile &t, uint32_t d, uint32_t s, bool first) {
+        if (t.z == 3) mma_block<1, false, true>(d, s, s + OPERAND, first);
+        else mma_block<1, true, true>(d, s, s + OPERAND, first);
     }
     static __device__ __forceinline__ void before(const Args &, const Tile &, const Epi &, int, Regs &) {}
     static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, Epi &e, int wrow, Regs &) {
-        const int row0 = t.m + wrow, rows = t.z ? p.h : p.d, cols = t.z ? p.d : p.h;
+        const bool x = t.z == 3;
+        const int row0 = t.m + wrow, row = row0 + e.lane;
+        const int rows = x ? p.T : t.z ? p.h : p.d, cols = t.z ? p.d : p.h;
         if (row0 >= rows) return;
-        const CUtensorMap *map = &p.o[t.z];
+        const CUtensorMap *map = x ? &p.xo : &p.wo[t.z];
+        const bool f32 = x ? DX32 : DW32;
+        // a store of 2 KB only waits for the one before the last: a 4 KB one of another
+        // tile has to have left both blocks
+        if (DX32 != DW32 && e.lane == 0) bulk_wait_read<0>();
 #pragma unroll 1
         for (int c = 0; c < BN / 2; c += 32) {
             const int col = t.n + e.col + c;
             if (col >= cols) break;
+            float add[32];
+            const bool more = x && p.dx_in;
+            if (more) fetch_dx(p, row, col, add);
             float v[32];
             read32(e.taddr + c, v);
-            if (F32) {
-                if (e.lane == 0) bulk_wait_read<0>();
-                __syncwarp();
+            if (more) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    *reinterpret_cast<float4 *>(e.blk + e.lane * 128 + ((q ^ (e.lane & 7)) * 16)) =
-                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (e.lane == 0) {
-                    tma_store_3d(map, smem_u32(e.blk), col, row0, 0);
-                    bulk_commit();
-                }
+                for (int i = 0; i < 32; ++i) v[i] += add[i];
+            }
+            if (f32) {
+                store_block32(e, v, map, col, row0);
             } else {
                 uint32_t w[16];
 #pragma unroll
@@ -253,7 +213,63 @@ struct Weight {
             }
         }
     }
+    // 32 columns of this lane's row of dx_in.
+    static __device__ __forceinline__ void fetch_dx(const Args &p, int row, int col, float (&v)[32]) {
+        const int64_t at = (int64_t)row * p.d + col;
+        if (DX32) {
+            const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.dx_in) + at);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 q = row < p.T && col + 4 * i < p.d ? __ldcs(src + i) : make_float4(0, 0, 0, 0);
+                v[4 * i] = q.x;
+                v[4 * i + 1] = q.y;
+                v[4 * i + 2] = q.z;
+                v[4 * i + 3] = q.w;
+            }
+        } else {
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.dx_in) + at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 q = row < p.T && col + 8 * i < p.d ? __ldcs(src + i) : make_uint4(0, 0, 0, 0);
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[8 * i + 2 * k] = bf16_lo(w[k]);
+                    v[8 * i + 2 * k + 1] = bf16_hi(w[k]);
+                }
+            }
+        }
+    }
+    // A 32 x 32 block of fp32 through the warp's 4 KB.
+    static __device__ __forceinline__ void store_block32(Epi &e, const float (&v)[32], const CUtensorMap *map, int x,
+                                                         int y) {
+        if (e.lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<float4 *>(e.blk + e.lane * 128 + ((q ^ (e.lane & 7)) * 16)) =
+                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (e.lane == 0) {
+            tma_store_3d(map, smem_u32(e.blk), x, y, 0);
+            bulk_commit();
+        }
+    }
 };
+
+// Shares of `units` pairs: nl long tiles of cost cl in turn, and ns short ones of cost cs
+// so that the pairs' costs come out even.
+inline void share(GradArgs &p, int units, int64_t nl, int64_t cl, int64_t ns, int64_t cs) {
+    p.q = (int)(nl / units);
+    p.r = (int)(nl % units);
+    const int64_t even = (nl * cl + ns * cs) / units;
+    const int64_t left = even - (p.q + 1) * cl;
+    p.sa = p.r == 0 || left <= 0 ? 0 : (int)std::min<int64_t>(left / cs, ns / p.r);
+    const int64_t rest = ns - (int64_t)p.r * p.sa;
+    p.sb = (int)(rest / (units - p.r));
+    p.se = (int)(rest % (units - p.r));
+}
 
 // out[t] = the sum of part[0..n)[t], in order.
 template <bool F32>
@@ -340,38 +356,33 @@ MOE_API moe_status moe_gated_ffn_backward(int32_t T, int32_t d, int32_t h, const
     f.scale = token_scale;
     f.part = dtoken_scale ? reinterpret_cast<float *>(base + at.part) : nullptr;
     f.status = status;
-    DxArgs g{};
+    GradArgs g{};
     g.T = T;
     g.d = d;
     g.h = h;
     g.mt = f.mt;
-    g.nt = (d + BN - 1) / BN;
+    g.md = (d + BN - 1) / BN;
+    g.nd = f.nt;
     g.hb = (h + BK - 1) / BK;
+    g.tb = (T + BK - 1) / BK;
     g.dx_in = dx_in;
-    g.dx32 = static_cast<float *>(dx);
     g.status = status;
-    WeightArgs w{};
-    w.T = T;
-    w.d = d;
-    w.h = h;
-    w.md = g.nt;
-    w.nd = f.nt;
-    w.status = status;
     const bool dx32 = dx_dtype == MOE_FP32;
     if (!map_k(&f.dy, dy, d, T) || !map_mn(&f.wd, w_down, h, d) || !map_store(&f.odg, base + at.dg, h, T) ||
         !map_store(&f.odu, base + at.du, h, T) || !map_store(&f.ohs, base + at.hs, h, T) ||
-        !map_k(&g.dg, base + at.dg, h, T) || !map_k(&g.du, base + at.du, h, T) || !map_mn(&g.wg, w_gate, d, h) ||
-        !map_mn(&g.wu, w_up, d, h) || (!dx32 && !map_store(&g.o, dx, d, T)) || !map_mn(&w.a[0], dy, d, T) ||
-        !map_mn(&w.a[1], base + at.dg, h, T) || !map_mn(&w.a[2], base + at.du, h, T) ||
-        !map_mn(&w.b[0], hs, h, T) || !map_mn(&w.b[1], x, d, T))
+        !map_k(&g.xa[0], base + at.dg, h, T) || !map_k(&g.xa[1], base + at.du, h, T) ||
+        !map_mn(&g.xb[0], w_gate, d, h) || !map_mn(&g.xb[1], w_up, d, h) ||
+        !(dx32 ? make_map_f32_3d(&g.xo, dx, d, T, 1) : map_store(&g.xo, dx, d, T)) || !map_mn(&g.wa[0], dy, d, T) ||
+        !map_mn(&g.wa[1], base + at.dg, h, T) || !map_mn(&g.wa[2], base + at.du, h, T) ||
+        !map_mn(&g.wb[0], hs, h, T) || !map_mn(&g.wb[1], x, d, T))
         return MOE_ERR_CUDA;
     void *dw[3] = {dw_down, dw_gate, dw_up};
     for (int i = 0; i < 3; ++i) {
         const uint64_t inner = i ? d : h, rows = i ? h : d;
-        if (!(dw32 ? make_map_f32_3d(&w.o[i], dw[i], inner, rows, 1) : map_store(&w.o[i], dw[i], inner, rows)))
+        if (!(dw32 ? make_map_f32_3d(&g.wo[i], dw[i], inner, rows, 1) : map_store(&g.wo[i], dw[i], inner, rows)))
             return MOE_ERR_CUDA;
     }
-    const int64_t ftiles = (int64_t)f.mt * f.nt, gtiles = (int64_t)g.mt * g.nt;
+    const int64_t ftiles = (int64_t)f.mt * f.nt;
     r = token_scale ? launch<Factor<true>>(f, ftiles, stream) : launch<Factor<false>>(f, ftiles, stream);
     if (r != MOE_OK) return r;
     if (dtoken_scale) {
@@ -379,8 +390,11 @@ MOE_API moe_status moe_gated_ffn_backward(int32_t T, int32_t d, int32_t h, const
                    (int)T, 2 * f.nt, f.part, dtoken_scale);
         if ((r = launch_status()) != MOE_OK) return r;
     }
-    r = dx32 ? launch<Dx<true>>(g, gtiles, stream) : launch<Dx<false>>(g, gtiles, stream);
-    if (r != MOE_OK) return r;
-    const int64_t wtiles = (int64_t)3 * w.md * w.nd;
-    return dw32 ? launch<Weight<true>>(w, wtiles, stream) : launch<Weight<false>>(w, wtiles, stream);
+    const int64_t wt = (int64_t)3 * g.md * g.nd, xt = (int64_t)g.mt * g.md;
+    const int units = pairs_for(wt + xt);
+    g.long_x = 2 * g.hb > g.tb;
+    if (g.long_x) share(g, units, xt, 2 * g.hb, wt, g.tb);
+    else share(g, units, wt, g.tb, xt, 2 * g.hb);
+    if (dx32) return dw32 ? launch<Grad<true, true>>(g, wt + xt, stream) : launch<Grad<true, false>>(g, wt + xt, stream);
+    return dw32 ? launch<Grad<false, true>>(g, wt + xt, stream) : launch<Grad<false, false>>(g, wt + xt, stream);
 }

@@ -203,9 +203,11 @@ struct Ns {
     static __device__ __forceinline__ int per_matrix(const Args &p) {
         return kSym ? p.mt * (p.mt + 1) / 2 : p.mt * p.nt;
     }
-    static __device__ __forceinline__ int tiles(const Args &p) { return p.B * per_matrix(p); }
-    static __device__ __forceinline__ Tile tile(const Args &p, int g) {
-        const int per = per_matrix(p), z = g / per;
+    static __device__ __forceinline__ int count(const Args &p, int unit, int units) {
+        return strided_count(p.B * per_matrix(p), unit, units);
+    }
+    static __device__ __forceinline__ Tile tile(const Args &p, int unit, int units, int i) {
+        const int g = unit + i * units, per = per_matrix(p), z = g / per;
         int r = g - z * per, m = 0, n;
         if (kSym) {  // row m of the upper triangle has mt - m tiles
             while (r >= p.mt - m) r -= p.mt - m++;

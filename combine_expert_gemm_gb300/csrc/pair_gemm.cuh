@@ -168,6 +168,11 @@ __device__ __forceinline__ void band_tile(int g, int mt, int nt, int &m, int &n)
     n = r / rows;
 }
 
+// Tiles g = unit, unit + units, ... of `total`.
+__device__ __forceinline__ int strided_count(int total, int unit, int units) {
+    return unit < total ? (total - unit - 1) / units + 1 : 0;
+}
+
 // 32 columns of the accumulator at taddr.
 __device__ __forceinline__ void read32(uint32_t taddr, float (&v)[32]) {
     uint32_t a[16], b[16];
@@ -225,7 +230,7 @@ __global__ void __launch_bounds__(threads<P>(), 1) pair_gemm(const __grid_consta
     int *status = p.status;
     const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
-    const int unit0 = (int)blockIdx.x / 2, units = (int)gridDim.x / 2;
+    const int unit = (int)blockIdx.x / 2, units = (int)gridDim.x / 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -246,7 +251,7 @@ __global__ void __launch_bounds__(threads<P>(), 1) pair_gemm(const __grid_consta
     cluster_sync_all();  // barriers of both CTAs exist before any remote arrival
     tc_fence_after();
     const uint32_t tmem_base = bars->tmem_base;
-    const int total = P::tiles(p);
+    const int count = P::count(p, unit, units);  // tiles of this pair
     // What came so far touches only this pair's own shared and tensor memory: it may
     // run beside the grid before this one, and every thread waits for that grid here.
     pdl_enter();
@@ -259,8 +264,8 @@ __global__ void __launch_bounds__(threads<P>(), 1) pair_gemm(const __grid_consta
             uint32_t phase = 0;
             int issued = 0;
             bool ok = true;
-            for (int g = unit0; g < total && ok; g += units) {
-                const Tile t = P::tile(p, g);
+            for (int i = 0; i < count && ok; ++i) {
+                const Tile t = P::tile(p, unit, units, i);
                 const int nk = P::k_blocks(p, t);
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!mbar_wait(smem_u32(&bars->empty[stage]), phase ^ 1, status, abort)) {
@@ -298,8 +303,8 @@ __global__ void __launch_bounds__(threads<P>(), 1) pair_gemm(const __grid_consta
             int acc = 0;
             uint32_t acc_phase = 0;
             bool ok = true;
-            for (int g = unit0; g < total && ok; g += units) {
-                const Tile t = P::tile(p, g);
+            for (int i = 0; i < count && ok; ++i) {
+                const Tile t = P::tile(p, unit, units, i);
                 const int nk = P::k_blocks(p, t);
                 for (int k0 = 0; k0 < nk && ok; k0 += P::kGroup ? P::kGroup : nk) {
                     const int k1 = P::kGroup ? min(nk, k0 + P::kGroup) : nk;
@@ -354,8 +359,8 @@ __global__ void __launch_bounds__(threads<P>(), 1) pair_gemm(const __grid_consta
                 acc_phase ^= 1;
             }
         };
-        for (int g = unit0; g < total && ok; g += units) {
-            const Tile t = P::tile(p, g);
+        for (int i = 0; i < count && ok; ++i) {
+            const Tile t = P::tile(p, unit, units, i);
             if constexpr (P::kGroup == 0) {
                 typename P::Regs regs;
                 P::before(p, t, e, wrow, regs);
@@ -401,12 +406,17 @@ __global__ void __launch_bounds__(threads<P>(), 1) pair_gemm(const __grid_consta
     }
 }
 
+// CTA pairs of a launch over so many tiles.
+inline int pairs_for(int64_t tiles) {
+    return (int)std::min<int64_t>(std::max(num_sms() / 2, 1), std::max<int64_t>(tiles, 1));
+}
+
 template <class P>
 moe_status launch(const typename P::Args &args, int64_t tiles, cudaStream_t st) {
     static PerDeviceOnce smem_attr;
     if (!device_once(smem_attr, [] { return set_smem_limit(pair_gemm<P>, smem_bytes<P>()); }))
         return MOE_ERR_CUDA;
-    const int pairs = (int)std::min<int64_t>(std::max(num_sms() / 2, 1), std::max<int64_t>(tiles, 1));
+    const int pairs = pairs_for(tiles);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
     cfg.blockDim = dim3(threads<P>());
