@@ -11,6 +11,7 @@
 // adds and scales in its epilogue.  Widths are multiples of 8 only: what a tile
 // reaches past T, d or h is read as zeros and never stored.
 #include "ffn_common.cuh"
+#include "small_gemm.cuh"
 
 namespace moe {
 namespace {
@@ -182,6 +183,101 @@ struct Out {
     }
 };
 
+// ------------------------------------------------------------- few tokens --
+
+__device__ __forceinline__ uint2 pack4(float a, float b, float c, float d) {
+    return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+}
+
+struct SmallHiddenArgs {
+    CUtensorMap wg, wu, x;
+    int T, h, nk, split;
+    uint16_t *o, *p, *q;
+    int *status;
+};
+
+// The tile's rows 0-63 are gate rows, 64-127 the up rows of the same units.
+template <int ACT, bool SAVE, int N>
+struct SmallHidden {
+    using Args = SmallHiddenArgs;
+    static constexpr int kN = N;
+    static constexpr bool kPairs = true, kEarly = false;
+    static constexpr int kAMn = 0;
+    static __device__ __forceinline__ void load_a(const Args &p, uint32_t s, uint32_t bar, int kb, int f0) {
+        small::load_box(s, &p.wg, bar, kb * BK, f0);
+        small::load_box(s + small::kABytes / 2, &p.wu, bar, kb * BK, f0);
+    }
+    static __device__ __forceinline__ void load_b(const Args &p, uint32_t s, uint32_t bar, int kb, int t0) {
+        small::load_box(s, &p.x, bar, kb * BK, t0);
+    }
+    static __device__ __forceinline__ void emit(const Args &p, bool ok, int t, int f, const float4 &g,
+                                                const float4 &u, int) {
+        if (!ok || f >= p.h) return;
+        float a[4], d[4];
+        activate<ACT>(g.x, a[0], d[0]);
+        activate<ACT>(g.y, a[1], d[1]);
+        activate<ACT>(g.z, a[2], d[2]);
+        activate<ACT>(g.w, a[3], d[3]);
+        const int64_t at = (int64_t)t * p.h + f;
+        *reinterpret_cast<uint2 *>(p.o + at) = pack4(a[0] * u.x, a[1] * u.y, a[2] * u.z, a[3] * u.w);
+        if (SAVE) {
+            *reinterpret_cast<uint2 *>(p.p + at) = pack4(a[0], a[1], a[2], a[3]);
+            *reinterpret_cast<uint2 *>(p.q + at) = pack4(u.x * d[0], u.y * d[1], u.z * d[2], u.w * d[3]);
+        }
+    }
+};
+
+struct SmallOutArgs {
+    CUtensorMap wd, hact;
+    int T, d, nk, split;
+    const uint16_t *add;
+    const float *scale;
+    uint16_t *y;
+    int *status;
+};
+
+// Runs right behind SmallHidden, so Wd is on its way before that has finished.
+template <int N>
+struct SmallOut {
+    using Args = SmallOutArgs;
+    static constexpr int kN = N;
+    static constexpr bool kPairs = false, kEarly = true;
+    static constexpr int kAMn = 0;
+    static __device__ __forceinline__ void load_a(const Args &p, uint32_t s, uint32_t bar, int kb, int f0) {
+        small::load_box(s, &p.wd, bar, kb * BK, f0);
+    }
+    static __device__ __forceinline__ void load_b(const Args &p, uint32_t s, uint32_t bar, int kb, int t0) {
+        small::load_box(s, &p.hact, bar, kb * BK, t0);
+    }
+    static __device__ __forceinline__ void emit(const Args &p, bool ok, int t, int f, const float4 &v,
+                                                const float4 &, int) {
+        if (!ok || f >= p.d) return;
+        const int64_t at = (int64_t)t * p.d + f;
+        float4 o = v;
+        if (p.scale) {
+            const float s = p.scale[t];
+            o = make_float4(o.x * s, o.y * s, o.z * s, o.w * s);
+        }
+        if (p.add) {
+            const uint2 a = *reinterpret_cast<const uint2 *>(p.add + at);
+            const float s = p.scale ? p.scale[t] : 1.0f;
+            o = make_float4(fmaf(s, v.x, bf16_lo(a.x)), fmaf(s, v.y, bf16_hi(a.x)), fmaf(s, v.z, bf16_lo(a.y)),
+                            fmaf(s, v.w, bf16_hi(a.y)));
+        }
+        *reinterpret_cast<uint2 *>(p.y + at) = pack4(o.x, o.y, o.z, o.w);
+    }
+};
+
+template <int ACT>
+moe_status launch_small_hidden(const SmallHiddenArgs &a, bool save, int ft, cudaStream_t st) {
+    return small::with_tokens(a.T, [&](auto n) {
+        constexpr int N = decltype(n)::value;
+        const int tt = (a.T + N - 1) / N;
+        return save ? small::launch<SmallHidden<ACT, true, N>>(a, ft, tt, st)
+                    : small::launch<SmallHidden<ACT, false, N>>(a, ft, tt, st);
+    });
+}
+
 template <int ACT>
 moe_status launch_hidden(const HiddenArgs &a, bool save, cudaStream_t st) {
     const int64_t tiles = (int64_t)a.mt * a.nt;
@@ -216,6 +312,41 @@ MOE_API moe_status moe_gated_ffn(int32_t T, int32_t d, int32_t h, int32_t act, c
     for (const void *q : ptrs)
         if (!aligned16(q)) return MOE_ERR_ALIGNMENT;
 
+    const bool save = p_save != nullptr;
+    const int ft1 = (h + small::kM / 2 - 1) / (small::kM / 2), ft2 = (d + small::kM - 1) / small::kM;
+    if (small::fits(ft1, T) && small::fits(ft2, T)) {
+        const int n = small::tile_tokens(T), tt = (T + n - 1) / n;
+        SmallHiddenArgs a{};
+        a.T = T;
+        a.h = h;
+        a.nk = (d + BK - 1) / BK;
+        a.split = small::split_for((int64_t)ft1 * tt, a.nk);
+        a.o = reinterpret_cast<uint16_t *>(h_act);
+        a.p = reinterpret_cast<uint16_t *>(p_save);
+        a.q = reinterpret_cast<uint16_t *>(q_save);
+        a.status = static_cast<int *>(ws);
+        SmallOutArgs o{};
+        o.T = T;
+        o.d = d;
+        o.nk = (h + BK - 1) / BK;
+        o.split = small::split_for((int64_t)ft2 * tt, o.nk);
+        o.add = reinterpret_cast<const uint16_t *>(add);
+        o.scale = token_scale;
+        o.y = reinterpret_cast<uint16_t *>(y);
+        o.status = a.status;
+        if (!make_map_16(&a.wg, w_gate, d, h, 1, d, 64, small::kM / 2) ||
+            !make_map_16(&a.wu, w_up, d, h, 1, d, 64, small::kM / 2) || !make_map_16(&a.x, x, d, T, 1, d, 64, n) ||
+            !make_map_16(&o.wd, w_down, h, d, 1, h, 64, small::kM) || !make_map_16(&o.hact, h_act, h, T, 1, h, 64, n))
+            return MOE_ERR_CUDA;
+        r = act == MOE_ACT_SILU   ? launch_small_hidden<MOE_ACT_SILU>(a, save, ft1, stream)
+            : act == MOE_ACT_GELU ? launch_small_hidden<MOE_ACT_GELU>(a, save, ft1, stream)
+                                  : launch_small_hidden<MOE_ACT_RELU>(a, save, ft1, stream);
+        if (r != MOE_OK) return r;
+        return small::with_tokens(T, [&](auto k) {
+            return small::launch<SmallOut<decltype(k)::value>>(o, ft2, tt, stream);
+        });
+    }
+
     HiddenArgs a{};
     a.T = T;
     a.d = d;
@@ -237,7 +368,6 @@ MOE_API moe_status moe_gated_ffn(int32_t T, int32_t d, int32_t h, int32_t act, c
         !map_store(&a.q, q_save ? q_save : h_act, h, T) || !map_k(&o.hact, h_act, h, T) ||
         !map_k(&o.wd, w_down, h, d) || !map_store(&o.o, y, d, T))
         return MOE_ERR_CUDA;
-    const bool save = p_save != nullptr;
     r = act == MOE_ACT_SILU   ? launch_hidden<MOE_ACT_SILU>(a, save, stream)
         : act == MOE_ACT_GELU ? launch_hidden<MOE_ACT_GELU>(a, save, stream)
                               : launch_hidden<MOE_ACT_RELU>(a, save, stream);
