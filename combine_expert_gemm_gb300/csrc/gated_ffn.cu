@@ -191,7 +191,7 @@ __device__ __forceinline__ uint2 pack4(float a, float b, float c, float d) {
 
 struct SmallHiddenArgs {
     CUtensorMap wg, wu, x;
-    int T, h, nk, split;
+    int T, h, nk, split, tt;
     uint16_t *o, *p, *q;
     int *status;
 };
@@ -202,16 +202,18 @@ struct SmallHidden {
     using Args = SmallHiddenArgs;
     static constexpr int kN = N;
     static constexpr bool kPairs = true, kEarly = false;
-    static constexpr int kAMn = 0;
-    static __device__ __forceinline__ void load_a(const Args &p, uint32_t s, uint32_t bar, int kb, int f0) {
+    static constexpr int kAMn = 0, kBMn = 0, kFmt = 1, kPieces = 1;
+    static __device__ __forceinline__ void load_a(const Args &p, uint32_t s, uint32_t bar, int kb, int f0, int,
+                                                  int) {
         small::load_box(s, &p.wg, bar, kb * BK, f0);
         small::load_box(s + small::kABytes / 2, &p.wu, bar, kb * BK, f0);
     }
-    static __device__ __forceinline__ void load_b(const Args &p, uint32_t s, uint32_t bar, int kb, int t0) {
+    static __device__ __forceinline__ void load_b(const Args &p, uint32_t s, uint32_t bar, int kb, int t0, int,
+                                                  int) {
         small::load_box(s, &p.x, bar, kb * BK, t0);
     }
-    static __device__ __forceinline__ void emit(const Args &p, bool ok, int t, int f, const float4 &g,
-                                                const float4 &u, int) {
+    static __device__ __forceinline__ void emit(const Args &p, bool ok, int t, int f, int, const float4 &g,
+                                                const float4 &u) {
         if (!ok || f >= p.h) return;
         float a[4], d[4];
         activate<ACT>(g.x, a[0], d[0]);
@@ -229,7 +231,7 @@ struct SmallHidden {
 
 struct SmallOutArgs {
     CUtensorMap wd, hact;
-    int T, d, nk, split;
+    int T, d, nk, split, tt;
     const uint16_t *add;
     const float *scale;
     uint16_t *y;
@@ -242,15 +244,17 @@ struct SmallOut {
     using Args = SmallOutArgs;
     static constexpr int kN = N;
     static constexpr bool kPairs = false, kEarly = true;
-    static constexpr int kAMn = 0;
-    static __device__ __forceinline__ void load_a(const Args &p, uint32_t s, uint32_t bar, int kb, int f0) {
+    static constexpr int kAMn = 0, kBMn = 0, kFmt = 1, kPieces = 1;
+    static __device__ __forceinline__ void load_a(const Args &p, uint32_t s, uint32_t bar, int kb, int f0, int,
+                                                  int) {
         small::load_box(s, &p.wd, bar, kb * BK, f0);
     }
-    static __device__ __forceinline__ void load_b(const Args &p, uint32_t s, uint32_t bar, int kb, int t0) {
+    static __device__ __forceinline__ void load_b(const Args &p, uint32_t s, uint32_t bar, int kb, int t0, int,
+                                                  int) {
         small::load_box(s, &p.hact, bar, kb * BK, t0);
     }
-    static __device__ __forceinline__ void emit(const Args &p, bool ok, int t, int f, const float4 &v,
-                                                const float4 &, int) {
+    static __device__ __forceinline__ void emit(const Args &p, bool ok, int t, int f, int, const float4 &v,
+                                                const float4 &) {
         if (!ok || f >= p.d) return;
         const int64_t at = (int64_t)t * p.d + f;
         float4 o = v;
@@ -272,9 +276,8 @@ template <int ACT>
 moe_status launch_small_hidden(const SmallHiddenArgs &a, bool save, int ft, cudaStream_t st) {
     return small::with_tokens(a.T, [&](auto n) {
         constexpr int N = decltype(n)::value;
-        const int tt = (a.T + N - 1) / N;
-        return save ? small::launch<SmallHidden<ACT, true, N>>(a, ft, tt, st)
-                    : small::launch<SmallHidden<ACT, false, N>>(a, ft, tt, st);
+        return save ? small::launch<SmallHidden<ACT, true, N>>(a, ft, 1, st)
+                    : small::launch<SmallHidden<ACT, false, N>>(a, ft, 1, st);
     });
 }
 
@@ -317,15 +320,16 @@ MOE_API moe_status moe_gated_ffn(int32_t T, int32_t d, int32_t h, int32_t act, c
     if (small::fits(ft1, T) && small::fits(ft2, T)) {
         const int n = small::tile_tokens(T), tt = (T + n - 1) / n;
         SmallHiddenArgs a{};
+        SmallOutArgs o{};
         a.T = T;
         a.h = h;
         a.nk = (d + BK - 1) / BK;
+        a.tt = o.tt = tt;
         a.split = small::split_for((int64_t)ft1 * tt, a.nk);
         a.o = reinterpret_cast<uint16_t *>(h_act);
         a.p = reinterpret_cast<uint16_t *>(p_save);
         a.q = reinterpret_cast<uint16_t *>(q_save);
         a.status = static_cast<int *>(ws);
-        SmallOutArgs o{};
         o.T = T;
         o.d = d;
         o.nk = (h + BK - 1) / BK;
@@ -343,7 +347,7 @@ MOE_API moe_status moe_gated_ffn(int32_t T, int32_t d, int32_t h, int32_t act, c
                                   : launch_small_hidden<MOE_ACT_RELU>(a, save, ft1, stream);
         if (r != MOE_OK) return r;
         return small::with_tokens(T, [&](auto k) {
-            return small::launch<SmallOut<decltype(k)::value>>(o, ft2, tt, stream);
+            return small::launch<SmallOut<decltype(k)::value>>(o, ft2, 1, stream);
         });
     }
 

@@ -10,6 +10,7 @@
 // are read MN-major, so nothing is transposed in memory.  dG and dU are rounded to bf16 between the products, as
 // the tensor core's operands have to be; all sums are fp32.
 #include "ffn_common.cuh"
+#include "small_gemm.cuh"
 
 namespace moe {
 namespace {
@@ -105,6 +106,64 @@ struct Factor {
             if (SCALE) store_block16(e, hs, &p.ohs, col, row0, 0);
         }
         if (SCALE && p.part && row < p.T) p.part[(int64_t)(colh / (BN / 2)) * p.T + row] = ds;
+    }
+};
+
+// The same for few tokens (small_gemm.cuh): the features are hidden units, Wd is
+// read MN-major.
+struct SmallFactorArgs {
+    CUtensorMap wd, dy;
+    int T, h, nk, split, tt;
+    const uint16_t *p, *q, *hact;
+    const float *scale;
+    uint16_t *dg, *du, *hs;
+    float *part;  // [ceil(h / 128) split][T], or NULL
+    int *status;
+};
+
+template <bool SCALE, int N>
+struct SmallFactor {
+    using Args = SmallFactorArgs;
+    static constexpr int kN = N;
+    static constexpr bool kPairs = false, kEarly = false;
+    static constexpr int kAMn = 1, kBMn = 0, kFmt = 1, kPieces = 1;
+    static __device__ __forceinline__ void load_a(const Args &p, uint32_t s, uint32_t bar, int kb, int f0, int, int) {
+        small::load_box(s, &p.wd, bar, f0, kb * BK);
+        small::load_box(s + BLK, &p.wd, bar, f0 + 64, kb * BK);
+    }
+    static __device__ __forceinline__ void load_b(const Args &p, uint32_t s, uint32_t bar, int kb, int t0, int, int) {
+        small::load_box(s, &p.dy, bar, kb * BK, t0);
+    }
+    static __device__ __forceinline__ uint2 load4(const uint16_t *p, int64_t at) {
+        return *reinterpret_cast<const uint2 *>(p + at);
+    }
+    static __device__ __forceinline__ void emit(const Args &p, bool ok, int t, int f, int, const float4 &r,
+                                                const float4 &) {
+        const int64_t at = (int64_t)t * p.h + f;
+        float ds = 0.0f;
+        if (ok && f < p.h) {
+            const uint2 a = load4(p.p, at), b = load4(p.q, at);
+            float4 v = r;
+            if (SCALE) {
+                const uint2 c = load4(p.hact, at);
+                const float s = p.scale[t];
+                const float h0 = bf16_lo(c.x), h1 = bf16_hi(c.x), h2 = bf16_lo(c.y), h3 = bf16_hi(c.y);
+                ds = fmaf(r.x, h0, fmaf(r.y, h1, fmaf(r.z, h2, r.w * h3)));
+                *reinterpret_cast<uint2 *>(p.hs + at) = make_uint2(pack_bf16x2(s * h0, s * h1), pack_bf16x2(s * h2, s * h3));
+                v = make_float4(s * r.x, s * r.y, s * r.z, s * r.w);
+            }
+            *reinterpret_cast<uint2 *>(p.du + at) = make_uint2(pack_bf16x2(v.x * bf16_lo(a.x), v.y * bf16_hi(a.x)),
+                                                               pack_bf16x2(v.z * bf16_lo(a.y), v.w * bf16_hi(a.y)));
+            *reinterpret_cast<uint2 *>(p.dg + at) = make_uint2(pack_bf16x2(v.x * bf16_lo(b.x), v.y * bf16_hi(b.x)),
+                                                               pack_bf16x2(v.z * bf16_lo(b.y), v.w * bf16_hi(b.y)));
+        }
+        if (SCALE && p.part) {
+            // the lanes of a token: this CTA's share of the tile's features (0 where
+            // it lies past h)
+            const int per = small::kM / 4 / p.split;
+            for (int o = per / 2; o; o >>= 1) ds += __shfl_xor_sync(0xFFFFFFFFu, ds, o);
+            if (ok && (threadIdx.x & (per - 1)) == 0) p.part[(int64_t)(f / (small::kM / p.split)) * p.T + t] = ds;
+        }
     }
 };
 
@@ -285,16 +344,28 @@ __global__ void __launch_bounds__(256) token_scale_sum(int T, int n, const float
 
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
+// Cluster size of SmallFactor, or 0 where the tiles are too many for it.
+inline int small_split(int T, int d, int h) {
+    const int ft = (h + small::kM - 1) / small::kM, n = small::tile_tokens(T);
+    return small::fits(ft, T) ? small::split_for((int64_t)ft * ((T + n - 1) / n), (d + BK - 1) / BK) : 0;
+}
+
+// Parts of dtoken_scale: half tiles of 256, or the shares of small tiles.
+inline int scale_parts(int T, int d, int h) {
+    const int split = small_split(T, d, h);
+    return split ? (h + small::kM - 1) / small::kM * split : 2 * ((h + BN - 1) / BN);
+}
+
 // Workspace: status, dG, dU, Hs [T, h] bf16, the parts of dtoken_scale.
 struct Layout {
     size_t dg, du, hs, part, bytes;
-    Layout(int64_t T, int64_t h) {
+    Layout(int64_t T, int64_t d, int64_t h) {
         const size_t a = align256((size_t)(T * h * 2));
         dg = 256;
         du = dg + a;
         hs = du + a;
         part = hs + a;
-        bytes = part + align256((size_t)(2 * ((h + BN - 1) / BN) * T * 4));
+        bytes = part + align256((size_t)(scale_parts((int)T, (int)d, (int)h) * T * 4));
     }
 };
 
@@ -305,7 +376,7 @@ using namespace moe;
 
 MOE_API size_t moe_gated_ffn_backward_workspace_bytes(int32_t T, int32_t d, int32_t h) {
     if (check_ffn(T, d, h) != MOE_OK) return 0;
-    return Layout(T, h).bytes;
+    return Layout(T, d, h).bytes;
 }
 
 MOE_API moe_status moe_gated_ffn_backward(int32_t T, int32_t d, int32_t h, const moe_bf16 *x,
@@ -325,7 +396,7 @@ MOE_API moe_status moe_gated_ffn_backward(int32_t T, int32_t d, int32_t h, const
     if (T > 0 && (!x || !h_act || !p_save || !q_save || !dy || !dx)) return MOE_ERR_INVALID_ARG;
     // the weights' gradients read x and dy after dx is written
     if (T > 0 && (dx == x || dx == dy)) return MOE_ERR_INVALID_ARG;
-    const Layout at(T, h);
+    const Layout at(T, d, h);
     if (!ws || ws_bytes < at.bytes || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_WORKSPACE;
     const void *ptrs[] = {x,  w_gate, w_up, w_down,  token_scale, h_act,   p_save,      q_save,
                           dy, dx_in,  dx,   dw_gate, dw_up,       dw_down, dtoken_scale};
@@ -383,11 +454,39 @@ MOE_API moe_status moe_gated_ffn_backward(int32_t T, int32_t d, int32_t h, const
             return MOE_ERR_CUDA;
     }
     const int64_t ftiles = (int64_t)f.mt * f.nt;
-    r = token_scale ? launch<Factor<true>>(f, ftiles, stream) : launch<Factor<false>>(f, ftiles, stream);
+    const int split = small_split(T, d, h);
+    if (split) {
+        SmallFactorArgs a{};
+        const int n = small::tile_tokens(T);
+        a.T = T;
+        a.h = h;
+        a.nk = (d + BK - 1) / BK;
+        a.split = split;
+        a.tt = (T + n - 1) / n;
+        a.p = f.p;
+        a.q = f.q;
+        a.hact = f.hact;
+        a.scale = token_scale;
+        a.dg = reinterpret_cast<uint16_t *>(base + at.dg);
+        a.du = reinterpret_cast<uint16_t *>(base + at.du);
+        a.hs = reinterpret_cast<uint16_t *>(base + at.hs);
+        a.part = f.part;
+        a.status = status;
+        a.wd = f.wd;
+        if (!make_map_16(&a.dy, dy, d, T, 1, d, 64, n)) return MOE_ERR_CUDA;
+        r = small::with_tokens(T, [&](auto k) {
+            constexpr int N = decltype(k)::value;
+            const int ft = (h + small::kM - 1) / small::kM;
+            return token_scale ? small::launch<SmallFactor<true, N>>(a, ft, 1, stream)
+                               : small::launch<SmallFactor<false, N>>(a, ft, 1, stream);
+        });
+    } else {
+        r = token_scale ? launch<Factor<true>>(f, ftiles, stream) : launch<Factor<false>>(f, ftiles, stream);
+    }
     if (r != MOE_OK) return r;
     if (dtoken_scale) {
         launch_pdl(dw32 ? token_scale_sum<true> : token_scale_sum<false>, (unsigned)((T + 255) / 256), 256, 0, stream,
-                   (int)T, 2 * f.nt, f.part, dtoken_scale);
+                   (int)T, scale_parts(T, d, h), f.part, dtoken_scale);
         if ((r = launch_status()) != MOE_OK) return r;
     }
     const int64_t wt = (int64_t)3 * g.md * g.nd, xt = (int64_t)g.mt * g.md;

@@ -31,7 +31,7 @@
 #include <cmath>
 
 #include "../../include/moe_dense.h"
-#include "pair_gemm.cuh"
+#include "small_gemm.cuh"
 
 namespace moe {
 namespace {
@@ -73,15 +73,25 @@ ns_norm(int64_t elems, const TIN *__restrict__ x, float *__restrict__ momentum, 
     pdl_enter();
     const int64_t base = (int64_t)blockIdx.y * elems;
     float s = 0.0f;
-    for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < elems;
-         i += (int64_t)gridDim.x * kNormThreads) {
-        float v = load_elem(x, base + i);
-        if (MUON) {
-            const float m = fmaf(mu, momentum[base + i], v);
-            momentum[base + i] = m;
-            v = nesterov ? fmaf(mu, m, v) : m;
+    constexpr int U = 8;  // elements of a thread in flight
+    const int64_t step = (int64_t)gridDim.x * kNormThreads;
+    for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < elems; i += U * step) {
+        float v[U], m[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = i + u * step < elems;
+            v[u] = in ? load_elem(x, base + i + u * step) : 0.0f;
+            if (MUON) m[u] = in ? momentum[base + i + u * step] : 0.0f;
         }
-        s = fmaf(v, v, s);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (MUON) {
+                m[u] = fmaf(mu, m[u], v[u]);
+                if (i + u * step < elems) momentum[base + i + u * step] = m[u];
+                v[u] = nesterov ? fmaf(mu, m[u], v[u]) : m[u];
+            }
+            s = fmaf(v[u], v[u], s);
+        }
     }
     __shared__ float red[kNormThreads / 32];
 #pragma unroll
@@ -108,6 +118,18 @@ ns_split(int rows, int cols, int tall, int64_t ld, const TIN *__restrict__ x, co
     __shared__ float tile[kSplitTile][kSplitTile + 1];
     __shared__ float inv_s;
     const int64_t b = blockIdx.z;
+    const int r0 = blockIdx.y * kSplitTile, c0 = blockIdx.x * kSplitTile;
+    const int64_t base = b * rows * cols;
+    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+    float v[kSplitTile / 4];  // the tile is on its way while the norm is added up
+#pragma unroll
+    for (int r = 0; r < kSplitTile / 4; ++r) {
+        const int row = r0 + 4 * r + ty;
+        const int64_t i = base + (int64_t)row * cols + c0 + tx;
+        const bool in = row < rows && c0 + tx < cols;
+        v[r] = in ? (MUON && !nesterov ? momentum[i] : load_elem(x, i)) : 0.0f;
+        if (MUON && nesterov && in) v[r] = fmaf(mu, momentum[i], v[r]);
+    }
     if (threadIdx.x < 32) {
         double s = 0.0;
         for (int i = threadIdx.x; i < parts; i += 32) s += part[b * parts + i];
@@ -117,20 +139,9 @@ ns_split(int rows, int cols, int tall, int64_t ld, const TIN *__restrict__ x, co
     }
     __syncthreads();
     const float inv = inv_s;
-    const int r0 = blockIdx.y * kSplitTile, c0 = blockIdx.x * kSplitTile;
-    const int64_t base = b * rows * cols;
     const int64_t out = b * (tall ? cols : rows) * ld;
-    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-    for (int r = ty; r < kSplitTile; r += 4) {
-        float v = 0.0f;
-        if (r0 + r < rows && c0 + tx < cols) {
-            const int64_t i = base + (int64_t)(r0 + r) * cols + c0 + tx;
-            v = load_elem(x, i);
-            if (MUON) v = nesterov ? fmaf(mu, momentum[i], v) : momentum[i];
-            v = v * inv * kScale;
-        }
-        tile[r][tx] = v;
-    }
+#pragma unroll
+    for (int r = 0; r < kSplitTile / 4; ++r) tile[4 * r + ty][tx] = v[r] * inv * kScale;
     __syncthreads();
     // rows of the iterate: of M, or its columns
     const int orow0 = tall ? c0 : r0, ocol0 = tall ? r0 : c0;
@@ -371,6 +382,128 @@ struct Ns {
     }
 };
 
+// ------------------------------------------------------------ few matrices --
+//
+// The same products for batches whose tiles do not fill the pairs (small_gemm.cuh).
+// All tiles of the symmetric products are computed here: there are SMs for them, and
+// no tile is stored twice.
+
+struct SmallNsArgs {
+    CUtensorMap a, b;  // features' and tokens' operand, planes as in NsArgs
+    int B, T, F, nk, split, tt;  // result [T, F]
+    float r, q, lin;
+    const uint16_t *s; // NS_POLY
+    uint16_t *o;       // pieces of the result, rows ld apart
+    int64_t ld;
+    void *out;         // NS_LAST: [B, T, F]
+    int out_f32;
+    float *w;
+    uint16_t *w_copy;
+    const float *lr;
+    float decay, factor;
+    int *status;
+};
+
+// NS_LAST with TALL: M's columns are the iterate's rows, so the features are C's rows and
+// the tokens the iterate's columns.
+template <int MODE, bool TALL, int N>
+struct SmallNs {
+    using Args = SmallNsArgs;
+    static constexpr int kN = N;
+    static constexpr bool kPairs = false, kEarly = false, kSym = MODE < NS_APPLY;
+    static constexpr int kFmt = 0, kPieces = 2;
+    static constexpr int kAMn = !kSym && !TALL, kBMn = !kSym && TALL;
+    static __device__ __forceinline__ void load_a(const Args &p, uint32_t s, uint32_t bar, int kb, int f0, int z,
+                                                  int q) {
+        if (kAMn) {
+            small::load_box(s, &p.a, bar, f0, kb * BK, z + q * p.B);
+            small::load_box(s + BLK, &p.a, bar, f0 + 64, kb * BK, z + q * p.B);
+        } else {
+            small::load_box(s, &p.a, bar, kb * BK, f0, z + q * p.B);
+        }
+    }
+    static __device__ __forceinline__ void load_b(const Args &p, uint32_t s, uint32_t bar, int kb, int t0, int z,
+                                                  int q) {
+        if (kBMn) {
+#pragma unroll
+            for (int i = 0; i < N / 64; ++i)
+                small::load_box(s + i * BLK, &p.b, bar, t0 + 64 * i, kb * BK, z + q * p.B);
+        } else {
+            small::load_box(s, &p.b, bar, kb * BK, t0, z + q * p.B);
+        }
+    }
+    static __device__ __forceinline__ void emit(const Args &p, bool ok, int t, int f, int z, const float4 &a,
+                                                const float4 &) {
+        if (!ok || f >= p.F) return;
+        float v[4] = {a.x, a.y, a.z, a.w};
+        if constexpr (MODE == NS_LAST) {
+            const int64_t at = ((int64_t)z * p.T + t) * p.F + f;
+            const int n = min(4, p.F - f);
+            const float lr = p.w ? *p.lr : 0.0f, keep = 1.0f - lr * p.decay;
+            const float c = p.w ? -lr * p.factor * (kUnscale * kUnscale) : kUnscale * kUnscale;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] *= c;
+            float *o32 = p.w ? p.w : p.out_f32 ? static_cast<float *>(p.out) : nullptr;
+            uint16_t *o16 = p.w ? p.w_copy : p.out_f32 ? nullptr : static_cast<uint16_t *>(p.out);
+            if (o32) {
+                float *dst = o32 + at;
+                if ((p.F & 3) == 0 && (reinterpret_cast<uintptr_t>(o32) & 15) == 0) {
+                    if (p.w) {
+                        const float4 w = *reinterpret_cast<const float4 *>(dst);
+                        v[0] = fmaf(keep, w.x, v[0]);
+                        v[1] = fmaf(keep, w.y, v[1]);
+                        v[2] = fmaf(keep, w.z, v[2]);
+                        v[3] = fmaf(keep, w.w, v[3]);
+                    }
+                    *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < n) {
+                            if (p.w) v[i] = fmaf(keep, dst[i], v[i]);
+                            dst[i] = v[i];
+                        }
+                }
+            }
+            if (o16) {
+                uint16_t *dst = o16 + at;
+                if ((p.F & 3) == 0 && (reinterpret_cast<uintptr_t>(o16) & 7) == 0) {
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < n) reinterpret_cast<__nv_bfloat16 *>(dst)[i] = __float2bfloat16_rn(v[i]);
+                }
+            }
+        } else {
+            const int64_t at = ((int64_t)z * p.T + t) * p.ld + f, plane = (int64_t)p.B * p.T * p.ld;
+            if constexpr (kSym) {
+                const float q = p.q * kUnscale, r = p.r * kScale;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = fmaf(q, v[i], t == f + i ? r : 0.0f);
+                if constexpr (MODE == NS_POLY) {
+                    const uint2 h = *reinterpret_cast<const uint2 *>(p.s + at);
+                    const uint2 l = *reinterpret_cast<const uint2 *>(p.s + plane + at);
+                    const float2 s0 = join2(h.x, l.x), s1 = join2(h.y, l.y);
+                    v[0] = fmaf(p.lin, s0.x, v[0]);
+                    v[1] = fmaf(p.lin, s0.y, v[1]);
+                    v[2] = fmaf(p.lin, s1.x, v[2]);
+                    v[3] = fmaf(p.lin, s1.y, v[3]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] *= kUnscale;
+            }
+            uint2 hi, lo;
+            split2(v[0], v[1], hi.x, lo.x);
+            split2(v[2], v[3], hi.y, lo.y);
+            // rows are padded to 8 elements, so four of them fit behind any column
+            *reinterpret_cast<uint2 *>(p.o + at) = hi;
+            *reinterpret_cast<uint2 *>(p.o + plane + at) = lo;
+        }
+    }
+};
+
 // -------------------------------------------------------------- host side --
 
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -445,6 +578,33 @@ moe_status check_steps(int steps, const float *coefficients, float eps, float (&
     return bounded(steps, coef) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
+// Tokens of a small tile: as few as leave every tile an SM of its own.
+inline int small_tokens(int64_t B, int T, int F, int least) {
+    const int64_t ft = (F + small::kM - 1) / small::kM;
+    int n = 128;
+    while (n > least && B * ft * ((T + n / 2 - 1) / (n / 2)) <= num_sms()) n /= 2;
+    return n;
+}
+
+template <int MODE, bool TALL>
+moe_status launch_small(SmallNsArgs a, const uint16_t *pa, int64_t lda, int arows, int acols, const uint16_t *pb,
+                        int64_t ldb, int brows, int bcols, cudaStream_t st) {
+    constexpr bool kSym = MODE < NS_APPLY;
+    constexpr bool a_mn = !kSym && !TALL, b_mn = !kSym && TALL;
+    const int n = small_tokens(a.B, a.T, a.F, b_mn ? 64 : 32);
+    const int ft = (a.F + small::kM - 1) / small::kM;
+    a.tt = (a.T + n - 1) / n;
+    a.split = small::split_for((int64_t)a.B * ft * a.tt, a.nk);
+    const uint64_t planes = 2 * (uint64_t)a.B;
+    if (!make_map_16(&a.a, pa, acols, arows, planes, lda, 64, a_mn ? 64 : small::kM) ||
+        !make_map_16(&a.b, pb, bcols, brows, planes, ldb, 64, b_mn ? 64 : n))
+        return MOE_ERR_CUDA;
+    if constexpr (!b_mn)
+        if (n == 32) return small::launch<SmallNs<MODE, TALL, 32>>(a, ft, a.B, st);
+    return n <= 64 ? small::launch<SmallNs<MODE, TALL, 64>>(a, ft, a.B, st)
+                   : small::launch<SmallNs<MODE, TALL, 128>>(a, ft, a.B, st);
+}
+
 template <bool MUON, typename TIN>
 moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float mu, int nesterov, int steps,
                const float *coef, float eps, const Update &up, char *ws, cudaStream_t st) {
@@ -484,8 +644,9 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
         if (!map_k(&xk[i], xs[i], n, m, planes, at.ldx) || !map_mn(&apply[i].b, xs[i], n, m, planes, at.ldx) ||
             !map_store(&apply[i].o, xs[1 - i], n, m, planes, at.ldx) || !map_k(&apply[i].a, c, m, m, planes, at.lds))
             return MOE_ERR_CUDA;
-    if (!map_store(&gram.o, s, m, m, planes, at.lds) || !map_k(&poly.a, s, m, m, planes, at.lds) ||
-        !map_store(&poly.o, c, m, m, planes, at.lds))
+    CUtensorMap to_s, to_c;
+    if (!map_store(&to_s, s, m, m, planes, at.lds) || !map_k(&poly.a, s, m, m, planes, at.lds) ||
+        !map_store(&to_c, c, m, m, planes, at.lds))
         return MOE_ERR_CUDA;
     poly.b = poly.a;
 
@@ -502,35 +663,74 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
                xs[0] + (int64_t)B * m * at.ldx);
     if ((r = launch_status()) != MOE_OK) return r;
     const int64_t tri = (int64_t)B * gram.mt * (gram.mt + 1) / 2, full = (int64_t)B * apply[0].mt * apply[0].nt;
-    const CUtensorMap gram_to_s = gram.o;
+    // few tiles: one round of 128 x 128 tiles on single SMs and not of pairs
+    const bool few = (int64_t)B * ((m + small::kM - 1) / small::kM) * ((n + small::kM - 1) / small::kM) <= num_sms();
+    SmallNsArgs sm{};
+    sm.B = B;
+    sm.status = gram.status;
+    sm.out = up.out;
+    sm.out_f32 = up.out_f32;
+    sm.w = up.w;
+    sm.w_copy = up.w_copy;
+    sm.lr = up.lr;
+    sm.decay = up.decay;
+    sm.factor = up.factor;
+    auto symmetric = [&](int mode, const uint16_t *in, int64_t ld, int k, uint16_t *o, double r0, double q,
+                         double lin) -> moe_status {
+        if (few) {
+            SmallNsArgs a = sm;
+            a.T = a.F = m;
+            a.nk = (k + BK - 1) / BK;
+            a.r = (float)r0;
+            a.q = (float)q;
+            a.lin = (float)lin;
+            a.s = s;
+            a.o = o;
+            a.ld = at.lds;
+            return mode == NS_GRAM     ? launch_small<NS_GRAM, false>(a, in, ld, m, k, in, ld, m, k, st)
+                   : mode == NS_SQUARE ? launch_small<NS_SQUARE, false>(a, in, ld, m, k, in, ld, m, k, st)
+                                       : launch_small<NS_POLY, false>(a, in, ld, m, k, in, ld, m, k, st);
+        }
+        NsArgs &a = mode == NS_GRAM ? gram : poly;
+        a.r = (float)r0;
+        a.q = (float)q;
+        a.lin = (float)lin;
+        a.o = o == s ? to_s : to_c;
+        return mode == NS_GRAM     ? launch<Ns<NS_GRAM>>(a, tri, st)
+               : mode == NS_SQUARE ? launch<Ns<NS_SQUARE>>(a, tri, st)
+                                   : launch<Ns<NS_POLY>>(a, tri, st);
+    };
     double most = 1.001;  // of X's singular values
     for (int k = 0; k < steps; ++k) {
         const int cur = k & 1;
         const double ca = coef[3 * k], cb = coef[3 * k + 1], cc = coef[3 * k + 2];
         gram.a = gram.b = xk[cur];
         if (cc == 0.0) {
-            gram.o = poly.o;
-            gram.r = (float)ca;
-            gram.q = (float)cb;
-            r = launch<Ns<NS_GRAM>>(gram, tri, st);
+            r = symmetric(NS_GRAM, xs[cur], at.ldx, n, c, ca, cb, 0.0);
         } else {
             const double shift = cb / (2 * cc);
             const bool square = std::fabs(shift) <= 8.0 && most * most + std::fabs(shift) < 60.0;
-            gram.o = gram_to_s;
-                    gram.r = square ? (float)shift : 0.0f;
-            gram.q = 1.0f;
-            if ((r = launch<Ns<NS_GRAM>>(gram, tri, st)) != MOE_OK) return r;
-            poly.q = (float)cc;
-            poly.r = (float)(square ? ca - cb * cb / (4 * cc) : ca);
-            poly.lin = (float)cb;
-            r = square ? launch<Ns<NS_SQUARE>>(poly, tri, st) : launch<Ns<NS_POLY>>(poly, tri, st);
+            if ((r = symmetric(NS_GRAM, xs[cur], at.ldx, n, s, square ? shift : 0.0, 1.0, 0.0)) != MOE_OK) return r;
+            r = square ? symmetric(NS_SQUARE, s, at.lds, m, c, ca - cb * cb / (4 * cc), cc, 0.0)
+                       : symmetric(NS_POLY, s, at.lds, m, c, ca, cc, cb);
         }
         if (r != MOE_OK) return r;
-        r = k + 1 < steps ? launch<Ns<NS_APPLY>>(apply[cur], full, st) : launch<Ns<NS_LAST>>(apply[cur], full, st);
+        const bool last = k + 1 == steps;
+        if (few) {
+            SmallNsArgs a = sm;
+            a.nk = (m + BK - 1) / BK;
+            a.T = last && tall ? n : m;
+            a.F = last && tall ? m : n;
+            a.o = xs[1 - cur];
+            a.ld = at.ldx;
+            r = !last  ? launch_small<NS_APPLY, false>(a, xs[cur], at.ldx, m, n, c, at.lds, m, m, st)
+                : tall ? launch_small<NS_LAST, true>(a, c, at.lds, m, m, xs[cur], at.ldx, m, n, st)
+                       : launch_small<NS_LAST, false>(a, xs[cur], at.ldx, m, n, c, at.lds, m, m, st);
+        } else {
+            r = last ? launch<Ns<NS_LAST>>(apply[cur], full, st) : launch<Ns<NS_APPLY>>(apply[cur], full, st);
+        }
         if (r != MOE_OK) return r;
-        double next = 0.0;
-        step_bound(most, ca, cb, cc, next);
-        most = next;
+        step_bound(most, ca, cb, cc, most);
     }
     return MOE_OK;
 }

@@ -1,22 +1,27 @@
-// The matrix product of few tokens (gated_ffn.cu, gated_ffn_bwd.cu): the weights'
-// rows or columns are the 128 rows of a tile (features), up to 128 tokens its
-// columns, so a tile multiplies what there is and not 256 padded rows; and the
-// reduction is split over the S CTAs of a cluster when there are fewer tiles than SMs.
+// The matrix product of few tiles (gated_ffn.cu, gated_ffn_bwd.cu, newton_schulz.cu).
+// The result's contiguous dimension (features: the weights' rows or columns) is the
+// 128 rows of a tile, its rows (tokens) are the up to 128 columns, so few tokens are
+// multiplied as few and not as 256 padded rows; and the reduction is split
+// over the S CTAs of a cluster where there are fewer tiles than SMs.
 //
-// What bounds it is the weights' way from memory and the latency of each step, so a
-// CTA keeps as many loads in flight as it has k-blocks, up to kStages; the partial
-// accumulators are added through distributed shared memory, each CTA a share of
-// the features, in rank order; and the epilogue runs over (token, 4 features) items
-// with neighbouring threads on neighbouring features, so loads and stores are
-// whole rows.
+// What bounds it is the operands' way from memory and the latency of each step, so a
+// CTA keeps its loads in flight ahead of the MMAs; the partial accumulators
+// are added through distributed shared memory, each CTA a share of the features,
+// in rank order; and the epilogue runs over (token, 4 features) items with
+// neighbouring threads on neighbouring features, so loads and stores are whole
+// rows.  The sums wait where the stages were.
 //
 // A problem P says what is loaded and what happens to a sum:
-//   kN       tokens of a tile (16, 32, 64 or 128), kPairs: the features are 64 pairs
-//            (rows 0-63 and 64-127 of the tile belong together);
-//   kAMn     the features are the inner dimension of the weight (MN-major);
-//   kEarly   the weights may be loaded before the wait for the grid ahead: that grid
-//            is one of ours that waited for all before it and writes no weights;
-//   load_a / load_b, emit.
+//   kN       tokens of a tile (16, 32, 64 or 128);
+//   kPairs   the features are 64 pairs (rows 0-63 and 64-127 belong together);
+//   kFmt     1 for bf16 operands, 0 for fp16;
+//   kPieces  1, or 2: each operand is a high and a low piece, a product the three
+//            of them that count (newton_schulz.cu), and the k-blocks of a CTA go to four
+//            accumulators, which are added in fp32 (pair_gemm.cuh says why);
+//   kAMn / kBMn  the operand's rows are its inner dimension (MN-major);
+//   kEarly   A may be loaded before the wait for the grid ahead: that grid is one of ours
+//            that waited for all before it and does not write A;
+//   load_a / load_b (of piece q), emit.
 #pragma once
 
 #include "pair_gemm.cuh"
@@ -31,9 +36,20 @@ constexpr int kThreads = 256;
 constexpr int kMaxSplit = 8;
 
 template <class P>
-__host__ __device__ constexpr int stage_bytes() { return kABytes + P::kN * kBK * 2; }
+__host__ __device__ constexpr int a_bytes() { return P::kPieces * kABytes; }
 template <class P>
-__host__ __device__ constexpr int stages() { return P::kN >= 128 ? 4 : 5; }
+__host__ __device__ constexpr int stage_bytes() { return a_bytes<P>() + P::kPieces * P::kN * kBK * 2; }
+// About 96 KB, so that two CTAs share an SM (and the grid behind starts beside
+// this one); twice that with pieces.
+template <class P>
+__host__ __device__ constexpr int stages() {
+    return P::kN >= 128 ? 3 : P::kN == 64 ? 4 : 5;
+}
+// Accumulators and the TMEM columns of all of them.
+template <class P>
+__host__ __device__ constexpr int accs() { return P::kPieces == 2 ? 4 : 1; }
+template <class P>
+__host__ __device__ constexpr int columns() { return accs<P>() * P::kN < 32 ? 32 : accs<P>() * P::kN; }
 
 struct alignas(8) Bars {
     uint64_t full[5], empty[5], done;
@@ -43,14 +59,16 @@ struct alignas(8) Bars {
 
 template <class P>
 constexpr size_t smem_bytes() {
-    return 1024 + (size_t)stages<P>() * stage_bytes<P>() + (size_t)P::kN * kM * 4 + sizeof(Bars) + 16;
+    static_assert((size_t)stages<P>() * stage_bytes<P>() >= (size_t)P::kN * kM * 4, "the sums fit the stages");
+    return 1024 + (size_t)stages<P>() * stage_bytes<P>() + sizeof(Bars) + 16;
 }
 
-__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y) {
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y,
+                                         int z = 0) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(0), "r"(bar)
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 
@@ -64,19 +82,21 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
 
 template <class P>
 __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ typename P::Args p) {
-    constexpr int STAGES = stages<P>(), SB = stage_bytes<P>(), N = P::kN;
-    constexpr int kCols = N < 32 ? 32 : N;  // TMEM columns
+    constexpr int STAGES = stages<P>(), SB = stage_bytes<P>(), AB = a_bytes<P>(), N = P::kN;
+    constexpr int kBBytes = N * kBK * 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem =
         reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    float *part = reinterpret_cast<float *>(smem + STAGES * SB);  // [N tokens][128 features]
-    Bars *bars = reinterpret_cast<Bars *>(part + N * kM);
+    float *part = reinterpret_cast<float *>(smem);  // [N tokens][128 features], once the stages are done
+    Bars *bars = reinterpret_cast<Bars *>(smem + STAGES * SB);
     volatile int *abort = &bars->abort;
     int *status = p.status;
     const int split = p.split, rank = split > 1 ? (int)cluster_rank() : 0;
-    const int f0 = (int)blockIdx.y * (P::kPairs ? kM / 2 : kM), t0 = (int)blockIdx.z * N;
+    const int f0 = (int)blockIdx.y * (P::kPairs ? kM / 2 : kM);
+    const int z = (int)blockIdx.z / p.tt, t0 = ((int)blockIdx.z - z * p.tt) * N;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kb0 = p.nk * rank / split, kb1 = p.nk * (rank + 1) / split, nk = kb1 - kb0;
+    const int group = (nk + accs<P>() - 1) / accs<P>();  // k-blocks of an accumulator
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -87,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
         bars->abort = 0;
         fence_mbar_init();
     }
-    if (warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), kCols);
+    if (warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), columns<P>());
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -95,30 +115,30 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
 
     const int first = min(nk, STAGES);
     auto stage_at = [&](int s) { return smem_u32(smem + s * SB); };
-    if (P::kEarly && threadIdx.x == 0) {
-        for (int i = 0; i < first; ++i) {
-            const uint32_t bar = smem_u32(&bars->full[i]);
-            mbar_arrive_expect_tx(bar, SB);
-            P::load_a(p, stage_at(i), bar, kb0 + i, f0);
-        }
-    }
+    auto issue_a = [&](int i) {
+        const uint32_t bar = smem_u32(&bars->full[i % STAGES]);
+        mbar_arrive_expect_tx(bar, SB);
+#pragma unroll
+        for (int q = 0; q < P::kPieces; ++q)
+            P::load_a(p, stage_at(i % STAGES) + q * kABytes, bar, kb0 + i, f0, z, q);
+    };
+    if (P::kEarly && threadIdx.x == 0)
+        for (int i = 0; i < first; ++i) issue_a(i);
     pdl_enter();
     if (threadIdx.x == 0) {
         bool ok = true;
         int issued = 0;
         for (int i = 0; i < nk; ++i, ++issued) {
             const int s = i % STAGES;
-            const uint32_t bar = smem_u32(&bars->full[s]);
             if (i >= STAGES &&
                 !mbar_wait(smem_u32(&bars->empty[s]), (uint32_t)((i / STAGES - 1) & 1), status, abort)) {
                 ok = false;
                 break;
             }
-            if (!P::kEarly || i >= first) {
-                mbar_arrive_expect_tx(bar, SB);
-                P::load_a(p, stage_at(s), bar, kb0 + i, f0);
-            }
-            P::load_b(p, stage_at(s) + kABytes, bar, kb0 + i, t0);
+            if (!P::kEarly || i >= first) issue_a(i);
+#pragma unroll
+            for (int q = 0; q < P::kPieces; ++q)
+                P::load_b(p, stage_at(s) + AB + q * kBBytes, smem_u32(&bars->full[s]), kb0 + i, t0, z, q);
         }
         if (!ok) {  // copies in flight land before the CTA leaves
             for (int i = max(0, issued - STAGES); i < issued; ++i) {
@@ -127,51 +147,69 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
             }
         }
     } else if (threadIdx.x == 32) {
-        constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)P::kAMn << 15) |
-                                   ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
+        constexpr uint32_t idesc = (1u << 4) | ((uint32_t)P::kFmt << 7) | ((uint32_t)P::kFmt << 10) |
+                                   ((uint32_t)P::kAMn << 15) | ((uint32_t)P::kBMn << 16) | ((uint32_t)(N >> 3) << 17) |
+                                   ((uint32_t)(kM >> 4) << 24);
+        // MN-major operands of fewer than 128 rows are one 64-element block
+        auto mma = [&](uint32_t d, uint32_t sa, uint32_t sb, bool fresh) {
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk)
+                tc_mma_bf16(d, P::kAMn ? pair::mn_desc(sa + kk * 2048) : sw128_kmajor_desc(sa + kk * 32),
+                            P::kBMn ? pair::mn_desc(sb + kk * 2048) : sw128_kmajor_desc(sb + kk * 32), idesc,
+                            fresh && kk == 0 ? 0u : 1u);
+        };
+        int acc = 0, left = group;
         for (int i = 0; i < nk; ++i) {
             const int s = i % STAGES;
             if (!mbar_wait(smem_u32(&bars->full[s]), (uint32_t)((i / STAGES) & 1), status, abort)) break;
             tc_fence_after();
-            const uint32_t sa = stage_at(s), sb = sa + kABytes;
-#pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-                tc_mma_bf16(tmem, P::kAMn ? pair::mn_desc(sa + kk * 2048) : sw128_kmajor_desc(sa + kk * 32),
-                            sw128_kmajor_desc(sb + kk * 32), idesc, (i | kk) != 0 ? 1u : 0u);
+            const uint32_t sa = stage_at(s), sb = sa + AB, d = tmem + acc * N;
+            const bool fresh = left == group;
+            if (P::kPieces == 2) {  // the small products first
+                mma(d, sa + kABytes, sb, fresh);
+                mma(d, sa, sb + kBBytes, false);
+                mma(d, sa, sb, false);
+            } else {
+                mma(d, sa, sb, fresh);
+            }
             tc_commit(smem_u32(&bars->empty[s]));
+            if (--left == 0) {
+                left = group;
+                ++acc;
+            }
         }
         // also after a wait that gave up: what was issued completes here
         tc_commit(smem_u32(&bars->done));
     }
     __syncwarp();
-    // the accumulator to shared memory, token by token: two warps a lane quadrant
+    // the accumulators to shared memory, token by token: two warps a lane quadrant
     mbar_wait(smem_u32(&bars->done), 0, status, abort);
     tc_fence_after();
     {
-        const int quad = warp & 3;
-        constexpr int kHalf = N / 2;  // columns of a warp, at least 8
+        const int quad = warp & 3, used = accs<P>() > 1 ? (nk + group - 1) / group : 1;
+        constexpr int kHalf = N == 16 ? 16 : N / 2;  // columns of a warp
         const int c0 = (warp >> 2) * kHalf;
         const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16);
         float *dst = part + quad * 32 + lane;
-        if (N == 16) {
-            if (warp < 4) {
-                uint32_t v[16];
-                tmem_ld16(at, v);
-                tmem_ld_wait();
-                reg_fence(v);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) dst[i * kM] = __uint_as_float(v[i]);
-            }
-        } else {
 #pragma unroll 1
-            for (int c = c0; c < c0 + kHalf; c += 16) {
-                uint32_t v[16];
-                tmem_ld16(at + c, v);
-                tmem_ld_wait();
-                reg_fence(v);
+        for (int c = c0; c < c0 + kHalf && c < N; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(at + c, v);
+            tmem_ld_wait();
+            reg_fence(v);
+            if (accs<P>() > 1) {
+#pragma unroll 1
+                for (int a = 1; a < used; ++a) {
+                    uint32_t w[16];
+                    tmem_ld16(at + a * N + c, w);
+                    tmem_ld_wait();
+                    reg_fence(w);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) dst[(c + i) * kM] = __uint_as_float(v[i]);
+                    for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+                }
             }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dst[(c + i) * kM] = __uint_as_float(v[i]);
         }
         tc_fence_before();
     }
@@ -180,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
 
     // this CTA's share of the features (pairs), summed over the cluster in rank order
     constexpr int kF = P::kPairs ? kM / 2 : kM;
-    const int share = kF / split, per = share / 4;  // float4 items a token; a power of two
+    const int share = kF / split, per = share / 4;  // items of 4 features a token: a power of two
     const int tokens = min(N, p.T - t0);
     const uint32_t base = smem_u32(part);
     const int items = tokens * per;
@@ -188,25 +226,34 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
     for (int i0 = warp * 32; i0 < items; i0 += kThreads) {
         const int i = i0 + lane;
         const bool ok = i < items;
-        const int t = ok ? i / per : 0, f = rank * share + (i % per) * 4;
-        float4 a = make_float4(0, 0, 0, 0), b = a;
+        const int t = ok ? i / per : 0, f = rank * share + (i & (per - 1)) * 4;
         const uint32_t at = base + (uint32_t)(t * kM + f) * 4;
-        for (int r = 0; r < split; ++r) {
-            const uint32_t src = split > 1 ? cluster_map(at, r) : at;
-            const float4 q = ld_cluster(src);
-            a = make_float4(a.x + q.x, a.y + q.y, a.z + q.z, a.w + q.w);
-            if (P::kPairs) {
-                const float4 w = ld_cluster(src + kM / 2 * 4);
-                b = make_float4(b.x + w.x, b.y + w.y, b.z + w.z, b.w + w.w);
+        float4 a, b = make_float4(0, 0, 0, 0);
+        if (split == 1) {
+            a = ld_cluster(at);
+            if (P::kPairs) b = ld_cluster(at + kM / 2 * 4);
+        } else {
+            a = b;
+            for (int r0 = 0; r0 < split; r0 += 2) {  // two ranks' loads at once
+                const uint32_t s0 = cluster_map(at, r0), s1 = cluster_map(at, r0 + 1);
+                const float4 q0 = ld_cluster(s0), q1 = ld_cluster(s1);
+                float4 w0, w1;
+                if (P::kPairs) {
+                    w0 = ld_cluster(s0 + kM / 2 * 4);
+                    w1 = ld_cluster(s1 + kM / 2 * 4);
+                }
+                a = make_float4(a.x + q0.x + q1.x, a.y + q0.y + q1.y, a.z + q0.z + q1.z, a.w + q0.w + q1.w);
+                if (P::kPairs)
+                    b = make_float4(b.x + w0.x + w1.x, b.y + w0.y + w1.y, b.z + w0.z + w1.z, b.w + w0.w + w1.w);
             }
         }
-        P::emit(p, ok, t0 + t, f0 + f, a, b, per);
+        P::emit(p, ok, t0 + t, f0 + f, z, a, b);
     }
     if (split > 1) cluster_sync_all();  // no CTA leaves while its sums are read
     else __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kCols);
+        tmem_dealloc(tmem, columns<P>());
     }
 }
 
@@ -220,12 +267,12 @@ inline int split_for(int64_t tiles, int nk) {
 }
 
 template <class P>
-moe_status launch(const typename P::Args &args, int ftiles, int ttiles, cudaStream_t st) {
+moe_status launch(const typename P::Args &args, int ftiles, int64_t planes, cudaStream_t st) {
     static PerDeviceOnce smem_attr;
     if (!device_once(smem_attr, [] { return set_smem_limit(small_gemm<P>, smem_bytes<P>()); }))
         return MOE_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)args.split, (unsigned)ftiles, (unsigned)ttiles);
+    cfg.gridDim = dim3((unsigned)args.split, (unsigned)ftiles, (unsigned)(args.tt * planes));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem_bytes<P>();
     cfg.stream = st;
@@ -259,10 +306,10 @@ inline moe_status with_tokens(int T, F &&f) {
     }
 }
 
-// Whether `features` of a tile each and T tokens fit the SMs in one round.
+// Whether so many feature tiles of T tokens fit the SMs in one round, two CTAs each.
 inline bool fits(int64_t ftiles, int T) {
     const int n = tile_tokens(T);
-    return ftiles * ((T + n - 1) / n) <= num_sms();
+    return ftiles * ((T + n - 1) / n) <= 2 * num_sms();
 }
 
 }  // namespace small
