@@ -212,8 +212,10 @@ struct SmallHidden {
                                                   int) {
         small::load_box(s, &p.x, bar, kb * BK, t0);
     }
+    struct In {};
+    static __device__ __forceinline__ void fetch(const Args &, int, int, int, In &) {}
     static __device__ __forceinline__ void emit(const Args &p, bool ok, int t, int f, int, const float4 &g,
-                                                const float4 &u) {
+                                                const float4 &u, const In &) {
         if (!ok || f >= p.h) return;
         float a[4], d[4];
         activate<ACT>(g.x, a[0], d[0]);
@@ -253,22 +255,22 @@ struct SmallOut {
                                                   int) {
         small::load_box(s, &p.hact, bar, kb * BK, t0);
     }
+    struct In {
+        uint2 add;
+        float s;
+    };
+    static __device__ __forceinline__ void fetch(const Args &p, int t, int f, int, In &in) {
+        in.s = p.scale ? p.scale[t] : 1.0f;
+        in.add = p.add && f < p.d ? *reinterpret_cast<const uint2 *>(p.add + (int64_t)t * p.d + f) : make_uint2(0, 0);
+    }
     static __device__ __forceinline__ void emit(const Args &p, bool ok, int t, int f, int, const float4 &v,
-                                                const float4 &) {
+                                                const float4 &, const In &in) {
         if (!ok || f >= p.d) return;
-        const int64_t at = (int64_t)t * p.d + f;
-        float4 o = v;
-        if (p.scale) {
-            const float s = p.scale[t];
-            o = make_float4(o.x * s, o.y * s, o.z * s, o.w * s);
-        }
-        if (p.add) {
-            const uint2 a = *reinterpret_cast<const uint2 *>(p.add + at);
-            const float s = p.scale ? p.scale[t] : 1.0f;
-            o = make_float4(fmaf(s, v.x, bf16_lo(a.x)), fmaf(s, v.y, bf16_hi(a.x)), fmaf(s, v.z, bf16_lo(a.y)),
-                            fmaf(s, v.w, bf16_hi(a.y)));
-        }
-        *reinterpret_cast<uint2 *>(p.y + at) = pack4(o.x, o.y, o.z, o.w);
+        float4 o = make_float4(in.s * v.x, in.s * v.y, in.s * v.z, in.s * v.w);
+        if (p.add)
+            o = make_float4(fmaf(in.s, v.x, bf16_lo(in.add.x)), fmaf(in.s, v.y, bf16_hi(in.add.x)),
+                            fmaf(in.s, v.z, bf16_lo(in.add.y)), fmaf(in.s, v.w, bf16_hi(in.add.y)));
+        *reinterpret_cast<uint2 *>(p.y + (int64_t)t * p.d + f) = pack4(o.x, o.y, o.z, o.w);
     }
 };
 
@@ -325,7 +327,7 @@ MOE_API moe_status moe_gated_ffn(int32_t T, int32_t d, int32_t h, int32_t act, c
         a.h = h;
         a.nk = (d + BK - 1) / BK;
         a.tt = o.tt = tt;
-        a.split = small::split_for((int64_t)ft1 * tt, a.nk);
+        a.split = small::split_for((int64_t)ft1 * tt, a.nk, small::tiles_per_sm(n));
         a.o = reinterpret_cast<uint16_t *>(h_act);
         a.p = reinterpret_cast<uint16_t *>(p_save);
         a.q = reinterpret_cast<uint16_t *>(q_save);
@@ -333,7 +335,7 @@ MOE_API moe_status moe_gated_ffn(int32_t T, int32_t d, int32_t h, int32_t act, c
         o.T = T;
         o.d = d;
         o.nk = (h + BK - 1) / BK;
-        o.split = small::split_for((int64_t)ft2 * tt, o.nk);
+        o.split = small::split_for((int64_t)ft2 * tt, o.nk, small::tiles_per_sm(n));
         o.add = reinterpret_cast<const uint16_t *>(add);
         o.scale = token_scale;
         o.y = reinterpret_cast<uint16_t *>(y);

@@ -134,19 +134,30 @@ struct SmallFactor {
     static __device__ __forceinline__ void load_b(const Args &p, uint32_t s, uint32_t bar, int kb, int t0, int, int) {
         small::load_box(s, &p.dy, bar, kb * BK, t0);
     }
-    static __device__ __forceinline__ uint2 load4(const uint16_t *p, int64_t at) {
-        return *reinterpret_cast<const uint2 *>(p + at);
+    struct In {
+        uint2 p, q, h;
+        float s;
+    };
+    static __device__ __forceinline__ void fetch(const Args &p, int t, int f, int, In &in) {
+        if (f >= p.h) return;
+        const int64_t at = (int64_t)t * p.h + f;
+        in.p = *reinterpret_cast<const uint2 *>(p.p + at);
+        in.q = *reinterpret_cast<const uint2 *>(p.q + at);
+        if (SCALE) {
+            in.h = *reinterpret_cast<const uint2 *>(p.hact + at);
+            in.s = p.scale[t];
+        }
     }
     static __device__ __forceinline__ void emit(const Args &p, bool ok, int t, int f, int, const float4 &r,
-                                                const float4 &) {
+                                                const float4 &, const In &in) {
         const int64_t at = (int64_t)t * p.h + f;
         float ds = 0.0f;
         if (ok && f < p.h) {
-            const uint2 a = load4(p.p, at), b = load4(p.q, at);
+            const uint2 a = in.p, b = in.q;
             float4 v = r;
             if (SCALE) {
-                const uint2 c = load4(p.hact, at);
-                const float s = p.scale[t];
+                const uint2 c = in.h;
+                const float s = in.s;
                 const float h0 = bf16_lo(c.x), h1 = bf16_hi(c.x), h2 = bf16_lo(c.y), h3 = bf16_hi(c.y);
                 ds = fmaf(r.x, h0, fmaf(r.y, h1, fmaf(r.z, h2, r.w * h3)));
                 *reinterpret_cast<uint2 *>(p.hs + at) = make_uint2(pack_bf16x2(s * h0, s * h1), pack_bf16x2(s * h2, s * h3));
@@ -347,7 +358,8 @@ inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 // Cluster size of SmallFactor, or 0 where the tiles are too many for it.
 inline int small_split(int T, int d, int h) {
     const int ft = (h + small::kM - 1) / small::kM, n = small::tile_tokens(T);
-    return small::fits(ft, T) ? small::split_for((int64_t)ft * ((T + n - 1) / n), (d + BK - 1) / BK) : 0;
+    return small::fits(ft, T) ? small::split_for((int64_t)ft * ((T + n - 1) / n), (d + BK - 1) / BK,
+                                                  small::tiles_per_sm(n)) : 0;
 }
 
 // Parts of dtoken_scale: half tiles of 256, or the shares of small tiles.

@@ -432,37 +432,57 @@ struct SmallNs {
             small::load_box(s, &p.b, bar, kb * BK, t0, z + q * p.B);
         }
     }
+    struct In {
+        float4 w;   // NS_LAST: the weights
+        uint2 h, l; // NS_POLY: S
+        float lr;
+    };
+    static __device__ __forceinline__ void fetch(const Args &p, int t, int f, int z, In &in) {
+        if (f >= p.F) return;
+        if (MODE == NS_LAST) {
+            in.lr = p.w ? *p.lr : 0.0f;
+            if (!p.w) return;
+            const float *src = p.w + ((int64_t)z * p.T + t) * p.F + f;
+            if ((p.F & 3) == 0 && (reinterpret_cast<uintptr_t>(p.w) & 15) == 0) {
+                in.w = *reinterpret_cast<const float4 *>(src);
+            } else {
+                const int n = p.F - f;
+                in.w = make_float4(src[0], n > 1 ? src[1] : 0.0f, n > 2 ? src[2] : 0.0f, n > 3 ? src[3] : 0.0f);
+            }
+        }
+        if (MODE == NS_POLY) {
+            const int64_t at = ((int64_t)z * p.T + t) * p.ld + f;
+            in.h = *reinterpret_cast<const uint2 *>(p.s + at);
+            in.l = *reinterpret_cast<const uint2 *>(p.s + (int64_t)p.B * p.T * p.ld + at);
+        }
+    }
     static __device__ __forceinline__ void emit(const Args &p, bool ok, int t, int f, int z, const float4 &a,
-                                                const float4 &) {
+                                                const float4 &, const In &in) {
         if (!ok || f >= p.F) return;
         float v[4] = {a.x, a.y, a.z, a.w};
         if constexpr (MODE == NS_LAST) {
             const int64_t at = ((int64_t)z * p.T + t) * p.F + f;
             const int n = min(4, p.F - f);
-            const float lr = p.w ? *p.lr : 0.0f, keep = 1.0f - lr * p.decay;
+            const float lr = in.lr, keep = 1.0f - lr * p.decay;
             const float c = p.w ? -lr * p.factor * (kUnscale * kUnscale) : kUnscale * kUnscale;
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] *= c;
+            if (p.w) {
+                v[0] = fmaf(keep, in.w.x, v[0]);
+                v[1] = fmaf(keep, in.w.y, v[1]);
+                v[2] = fmaf(keep, in.w.z, v[2]);
+                v[3] = fmaf(keep, in.w.w, v[3]);
+            }
             float *o32 = p.w ? p.w : p.out_f32 ? static_cast<float *>(p.out) : nullptr;
             uint16_t *o16 = p.w ? p.w_copy : p.out_f32 ? nullptr : static_cast<uint16_t *>(p.out);
             if (o32) {
                 float *dst = o32 + at;
                 if ((p.F & 3) == 0 && (reinterpret_cast<uintptr_t>(o32) & 15) == 0) {
-                    if (p.w) {
-                        const float4 w = *reinterpret_cast<const float4 *>(dst);
-                        v[0] = fmaf(keep, w.x, v[0]);
-                        v[1] = fmaf(keep, w.y, v[1]);
-                        v[2] = fmaf(keep, w.z, v[2]);
-                        v[3] = fmaf(keep, w.w, v[3]);
-                    }
                     *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (i < n) {
-                            if (p.w) v[i] = fmaf(keep, dst[i], v[i]);
-                            dst[i] = v[i];
-                        }
+                        if (i < n) dst[i] = v[i];
                 }
             }
             if (o16) {
@@ -482,9 +502,7 @@ struct SmallNs {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = fmaf(q, v[i], t == f + i ? r : 0.0f);
                 if constexpr (MODE == NS_POLY) {
-                    const uint2 h = *reinterpret_cast<const uint2 *>(p.s + at);
-                    const uint2 l = *reinterpret_cast<const uint2 *>(p.s + plane + at);
-                    const float2 s0 = join2(h.x, l.x), s1 = join2(h.y, l.y);
+                    const float2 s0 = join2(in.h.x, in.l.x), s1 = join2(in.h.y, in.l.y);
                     v[0] = fmaf(p.lin, s0.x, v[0]);
                     v[1] = fmaf(p.lin, s0.y, v[1]);
                     v[2] = fmaf(p.lin, s1.x, v[2]);
@@ -578,30 +596,25 @@ moe_status check_steps(int steps, const float *coefficients, float eps, float (&
     return bounded(steps, coef) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
-// Tokens of a small tile: as few as leave every tile an SM of its own.
-inline int small_tokens(int64_t B, int T, int F, int least) {
-    const int64_t ft = (F + small::kM - 1) / small::kM;
-    int n = 128;
-    while (n > least && B * ft * ((T + n / 2 - 1) / (n / 2)) <= num_sms()) n /= 2;
-    return n;
-}
-
 template <int MODE, bool TALL>
 moe_status launch_small(SmallNsArgs a, const uint16_t *pa, int64_t lda, int arows, int acols, const uint16_t *pb,
                         int64_t ldb, int brows, int bcols, cudaStream_t st) {
     constexpr bool kSym = MODE < NS_APPLY;
     constexpr bool a_mn = !kSym && !TALL, b_mn = !kSym && TALL;
-    const int n = small_tokens(a.B, a.T, a.F, b_mn ? 64 : 32);
     const int ft = (a.F + small::kM - 1) / small::kM;
+    // as few tokens a tile as leave every tile an SM of its own (an MN-major operand
+    // comes in blocks of 64)
+    int n = 128;
+    while (n > (b_mn ? 64 : 32) && (int64_t)a.B * ft * ((a.T + n / 2 - 1) / (n / 2)) <= num_sms()) n /= 2;
     a.tt = (a.T + n - 1) / n;
-    a.split = small::split_for((int64_t)a.B * ft * a.tt, a.nk);
+    a.split = small::split_for((int64_t)a.B * ft * a.tt, a.nk, 1);
     const uint64_t planes = 2 * (uint64_t)a.B;
     if (!make_map_16(&a.a, pa, acols, arows, planes, lda, 64, a_mn ? 64 : small::kM) ||
         !make_map_16(&a.b, pb, bcols, brows, planes, ldb, 64, b_mn ? 64 : n))
         return MOE_ERR_CUDA;
     if constexpr (!b_mn)
         if (n == 32) return small::launch<SmallNs<MODE, TALL, 32>>(a, ft, a.B, st);
-    return n <= 64 ? small::launch<SmallNs<MODE, TALL, 64>>(a, ft, a.B, st)
+    return n == 64 ? small::launch<SmallNs<MODE, TALL, 64>>(a, ft, a.B, st)
                    : small::launch<SmallNs<MODE, TALL, 128>>(a, ft, a.B, st);
 }
 
@@ -663,7 +676,7 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
                xs[0] + (int64_t)B * m * at.ldx);
     if ((r = launch_status()) != MOE_OK) return r;
     const int64_t tri = (int64_t)B * gram.mt * (gram.mt + 1) / 2, full = (int64_t)B * apply[0].mt * apply[0].nt;
-    // few tiles: one round of 128 x 128 tiles on single SMs and not of pairs
+    // few tiles: one round of 128 x 128 tiles on single SMs
     const bool few = (int64_t)B * ((m + small::kM - 1) / small::kM) * ((n + small::kM - 1) / small::kM) <= num_sms();
     SmallNsArgs sm{};
     sm.B = B;

@@ -9,7 +9,9 @@
 // are added through distributed shared memory, each CTA a share of the features,
 // in rank order; and the epilogue runs over (token, 4 features) items with
 // neighbouring threads on neighbouring features, so loads and stores are whole
-// rows.  The sums wait where the stages were.
+// rows.  An epilogue thread has kItems of them on their way at once, the first before
+// the product is done (one at a time, a tile of 128 tokens took 15 us).  The sums
+// wait where the stages were.
 //
 // A problem P says what is loaded and what happens to a sum:
 //   kN       tokens of a tile (16, 32, 64 or 128);
@@ -21,7 +23,7 @@
 //   kAMn / kBMn  the operand's rows are its inner dimension (MN-major);
 //   kEarly   A may be loaded before the wait for the grid ahead: that grid is one of ours
 //            that waited for all before it and does not write A;
-//   load_a / load_b (of piece q), emit.
+//   load_a / load_b (of piece q); In and fetch, what an item needs from memory; emit.
 #pragma once
 
 #include "pair_gemm.cuh"
@@ -34,16 +36,17 @@ constexpr int kBK = 64;
 constexpr int kABytes = kM * kBK * 2;         // 16 KB
 constexpr int kThreads = 256;
 constexpr int kMaxSplit = 8;
+constexpr int kItems = 4;                     // items of an epilogue thread in flight
 
 template <class P>
 __host__ __device__ constexpr int a_bytes() { return P::kPieces * kABytes; }
 template <class P>
 __host__ __device__ constexpr int stage_bytes() { return a_bytes<P>() + P::kPieces * P::kN * kBK * 2; }
-// About 96 KB, so that two CTAs share an SM (and the grid behind starts beside
-// this one); twice that with pieces.
+// Up to 64 tokens without pieces: about 96 KB, so that two CTAs share an SM and the
+// grid behind starts beside this one.  More: as many as an SM holds.
 template <class P>
 __host__ __device__ constexpr int stages() {
-    return P::kN >= 128 ? 3 : P::kN == 64 ? 4 : 5;
+    return P::kPieces == 2 ? (P::kN >= 128 ? 3 : P::kN == 64 ? 4 : 5) : P::kN >= 128 ? 6 : P::kN == 64 ? 4 : 5;
 }
 // Accumulators and the TMEM columns of all of them.
 template <class P>
@@ -52,7 +55,7 @@ template <class P>
 __host__ __device__ constexpr int columns() { return accs<P>() * P::kN < 32 ? 32 : accs<P>() * P::kN; }
 
 struct alignas(8) Bars {
-    uint64_t full[5], empty[5], done;
+    uint64_t full[6], empty[6], done;
     uint32_t tmem_base;
     int abort;
 };
@@ -125,6 +128,23 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
     if (P::kEarly && threadIdx.x == 0)
         for (int i = 0; i < first; ++i) issue_a(i);
     pdl_enter();
+
+    // this CTA's share of the features (pairs): items of 4 features a token
+    constexpr int kF = P::kPairs ? kM / 2 : kM;
+    const int share = kF / split, per = share / 4;  // a power of two
+    const int items = min(N, p.T - t0) * per;
+    auto item_t = [&](int i) { return t0 + i / per; };
+    auto item_f = [&](int i) { return rank * share + (i & (per - 1)) * 4; };
+    typename P::In in[kItems];
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < kItems; ++u) {
+            const int i = i0 + u * kThreads + (int)threadIdx.x;
+            if (i < items) P::fetch(p, item_t(i), f0 + item_f(i), z, in[u]);
+        }
+    };
+    fetch(0);
+
     if (threadIdx.x == 0) {
         bool ok = true;
         int issued = 0;
@@ -216,38 +236,39 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
     if (split > 1) cluster_sync_all();
     else __syncthreads();
 
-    // this CTA's share of the features (pairs), summed over the cluster in rank order
-    constexpr int kF = P::kPairs ? kM / 2 : kM;
-    const int share = kF / split, per = share / 4;  // items of 4 features a token: a power of two
-    const int tokens = min(N, p.T - t0);
+    // the sums over the cluster, in rank order
     const uint32_t base = smem_u32(part);
-    const int items = tokens * per;
 #pragma unroll 1
-    for (int i0 = warp * 32; i0 < items; i0 += kThreads) {
-        const int i = i0 + lane;
-        const bool ok = i < items;
-        const int t = ok ? i / per : 0, f = rank * share + (i & (per - 1)) * 4;
-        const uint32_t at = base + (uint32_t)(t * kM + f) * 4;
-        float4 a, b = make_float4(0, 0, 0, 0);
-        if (split == 1) {
-            a = ld_cluster(at);
-            if (P::kPairs) b = ld_cluster(at + kM / 2 * 4);
-        } else {
-            a = b;
-            for (int r0 = 0; r0 < split; r0 += 2) {  // two ranks' loads at once
-                const uint32_t s0 = cluster_map(at, r0), s1 = cluster_map(at, r0 + 1);
-                const float4 q0 = ld_cluster(s0), q1 = ld_cluster(s1);
-                float4 w0, w1;
-                if (P::kPairs) {
-                    w0 = ld_cluster(s0 + kM / 2 * 4);
-                    w1 = ld_cluster(s1 + kM / 2 * 4);
+    for (int i0 = 0; i0 < items; i0 += kItems * kThreads) {
+        if (i0) fetch(i0);
+#pragma unroll
+        for (int u = 0; u < kItems; ++u) {
+            const int i = i0 + u * kThreads + (int)threadIdx.x;
+            if (i - lane >= items) break;  // the whole warp
+            const bool ok = i < items;
+            const int t = ok ? item_t(i) : t0, f = item_f(i);
+            const uint32_t at = base + (uint32_t)((t - t0) * kM + f) * 4;
+            float4 a, b = make_float4(0, 0, 0, 0);
+            if (split == 1) {
+                a = ld_cluster(at);
+                if (P::kPairs) b = ld_cluster(at + kM / 2 * 4);
+            } else {
+                a = b;
+                for (int r0 = 0; r0 < split; r0 += 2) {  // two ranks' loads at once
+                    const uint32_t s0 = cluster_map(at, r0), s1 = cluster_map(at, r0 + 1);
+                    const float4 q0 = ld_cluster(s0), q1 = ld_cluster(s1);
+                    float4 w0, w1;
+                    if (P::kPairs) {
+                        w0 = ld_cluster(s0 + kM / 2 * 4);
+                        w1 = ld_cluster(s1 + kM / 2 * 4);
+                    }
+                    a = make_float4(a.x + q0.x + q1.x, a.y + q0.y + q1.y, a.z + q0.z + q1.z, a.w + q0.w + q1.w);
+                    if (P::kPairs)
+                        b = make_float4(b.x + w0.x + w1.x, b.y + w0.y + w1.y, b.z + w0.z + w1.z, b.w + w0.w + w1.w);
                 }
-                a = make_float4(a.x + q0.x + q1.x, a.y + q0.y + q1.y, a.z + q0.z + q1.z, a.w + q0.w + q1.w);
-                if (P::kPairs)
-                    b = make_float4(b.x + w0.x + w1.x, b.y + w0.y + w1.y, b.z + w0.z + w1.z, b.w + w0.w + w1.w);
             }
+            P::emit(p, ok, t, f0 + f, z, a, b, in[u]);
         }
-        P::emit(p, ok, t0 + t, f0 + f, z, a, b);
     }
     if (split > 1) cluster_sync_all();  // no CTA leaves while its sums are read
     else __syncthreads();
@@ -257,12 +278,13 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
     }
 }
 
-// CTAs of a cluster: as many as the SMs hold beside the other tiles (clusters of
-// eight need eight SMs of one GPC: 16 of them fit at once), with two k-blocks each at
-// least.
-inline int split_for(int64_t tiles, int nk) {
+// CTAs of a cluster: as many as the SMs hold beside the other tiles, `slots` CTAs in
+// all, with two k-blocks each at least.  Clusters of eight leave SMs of a GPC unused: 16
+// of them fit at once with an SM a CTA.
+inline int split_for(int64_t tiles, int nk, int per_sm) {
+    const int slots = per_sm * (num_sms() - num_sms() % 8);
     int s = 1;
-    while (s < kMaxSplit && tiles * (2 * s) <= (s == 4 ? 128 : num_sms() - num_sms() % 8) && nk >= 4 * s) s *= 2;
+    while (s < kMaxSplit && tiles * (2 * s) <= (s == 4 ? per_sm * 128 : slots) && nk >= 4 * s) s *= 2;
     return s;
 }
 
@@ -288,8 +310,11 @@ moe_status launch(const typename P::Args &args, int ftiles, int64_t planes, cuda
     return launch_status();
 }
 
-// Tokens of a tile: the smallest that holds them all, or 128 with several tiles.
+// Tokens of a tile: the smallest that holds them all, or 128 with several tiles (a
+// weight row is then read by fewer tiles: 96 tokens in tiles of 64 took 1 us more than in
+// one of 128, 1537 in 300 tiles of 64 half as long again as the pairs' 42).
 inline int tile_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
+inline int tiles_per_sm(int n) { return n == 128 ? 1 : 2; }
 
 // Calls f with std::integral_constant-like N of tile_tokens(T).
 template <int N>
@@ -306,10 +331,10 @@ inline moe_status with_tokens(int T, F &&f) {
     }
 }
 
-// Whether so many feature tiles of T tokens fit the SMs in one round, two CTAs each.
+// Whether so many feature tiles of T tokens fit the SMs in one round.
 inline bool fits(int64_t ftiles, int T) {
     const int n = tile_tokens(T);
-    return ftiles * ((T + n - 1) / n) <= 2 * num_sms();
+    return ftiles * ((T + n - 1) / n) <= tiles_per_sm(n) * num_sms();
 }
 
 }  // namespace small
