@@ -203,6 +203,7 @@ struct SmallHidden {
     static constexpr int kN = N;
     static constexpr bool kPairs = true, kEarly = false;
     static constexpr int kAMn = 0, kBMn = 0, kFmt = 1, kPieces = 1;
+    static constexpr bool kMirror = false;
     static __device__ __forceinline__ void load_a(const Args &p, uint32_t s, uint32_t bar, int kb, int f0, int,
                                                   int) {
         small::load_box(s, &p.wg, bar, kb * BK, f0);
@@ -211,6 +212,11 @@ struct SmallHidden {
     static __device__ __forceinline__ void load_b(const Args &p, uint32_t s, uint32_t bar, int kb, int t0, int,
                                                   int) {
         small::load_box(s, &p.x, bar, kb * BK, t0);
+    }
+    static __device__ __forceinline__ void prefetch_maps(const Args &p) {
+        tma_prefetch_desc(&p.wg);
+        tma_prefetch_desc(&p.wu);
+        tma_prefetch_desc(&p.x);
     }
     struct In {};
     static __device__ __forceinline__ void fetch(const Args &, int, int, int, In &) {}
@@ -240,13 +246,15 @@ struct SmallOutArgs {
     int *status;
 };
 
-// Runs right behind SmallHidden, so Wd is on its way before that has finished.
+// Runs right behind the product that makes H, which reads no more than its grid ahead
+// has left and writes no weights, so Wd is on its way before that has finished.
 template <int N>
 struct SmallOut {
     using Args = SmallOutArgs;
     static constexpr int kN = N;
     static constexpr bool kPairs = false, kEarly = true;
     static constexpr int kAMn = 0, kBMn = 0, kFmt = 1, kPieces = 1;
+    static constexpr bool kMirror = false;
     static __device__ __forceinline__ void load_a(const Args &p, uint32_t s, uint32_t bar, int kb, int f0, int,
                                                   int) {
         small::load_box(s, &p.wd, bar, kb * BK, f0);
@@ -254,6 +262,10 @@ struct SmallOut {
     static __device__ __forceinline__ void load_b(const Args &p, uint32_t s, uint32_t bar, int kb, int t0, int,
                                                   int) {
         small::load_box(s, &p.hact, bar, kb * BK, t0);
+    }
+    static __device__ __forceinline__ void prefetch_maps(const Args &p) {
+        tma_prefetch_desc(&p.wd);
+        tma_prefetch_desc(&p.hact);
     }
     struct In {
         uint2 add;
@@ -318,65 +330,70 @@ MOE_API moe_status moe_gated_ffn(int32_t T, int32_t d, int32_t h, int32_t act, c
         if (!aligned16(q)) return MOE_ERR_ALIGNMENT;
 
     const bool save = p_save != nullptr;
+    int *const status = static_cast<int *>(ws);
+    // each product in the form that its tiles are made for
+    const int n = small::tile_tokens(T), tt = (T + n - 1) / n;
     const int ft1 = (h + small::kM / 2 - 1) / (small::kM / 2), ft2 = (d + small::kM - 1) / small::kM;
-    if (small::fits(ft1, T) && small::fits(ft2, T)) {
-        const int n = small::tile_tokens(T), tt = (T + n - 1) / n;
+    const bool few1 = small::fits(ft1, T), few2 = small::fits(ft2, T);
+    if (few1) {
         SmallHiddenArgs a{};
-        SmallOutArgs o{};
         a.T = T;
         a.h = h;
         a.nk = (d + BK - 1) / BK;
-        a.tt = o.tt = tt;
+        a.tt = tt;
         a.split = small::split_for((int64_t)ft1 * tt, a.nk, small::tiles_per_sm(n));
         a.o = reinterpret_cast<uint16_t *>(h_act);
         a.p = reinterpret_cast<uint16_t *>(p_save);
         a.q = reinterpret_cast<uint16_t *>(q_save);
-        a.status = static_cast<int *>(ws);
-        o.T = T;
-        o.d = d;
-        o.nk = (h + BK - 1) / BK;
-        o.split = small::split_for((int64_t)ft2 * tt, o.nk, small::tiles_per_sm(n));
-        o.add = reinterpret_cast<const uint16_t *>(add);
-        o.scale = token_scale;
-        o.y = reinterpret_cast<uint16_t *>(y);
-        o.status = a.status;
+        a.status = status;
         if (!make_map_16(&a.wg, w_gate, d, h, 1, d, 64, small::kM / 2) ||
-            !make_map_16(&a.wu, w_up, d, h, 1, d, 64, small::kM / 2) || !make_map_16(&a.x, x, d, T, 1, d, 64, n) ||
-            !make_map_16(&o.wd, w_down, h, d, 1, h, 64, small::kM) || !make_map_16(&o.hact, h_act, h, T, 1, h, 64, n))
+            !make_map_16(&a.wu, w_up, d, h, 1, d, 64, small::kM / 2) || !make_map_16(&a.x, x, d, T, 1, d, 64, n))
             return MOE_ERR_CUDA;
         r = act == MOE_ACT_SILU   ? launch_small_hidden<MOE_ACT_SILU>(a, save, ft1, stream)
             : act == MOE_ACT_GELU ? launch_small_hidden<MOE_ACT_GELU>(a, save, ft1, stream)
                                   : launch_small_hidden<MOE_ACT_RELU>(a, save, ft1, stream);
-        if (r != MOE_OK) return r;
+    } else {
+        HiddenArgs a{};
+        a.T = T;
+        a.d = d;
+        a.h = h;
+        a.mt = (T + PM - 1) / PM;
+        a.nt = (h + BN / 2 - 1) / (BN / 2);
+        a.status = status;
+        if (!map_k(&a.x, x, d, T) || !map_k(&a.wg, w_gate, d, h) || !map_k(&a.wu, w_up, d, h) ||
+            !map_store(&a.o, h_act, h, T) || (save && (!map_store(&a.p, p_save, h, T) || !map_store(&a.q, q_save, h, T))))
+            return MOE_ERR_CUDA;
+        r = act == MOE_ACT_SILU   ? launch_hidden<MOE_ACT_SILU>(a, save, stream)
+            : act == MOE_ACT_GELU ? launch_hidden<MOE_ACT_GELU>(a, save, stream)
+                                  : launch_hidden<MOE_ACT_RELU>(a, save, stream);
+    }
+    if (r != MOE_OK) return r;
+    if (few2) {
+        SmallOutArgs o{};
+        o.T = T;
+        o.d = d;
+        o.nk = (h + BK - 1) / BK;
+        o.tt = tt;
+        o.split = small::split_for((int64_t)ft2 * tt, o.nk, small::tiles_per_sm(n));
+        o.add = reinterpret_cast<const uint16_t *>(add);
+        o.scale = token_scale;
+        o.y = reinterpret_cast<uint16_t *>(y);
+        o.status = status;
+        if (!make_map_16(&o.wd, w_down, h, d, 1, h, 64, small::kM) || !make_map_16(&o.hact, h_act, h, T, 1, h, 64, n))
+            return MOE_ERR_CUDA;
         return small::with_tokens(T, [&](auto k) {
             return small::launch<SmallOut<decltype(k)::value>>(o, ft2, 1, stream);
         });
     }
-
-    HiddenArgs a{};
-    a.T = T;
-    a.d = d;
-    a.h = h;
-    a.mt = (T + PM - 1) / PM;
-    a.nt = (h + BN / 2 - 1) / (BN / 2);
-    a.status = static_cast<int *>(ws);
     OutArgs o{};
     o.T = T;
     o.d = d;
     o.h = h;
-    o.mt = a.mt;
+    o.mt = (T + PM - 1) / PM;
     o.nt = (d + BN - 1) / BN;
     o.add = reinterpret_cast<const uint16_t *>(add);
     o.scale = token_scale;
-    o.status = a.status;
-    if (!map_k(&a.x, x, d, T) || !map_k(&a.wg, w_gate, d, h) || !map_k(&a.wu, w_up, d, h) ||
-        !map_store(&a.o, h_act, h, T) || !map_store(&a.p, p_save ? p_save : h_act, h, T) ||
-        !map_store(&a.q, q_save ? q_save : h_act, h, T) || !map_k(&o.hact, h_act, h, T) ||
-        !map_k(&o.wd, w_down, h, d) || !map_store(&o.o, y, d, T))
-        return MOE_ERR_CUDA;
-    r = act == MOE_ACT_SILU   ? launch_hidden<MOE_ACT_SILU>(a, save, stream)
-        : act == MOE_ACT_GELU ? launch_hidden<MOE_ACT_GELU>(a, save, stream)
-                              : launch_hidden<MOE_ACT_RELU>(a, save, stream);
-    if (r != MOE_OK) return r;
+    o.status = status;
+    if (!map_k(&o.hact, h_act, h, T) || !map_k(&o.wd, w_down, h, d) || !map_store(&o.o, y, d, T)) return MOE_ERR_CUDA;
     return launch<Out>(o, (int64_t)o.mt * o.nt, stream);
 }

@@ -127,12 +127,17 @@ struct SmallFactor {
     static constexpr int kN = N;
     static constexpr bool kPairs = false, kEarly = false;
     static constexpr int kAMn = 1, kBMn = 0, kFmt = 1, kPieces = 1;
+    static constexpr bool kMirror = false;
     static __device__ __forceinline__ void load_a(const Args &p, uint32_t s, uint32_t bar, int kb, int f0, int, int) {
         small::load_box(s, &p.wd, bar, f0, kb * BK);
         small::load_box(s + BLK, &p.wd, bar, f0 + 64, kb * BK);
     }
     static __device__ __forceinline__ void load_b(const Args &p, uint32_t s, uint32_t bar, int kb, int t0, int, int) {
         small::load_box(s, &p.dy, bar, kb * BK, t0);
+    }
+    static __device__ __forceinline__ void prefetch_maps(const Args &p) {
+        tma_prefetch_desc(&p.wd);
+        tma_prefetch_desc(&p.dy);
     }
     struct In {
         uint2 p, q, h;

@@ -385,8 +385,8 @@ struct Ns {
 // ------------------------------------------------------------ few matrices --
 //
 // The same products for batches whose tiles do not fill the pairs (small_gemm.cuh).
-// All tiles of the symmetric products are computed here: there are SMs for them, and
-// no tile is stored twice.
+// Of the symmetric products, tiles of 128 x 128 are computed on and above the diagonal
+// only; narrower ones all, there being SMs for them.
 
 struct SmallNsArgs {
     CUtensorMap a, b;  // features' and tokens' operand, planes as in NsArgs
@@ -413,6 +413,11 @@ struct SmallNs {
     static constexpr bool kPairs = false, kEarly = false, kSym = MODE < NS_APPLY;
     static constexpr int kFmt = 0, kPieces = 2;
     static constexpr int kAMn = !kSym && !TALL, kBMn = !kSym && TALL;
+    static constexpr bool kMirror = kSym && N == small::kM;
+    static __device__ __forceinline__ void prefetch_maps(const Args &p) {
+        tma_prefetch_desc(&p.a);
+        tma_prefetch_desc(&p.b);
+    }
     static __device__ __forceinline__ void load_a(const Args &p, uint32_t s, uint32_t bar, int kb, int f0, int z,
                                                   int q) {
         if (kAMn) {
@@ -606,16 +611,21 @@ moe_status launch_small(SmallNsArgs a, const uint16_t *pa, int64_t lda, int arow
     // comes in blocks of 64)
     int n = 128;
     while (n > (b_mn ? 64 : 32) && (int64_t)a.B * ft * ((a.T + n / 2 - 1) / (n / 2)) <= num_sms()) n /= 2;
+    int tiles = ft;  // of a matrix and token tile, or of a triangle
     a.tt = (a.T + n - 1) / n;
-    a.split = small::split_for((int64_t)a.B * ft * a.tt, a.nk, 1);
+    if (kSym && n == small::kM) {
+        tiles = ft * (ft + 1) / 2;
+        a.tt = 1;
+    }
+    a.split = small::split_for((int64_t)a.B * tiles * a.tt, a.nk, 1);
     const uint64_t planes = 2 * (uint64_t)a.B;
     if (!make_map_16(&a.a, pa, acols, arows, planes, lda, 64, a_mn ? 64 : small::kM) ||
         !make_map_16(&a.b, pb, bcols, brows, planes, ldb, 64, b_mn ? 64 : n))
         return MOE_ERR_CUDA;
     if constexpr (!b_mn)
-        if (n == 32) return small::launch<SmallNs<MODE, TALL, 32>>(a, ft, a.B, st);
-    return n == 64 ? small::launch<SmallNs<MODE, TALL, 64>>(a, ft, a.B, st)
-                   : small::launch<SmallNs<MODE, TALL, 128>>(a, ft, a.B, st);
+        if (n == 32) return small::launch<SmallNs<MODE, TALL, 32>>(a, tiles, a.B, st);
+    return n == 64 ? small::launch<SmallNs<MODE, TALL, 64>>(a, tiles, a.B, st)
+                   : small::launch<SmallNs<MODE, TALL, 128>>(a, tiles, a.B, st);
 }
 
 template <bool MUON, typename TIN>

@@ -9,7 +9,7 @@
 // are added through distributed shared memory, each CTA a share of the features,
 // in rank order; and the epilogue runs over (token, 4 features) items with
 // neighbouring threads on neighbouring features, so loads and stores are whole
-// rows.  An epilogue thread has kItems of them on their way at once, the first before
+// rows.  An epilogue thread has several of them on their way at once, the first before
 // the product is done (one at a time, a tile of 128 tokens took 15 us).  The sums
 // wait where the stages were.
 //
@@ -21,6 +21,9 @@
 //            of them that count (newton_schulz.cu), and the k-blocks of a CTA go to four
 //            accumulators, which are added in fp32 (pair_gemm.cuh says why);
 //   kAMn / kBMn  the operand's rows are its inner dimension (MN-major);
+//   kMirror  the result is symmetric and the operands one: only tiles on and above the
+//            diagonal are computed (kN is 128), and each is stored twice, once from
+//            a transposed copy of the sums;
 //   kEarly   A may be loaded before the wait for the grid ahead: that grid is one of ours
 //            that waited for all before it and does not write A;
 //   load_a / load_b (of piece q); In and fetch, what an item needs from memory; emit.
@@ -36,7 +39,6 @@ constexpr int kBK = 64;
 constexpr int kABytes = kM * kBK * 2;         // 16 KB
 constexpr int kThreads = 256;
 constexpr int kMaxSplit = 8;
-constexpr int kItems = 4;                     // items of an epilogue thread in flight
 
 template <class P>
 __host__ __device__ constexpr int a_bytes() { return P::kPieces * kABytes; }
@@ -48,6 +50,10 @@ template <class P>
 __host__ __device__ constexpr int stages() {
     return P::kPieces == 2 ? (P::kN >= 128 ? 3 : P::kN == 64 ? 4 : 5) : P::kN >= 128 ? 6 : P::kN == 64 ? 4 : 5;
 }
+// Items of an epilogue thread in flight: as many as the larger tiles have work for (with
+// four for 16 tokens, the longer code came in 2 us later for one token).
+template <class P>
+__host__ __device__ constexpr int items_ahead() { return P::kN >= 128 ? 4 : P::kN == 64 ? 2 : 1; }
 // Accumulators and the TMEM columns of all of them.
 template <class P>
 __host__ __device__ constexpr int accs() { return P::kPieces == 2 ? 4 : 1; }
@@ -60,8 +66,13 @@ struct alignas(8) Bars {
     int abort;
 };
 
+// Floats of a row of the transposed sums: 16-byte stores of 8 lanes hit 32 banks.
+constexpr int kPitchT = kM + 4;
+
 template <class P>
 constexpr size_t smem_bytes() {
+    static_assert(!P::kMirror || (P::kN == kM && (size_t)stages<P>() * stage_bytes<P>() >=
+                                                     (size_t)kM * (kM + kPitchT) * 4), "both copies fit");
     static_assert((size_t)stages<P>() * stage_bytes<P>() >= (size_t)P::kN * kM * 4, "the sums fit the stages");
     return 1024 + (size_t)stages<P>() * stage_bytes<P>() + sizeof(Bars) + 16;
 }
@@ -79,14 +90,15 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr));
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
 template <class P>
 __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ typename P::Args p) {
     constexpr int STAGES = stages<P>(), SB = stage_bytes<P>(), AB = a_bytes<P>(), N = P::kN;
-    constexpr int kBBytes = N * kBK * 2;
+    constexpr int kBBytes = N * kBK * 2, kItems = items_ahead<P>();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem =
         reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -95,8 +107,15 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
     volatile int *abort = &bars->abort;
     int *status = p.status;
     const int split = p.split, rank = split > 1 ? (int)cluster_rank() : 0;
-    const int f0 = (int)blockIdx.y * (P::kPairs ? kM / 2 : kM);
-    const int z = (int)blockIdx.z / p.tt, t0 = ((int)blockIdx.z - z * p.tt) * N;
+    const int z = (int)blockIdx.z / p.tt;
+    int f0 = (int)blockIdx.y * (P::kPairs ? kM / 2 : kM), t0 = ((int)blockIdx.z - z * p.tt) * N;
+    if (P::kMirror) {  // blockIdx.y runs over the tiles of the upper triangle, row by row
+        const int mt = (p.T + kM - 1) / kM;
+        int r = (int)blockIdx.y, m = 0;
+        while (r >= mt - m) r -= mt - m++;
+        t0 = m * kM;
+        f0 = (m + r) * kM;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kb0 = p.nk * rank / split, kb1 = p.nk * (rank + 1) / split, nk = kb1 - kb0;
     const int group = (nk + accs<P>() - 1) / accs<P>();  // k-blocks of an accumulator
@@ -110,6 +129,7 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
         bars->abort = 0;
         fence_mbar_init();
     }
+    if (threadIdx.x == 64) P::prefetch_maps(p);
     if (warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), columns<P>());
     tc_fence_before();
     __syncthreads();
@@ -131,19 +151,17 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
 
     // this CTA's share of the features (pairs): items of 4 features a token
     constexpr int kF = P::kPairs ? kM / 2 : kM;
-    const int share = kF / split, per = share / 4;  // a power of two
-    const int items = min(N, p.T - t0) * per;
-    auto item_t = [&](int i) { return t0 + i / per; };
+    const int share = kF / split, per = share / 4, shift = 31 - __clz(per);  // a power of two
     auto item_f = [&](int i) { return rank * share + (i & (per - 1)) * 4; };
     typename P::In in[kItems];
-    auto fetch = [&](int i0) {
+    auto fetch = [&](int i0, int items, int row0, int col0) {
 #pragma unroll
         for (int u = 0; u < kItems; ++u) {
             const int i = i0 + u * kThreads + (int)threadIdx.x;
-            if (i < items) P::fetch(p, item_t(i), f0 + item_f(i), z, in[u]);
+            if (i < items) P::fetch(p, row0 + (i >> shift), col0 + item_f(i), z, in[u]);
         }
     };
-    fetch(0);
+    fetch(0, min(N, p.T - t0) * per, t0, f0);
 
     if (threadIdx.x == 0) {
         bool ok = true;
@@ -230,44 +248,59 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) dst[(c + i) * kM] = __uint_as_float(v[i]);
+            if (P::kMirror) {  // row feature, columns tokens
+                uint4 *dt = reinterpret_cast<uint4 *>(part + kM * kM + (quad * 32 + lane) * kPitchT + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dt[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
         }
         tc_fence_before();
     }
     if (split > 1) cluster_sync_all();
     else __syncthreads();
 
-    // the sums over the cluster, in rank order
-    const uint32_t base = smem_u32(part);
+    // the sums over the cluster, in rank order; the mirrored tile in a second pass
+    const int passes = P::kMirror && t0 != f0 ? 2 : 1;
 #pragma unroll 1
-    for (int i0 = 0; i0 < items; i0 += kItems * kThreads) {
-        if (i0) fetch(i0);
+    for (int pass = 0; pass < passes; ++pass) {
+        const int row0 = pass ? f0 : t0, col0 = pass ? t0 : f0;
+        const uint32_t base = smem_u32(pass ? part + kM * kM : part);
+        const int pitch = pass ? kPitchT : kM;
+        const int items = min(pass ? kM : N, p.T - row0) * per;
+#pragma unroll 1
+        for (int i0 = 0; i0 < items; i0 += kItems * kThreads) {
+            if (i0 || pass) fetch(i0, items, row0, col0);
+            float4 a[kItems], b[kItems];
+            const float4 zero = make_float4(0, 0, 0, 0);
 #pragma unroll
-        for (int u = 0; u < kItems; ++u) {
-            const int i = i0 + u * kThreads + (int)threadIdx.x;
-            if (i - lane >= items) break;  // the whole warp
-            const bool ok = i < items;
-            const int t = ok ? item_t(i) : t0, f = item_f(i);
-            const uint32_t at = base + (uint32_t)((t - t0) * kM + f) * 4;
-            float4 a, b = make_float4(0, 0, 0, 0);
-            if (split == 1) {
-                a = ld_cluster(at);
-                if (P::kPairs) b = ld_cluster(at + kM / 2 * 4);
-            } else {
-                a = b;
-                for (int r0 = 0; r0 < split; r0 += 2) {  // two ranks' loads at once
-                    const uint32_t s0 = cluster_map(at, r0), s1 = cluster_map(at, r0 + 1);
-                    const float4 q0 = ld_cluster(s0), q1 = ld_cluster(s1);
-                    float4 w0, w1;
-                    if (P::kPairs) {
-                        w0 = ld_cluster(s0 + kM / 2 * 4);
-                        w1 = ld_cluster(s1 + kM / 2 * 4);
-                    }
-                    a = make_float4(a.x + q0.x + q1.x, a.y + q0.y + q1.y, a.z + q0.z + q1.z, a.w + q0.w + q1.w);
+            for (int u = 0; u < kItems; ++u) a[u] = b[u] = zero;
+#pragma unroll 4
+            for (int r = 0; r < split; ++r) {
+                // all items' loads of up to four ranks at once: one by one they take the
+                // distributed memory's latency each
+                const uint32_t from = split > 1 ? cluster_map(base, r) : base;
+                float4 q[kItems], w[kItems];
+#pragma unroll
+                for (int u = 0; u < kItems; ++u) {
+                    const int i = i0 + u * kThreads + (int)threadIdx.x;
+                    if (i >= items) continue;
+                    const uint32_t at = from + (uint32_t)((i >> shift) * pitch + item_f(i)) * 4;
+                    q[u] = ld_cluster(at);
+                    if (P::kPairs) w[u] = ld_cluster(at + kM / 2 * 4);
+                }
+#pragma unroll
+                for (int u = 0; u < kItems; ++u) {
+                    a[u] = make_float4(a[u].x + q[u].x, a[u].y + q[u].y, a[u].z + q[u].z, a[u].w + q[u].w);
                     if (P::kPairs)
-                        b = make_float4(b.x + w0.x + w1.x, b.y + w0.y + w1.y, b.z + w0.z + w1.z, b.w + w0.w + w1.w);
+                        b[u] = make_float4(b[u].x + w[u].x, b[u].y + w[u].y, b[u].z + w[u].z, b[u].w + w[u].w);
                 }
             }
-            P::emit(p, ok, t, f0 + f, z, a, b, in[u]);
+#pragma unroll
+            for (int u = 0; u < kItems; ++u) {
+                const int i = i0 + u * kThreads + (int)threadIdx.x;
+                if (i - lane >= items) break;  // the whole warp
+                P::emit(p, i < items, row0 + (i >> shift), col0 + item_f(i), z, a[u], b[u], in[u]);
+            }
         }
     }
     if (split > 1) cluster_sync_all();  // no CTA leaves while its sums are read
