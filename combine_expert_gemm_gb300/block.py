@@ -297,10 +297,11 @@ def _keep(dst, src, stream):
 
 
 def block_forward(st, sc, x, add, gamma, beta, w_router, bias, w_gate, w_up, w_down, eps=1e-5,
-                  token_mask=None, stream=None):
+                  token_mask=None, stream=None, shared=None, shared_scale=None):
     """One pre-norm block: h = x + add (add: the previous block's output, or None),
     n = layer norm of h, and the routed-expert layer of n; its output is returned
-    (sc.fwd.y, which the next block takes as add).  st keeps what block_backward needs,
+    (sc.fwd.y, which the next block takes as add).  shared (a SharedExpert, or None) adds its
+    own output of n, times shared_scale [T] fp32 where that is given.  st keeps what block_backward needs,
     the experts' buffers in 8 bits, and st.losses the balance and z loss over the tokens
     that token_mask [T] uint8 (or None: all) counts.  x, add and token_mask are copied
     where the backward needs them and may be overwritten once these calls have run."""
@@ -329,11 +330,13 @@ def block_forward(st, sc, x, add, gamma, beta, w_router, bias, w_gate, w_up, w_d
     checkpoint_save(s, st.expert_offset, f.g_save, f.u_save, f.y_disp, st.g_q, st.g_scale, st.u_q,
                     st.u_scale, st.y_q, st.y_scale, stream)
     combine(s, f.y_disp, st.route_row, st.topk_gate, f.y, stream)
+    if shared is not None:
+        shared.forward(st.n, f.y, f.y, shared_scale, stream)
     return f.y
 
 
 def block_backward(st, sc, dh, dx, dlosses, gamma, beta, w_router, bias, w_gate, w_up, w_down,
-                   stream=None):
+                   stream=None, shared=None):
     """The backward of block_forward.  dh [T, d] bf16 is the gradient of h + y (the next
     block's dx): it reaches h directly and through the layer.  dx [T, d] bf16 (dh itself
     is allowed) gets the gradient of h; dlosses [2] fp32 on the device are the gradients
@@ -349,6 +352,8 @@ def block_backward(st, sc, dh, dx, dlosses, gamma, beta, w_router, bias, w_gate,
                         f.g_save, f.u_save, f.h_act, b.dy_disp, b.dx_disp, b.dw_gate, b.dw_up,
                         b.dw_down, b.ws, stream)
     dispatch_backward(s, b.dx_disp, st.route_row, b.dx, stream)
+    if shared is not None:
+        shared.backward(st.n, dh, b.dx, b.dx, stream)
     balance_loss_backward(s, route_logits(s, st.route_ws), st.topk_idx, st.token_mask,
                           st.routed_count, st.token_count, st.lse, dlosses, b.dlogit, sc.dlogits,
                           stream)

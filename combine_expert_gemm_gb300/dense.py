@@ -11,11 +11,11 @@ import ctypes
 import torch
 
 from . import _P, _SZ, _bf16, _check, _f32, _lib
-from .block import _DTYPE, _arg, _float_type, _on, _ws
+from .block import _DTYPE, _arg, _float_type, _keep, _on, _ws
 
 __all__ = ["gated_ffn", "gated_ffn_workspace_bytes", "gated_ffn_backward",
            "gated_ffn_backward_workspace_bytes", "newton_schulz", "newton_schulz_workspace_bytes",
-           "muon_step"]
+           "muon_step", "SharedExpert", "Muon"]
 
 _I, _F = ctypes.c_int32, ctypes.c_float
 _SIG = {
@@ -147,3 +147,81 @@ def muon_step(w, w_copy, momentum, grad, lr, mu, weight_decay, scale, ws, nester
         _arg(momentum, _f32, "momentum", n, dev), _arg(grad, _f32, "grad", n, dev),
         _arg(lr, _f32, "lr", 1, dev), mu, weight_decay, scale, 1 if nesterov else 0, steps,
         _coefficients(coefficients, steps), eps, wp, wn, _on(stream, dev)), "moe_muon_step")
+
+
+# ------------------------------------------------------------- shared expert --
+
+class SharedExpert:
+    """A shared expert of a block (block_forward's and block_backward's `shared`): its bf16
+    weights w_gate, w_up [h, d] and w_down [d, h], what its forward keeps for the backward
+    (three [T, h] bf16 buffers and the token scale), and the gradients, which hold the last
+    backward's results: dw_gate, dw_up, dw_down and, with a token scale, dtoken_scale,
+    all fp32."""
+
+    def __init__(self, T, w_gate, w_up, w_down, act="silu"):
+        h, d = w_gate.shape
+        e = dict(device=w_gate.device)
+        self.T, self.act = T, act
+        self.w_gate, self.w_up, self.w_down = w_gate, w_up, w_down
+        self.h_act, self.p_save, self.q_save = (torch.empty((T, h), dtype=_bf16, **e) for _ in range(3))
+        self.token_scale = None                        # scale, or None where every token's is 1
+        self.scale = torch.empty(T, **e)
+        self.dw_gate, self.dw_up = (torch.empty((h, d), **e) for _ in range(2))
+        self.dw_down = torch.empty((d, h), **e)
+        self.dtoken_scale = torch.empty(T, **e)
+        n = max(gated_ffn_workspace_bytes(T, d, h), gated_ffn_backward_workspace_bytes(T, d, h), 256)
+        self.ws = torch.zeros(n, dtype=torch.uint8, **e)
+
+    def forward(self, x, add, y, token_scale=None, stream=None):
+        """y = add + token_scale * expert(x); y may be add.  token_scale [T] fp32 (or None: 1)
+        is copied for the backward."""
+        if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[0] != self.T:
+            raise ValueError(f"x: expected [{self.T}, d]")
+        if token_scale is not None:
+            _arg(token_scale, _f32, "token_scale", self.T, torch.cuda.current_device())
+            self.token_scale = _keep(self.scale, token_scale.view(-1)[:self.T], stream)
+        else:
+            self.token_scale = None
+        gated_ffn(x, self.w_gate, self.w_up, self.w_down, add, self.token_scale, y, self.h_act,
+                  self.p_save, self.q_save, self.ws, self.act, stream)
+
+    def backward(self, x, dy, dx_in, dx, stream=None):
+        """dx = dx_in + the gradient of the forward's x (which x is), and the weights'."""
+        if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[0] != self.T:
+            raise ValueError(f"x: expected [{self.T}, d]")
+        gated_ffn_backward(x, self.w_gate, self.w_up, self.w_down, self.token_scale, self.h_act,
+                           self.p_save, self.q_save, dy, dx_in, dx, self.dw_gate, self.dw_up,
+                           self.dw_down, None if self.token_scale is None else self.dtoken_scale,
+                           self.ws, stream)
+
+
+# ------------------------------------------------------------------- Muon --
+
+class Muon:
+    """Muon over weight matrices.  weights: (w, w_copy) pairs, w [B, rows, cols] or
+    [rows, cols] fp32 and w_copy its bf16 copy that the layer reads, or None.  lr is a [1]
+    fp32 tensor on the device, which a schedule may fill between steps; scale multiplies the
+    orthogonal factor (None: sqrt(max(1, rows / cols)) of each).  All steps run on one stream:
+    the workspace is one for all weights."""
+
+    def __init__(self, weights, lr=0.02, mu=0.95, weight_decay=0.0, nesterov=True, steps=5,
+                 coefficients=None, scale=None, eps=1e-7):
+        self.weights = list(weights)
+        dev = self.weights[0][0].device
+        self.momentum = [torch.zeros_like(w) for w, _ in self.weights]
+        self.lr = torch.tensor([lr], dtype=_f32, device=dev)
+        self.mu, self.weight_decay, self.nesterov, self.steps = mu, weight_decay, nesterov, steps
+        self.coefficients, self.scale, self.eps = coefficients, scale, eps
+        n = max(newton_schulz_workspace_bytes(*_matrices(w, "w")) for w, _ in self.weights)
+        self.ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=dev)
+
+    def step(self, grads, stream=None):
+        """One step of every weight; grads: fp32 tensors of the weights' shapes, in order."""
+        grads = list(grads)
+        if len(grads) != len(self.weights):
+            raise ValueError(f"grads: {len(grads)} tensors, {len(self.weights)} weights")
+        for (w, copy), v, g in zip(self.weights, self.momentum, grads):
+            rows, cols = w.shape[-2:]
+            scale = max(1.0, rows / cols) ** 0.5 if self.scale is None else self.scale
+            muon_step(w, copy, v, g, self.lr, self.mu, self.weight_decay, scale, self.ws, self.nesterov,
+                      self.steps, self.coefficients, self.eps, stream)
