@@ -126,7 +126,7 @@ def _bounds(t, f, b=None, dt=BF):
 
 FFN = [(1, 8, 8), (1, 64, 128), (2, 72, 40), (7, 200, 136), (31, 64, 64), (33, 136, 264), (64, 512, 256), (65, 520, 72),
        (127, 128, 384), (129, 256, 128), (255, 264, 520), (257, 520, 264), (300, 1000, 712), (700, 256, 1416),
-       (1100, 64, 2056)]
+       (1100, 64, 2056), (1100, 2056, 64), (2500, 1000, 1416)]
 
 
 @pytest.mark.parametrize("T,d,h", FFN)
@@ -171,7 +171,7 @@ def test_gated_ffn_no_tokens(moe):
         assert not g[k].any()
 
 
-@pytest.mark.parametrize("T,d,h", [(5, 64, 72), (300, 264, 128)])
+@pytest.mark.parametrize("T,d,h", [(5, 64, 72), (300, 264, 128), (9000, 520, 264)])
 def test_gated_ffn_in_place_and_rows_behind(moe, T, d, h):
     t = _ffn_inputs(T, d, h, True, True, seed=2)
     o = _forward(moe, t, "silu")
@@ -208,7 +208,7 @@ def test_gated_ffn_large_arguments(moe):
     # gates far out on both sides: the slope is 0 or 1 there, never a NaN
     T, d, h = 4, 8, 8
     t = _ffn_inputs(T, d, h, False, False)
-    t["x"] = torch.eye(8)[:4].mul(1e4).to(BF)
+    t["x"] = torch.eye(8)[:4].mul(1e4).to(BF)  # sums of one product: G and U are exact
     t["x"][1:2] *= -1
     t["x"][2:3] *= 1e16
     t["x"][3:4] *= -1e16
@@ -222,7 +222,7 @@ def test_gated_ffn_large_arguments(moe):
             _within(o[k], f[k], H * f[k].abs() * 1.01, f"{act} {k}")
 
 
-@pytest.mark.parametrize("T", [3, 200])
+@pytest.mark.parametrize("T", [3, 200, 20000])
 def test_gated_ffn_streams_graphs_and_repeats(moe, T):
     d, h = 256, 128
     t = _ffn_inputs(T, d, h, True, True, seed=4)
@@ -289,6 +289,28 @@ def test_gated_ffn_argument_checks(moe):
         moe.gated_ffn(*ok, act="tanh")
 
 
+def test_gated_ffn_past_32_bit_offsets(moe):
+    # x, y, dy and dx have more than 2^31 elements; the last rows are checked
+    T, d, h, n = 1050001, 2056, 8, 50
+    g = torch.Generator(device=DEV).manual_seed(1)
+    r = lambda *s, std=1.0: (torch.randn(*s, generator=g, device=DEV, dtype=BF) * std)
+    x, dy = r(T, d), r(T, d)
+    wg, wu, wd = r(h, d, std=d ** -0.5), r(h, d, std=d ** -0.5), r(d, h, std=h ** -0.5)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    hb, p, q = (torch.empty(T, h, dtype=BF, device=DEV) for _ in range(3))
+    ws = _ws(max(moe.gated_ffn_workspace_bytes(T, d, h), moe.gated_ffn_backward_workspace_bytes(T, d, h)))
+    dw = [torch.empty(s, device=DEV) for s in ((h, d), (h, d), (d, h))]
+    moe.gated_ffn(x, wg, wu, wd, None, None, y, hb, p, q, ws)
+    moe.gated_ffn_backward(x, wg, wu, wd, None, hb, p, q, dy, None, dx, *dw, None, ws)
+    assert moe.read_device_error(ws) == 0
+    t = dict(x=x[-n:].cpu(), wg=wg.cpu(), wu=wu.cpu(), wd=wd.cpu(), add=None, scale=None, dy=dy[-n:].cpu())
+    f = ref.ffn(t["x"], t["wg"], t["wu"], t["wd"], None, None, "silu")
+    b = ref.ffn_backward(f, t["x"], t["wg"], t["wu"], t["wd"], t["dy"], None)
+    e = _bounds(t, f, b)
+    _within(y[-n:], f["y"], e["y"], "y", 6e-3)
+    _within(dx[-n:], b["dx"], e["dx"], "dx", 6e-3)
+
+
 # ------------------------------------------------------------ Newton-Schulz --
 
 def _mats(B, rows, cols, seed=0, floor=0.3):
@@ -319,7 +341,9 @@ def _check_ns(got, want, bound, what):
 
 
 SIZES = [(1, 1, 1), (2, 1, 9), (1, 9, 1), (3, 7, 5), (2, 16, 64), (5, 33, 31), (2, 64, 64), (1, 130, 70), (3, 100, 300),
-         (2, 255, 257), (1, 257, 256), (2, 256, 128), (1, 513, 700), (9, 128, 256), (40, 60, 128), (1, 1000, 90)]
+         (2, 255, 257), (1, 257, 256), (2, 256, 128), (1, 513, 700), (9, 128, 256), (40, 60, 128), (1, 1000, 90),
+         # more tiles than SMs
+         (40, 130, 300), (160, 60, 128), (200, 33, 20), (2, 1100, 1201), (30, 300, 200), (2, 1303, 1000)]
 
 
 @pytest.mark.parametrize("B,rows,cols", SIZES)
@@ -343,7 +367,7 @@ def test_newton_schulz_transposes(moe):
     _check_ns(a, want, _ns_bound(norms, 5), "straight")
 
 
-@pytest.mark.parametrize("B,rows,cols", [(2, 60, 77), (1, 150, 300)])
+@pytest.mark.parametrize("B,rows,cols", [(2, 60, 77), (1, 150, 300), (40, 301, 130), (40, 130, 301)])
 def test_newton_schulz_coefficients_in_place_and_unaligned(moe, B, rows, cols):
     m = _mats(B, rows, cols)
     cubic = (1.5, -0.5, 0.0)
@@ -364,7 +388,7 @@ def test_newton_schulz_coefficients_in_place_and_unaligned(moe, B, rows, cols):
     assert torch.equal(view, plain) and float(buf[0]) == 0.0
 
 
-@pytest.mark.parametrize("rows,cols", [(40, 50), (140, 300)])
+@pytest.mark.parametrize("rows,cols", [(40, 50), (140, 300), (900, 1000)])
 def test_newton_schulz_special_matrices(moe, rows, cols):
     m = _mats(4, rows, cols)
     clean = _ns(moe, m)
@@ -391,7 +415,8 @@ def test_newton_schulz_special_matrices(moe, rows, cols):
 
 @pytest.mark.parametrize("B,rows,cols,nesterov,copy", [(2, 60, 40, True, True), (1, 128, 300, False, True),
                                                       (3, 33, 65, True, False), (8, 256, 128, True, True),
-                                                      (1, 300, 200, True, True)])
+                                                      (1, 300, 200, True, True), (40, 131, 300, True, True),
+                                                      (40, 300, 131, True, True), (40, 300, 136, False, False)])
 def test_muon_step(moe, B, rows, cols, nesterov, copy):
     g = torch.Generator().manual_seed(rows)
     w = torch.randn(B, rows, cols, generator=g) * cols ** -0.5
@@ -420,7 +445,7 @@ def test_muon_step(moe, B, rows, cols, nesterov, copy):
     assert moe.read_device_error(ws) == 0
 
 
-@pytest.mark.parametrize("B,rows,cols", [(2, 96, 64), (1, 160, 300)])
+@pytest.mark.parametrize("B,rows,cols", [(2, 96, 64), (1, 160, 300), (40, 160, 300)])
 def test_muon_step_captured(moe, B, rows, cols):
     w = torch.randn(B, rows, cols, generator=torch.Generator().manual_seed(2)).to(DEV)
     v, grad = torch.zeros(B, rows, cols, device=DEV), _mats(B, rows, cols).to(DEV)
@@ -446,6 +471,26 @@ def test_muon_step_captured(moe, B, rows, cols):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(w, want) and torch.equal(v, want_v)
+
+
+def test_muon_past_32_bit_offsets(moe):
+    # more than 2^31 elements; the last matrix against the same step of it alone
+    B, rows, cols = 130, 4096, 4100
+    g = torch.Generator(device=DEV).manual_seed(2)
+    w = torch.randn(B, rows, cols, generator=g, device=DEV)
+    grad = torch.randn(B, rows, cols, generator=g, device=DEV)
+    v = torch.zeros_like(w)
+    lr = torch.tensor([0.1], device=DEV)
+    last = [t[-1:].clone() for t in (w, v, grad)]
+    ws = _ws(moe.newton_schulz_workspace_bytes(B, rows, cols))
+    moe.muon_step(w, None, v, grad, lr, 0.9, 0.0, 1.0, ws, steps=2)
+    assert moe.read_device_error(ws) == 0
+    moe.muon_step(last[0], None, last[1], last[2], lr, 0.9, 0.0, 1.0, ws, steps=2)
+    assert torch.equal(v[-1:], last[1])
+    # the norms are summed in another order: 2^-20 of the factor covers it; and two sums
+    # on either side of a rounding boundary become neighbouring fp32 values, which are
+    # 2^-23 of an element apart at most
+    assert float((w[-1:] - last[0]).norm()) <= 2.0 ** -20 * 0.1 * 3.4445 ** 2 + 2.0 ** -23 * float(last[0].norm())
 
 
 def test_newton_schulz_argument_checks(moe):
