@@ -25,9 +25,11 @@
 // the third MMA loads nothing.  The accumulators hold kGroup k-blocks and
 // are added in fp32 registers (pair_gemm.cuh says why).
 //
-// Launches: one or two passes over the matrices (momentum and sums of squares;
-// scaling, splitting and transposing), three products a step; the last
-// product's epilogue writes the result or updates the weights.
+// Launches: two passes over the matrices (momentum and sums of squares; scaling,
+// splitting and transposing), three products a step; the last product's epilogue
+// writes the result or updates the weights.  The products have three forms: CTA
+// pairs (pair_gemm.cuh); single SMs where one round of 128 x 128 tiles holds them
+// (small_gemm.cuh); and one CTA a matrix for all steps where it fits an SM.
 #include <cmath>
 
 #include "../../include/moe_dense.h"
@@ -527,6 +529,289 @@ struct SmallNs {
     }
 };
 
+// ----------------------------------------------------- small matrices, fused --
+//
+// A matrix of at most 128 x 256 (its sides in either order) never leaves one SM: the
+// pieces of X, [m][n] in blocks of 64 columns (128 rows of 128 swizzled bytes each),
+// and those of S or C over each other, 192 KB in all; the sums in tensor memory.
+// One image of X is both a K-major operand (for X X^T) and an MN-major one (for C X).
+// A step is three products of 12 to 24 MMAs and three passes of the CTA over the
+// sums; as launches of their own the same products took 4.6 us each, 15 of them and
+// two passes before them 78 us for 8 matrices of 256 x 128.
+
+constexpr int kFuseM = 128, kFuseN = 256;
+constexpr int kFuseBlk = kFuseM * 128;  // 64 columns of a piece: 16 KB
+constexpr int kFuseThreads = 512;
+
+struct FuseStep {
+    float gr, gq;        // the Gram matrix's: r I + q X X^T
+    float pr, pq, plin;  // r I + q S S + lin S
+    int poly;            // whether there is a second product
+};
+
+struct FuseArgs {
+    int rows, cols, tall, m, n, nb;  // nb: blocks of 64 columns
+    int steps;
+    float eps;
+    const void *x;       // the matrices, or the gradients
+    float *momentum;
+    float mu;
+    int nesterov;
+    void *out;
+    int out_f32;
+    float *w;
+    uint16_t *w_copy;
+    const float *lr;
+    float decay, factor;
+    FuseStep step[MOE_NS_MAX_STEPS];
+    int *status;
+};
+
+inline size_t fuse_smem(int nb) { return 1024 + (size_t)(2 * nb + 4) * kFuseBlk + 64; }
+
+// MN-major operand of blocks kFuseBlk apart.
+__device__ __forceinline__ uint64_t fuse_mn_desc(uint32_t a) {
+    return (pair::mn_desc(a) & ~((uint64_t)0x3FFF << 16)) | (uint64_t)(kFuseBlk >> 4) << 16;
+}
+
+template <bool MUON, typename TIN>
+__global__ void __launch_bounds__(kFuseThreads, 1) ns_fused(const __grid_constant__ FuseArgs p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem =
+        reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *xh = smem, *xl = xh + p.nb * kFuseBlk, *sh = xl + p.nb * kFuseBlk, *sl = sh + 2 * kFuseBlk;
+    __shared__ uint64_t bar;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort;
+    __shared__ float red[kFuseThreads / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&bar), 1);
+        abort = 0;
+        fence_mbar_init();
+    }
+    pdl_enter();
+    if (warp == 0) tmem_alloc(smem_u32(&tmem_base), 512);
+
+    const int elems = p.rows * p.cols;
+    const int64_t base = (int64_t)blockIdx.x * elems;
+    {
+        // The update direction in registers: pairs of neighbouring columns of the iterate,
+        // the lanes along M's rows, kBatch pairs of loads on their way at once.
+        constexpr int kBatch = 8, kPairs = kFuseM * kFuseN / 2 / kFuseThreads;
+        const TIN *x = static_cast<const TIN *>(p.x) + base;
+        float *mom = MUON ? p.momentum + base : nullptr;
+        const int np = 32 * p.nb;  // pairs of a row, padded
+        const int next = p.tall ? p.cols : 1;
+        float a[kPairs], b[kPairs];
+        float s = 0.0f;
+        auto place = [&](int u, int &r, int &c) {
+            const int i = u * kFuseThreads + (int)threadIdx.x;
+            r = p.tall ? i & (kFuseM - 1) : i / np;
+            c = 2 * (p.tall ? i / kFuseM : i - r * np);
+        };
+#pragma unroll
+        for (int u0 = 0; u0 < kPairs; u0 += kBatch) {
+            if (u0 * kFuseThreads >= kFuseM * np) break;  // the same for all
+            float ma[kBatch], mb[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                int r, c;
+                place(u0 + u, r, c);
+                const int at = p.tall ? c * p.cols + r : r * p.cols + c;
+                const bool in = r < p.m && c < p.n, in1 = r < p.m && c + 1 < p.n;
+                a[u0 + u] = in ? load_elem(x, at) : 0.0f;
+                b[u0 + u] = in1 ? load_elem(x, at + next) : 0.0f;
+                if (MUON) {
+                    ma[u] = in ? mom[at] : 0.0f;
+                    mb[u] = in1 ? mom[at + next] : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (MUON) {
+                    int r, c;
+                    place(u0 + u, r, c);
+                    const int at = p.tall ? c * p.cols + r : r * p.cols + c;
+                    float &va = a[u0 + u], &vb = b[u0 + u];
+                    ma[u] = fmaf(p.mu, ma[u], va);
+                    mb[u] = fmaf(p.mu, mb[u], vb);
+                    if (r < p.m && c < p.n) mom[at] = ma[u];
+                    if (r < p.m && c + 1 < p.n) mom[at + next] = mb[u];
+                    va = p.nesterov ? fmaf(p.mu, ma[u], va) : ma[u];
+                    vb = p.nesterov ? fmaf(p.mu, mb[u], vb) : mb[u];
+                }
+                s = fmaf(a[u0 + u], a[u0 + u], s);
+                s = fmaf(b[u0 + u], b[u0 + u], s);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        if (lane == 0) red[warp] = s;
+        __syncthreads();
+        float inv = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kFuseThreads / 32; ++i) inv += red[i];
+        inv = 1.0f / (sqrtf(inv) + p.eps);
+#pragma unroll
+        for (int u = 0; u < kPairs; ++u) {
+            if (u * kFuseThreads >= kFuseM * np) break;
+            int r, c;
+            place(u, r, c);
+            uint32_t h, l;
+            split2(a[u] * inv * kScale, b[u] * inv * kScale, h, l);
+            const int at = (c >> 6) * kFuseBlk + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4) + (c & 7) * 2;
+            *reinterpret_cast<uint32_t *>(xh + at) = h;
+            *reinterpret_cast<uint32_t *>(xl + at) = l;
+        }
+    }
+    const uint32_t tmem = tmem_base;
+
+    uint32_t parity = 0;
+    // What the threads wrote is seen by the tensor core; one thread issues the three
+    // products of pieces of k-blocks [0, kb), each into an accumulator of its own, `stride`
+    // columns apart; everyone waits.
+    auto multiply = [&](uint8_t *ah, uint8_t *al, uint8_t *bh, uint8_t *bl, bool b_mn, int cols, int kb, int stride) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            tc_fence_after();
+            const uint32_t idesc = (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(cols >> 3) << 17) |
+                                   ((uint32_t)(kFuseM >> 4) << 24);
+            for (int k = 0; k < kb; ++k) {
+#pragma unroll 1
+                for (int q = 0; q < 3; ++q) {  // lo hi, hi lo, hi hi
+                    const uint32_t a = smem_u32(q == 0 ? al : ah) + k * kFuseBlk;
+                    const uint32_t b = smem_u32(q == 1 ? bl : bh) + k * (b_mn ? 64 * 128 : kFuseBlk);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_bf16(tmem + k * stride, sw128_kmajor_desc(a + kk * 32),
+                                    b_mn ? fuse_mn_desc(b + kk * 2048) : sw128_kmajor_desc(b + kk * 32), idesc,
+                                    (q | kk) != 0 ? 1u : 0u);
+                }
+            }
+            tc_commit(smem_u32(&bar));
+        }
+        __syncwarp();
+        mbar_wait(smem_u32(&bar), parity, p.status, &abort);
+        parity ^= 1;
+        tc_fence_after();
+    };
+    const int row = (warp & 3) * 32 + lane, part = warp >> 2;  // a quarter of the columns
+    const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    // 16 columns from c of this lane's row, the accumulators added
+    auto sum16 = [&](int c, int kb, int stride, float (&v)[16]) {
+        uint32_t t[16];
+        tmem_ld16(tlane + c, t);
+        tmem_ld_wait();
+        reg_fence(t);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(t[i]);
+#pragma unroll 1
+        for (int k = 1; k < kb; ++k) {
+            tmem_ld16(tlane + k * stride + c, t);
+            tmem_ld_wait();
+            reg_fence(t);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(t[i]);
+        }
+    };
+    auto put16 = [&](uint8_t *hi, uint8_t *lo, int c, const float (&v)[16]) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split2(v[8 * q + 2 * i], v[8 * q + 2 * i + 1], h[i], l[i]);
+            const int at = (c >> 6) * kFuseBlk + row * 128 + (((((c >> 3) & 7) + q) ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4 *>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
+    };
+    const int kbm = (p.m + 63) / 64, scols = 64 * kbm, xcols = 64 * p.nb;
+    // r I + q sum (+ lin S) into S's place: what lies past m stays 0
+    auto symmetric = [&](int kb, float r, float q, float lin) {
+#pragma unroll 1
+        for (int c = part * (scols / 4); c < (part + 1) * (scols / 4); c += 16) {
+            float v[16];
+            sum16(c, kb, kFuseM, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = fmaf(q * kUnscale, v[i], row == c + i && row < p.m ? r * kScale : 0.0f);
+            if (lin != 0.0f) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int at = (c >> 6) * kFuseBlk + row * 128 + (((((c >> 3) & 7) + j) ^ (row & 7)) << 4);
+                    const uint4 h = *reinterpret_cast<const uint4 *>(sh + at);
+                    const uint4 l = *reinterpret_cast<const uint4 *>(sl + at);
+                    const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 s = join2(hw[i], lw[i]);
+                        v[8 * j + 2 * i] = fmaf(lin, s.x, v[8 * j + 2 * i]);
+                        v[8 * j + 2 * i + 1] = fmaf(lin, s.y, v[8 * j + 2 * i + 1]);
+                    }
+                }
+            }
+            put16(sh, sl, c, v);
+        }
+    };
+#pragma unroll 1
+    for (int k = 0; k < p.steps; ++k) {
+        const FuseStep &t = p.step[k];
+        multiply(xh, xl, xh, xl, false, scols, p.nb, kFuseM);
+        symmetric(p.nb, t.gr, t.gq, 0.0f);
+        if (t.poly) {
+            multiply(sh, sl, sh, sl, false, scols, kbm, kFuseM);
+            symmetric(kbm, t.pr, t.pq, t.plin);
+        }
+        multiply(sh, sl, xh, xl, true, xcols, kbm, kFuseN);
+        if (k + 1 < p.steps) {
+#pragma unroll 1
+            for (int c = part * (xcols / 4); c < (part + 1) * (xcols / 4); c += 16) {
+                float v[16];
+                sum16(c, kbm, kFuseN, v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] *= kUnscale;
+                put16(xh, xl, c, v);
+            }
+        }
+    }
+    // the last iterate to M's layout, 16 columns of this lane's row at a time
+    const float lr = p.w ? *p.lr : 0.0f, keep = 1.0f - lr * p.decay;
+    const float f = p.w ? -lr * p.factor * (kUnscale * kUnscale) : kUnscale * kUnscale;
+    float *const o32 = p.w ? p.w + base : p.out_f32 ? static_cast<float *>(p.out) + base : nullptr;
+    uint16_t *const o16 = p.w        ? (p.w_copy ? p.w_copy + base : nullptr)
+                          : p.out_f32 ? nullptr
+                                      : static_cast<uint16_t *>(p.out) + base;
+    const int step = p.tall ? p.cols : 1;
+#pragma unroll 1
+    for (int c = part * (xcols / 4); c < (part + 1) * (xcols / 4); c += 16) {
+        const int at = p.tall ? c * p.cols + row : row * p.cols + c;
+        const int n = row < p.m ? min(16, p.n - c) : 0;
+        float w[16], v[16];
+        if (p.w) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = i < n ? o32[at + i * step] : 0.0f;
+        }
+        sum16(c, kbm, kFuseN, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            v[i] *= f;
+            if (p.w) v[i] = fmaf(keep, w[i], v[i]);
+            if (i < n) {
+                if (o32) o32[at + i * step] = v[i];
+                if (o16) reinterpret_cast<__nv_bfloat16 *>(o16)[at + i * step] = __float2bfloat16_rn(v[i]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 // -------------------------------------------------------------- host side --
 
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -578,6 +863,31 @@ inline bool bounded(int steps, const float *coef) {
         if (!step_bound(r, coef[3 * k], coef[3 * k + 1], coef[3 * k + 2], r)) return false;
     return true;
 }
+
+// A step's symmetric products: S' = gr I + gq X X^T, then, where there is a second one,
+// C = pr I + pq S' S' + plin S'.  `most` is the bound of X's singular values, before and
+// after.  The square is completed where the shift stays inside the pieces' range.
+struct Products {
+    double gr, gq, pr = 0.0, pq = 0.0, plin = 0.0;
+    bool poly;
+    Products(const float *coef, double &most) {
+        const double a = coef[0], b = coef[1], c = coef[2];
+        poly = c != 0.0;
+        if (!poly) {
+            gr = a;
+            gq = b;
+        } else {
+            const double shift = b / (2 * c);
+            const bool square = std::fabs(shift) <= 8.0 && most * most + std::fabs(shift) < 60.0;
+            gr = square ? shift : 0.0;
+            gq = 1.0;
+            pr = square ? a - b * b / (4 * c) : a;
+            pq = c;
+            plin = square ? 0.0 : b;
+        }
+        step_bound(most, a, b, c, most);
+    }
+};
 
 constexpr float kDefault[3] = {3.4445f, -4.7750f, 2.0315f};
 
@@ -634,6 +944,39 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
     const Layout at(B, rows, cols);
     const int m = at.m, n = at.n;
     const int tall = rows > cols;
+    if (m <= kFuseM && n <= kFuseN) {
+        FuseArgs a{};
+        a.rows = rows;
+        a.cols = cols;
+        a.tall = tall;
+        a.m = m;
+        a.n = n;
+        a.nb = (n + 63) / 64;
+        a.steps = steps;
+        a.eps = eps;
+        a.x = x;
+        a.momentum = momentum;
+        a.mu = mu;
+        a.nesterov = nesterov;
+        a.out = up.out;
+        a.out_f32 = up.out_f32;
+        a.w = up.w;
+        a.w_copy = up.w_copy;
+        a.lr = up.lr;
+        a.decay = up.decay;
+        a.factor = up.factor;
+        a.status = reinterpret_cast<int *>(ws);
+        double most = 1.001;
+        for (int k = 0; k < steps; ++k) {
+            const Products t(coef + 3 * k, most);
+            a.step[k] = FuseStep{(float)t.gr, (float)t.gq, (float)t.pr, (float)t.pq, (float)t.plin, t.poly};
+        }
+        static PerDeviceOnce attr;
+        if (!device_once(attr, [] { return set_smem_limit(ns_fused<MUON, TIN>, fuse_smem(kFuseN / 64)); }))
+            return MOE_ERR_CUDA;
+        launch_pdl(ns_fused<MUON, TIN>, (unsigned)B, kFuseThreads, fuse_smem(a.nb), st, a);
+        return launch_status();
+    }
     uint16_t *xs[2] = {reinterpret_cast<uint16_t *>(ws + at.x[0]), reinterpret_cast<uint16_t *>(ws + at.x[1])};
     uint16_t *s = reinterpret_cast<uint16_t *>(ws + at.s), *c = reinterpret_cast<uint16_t *>(ws + at.c);
     NsArgs gram{}, poly{}, apply[2] = {};
@@ -726,17 +1069,11 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
     double most = 1.001;  // of X's singular values
     for (int k = 0; k < steps; ++k) {
         const int cur = k & 1;
-        const double ca = coef[3 * k], cb = coef[3 * k + 1], cc = coef[3 * k + 2];
+        const Products t(coef + 3 * k, most);
         gram.a = gram.b = xk[cur];
-        if (cc == 0.0) {
-            r = symmetric(NS_GRAM, xs[cur], at.ldx, n, c, ca, cb, 0.0);
-        } else {
-            const double shift = cb / (2 * cc);
-            const bool square = std::fabs(shift) <= 8.0 && most * most + std::fabs(shift) < 60.0;
-            if ((r = symmetric(NS_GRAM, xs[cur], at.ldx, n, s, square ? shift : 0.0, 1.0, 0.0)) != MOE_OK) return r;
-            r = square ? symmetric(NS_SQUARE, s, at.lds, m, c, ca - cb * cb / (4 * cc), cc, 0.0)
-                       : symmetric(NS_POLY, s, at.lds, m, c, ca, cc, cb);
-        }
+        r = symmetric(NS_GRAM, xs[cur], at.ldx, n, t.poly ? s : c, t.gr, t.gq, 0.0);
+        if (r == MOE_OK && t.poly)
+            r = symmetric(t.plin == 0.0 ? NS_SQUARE : NS_POLY, s, at.lds, m, c, t.pr, t.pq, t.plin);
         if (r != MOE_OK) return r;
         const bool last = k + 1 == steps;
         if (few) {
@@ -753,7 +1090,6 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
             r = last ? launch<Ns<NS_LAST>>(apply[cur], full, st) : launch<Ns<NS_APPLY>>(apply[cur], full, st);
         }
         if (r != MOE_OK) return r;
-        step_bound(most, ca, cb, cc, most);
     }
     return MOE_OK;
 }

@@ -245,6 +245,10 @@ __global__ void __launch_bounds__(threads<P>(), 1) pair_gemm(const __grid_consta
         bars->abort = 0;
         fence_mbar_init();
     }
+    // What came so far touches only this pair's own shared memory and may run beside the
+    // grid before this one.  Tensor memory is taken behind the wait: a grid
+    // ahead that takes its own after letting this one start would wait for ours.
+    pdl_enter();
     if (warp == 1) tmem_alloc_pair(smem_u32(&bars->tmem_base), kTmemCols);
     tc_fence_before();
     __syncthreads();
@@ -252,9 +256,6 @@ __global__ void __launch_bounds__(threads<P>(), 1) pair_gemm(const __grid_consta
     tc_fence_after();
     const uint32_t tmem_base = bars->tmem_base;
     const int count = P::count(p, unit, units);  // tiles of this pair
-    // What came so far touches only this pair's own shared and tensor memory: it may
-    // run beside the grid before this one, and every thread waits for that grid here.
-    pdl_enter();
 
     if (warp < epi_warp0<P>()) {
         // with kGroup > 0 the whole first warpgroup, at this one instruction

@@ -130,11 +130,7 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
         fence_mbar_init();
     }
     if (threadIdx.x == 64) P::prefetch_maps(p);
-    if (warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), columns<P>());
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = bars->tmem_base;
 
     const int first = min(nk, STAGES);
     auto stage_at = [&](int s) { return smem_u32(smem + s * SB); };
@@ -148,6 +144,12 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
     if (P::kEarly && threadIdx.x == 0)
         for (int i = 0; i < first; ++i) issue_a(i);
     pdl_enter();
+    // behind the wait, as in pair_gemm.cuh
+    if (warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), columns<P>());
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
 
     // this CTA's share of the features (pairs): items of 4 features a token
     constexpr int kF = P::kPairs ? kM / 2 : kM;
