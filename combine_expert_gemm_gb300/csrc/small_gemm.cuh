@@ -143,9 +143,11 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
     };
     if (P::kEarly && threadIdx.x == 0)
         for (int i = 0; i < first; ++i) issue_a(i);
+    // Tensor memory is taken behind the wait, as in pair_gemm.cuh, but behind a grid of
+    // ours: two of these take 256 of the 512 columns at most.
+    if (P::kEarly && warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), columns<P>());
     pdl_enter();
-    // behind the wait, as in pair_gemm.cuh
-    if (warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), columns<P>());
+    if (!P::kEarly && warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), columns<P>());
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
