@@ -49,12 +49,12 @@ __device__ __forceinline__ void activate(float g, float &a, float &da) {
     da = s == 0.0f || s == 1.0f ? s : fmaf(gz * s, 1.0f - s, s);
 }
 
-template <int ACT, bool SAVE>
+template <int ACT, bool SAVE, int N>
 struct Hidden {
     using Args = HiddenArgs;
     struct Regs {};
-    static constexpr int kStages = 6;
-    static constexpr int kStageBytes = 2 * OPERAND;
+    static constexpr int kN = N, kStages = N == 256 ? 6 : 8;
+    static constexpr int kStageBytes = OPERAND + b_bytes(N);
     static constexpr int kGroup = 0;
     static __device__ __forceinline__ int count(const Args &p, int unit, int units) {
         return strided_count(p.mt * p.nt, unit, units);
@@ -62,7 +62,7 @@ struct Hidden {
     static __device__ __forceinline__ Tile tile(const Args &p, int unit, int units, int i) {
         int m, n;
         band_tile(unit + i * units, p.mt, p.nt, m, n);
-        return Tile{0, m * PM, n * (BN / 2)};
+        return Tile{0, m * PM, n * (N / 2)};
     }
     static __device__ __forceinline__ int k_blocks(const Args &p, const Tile &) { return (p.d + BK - 1) / BK; }
     static __device__ __forceinline__ void load(const Args &p, const Tile &t, int kb, uint32_t s, uint32_t bar,
@@ -71,22 +71,22 @@ struct Hidden {
         load_k(s + OPERAND, rank ? &p.wu : &p.wg, bar, kb * BK, t.n, 0);
     }
     static __device__ __forceinline__ void mma(const Args &, const Tile &, uint32_t d, uint32_t s, bool first) {
-        mma_block<1, false, false>(d, s, s + OPERAND, first);
+        mma_block<1, N, false, false>(d, s, s + OPERAND, first);
     }
     static __device__ __forceinline__ void before(const Args &, const Tile &, const Epi &, int, Regs &) {}
     static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, Epi &e, int wrow, Regs &) {
         const int row0 = t.m + wrow;
         if (row0 >= p.T) return;
-        // G in columns 0-127 of the tile, U in 128-255: this warp's 64 hidden units
+        // G in the first half of the tile's columns, U in the second: this warp's N / 4 units
         const int unit = e.col / 2;
         const uint32_t gat = e.taddr - (uint32_t)(e.col - unit);
 #pragma unroll 1
-        for (int c = 0; c < 64; c += 32) {
+        for (int c = 0; c < N / 4; c += 32) {
             const int col = t.n + unit + c;
             if (col >= p.h) break;
             float g[32], u[32];
             read32(gat + c, g);
-            read32(gat + BN / 2 + c, u);
+            read32(gat + N / 2 + c, u);
             uint32_t hw[16], pw[16], qw[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -116,14 +116,15 @@ struct OutArgs {
     int *status;
 };
 
+template <int N>
 struct Out {
     using Args = OutArgs;
     struct Regs {
-        uint4 add[16];  // this lane's 128 columns of add
+        uint4 add[N / 16];  // this lane's columns of add
         float s;
     };
-    static constexpr int kStages = 6;
-    static constexpr int kStageBytes = 2 * OPERAND;
+    static constexpr int kN = N, kStages = N == 256 ? 6 : 8;
+    static constexpr int kStageBytes = OPERAND + b_bytes(N);
     static constexpr int kGroup = 0;
     static __device__ __forceinline__ int count(const Args &p, int unit, int units) {
         return strided_count(p.mt * p.nt, unit, units);
@@ -131,16 +132,16 @@ struct Out {
     static __device__ __forceinline__ Tile tile(const Args &p, int unit, int units, int i) {
         int m, n;
         band_tile(unit + i * units, p.mt, p.nt, m, n);
-        return Tile{0, m * PM, n * BN};
+        return Tile{0, m * PM, n * N};
     }
     static __device__ __forceinline__ int k_blocks(const Args &p, const Tile &) { return (p.h + BK - 1) / BK; }
     static __device__ __forceinline__ void load(const Args &p, const Tile &t, int kb, uint32_t s, uint32_t bar,
                                                 int rank) {
         load_k(s, &p.hact, bar, kb * BK, t.m + rank * BM, 0);
-        load_k(s + OPERAND, &p.wd, bar, kb * BK, t.n + rank * BM, 0);
+        load_k(s + OPERAND, &p.wd, bar, kb * BK, t.n + rank * (N / 2), 0);
     }
     static __device__ __forceinline__ void mma(const Args &, const Tile &, uint32_t d, uint32_t s, bool first) {
-        mma_block<1, false, false>(d, s, s + OPERAND, first);
+        mma_block<1, N, false, false>(d, s, s + OPERAND, first);
     }
     static __device__ __forceinline__ void before(const Args &p, const Tile &t, Epi &e, int wrow, Regs &r) {
         const int row = t.m + wrow + e.lane;
@@ -149,7 +150,7 @@ struct Out {
             const int col = t.n + e.col;
             const uint16_t *src = p.add + (int64_t)row * p.d + col;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < N / 16; ++i)
                 r.add[i] = row < p.T && col + 8 * i < p.d ? __ldcs(reinterpret_cast<const uint4 *>(src) + i)
                                                           : make_uint4(0, 0, 0, 0);
         }
@@ -158,7 +159,7 @@ struct Out {
         const int row0 = t.m + wrow;
         if (row0 >= p.T) return;
 #pragma unroll
-        for (int c = 0; c < BN / 2; c += 32) {
+        for (int c = 0; c < N / 2; c += 32) {
             const int col = t.n + e.col + c;
             if (col >= p.d) break;
             float v[32];
@@ -296,9 +297,11 @@ moe_status launch_small_hidden(const SmallHiddenArgs &a, bool save, int ft, cuda
 }
 
 template <int ACT>
-moe_status launch_hidden(const HiddenArgs &a, bool save, cudaStream_t st) {
+moe_status launch_hidden(const HiddenArgs &a, bool wide, bool save, cudaStream_t st) {
     const int64_t tiles = (int64_t)a.mt * a.nt;
-    return save ? launch<Hidden<ACT, true>>(a, tiles, st) : launch<Hidden<ACT, false>>(a, tiles, st);
+    if (wide)
+        return save ? launch<Hidden<ACT, true, 256>>(a, tiles, st) : launch<Hidden<ACT, false, 256>>(a, tiles, st);
+    return save ? launch<Hidden<ACT, true, 128>>(a, tiles, st) : launch<Hidden<ACT, false, 128>>(a, tiles, st);
 }
 
 }  // namespace
@@ -358,14 +361,17 @@ MOE_API moe_status moe_gated_ffn(int32_t T, int32_t d, int32_t h, int32_t act, c
         a.d = d;
         a.h = h;
         a.mt = (T + PM - 1) / PM;
-        a.nt = (h + BN / 2 - 1) / (BN / 2);
+        const bool wide = !narrow((int64_t)a.mt * ((h + 127) / 128), (int64_t)a.mt * ((h + 63) / 64));
+        const int units = wide ? 128 : 64;  // hidden units of a tile
+        a.nt = (h + units - 1) / units;
         a.status = status;
-        if (!map_k(&a.x, x, d, T) || !map_k(&a.wg, w_gate, d, h) || !map_k(&a.wu, w_up, d, h) ||
+        if (!map_k(&a.x, x, d, T) || !map_k(&a.wg, w_gate, d, h, 1, 0, units) ||
+            !map_k(&a.wu, w_up, d, h, 1, 0, units) ||
             !map_store(&a.o, h_act, h, T) || (save && (!map_store(&a.p, p_save, h, T) || !map_store(&a.q, q_save, h, T))))
             return MOE_ERR_CUDA;
-        r = act == MOE_ACT_SILU   ? launch_hidden<MOE_ACT_SILU>(a, save, stream)
-            : act == MOE_ACT_GELU ? launch_hidden<MOE_ACT_GELU>(a, save, stream)
-                                  : launch_hidden<MOE_ACT_RELU>(a, save, stream);
+        r = act == MOE_ACT_SILU   ? launch_hidden<MOE_ACT_SILU>(a, wide, save, stream)
+            : act == MOE_ACT_GELU ? launch_hidden<MOE_ACT_GELU>(a, wide, save, stream)
+                                  : launch_hidden<MOE_ACT_RELU>(a, wide, save, stream);
     }
     if (r != MOE_OK) return r;
     if (few2) {
@@ -390,10 +396,13 @@ MOE_API moe_status moe_gated_ffn(int32_t T, int32_t d, int32_t h, int32_t act, c
     o.d = d;
     o.h = h;
     o.mt = (T + PM - 1) / PM;
-    o.nt = (d + BN - 1) / BN;
+    const bool wide = !narrow((int64_t)o.mt * ((d + 255) / 256), (int64_t)o.mt * ((d + 127) / 128));
+    o.nt = wide ? (d + 255) / 256 : (d + 127) / 128;
     o.add = reinterpret_cast<const uint16_t *>(add);
     o.scale = token_scale;
     o.status = status;
-    if (!map_k(&o.hact, h_act, h, T) || !map_k(&o.wd, w_down, h, d) || !map_store(&o.o, y, d, T)) return MOE_ERR_CUDA;
-    return launch<Out>(o, (int64_t)o.mt * o.nt, stream);
+    if (!map_k(&o.hact, h_act, h, T) || !map_k(&o.wd, w_down, h, d, 1, 0, wide ? 128 : 64) ||
+        !map_store(&o.o, y, d, T))
+        return MOE_ERR_CUDA;
+    return wide ? launch<Out<256>>(o, (int64_t)o.mt * o.nt, stream) : launch<Out<128>>(o, (int64_t)o.mt * o.nt, stream);
 }

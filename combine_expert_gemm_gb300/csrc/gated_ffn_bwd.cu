@@ -17,7 +17,7 @@ namespace {
 
 using namespace pair;
 
-// Row sums of R H: one fp32 a row and 128-column half tile.
+// Row sums of R H: one fp32 a row and half tile.
 struct FactorArgs {
     CUtensorMap dy, wd, odg, odu, ohs;
     int T, d, h, mt, nt;
@@ -27,15 +27,15 @@ struct FactorArgs {
     int *status;
 };
 
-template <bool SCALE>
+template <bool SCALE, int N>
 struct Factor {
     using Args = FactorArgs;
     struct Regs {
         float s;
         uint4 p[4], q[4], h[4];  // the factors of the 32 columns to come
     };
-    static constexpr int kStages = 6;
-    static constexpr int kStageBytes = 2 * OPERAND;
+    static constexpr int kN = N, kStages = N == 256 ? 6 : 8;
+    static constexpr int kStageBytes = OPERAND + b_bytes(N);
     static constexpr int kGroup = 0;
     static __device__ __forceinline__ int count(const Args &p, int unit, int units) {
         return strided_count(p.mt * p.nt, unit, units);
@@ -43,16 +43,16 @@ struct Factor {
     static __device__ __forceinline__ Tile tile(const Args &p, int unit, int units, int i) {
         int m, n;
         band_tile(unit + i * units, p.mt, p.nt, m, n);
-        return Tile{0, m * PM, n * BN};
+        return Tile{0, m * PM, n * N};
     }
     static __device__ __forceinline__ int k_blocks(const Args &p, const Tile &) { return (p.d + BK - 1) / BK; }
     static __device__ __forceinline__ void load(const Args &p, const Tile &t, int kb, uint32_t s, uint32_t bar,
                                                 int rank) {
         load_k(s, &p.dy, bar, kb * BK, t.m + rank * BM, 0);
-        load_mn(s + OPERAND, &p.wd, bar, t.n + rank * BM, kb * BK, 0);
+        load_mn<N / 2>(s + OPERAND, &p.wd, bar, t.n + rank * (N / 2), kb * BK, 0);
     }
     static __device__ __forceinline__ void mma(const Args &, const Tile &, uint32_t d, uint32_t s, bool first) {
-        mma_block<1, false, true>(d, s, s + OPERAND, first);
+        mma_block<1, N, false, true>(d, s, s + OPERAND, first);
     }
     static __device__ __forceinline__ void before(const Args &p, const Tile &t, Epi &e, int wrow, Regs &r) {
         const int row = t.m + wrow + e.lane;
@@ -76,7 +76,7 @@ struct Factor {
         float ds = 0.0f;
         const int colh = t.n + e.col;
 #pragma unroll 1
-        for (int c = 0; c < BN / 2; c += 32) {
+        for (int c = 0; c < N / 2; c += 32) {
             const int col = colh + c;
             if (col >= p.h) break;
             float v[32];
@@ -100,12 +100,12 @@ struct Factor {
                 du[i] = pack_bf16x2(a * bf16_lo(pw[i]), b * bf16_hi(pw[i]));
                 dg[i] = pack_bf16x2(a * bf16_lo(qw[i]), b * bf16_hi(qw[i]));
             }
-            if (c + 32 < BN / 2) factors(p, row, col + 32, r);
+            if (c + 32 < N / 2) factors(p, row, col + 32, r);
             store_block16(e, du, &p.odu, col, row0, 0);
             store_block16(e, dg, &p.odg, col, row0, 0);
             if (SCALE) store_block16(e, hs, &p.ohs, col, row0, 0);
         }
-        if (SCALE && p.part && row < p.T) p.part[(int64_t)(colh / (BN / 2)) * p.T + row] = ds;
+        if (SCALE && p.part && row < p.T) p.part[(int64_t)(colh / (N / 2)) * p.T + row] = ds;
     }
 };
 
@@ -197,7 +197,8 @@ struct GradArgs {
     CUtensorMap xb[2];     // Wg, Wu
     CUtensorMap xo;
     int T, d, h;
-    int mt, md, nd;        // 256-tiles of T, d and h
+    int mt, md, mh;        // 256-row tiles of T, d and h
+    int nd, nh;            // N-column tiles of d and h
     int hb, tb;            // k-blocks of h and T
     const void *dx_in;
     int long_x;            // the longer tiles are dx's
@@ -207,12 +208,12 @@ struct GradArgs {
     int *status;
 };
 
-template <bool DX32, bool DW32>
+template <bool DX32, bool DW32, int N>
 struct Grad {
     using Args = GradArgs;
     struct Regs {};
-    static constexpr int kStages = 6;
-    static constexpr int kStageBytes = 2 * OPERAND;
+    static constexpr int kN = N, kStages = N == 256 ? 6 : 8;
+    static constexpr int kStageBytes = OPERAND + b_bytes(N);
     static constexpr int kGroup = 0;
     static __device__ __forceinline__ int longs(const Args &p, int unit) { return p.q + (unit < p.r ? 1 : 0); }
     static __device__ __forceinline__ int count(const Args &p, int unit, int) {
@@ -231,12 +232,17 @@ struct Grad {
         }
         int m, n;
         if (x) {
-            band_tile(g, p.mt, p.md, m, n);
-            return Tile{3, m * PM, n * BN};
+            band_tile(g, p.mt, p.nd, m, n);
+            return Tile{3, m * PM, n * N};
         }
-        const int per = p.md * p.nd, z = g / per;
-        band_tile(g - z * per, z ? p.nd : p.md, z ? p.md : p.nd, m, n);
-        return Tile{z, m * PM, n * BN};
+        const int down = p.md * p.nh, per = p.mh * p.nd;  // tiles of dWd, of dWg and dWu each
+        if (g < down) {
+            band_tile(g, p.md, p.nh, m, n);
+            return Tile{0, m * PM, n * N};
+        }
+        const int z = 1 + (g - down) / per;
+        band_tile(g - down - (z - 1) * per, p.mh, p.nd, m, n);
+        return Tile{z, m * PM, n * N};
     }
     static __device__ __forceinline__ int k_blocks(const Args &p, const Tile &t) { return t.z == 3 ? 2 * p.hb : p.tb; }
     static __device__ __forceinline__ void load(const Args &p, const Tile &t, int kb, uint32_t s, uint32_t bar,
@@ -244,15 +250,15 @@ struct Grad {
         if (t.z == 3) {
             const int up = kb >= p.hb, k = (kb - up * p.hb) * BK;
             load_k(s, &p.xa[up], bar, k, t.m + rank * BM, 0);
-            load_mn(s + OPERAND, &p.xb[up], bar, t.n + rank * BM, k, 0);
+            load_mn<N / 2>(s + OPERAND, &p.xb[up], bar, t.n + rank * (N / 2), k, 0);
         } else {
-            load_mn(s, &p.wa[t.z], bar, t.m + rank * BM, kb * BK, 0);
-            load_mn(s + OPERAND, &p.wb[t.z ? 1 : 0], bar, t.n + rank * BM, kb * BK, 0);
+            load_mn<BM>(s, &p.wa[t.z], bar, t.m + rank * BM, kb * BK, 0);
+            load_mn<N / 2>(s + OPERAND, &p.wb[t.z ? 1 : 0], bar, t.n + rank * (N / 2), kb * BK, 0);
         }
     }
     static __device__ __forceinline__ void mma(const Args &, const Tile &t, uint32_t d, uint32_t s, bool first) {
-        if (t.z == 3) mma_block<1, false, true>(d, s, s + OPERAND, first);
-        else mma_block<1, true, true>(d, s, s + OPERAND, first);
+        if (t.z == 3) mma_block<1, N, false, true>(d, s, s + OPERAND, first);
+        else mma_block<1, N, true, true>(d, s, s + OPERAND, first);
     }
     static __device__ __forceinline__ void before(const Args &, const Tile &, const Epi &, int, Regs &) {}
     static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, Epi &e, int wrow, Regs &) {
@@ -266,7 +272,7 @@ struct Grad {
         // tile has to have left both blocks
         if (DX32 != DW32 && e.lane == 0) bulk_wait_read<0>();
 #pragma unroll 1
-        for (int c = 0; c < BN / 2; c += 32) {
+        for (int c = 0; c < N / 2; c += 32) {
             const int col = t.n + e.col + c;
             if (col >= cols) break;
             float add[32];
@@ -346,6 +352,12 @@ inline void share(GradArgs &p, int units, int64_t nl, int64_t cl, int64_t ns, in
     p.se = (int)(rest % (units - p.r));
 }
 
+template <int N>
+moe_status launch_grad(const GradArgs &g, bool dx32, bool dw32, int64_t tiles, cudaStream_t st) {
+    if (dx32) return dw32 ? launch<Grad<true, true, N>>(g, tiles, st) : launch<Grad<true, false, N>>(g, tiles, st);
+    return dw32 ? launch<Grad<false, true, N>>(g, tiles, st) : launch<Grad<false, false, N>>(g, tiles, st);
+}
+
 // out[t] = the sum of part[0..n)[t], in order.
 template <bool F32>
 __global__ void __launch_bounds__(256) token_scale_sum(int T, int n, const float *__restrict__ part, void *out) {
@@ -367,10 +379,16 @@ inline int small_split(int T, int d, int h) {
                                                   small::tiles_per_sm(n)) : 0;
 }
 
-// Parts of dtoken_scale: half tiles of 256, or the shares of small tiles.
+// Columns of Factor's tiles.
+inline int factor_columns(int T, int h) {
+    const int64_t mt = (T + PM - 1) / PM;
+    return narrow(mt * ((h + 255) / 256), mt * ((h + 127) / 128)) ? 128 : 256;
+}
+
+// Parts of dtoken_scale: half tiles, or the shares of small tiles.
 inline int scale_parts(int T, int d, int h) {
-    const int split = small_split(T, d, h);
-    return split ? (h + small::kM - 1) / small::kM * split : 2 * ((h + BN - 1) / BN);
+    const int split = small_split(T, d, h), n = factor_columns(T, h);
+    return split ? (h + small::kM - 1) / small::kM * split : 2 * ((h + n - 1) / n);
 }
 
 // Workspace: status, dG, dU, Hs [T, h] bf16, the parts of dtoken_scale.
@@ -437,7 +455,8 @@ MOE_API moe_status moe_gated_ffn_backward(int32_t T, int32_t d, int32_t h, const
     f.d = d;
     f.h = h;
     f.mt = (T + PM - 1) / PM;
-    f.nt = (h + BN - 1) / BN;
+    const int fn = factor_columns(T, h);
+    f.nt = (h + fn - 1) / fn;
     f.p = reinterpret_cast<const uint16_t *>(p_save);
     f.q = reinterpret_cast<const uint16_t *>(q_save);
     f.hact = reinterpret_cast<const uint16_t *>(h_act);
@@ -449,8 +468,8 @@ MOE_API moe_status moe_gated_ffn_backward(int32_t T, int32_t d, int32_t h, const
     g.d = d;
     g.h = h;
     g.mt = f.mt;
-    g.md = (d + BN - 1) / BN;
-    g.nd = f.nt;
+    g.md = (d + PM - 1) / PM;
+    g.mh = (h + PM - 1) / PM;
     g.hb = (h + BK - 1) / BK;
     g.tb = (T + BK - 1) / BK;
     g.dx_in = dx_in;
@@ -498,7 +517,10 @@ MOE_API moe_status moe_gated_ffn_backward(int32_t T, int32_t d, int32_t h, const
                                : small::launch<SmallFactor<false, N>>(a, ft, 1, stream);
         });
     } else {
-        r = token_scale ? launch<Factor<true>>(f, ftiles, stream) : launch<Factor<false>>(f, ftiles, stream);
+        r = fn == 256 ? (token_scale ? launch<Factor<true, 256>>(f, ftiles, stream)
+                                     : launch<Factor<false, 256>>(f, ftiles, stream))
+                      : (token_scale ? launch<Factor<true, 128>>(f, ftiles, stream)
+                                     : launch<Factor<false, 128>>(f, ftiles, stream));
     }
     if (r != MOE_OK) return r;
     if (dtoken_scale) {
@@ -506,11 +528,23 @@ MOE_API moe_status moe_gated_ffn_backward(int32_t T, int32_t d, int32_t h, const
                    (int)T, scale_parts(T, d, h), f.part, dtoken_scale);
         if ((r = launch_status()) != MOE_OK) return r;
     }
-    const int64_t wt = (int64_t)3 * g.md * g.nd, xt = (int64_t)g.mt * g.md;
-    const int units = pairs_for(wt + xt);
-    g.long_x = 2 * g.hb > g.tb;
-    if (g.long_x) share(g, units, xt, 2 * g.hb, wt, g.tb);
-    else share(g, units, wt, g.tb, xt, 2 * g.hb);
-    if (dx32) return dw32 ? launch<Grad<true, true>>(g, wt + xt, stream) : launch<Grad<true, false>>(g, wt + xt, stream);
-    return dw32 ? launch<Grad<false, true>>(g, wt + xt, stream) : launch<Grad<false, false>>(g, wt + xt, stream);
+    // tiles of 128 columns, which take 1.7 times as long for the same products, where a
+    // pair's share of those is still less than the longest tile of 256
+    const int64_t cx = 2 * g.hb, cw = g.tb;
+    auto count = [&](int n, int64_t &wt, int64_t &xt) {
+        g.nd = (d + n - 1) / n;
+        g.nh = (h + n - 1) / n;
+        wt = (int64_t)g.md * g.nh + (int64_t)2 * g.mh * g.nd;
+        xt = (int64_t)g.mt * g.nd;
+    };
+    int64_t wt, xt;
+    count(256, wt, xt);
+    const bool wide = 17 * (wt * cw + xt * cx) > 10 * std::max(cx, cw) * pairs_for((int64_t)1 << 40);
+    if (!wide) count(128, wt, xt);
+    const int64_t tiles = wt + xt;
+    const int units = pairs_for(tiles);
+    g.long_x = cx > cw;
+    if (g.long_x) share(g, units, xt, cx, wt, cw);
+    else share(g, units, wt, cw, xt, cx);
+    return wide ? launch_grad<256>(g, dx32, dw32, tiles, stream) : launch_grad<128>(g, dx32, dw32, tiles, stream);
 }

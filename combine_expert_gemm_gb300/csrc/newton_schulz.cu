@@ -204,17 +204,18 @@ __device__ __forceinline__ void store_mirrored(Epi &e, const uint32_t (&w)[16], 
     }
 }
 
-template <int MODE>
+template <int MODE, int N>
 struct Ns {
     using Args = NsArgs;
     struct Regs {};
-    static constexpr int kStages = 3;
-    static constexpr int kStageBytes = 4 * OPERAND;  // hi and lo of A, hi and lo of B
+    static constexpr int kN = N, kStages = N == 256 ? 3 : 4;
+    static constexpr int kStageBytes = 2 * OPERAND + 2 * b_bytes(N);  // hi and lo of A, hi and lo of B
     static constexpr int kGroup = 2;
-    static constexpr int COLS = BN / 2;
+    static constexpr int COLS = N / 2;
     static constexpr bool kSym = MODE < NS_APPLY;
     static __device__ __forceinline__ int per_matrix(const Args &p) {
-        return kSym ? p.mt * (p.mt + 1) / 2 : p.mt * p.nt;
+        // row m of the upper triangle has nt - m PM / N tiles
+        return kSym ? p.mt * p.nt - p.mt * (p.mt - 1) / 2 * (PM / N) : p.mt * p.nt;
     }
     static __device__ __forceinline__ int count(const Args &p, int unit, int units) {
         return strided_count(p.B * per_matrix(p), unit, units);
@@ -222,33 +223,33 @@ struct Ns {
     static __device__ __forceinline__ Tile tile(const Args &p, int unit, int units, int i) {
         const int g = unit + i * units, per = per_matrix(p), z = g / per;
         int r = g - z * per, m = 0, n;
-        if (kSym) {  // row m of the upper triangle has mt - m tiles
-            while (r >= p.mt - m) r -= p.mt - m++;
-            n = m + r;
+        if (kSym) {
+            while (r >= p.nt - m * (PM / N)) r -= p.nt - PM / N * m++;
+            n = m * (PM / N) + r;
         } else {
             band_tile(r, p.mt, p.nt, m, n);
         }
-        return Tile{z, m * PM, n * BN};
+        return Tile{z, m * PM, n * N};
     }
     static __device__ __forceinline__ int k_blocks(const Args &p, const Tile &) { return (p.k + BK - 1) / BK; }
     static __device__ __forceinline__ void load(const Args &p, const Tile &t, int kb, uint32_t s, uint32_t bar,
                                                 int rank) {
-        const int k = kb * BK, row = t.m + rank * BM, col = t.n + rank * BM;
+        const int k = kb * BK, row = t.m + rank * BM, col = t.n + rank * (N / 2);
         load_k(s, &p.a, bar, k, row, t.z);
         load_k(s + OPERAND, &p.a, bar, k, row, t.z + p.B);
         if (kSym) {
             load_k(s + 2 * OPERAND, &p.b, bar, k, col, t.z);
-            load_k(s + 3 * OPERAND, &p.b, bar, k, col, t.z + p.B);
+            load_k(s + 2 * OPERAND + b_bytes(N), &p.b, bar, k, col, t.z + p.B);
         } else {
-            load_mn(s + 2 * OPERAND, &p.b, bar, col, k, t.z);
-            load_mn(s + 3 * OPERAND, &p.b, bar, col, k, t.z + p.B);
+            load_mn<N / 2>(s + 2 * OPERAND, &p.b, bar, col, k, t.z);
+            load_mn<N / 2>(s + 2 * OPERAND + b_bytes(N), &p.b, bar, col, k, t.z + p.B);
         }
     }
     static __device__ __forceinline__ void mma(const Args &, const Tile &, uint32_t d, uint32_t s, bool first) {
         // the small products first: what they leave is cut least
-        mma_block<0, false, !kSym>(d, s + OPERAND, s + 2 * OPERAND, first);
-        mma_block<0, false, !kSym>(d, s, s + 3 * OPERAND, false);
-        mma_block<0, false, !kSym>(d, s, s + 2 * OPERAND, false);
+        mma_block<0, N, false, !kSym>(d, s + OPERAND, s + 2 * OPERAND, first);
+        mma_block<0, N, false, !kSym>(d, s, s + 2 * OPERAND + b_bytes(N), false);
+        mma_block<0, N, false, !kSym>(d, s, s + 2 * OPERAND, false);
     }
     // The chunks of 32 columns one after the other in a loop, which picks its sums by
     // selections, as registers have no index: unrolled over the four chunks, the
@@ -269,8 +270,11 @@ struct Ns {
             float v[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                const float a = c & 1 ? sum[32 + i] : sum[i], b = c & 1 ? sum[96 + i] : sum[64 + i];
-                v[i] = c & 2 ? b : a;
+                v[i] = c & 1 ? sum[32 + i] : sum[i];
+                if constexpr (COLS > 64) {
+                    const float b = c & 1 ? sum[96 + i] : sum[64 + i];
+                    v[i] = c & 2 ? b : v[i];
+                }
             }
             if constexpr (MODE == NS_LAST) {
                 last(p, t, e, row0, col, v);
@@ -299,7 +303,7 @@ struct Ns {
             for (int i = 0; i < 16; ++i) split2(v[2 * i], v[2 * i + 1], hi[i], lo[i]);
             store_block16(e, hi, &p.o, col, row0, t.z);
             store_block16(e, lo, &p.o, col, row0, t.z + p.B);
-            if (kSym && t.m != t.n) {
+            if (kSym && t.n >= t.m + PM) {
                 store_mirrored(e, hi, &p.o, row0, col, t.z);
                 store_mirrored(e, lo, &p.o, row0, col, t.z + p.B);
             }
@@ -911,6 +915,11 @@ moe_status check_steps(int steps, const float *coefficients, float eps, float (&
     return bounded(steps, coef) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
+template <int MODE>
+moe_status launch_ns(const NsArgs &a, int columns, int64_t tiles, cudaStream_t st) {
+    return columns == 128 ? launch<Ns<MODE, 128>>(a, tiles, st) : launch<Ns<MODE, 256>>(a, tiles, st);
+}
+
 template <int MODE, bool TALL>
 moe_status launch_small(SmallNsArgs a, const uint16_t *pa, int64_t lda, int arows, int acols, const uint16_t *pb,
                         int64_t ldb, int brows, int bcols, cudaStream_t st) {
@@ -984,7 +993,12 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
     gram.status = reinterpret_cast<int *>(ws);
     gram.m = gram.n = m;
     gram.k = n;
-    gram.mt = gram.nt = (m + PM - 1) / PM;
+    gram.mt = (m + PM - 1) / PM;
+    auto triangle = [&](int c) {  // tiles of c columns
+        return (int64_t)B * (gram.mt * ((m + c - 1) / c) - gram.mt * (gram.mt - 1) / 2 * (PM / c));
+    };
+    const int sn = narrow(triangle(256), triangle(128)) ? 128 : 256;  // columns of the symmetric products' tiles
+    gram.nt = (m + sn - 1) / sn;
     gram.lds = at.lds;
     poly = gram;
     poly.k = m;
@@ -992,7 +1006,8 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
     apply[0] = gram;
     apply[0].n = n;
     apply[0].k = m;
-    apply[0].nt = (n + BN - 1) / BN;
+    const int an = narrow((int64_t)B * gram.mt * ((n + 255) / 256), (int64_t)B * gram.mt * ((n + 127) / 128)) ? 128 : 256;
+    apply[0].nt = (n + an - 1) / an;
     apply[0].rows = rows;
     apply[0].cols = cols;
     apply[0].tall = tall;
@@ -1005,16 +1020,15 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
     apply[0].factor = up.factor;
     apply[1] = apply[0];
     const uint64_t planes = 2 * (uint64_t)B;
-    CUtensorMap xk[2];
+    CUtensorMap xk[2], xb[2];  // X as the Gram product's two operands
     for (int i = 0; i < 2; ++i)
-        if (!map_k(&xk[i], xs[i], n, m, planes, at.ldx) || !map_mn(&apply[i].b, xs[i], n, m, planes, at.ldx) ||
+        if (!map_k(&xk[i], xs[i], n, m, planes, at.ldx) || !map_k(&xb[i], xs[i], n, m, planes, at.ldx, sn / 2) || !map_mn(&apply[i].b, xs[i], n, m, planes, at.ldx) ||
             !map_store(&apply[i].o, xs[1 - i], n, m, planes, at.ldx) || !map_k(&apply[i].a, c, m, m, planes, at.lds))
             return MOE_ERR_CUDA;
     CUtensorMap to_s, to_c;
     if (!map_store(&to_s, s, m, m, planes, at.lds) || !map_k(&poly.a, s, m, m, planes, at.lds) ||
-        !map_store(&to_c, c, m, m, planes, at.lds))
+        !map_k(&poly.b, s, m, m, planes, at.lds, sn / 2) || !map_store(&to_c, c, m, m, planes, at.lds))
         return MOE_ERR_CUDA;
-    poly.b = poly.a;
 
     const int64_t elems = (int64_t)rows * cols;
     const int want = std::max(1, 8 * num_sms() / B);
@@ -1028,7 +1042,7 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
                cols, tall, at.ldx, x, momentum, mu, nesterov, eps, part, parts, xs[0],
                xs[0] + (int64_t)B * m * at.ldx);
     if ((r = launch_status()) != MOE_OK) return r;
-    const int64_t tri = (int64_t)B * gram.mt * (gram.mt + 1) / 2, full = (int64_t)B * apply[0].mt * apply[0].nt;
+    const int64_t tri = triangle(sn), full = (int64_t)B * apply[0].mt * apply[0].nt;
     // few tiles: one round of 128 x 128 tiles on single SMs
     const bool few = (int64_t)B * ((m + small::kM - 1) / small::kM) * ((n + small::kM - 1) / small::kM) <= num_sms();
     SmallNsArgs sm{};
@@ -1062,15 +1076,16 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
         a.q = (float)q;
         a.lin = (float)lin;
         a.o = o == s ? to_s : to_c;
-        return mode == NS_GRAM     ? launch<Ns<NS_GRAM>>(a, tri, st)
-               : mode == NS_SQUARE ? launch<Ns<NS_SQUARE>>(a, tri, st)
-                                   : launch<Ns<NS_POLY>>(a, tri, st);
+        return mode == NS_GRAM     ? launch_ns<NS_GRAM>(a, sn, tri, st)
+               : mode == NS_SQUARE ? launch_ns<NS_SQUARE>(a, sn, tri, st)
+                                   : launch_ns<NS_POLY>(a, sn, tri, st);
     };
     double most = 1.001;  // of X's singular values
     for (int k = 0; k < steps; ++k) {
         const int cur = k & 1;
         const Products t(coef + 3 * k, most);
-        gram.a = gram.b = xk[cur];
+        gram.a = xk[cur];
+        gram.b = xb[cur];
         r = symmetric(NS_GRAM, xs[cur], at.ldx, n, t.poly ? s : c, t.gr, t.gq, 0.0);
         if (r == MOE_OK && t.poly)
             r = symmetric(t.plin == 0.0 ? NS_SQUARE : NS_POLY, s, at.lds, m, c, t.pr, t.pq, t.plin);
@@ -1087,7 +1102,7 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
                 : tall ? launch_small<NS_LAST, true>(a, c, at.lds, m, m, xs[cur], at.ldx, m, n, st)
                        : launch_small<NS_LAST, false>(a, xs[cur], at.ldx, m, n, c, at.lds, m, m, st);
         } else {
-            r = last ? launch<Ns<NS_LAST>>(apply[cur], full, st) : launch<Ns<NS_APPLY>>(apply[cur], full, st);
+            r = last ? launch_ns<NS_LAST>(apply[cur], an, full, st) : launch_ns<NS_APPLY>(apply[cur], an, full, st);
         }
         if (r != MOE_OK) return r;
     }

@@ -6,10 +6,11 @@
 // Clusters of two CTAs, one CTA per SM:
 //   warp 0     TMA producer (both CTAs) into a ring of P::kStages stages;
 //   warp 1     in the leader one thread issues tcgen05.mma.cta_group::2 (M = 256
-//              across the pair, N = 256, K = 16) into two fp32 accumulators of
-//              256 TMEM columns, used in turn;
+//              across the pair, N = P::kN, K = 16) into two fp32 accumulators of
+//              kN TMEM columns, used in turn;
 //   8 more     epilogue, two warps per TMEM lane quadrant, each with half of the
-//              256 columns of its 32 rows.
+//              kN columns of its 32 rows.
+// kN is 256, or 128 where tiles of 256 columns leave too many pairs without one.
 // Both CTAs' loads complete on the leader's full barrier; the leader's commits
 // release stages and announce accumulators in both CTAs; both CTAs' epilogue
 // warps release an accumulator on the leader's barrier.
@@ -35,8 +36,9 @@ namespace pair {
 constexpr int BM = 128;              // rows of A a CTA
 constexpr int PM = 2 * BM;           // rows of A a pair
 constexpr int BK = 64;               // k of a k-block
-constexpr int BN = 256;              // columns of a tile
 constexpr int OPERAND = BM * BK * 2; // one CTA's 128 x 64 16-bit operand: 16 KB
+// One CTA's half of the N columns of B in a k-block.
+__host__ __device__ constexpr int b_bytes(int n) { return n / 2 * BK * 2; }
 constexpr int BLK = 64 * BK * 2;     // a 64 x 64 MN-major block: 8 KB
 constexpr int kTmemCols = 512;
 constexpr int kEpiWarps = 8;
@@ -89,11 +91,11 @@ inline bool make_map_16(CUtensorMap *m, const void *base, uint64_t inner, uint64
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// K-major operand (128 rows of 64 k), MN-major operand (64 k of 64 columns, two
-// boxes an operand) and 32 x 32 store blocks of one [planes, rows, inner] matrix.
+// K-major operand (128 or `box` rows of 64 k), MN-major operand (64 k of 64 columns a
+// box) and 32 x 32 store blocks of one [planes, rows, inner] matrix.
 inline bool map_k(CUtensorMap *m, const void *p, uint64_t inner, uint64_t rows, uint64_t planes = 1,
-                  uint64_t ld = 0) {
-    return make_map_16(m, p, inner, rows, planes, ld ? ld : inner, 64, BM);
+                  uint64_t ld = 0, int box = BM) {
+    return make_map_16(m, p, inner, rows, planes, ld ? ld : inner, 64, (uint32_t)box);
 }
 inline bool map_mn(CUtensorMap *m, const void *p, uint64_t inner, uint64_t rows, uint64_t planes = 1,
                    uint64_t ld = 0) {
@@ -115,16 +117,17 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, u
         : "memory");
 }
 
-// This CTA's 128 x 64 operand: K-major rows row.. of k.., or MN-major columns
-// col.. of k-rows k.. (two 64-column blocks).
+// This CTA's operand: K-major rows row.. of k.., or MN-major columns col.. of k-rows
+// k.. in blocks of 64 columns.
 __device__ __forceinline__ void load_k(uint32_t dst, const CUtensorMap *map, uint32_t bar, int k, int row,
                                        int z) {
     load_box(dst, map, bar, k, row, z);
 }
+template <int COLS>
 __device__ __forceinline__ void load_mn(uint32_t dst, const CUtensorMap *map, uint32_t bar, int col, int k,
                                         int z) {
-    load_box(dst, map, bar, col, k, z);
-    load_box(dst + BLK, map, bar, col + 64, k, z);
+#pragma unroll
+    for (int c = 0; c < COLS; c += 64) load_box(dst + c / 64 * BLK, map, bar, col + c, k, z);
 }
 
 // Descriptor of an MN-major operand: 128-byte rows of 64 elements of one k, 8-row
@@ -141,15 +144,15 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t smem_addr) {
 
 // Instruction descriptor: fp32 accumulator, A and B both bf16 (fmt 1) or both
 // fp16 (fmt 0), each K-major (0) or MN-major (1).
-__host__ __device__ constexpr uint32_t idesc16(int fmt, int a_mn, int b_mn) {
+__host__ __device__ constexpr uint32_t idesc16(int fmt, int n, int a_mn, int b_mn) {
     return (1u << 4) | ((uint32_t)fmt << 7) | ((uint32_t)fmt << 10) | ((uint32_t)a_mn << 15) |
-           ((uint32_t)b_mn << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(PM >> 4) << 24);
+           ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(PM >> 4) << 24);
 }
 
 // The four K = 16 steps of one k-block.
-template <int FMT, bool A_MN, bool B_MN>
+template <int FMT, int N, bool A_MN, bool B_MN>
 __device__ __forceinline__ void mma_block(uint32_t d_tmem, uint32_t sa, uint32_t sb, bool first) {
-    constexpr uint32_t idesc = idesc16(FMT, A_MN, B_MN);
+    constexpr uint32_t idesc = idesc16(FMT, N, A_MN, B_MN);
 #pragma unroll
     for (int kk = 0; kk < BK / 16; ++kk)
         tc_mma_bf16_pair(d_tmem, A_MN ? mn_desc(sa + kk * 2048) : sw128_kmajor_desc(sa + kk * 32),
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(threads<P>(), 1) pair_gemm(const __grid_consta
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+                    const uint32_t d_tmem = tmem_base + (uint32_t)(acc * P::kN);
                     for (int kb = k0; kb < k1; ++kb) {
                         if (!mbar_wait(smem_u32(&bars->full[stage]), phase, status, abort)) {
                             ok = false;
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(threads<P>(), 1) pair_gemm(const __grid_consta
     } else {
         if constexpr (P::kGroup > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int quad = warp & 3, ew = warp - epi_warp0<P>();
-        constexpr int COLS = BN / 2;
+        constexpr int COLS = P::kN / 2;
         Epi e;
         e.col = (ew >> 2) * COLS;
         e.lane = lane;
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(threads<P>(), 1) pair_gemm(const __grid_consta
                 P::before(p, t, e, wrow, regs);
                 if (!mbar_wait(smem_u32(&bars->tfull[acc]), acc_phase, status, abort)) break;
                 tc_fence_after();
-                e.taddr = tlane + (uint32_t)(acc * BN);
+                e.taddr = tlane + (uint32_t)(acc * P::kN);
                 P::epilogue(p, t, e, wrow, regs);
                 release();
             } else {
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(threads<P>(), 1) pair_gemm(const __grid_consta
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t at = tlane + (uint32_t)(acc * BN);
+                    const uint32_t at = tlane + (uint32_t)(acc * P::kN);
 #pragma unroll
                     for (int c = 0; c < COLS; c += 16) {
                         uint32_t v[16];
@@ -410,6 +413,16 @@ __global__ void __launch_bounds__(threads<P>(), 1) pair_gemm(const __grid_consta
 // CTA pairs of a launch over so many tiles.
 inline int pairs_for(int64_t tiles) {
     return (int)std::min<int64_t>(std::max(num_sms() / 2, 1), std::max<int64_t>(tiles, 1));
+}
+
+// Whether tiles of 128 columns serve better than half as many of 256.  They read as much
+// of A for half the products and take 0.6 to 0.86 of a wide tile's time (the Gram
+// product of one 2048 x 4096 matrix, 72 narrow tiles or 36 wide ones on 76 pairs: 50
+// against 63 us; the hidden units of 8192 tokens, 512 or 256 tiles: 72 against 48), so only
+// where they need no more rounds.
+inline bool narrow(int64_t wide_tiles, int64_t narrow_tiles) {
+    const int64_t pairs = std::max(num_sms() / 2, 1);
+    return (narrow_tiles + pairs - 1) / pairs <= (wide_tiles + pairs - 1) / pairs;
 }
 
 template <class P>
