@@ -212,6 +212,7 @@ struct Ns {
     static constexpr int kStageBytes = 2 * OPERAND + 2 * b_bytes(N);  // hi and lo of A, hi and lo of B
     static constexpr int kGroup = 2;
     static constexpr int COLS = N / 2;
+    static constexpr int kRows = 16;  // M's rows of a lane in flight in the last epilogue
     static constexpr bool kSym = MODE < NS_APPLY;
     static __device__ __forceinline__ int per_matrix(const Args &p) {
         // row m of the upper triangle has nt - m PM / N tiles
@@ -261,6 +262,8 @@ struct Ns {
         const int row0 = t.m + wrow;
         if (row0 >= p.m) return;
         const int col0 = t.n + e.col, row = row0 + e.lane;
+        float ahead[kRows];  // NS_LAST: the weights of the rows to come
+        if constexpr (MODE == NS_LAST) fetch_w(p, t.z, row0, col0, 0, e.lane, ahead);
         uint4 s4[8];  // NS_POLY: S's pieces of the 32 columns to come
         if constexpr (MODE == NS_POLY) fetch_s(p, t.z, row, col0, s4);
 #pragma unroll 1
@@ -277,7 +280,7 @@ struct Ns {
                 }
             }
             if constexpr (MODE == NS_LAST) {
-                last(p, t, e, row0, col, v);
+                last(p, t, e, row0, col, c + 1 < COLS / 32, v, ahead);
                 continue;
             }
             uint32_t hi[16], lo[16];
@@ -320,13 +323,24 @@ struct Ns {
             v[4 + i] = in ? reinterpret_cast<const uint4 *>(sl)[i] : make_uint4(0, 0, 0, 0);
         }
     }
+    // The weights of rows [i0, i0 + kRows) of the 32 x 32 block at (row0, col) of the
+    // iterate, in M's orientation.
+    static __device__ __forceinline__ void fetch_w(const Args &p, int z, int row0, int col, int i0, int lane,
+                                                   float (&w)[kRows]) {
+        if (!p.w) return;
+        const int r = (p.tall ? col : row0) + i0, j = (p.tall ? row0 : col) + lane;
+        const int n = j < p.cols ? p.rows - r : 0;
+        const float *src = p.w + ((int64_t)z * p.rows + r) * p.cols + j;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i, src += p.cols) w[i] = i < n ? *src : 0.0f;
+    }
     // 32 x 32 values of the last iterate (rows row0.., columns col..) to M's own
     // layout, whatever its alignment is: through shared memory, so that the lanes run
     // along M's rows (the iterate's columns where M is tall) and the loop over M's rows is
-    // short.  kRows rows of a lane are on their way at once.
-    static __device__ __forceinline__ void last(const Args &p, const Tile &t, Epi &e, int row0, int col,
-                                                const float (&v)[32]) {
-        constexpr int kRows = 16;
+    // short.  The weights of the kRows rows to come are on their way while kRows are
+    // updated; `more`: another block of this tile follows.
+    static __device__ __forceinline__ void last(const Args &p, const Tile &t, Epi &e, int row0, int col, bool more,
+                                                const float (&v)[32], float (&ahead)[kRows]) {
         float *blk = reinterpret_cast<float *>(e.blk);  // row i of M: 32 columns, rotated by i
         __syncwarp();
         if (p.tall) {
@@ -352,11 +366,10 @@ struct Ns {
         for (int i0 = 0; i0 < rows; i0 += kRows, at += kRows * step) {
             const int n = in ? rows - i0 : 0;
             float u[kRows];
-            if (p.w) {
-                const float *src = p.w + at;
 #pragma unroll
-                for (int i = 0; i < kRows; ++i, src += step) u[i] = i < n ? *src : 0.0f;
-            }
+            for (int i = 0; i < kRows; ++i) u[i] = ahead[i];
+            const bool down = i0 + kRows < rows;
+            if (down || more) fetch_w(p, t.z, row0, down ? col : col + 32, down ? i0 + kRows : 0, e.lane, ahead);
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
                 const float o = f * blk[(i0 + i) * 32 + ((e.lane + i0 + i) & 31)];
