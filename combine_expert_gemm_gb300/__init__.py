@@ -1,5 +1,6 @@
 """Python binding of the routed-expert layer C ABI (``include/moe.h`` and
-``include/moe_mxfp8.h``).
+``include/moe_mxfp8.h``); ``block`` and ``dense`` bind ``include/moe_block.h`` and
+``include/moe_dense.h``.
 
 Argument marshalling only: every step of the layer runs in the sm_103a
 kernels of ``_build/libmoe_gb300.so``.  Tensors are torch CUDA tensors (the

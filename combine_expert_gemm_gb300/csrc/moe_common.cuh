@@ -55,7 +55,9 @@ inline int64_t buffer_rows(const moe_shape *s) {
 // grid launch.  The next grid's CTAs are thus scheduled, up to their own
 // wait, while this grid runs, which hides the launch gap between kernels.
 // The wait comes before any memory access and before any early return, so a
-// grid never completes ahead of its predecessor.
+// grid never completes ahead of its predecessor.  (The products of pair_gemm.cuh
+// and small_gemm.cuh set up their barriers before it, and a grid of the latter
+// loads weights there where the grid ahead has waited for their writers.)
 __device__ __forceinline__ void pdl_enter() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

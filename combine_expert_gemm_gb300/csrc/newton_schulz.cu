@@ -848,7 +848,7 @@ struct Layout {
         x[1] = x[0] + xb;
         s = x[1] + xb;
         c = s + sb;
-        bytes = c + sb;
+        bytes = m <= kFuseM && n <= kFuseN ? 256 : c + sb;  // one CTA a matrix needs the status word only
     }
 };
 
@@ -895,7 +895,9 @@ struct Products {
             gq = b;
         } else {
             const double shift = b / (2 * c);
-            const bool square = std::fabs(shift) <= 8.0 && most * most + std::fabs(shift) < 60.0;
+            // beyond four times S's size the squares' rounding would outgrow b S's
+            const double size = std::max(1.0, most * most);
+            const bool square = std::fabs(shift) <= std::min(8.0, 4.0 * size) && size + std::fabs(shift) < 60.0;
             gr = square ? shift : 0.0;
             gq = 1.0;
             pr = square ? a - b * b / (4 * c) : a;

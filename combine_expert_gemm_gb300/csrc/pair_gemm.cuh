@@ -428,7 +428,17 @@ inline bool narrow(int64_t wide_tiles, int64_t narrow_tiles) {
 template <class P>
 moe_status launch(const typename P::Args &args, int64_t tiles, cudaStream_t st) {
     static PerDeviceOnce smem_attr;
-    if (!device_once(smem_attr, [] { return set_smem_limit(pair_gemm<P>, smem_bytes<P>()); }))
+    if (!device_once(smem_attr, [] {
+            if (P::kGroup > 0) {
+                // the epilogue's share has to fit what the block is launched with: a
+                // setmaxnreg past it would wait for ever
+                cudaFuncAttributes at;
+                if (cudaFuncGetAttributes(&at, pair_gemm<P>) != cudaSuccess ||
+                    at.numRegs * threads<P>() < 128 * 40 + 256 * 232)
+                    return false;
+            }
+            return set_smem_limit(pair_gemm<P>, smem_bytes<P>());
+        }))
         return MOE_ERR_CUDA;
     const int pairs = pairs_for(tiles);
     cudaLaunchConfig_t cfg = {};

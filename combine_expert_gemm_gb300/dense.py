@@ -114,7 +114,8 @@ def _coefficients(c, steps):
     for each."""
     if c is None:
         return None
-    c = [float(v) for v in c] if not hasattr(c[0], "__len__") else [float(v) for t in c for v in t]
+    rows = [list(t) if getattr(t, "ndim", 1) and hasattr(t, "__iter__") else [t] for t in c]
+    c = [float(v) for t in rows for v in t]
     if len(c) == 3:
         c = c * steps
     if len(c) != 3 * steps:
@@ -164,6 +165,7 @@ class SharedExpert:
         self.T, self.act = T, act
         self.w_gate, self.w_up, self.w_down = w_gate, w_up, w_down
         self.h_act, self.p_save, self.q_save = (torch.empty((T, h), dtype=_bf16, **e) for _ in range(3))
+        self.saved = False                             # whether a forward has run
         self.token_scale = None                        # scale, or None where every token's is 1
         self.scale = torch.empty(T, **e)
         self.dw_gate, self.dw_up = (torch.empty((h, d), **e) for _ in range(2))
@@ -184,9 +186,12 @@ class SharedExpert:
             self.token_scale = None
         gated_ffn(x, self.w_gate, self.w_up, self.w_down, add, self.token_scale, y, self.h_act,
                   self.p_save, self.q_save, self.ws, self.act, stream)
+        self.saved = True
 
     def backward(self, x, dy, dx_in, dx, stream=None):
         """dx = dx_in + the gradient of the forward's x (which x is), and the weights'."""
+        if not self.saved:
+            raise RuntimeError("backward of a shared expert without a forward")
         if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[0] != self.T:
             raise ValueError(f"x: expected [{self.T}, d]")
         gated_ffn_backward(x, self.w_gate, self.w_up, self.w_down, self.token_scale, self.h_act,
@@ -207,6 +212,8 @@ class Muon:
     def __init__(self, weights, lr=0.02, mu=0.95, weight_decay=0.0, nesterov=True, steps=5,
                  coefficients=None, scale=None, eps=1e-7):
         self.weights = list(weights)
+        if not self.weights:
+            raise ValueError("weights: none given")
         dev = self.weights[0][0].device
         self.momentum = [torch.zeros_like(w) for w, _ in self.weights]
         self.lr = torch.tensor([lr], dtype=_f32, device=dev)

@@ -89,7 +89,7 @@ moe_status moe_gated_ffn_backward(int32_t T, int32_t d, int32_t h, const moe_bf1
 
 /* Bytes of workspace of moe_newton_schulz and moe_muon_step (0 if a size is
  * invalid): the iterates of all B matrices, about 4 B (2 m n + 2 m^2) bytes with m
- * the short and n the long side. */
+ * the short and n the long side; the status word alone up to 128 x 256. */
 size_t moe_newton_schulz_workspace_bytes(int32_t B, int32_t rows, int32_t cols);
 
 /*
@@ -111,6 +111,7 @@ size_t moe_newton_schulz_workspace_bytes(int32_t B, int32_t rows, int32_t cols);
  * coefficients that can take a singular value in [0, 1] past 7.5, or the factor
  * a + b s^2 + c s^4 past 60, are refused (MOE_ERR_UNSUPPORTED).  A matrix with an
  * infinity or a NaN gives NaNs, in its own entries only.
+ * |M|_F is summed in fp32: above 1.8e19 it is infinite there and out is 0.
  * rows and cols are at most 65536, eps is finite and >= 1e-30.  B = 0 does nothing.
  */
 moe_status moe_newton_schulz(int32_t B, int32_t rows, int32_t cols, int32_t x_dtype, const void *x,

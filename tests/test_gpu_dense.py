@@ -311,6 +311,30 @@ def test_gated_ffn_past_32_bit_offsets(moe):
     _within(dx[-n:], b["dx"], e["dx"], "dx", 6e-3)
 
 
+@pytest.mark.parametrize("T", [1, 20, 60, 100])
+def test_gated_ffn_reads_weights_written_just_before(moe, T):
+    """The second product's weights are loaded while the first runs: they are those that
+    the kernel ahead of the call has written."""
+    d, h = 1024, 512
+    t = _ffn_inputs(T, d, h, False, False, seed=5)
+    x, wg, wu, wd = (_dev(t[k]) for k in ("x", "wg", "wu", "wd"))
+    sources = [(wd * s).contiguous() for s in (1.0, -2.0, 0.5)]
+    y, hb = torch.empty(T, d, dtype=BF, device=DEV), torch.empty(T, h, dtype=BF, device=DEV)
+    ws = _ws(moe.gated_ffn_workspace_bytes(T, d, h))
+    want = []
+    for s in sources:
+        moe.gated_ffn(x, wg, wu, s, None, None, y, hb, None, None, ws)
+        torch.cuda.synchronize()
+        want.append(y.clone())
+    live, got = torch.empty_like(wd), []
+    for i in range(30):
+        live.copy_(sources[i % 3])
+        moe.gated_ffn(x, wg, wu, live, None, None, y, hb, None, None, ws)
+        got.append(y.clone())
+    for i, g in enumerate(got):
+        assert torch.equal(g, want[i % 3]), i
+
+
 # ------------------------------------------------------------ Newton-Schulz --
 
 def _mats(B, rows, cols, seed=0, floor=0.3):
@@ -380,6 +404,13 @@ def test_newton_schulz_coefficients_in_place_and_unaligned(moe, B, rows, cols):
     _check_ns(_ns(moe, m, steps=4, coefficients=cubic), want, _ns_bound(norms, 4), "one triple")
     want, norms = ref.newton_schulz(m, 1)
     _check_ns(_ns(moe, m, steps=1), want, _ns_bound(norms, 1), "one step")
+    for c in (torch.tensor(ref.COEF), torch.tensor([ref.COEF]), [list(ref.COEF)]):
+        assert torch.equal(_ns(moe, m, steps=1, coefficients=c), _ns(moe, m, steps=1))
+    # a shift of the square beyond its range: S is read instead (slopes below 4, and the
+    # weights of the bound's rounding, a + 3 |b| r^2 + 5 |c| r^4, below 42)
+    wide = [(3.0, -1.5, 0.05)] + [cubic] * 3
+    want, norms = ref.newton_schulz(m, 4, wide)
+    _check_ns(_ns(moe, m, steps=4, coefficients=wide), want, _ns_bound(norms, 4), "wide shift")
     plain = _ns(moe, m)
     buf = torch.zeros(m.numel() + 1, device=DEV)
     view = buf[1:].view(B, rows, cols)  # 4-byte aligned only
@@ -500,7 +531,7 @@ def test_newton_schulz_argument_checks(moe):
     moe.newton_schulz(m, out, ws)
     moe.newton_schulz(m[0], out[0], ws)
     for a, err in [((m.half(), out, ws), TypeError), ((m[0, 0], out, ws), ValueError), ((m, out[:1], ws), ValueError),
-                   ((m, out, ws[:300]), moe.MoEError), ((m.cpu(), out, ws), ValueError),
+                   ((m, out, ws[:200]), moe.MoEError), ((m.cpu(), out, ws), ValueError),
                    ((m.transpose(1, 2), out, ws), ValueError)]:
         with pytest.raises(err):
             moe.newton_schulz(*a)

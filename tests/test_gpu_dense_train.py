@@ -100,6 +100,22 @@ def test_block_with_shared_expert(moe, scaled, act):
         assert off(shared.dtoken_scale, s64.grad) < TOL
 
 
+def test_shared_expert_refuses(moe):
+    w = [torch.zeros(*q, dtype=BF, device=DEV) for q in ((64, 64), (64, 64), (64, 64))]
+    e = moe.SharedExpert(10, *w)
+    x, y = torch.zeros(10, 64, dtype=BF, device=DEV), torch.zeros(10, 64, dtype=BF, device=DEV)
+    with pytest.raises(RuntimeError):
+        e.backward(x, y, None, torch.zeros_like(x))
+    with pytest.raises(ValueError):
+        e.forward(x[:9], None, y)
+    with pytest.raises(ValueError):
+        e.forward(x, None, y, torch.ones(9, device=DEV))
+    with pytest.raises(ValueError):
+        moe.Muon([])
+    e.forward(x, None, y)
+    e.backward(x, y, None, torch.empty_like(x))
+
+
 def test_block_without_shared_expert_keeps_its_bits(moe):
     s, p, e, x, dout, _ = _setup(moe, 100, 64, 4, 2, 64, 64, 6)
     w = [p[k].to(DEV) for k in ("gamma", "beta", "w_router", "bias", "w_gate", "w_up", "w_down")]
