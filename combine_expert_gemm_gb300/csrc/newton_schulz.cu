@@ -943,8 +943,9 @@ moe_status launch_small(SmallNsArgs a, const uint16_t *pa, int64_t lda, int arow
     const int ft = (a.F + small::kM - 1) / small::kM;
     // as few tokens a tile as leave every tile an SM of its own (an MN-major operand
     // comes in blocks of 64)
+    // (one tile of a symmetric product is best whole: it loads one operand)
     int n = 128;
-    while (n > (b_mn ? 64 : 32) && (int64_t)a.B * ft * ((a.T + n / 2 - 1) / (n / 2)) <= num_sms()) n /= 2;
+    while (!(kSym && a.T <= small::kM) && n > (b_mn ? 64 : 32) && (int64_t)a.B * ft * ((a.T + n / 2 - 1) / (n / 2)) <= num_sms()) n /= 2;
     int tiles = ft;  // of a matrix and token tile, or of a triangle
     a.tt = (a.T + n - 1) / n;
     if (kSym && n == small::kM) {
@@ -1058,8 +1059,10 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
                xs[0] + (int64_t)B * m * at.ldx);
     if ((r = launch_status()) != MOE_OK) return r;
     const int64_t tri = triangle(sn), full = (int64_t)B * apply[0].mt * apply[0].nt;
-    // few tiles: one round of 128 x 128 tiles on single SMs
-    const bool few = (int64_t)B * ((m + small::kM - 1) / small::kM) * ((n + small::kM - 1) / small::kM) <= num_sms();
+    // Single SMs where one round of 128 x 128 tiles holds the products, and where m fits one
+    // tile: half of a pair's rows would be padding (45 matrices of 1873 x 70: 375 us).
+    const bool few = (m <= small::kM && (int64_t)B * ((n + 63) / 64) <= 65535) ||
+                     (int64_t)B * ((m + small::kM - 1) / small::kM) * ((n + small::kM - 1) / small::kM) <= num_sms();
     SmallNsArgs sm{};
     sm.B = B;
     sm.status = gram.status;

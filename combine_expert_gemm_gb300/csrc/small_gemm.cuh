@@ -18,15 +18,15 @@
 //   kPairs   the features are 64 pairs (rows 0-63 and 64-127 belong together);
 //   kFmt     1 for bf16 operands, 0 for fp16;
 //   kPieces  1, or 2: each operand is a high and a low piece, a product the three
-//            of them that count (newton_schulz.cu), and the k-blocks of a CTA go to four
-//            accumulators, which are added in fp32 (pair_gemm.cuh says why);
+//            of them that count (newton_schulz.cu), and an accumulator holds one
+//            k-block, which are added in fp32 registers (pair_gemm.cuh says why);
 //   kAMn / kBMn  the operand's rows are its inner dimension (MN-major);
 //   kMirror  the result is symmetric and the operands one: only tiles on and above the
 //            diagonal are computed (kN is 128), and each is stored twice, once from
-//            a transposed copy of the sums;
+//            a transposed copy of the sums; one on the diagonal loads A alone;
 //   kEarly   A may be loaded before the wait for the grid ahead: that grid is one of ours
 //            that waited for all before it and does not write A;
-//   load_a / load_b (of piece q); In and fetch, what an item needs from memory; emit.
+//   load_a / load_b (of piece q), prefetch_maps; In and fetch, what an item needs from memory; emit.
 #pragma once
 
 #include "pair_gemm.cuh"
@@ -37,7 +37,7 @@ namespace small {
 constexpr int kM = 128;                       // features of a tile
 constexpr int kBK = 64;
 constexpr int kABytes = kM * kBK * 2;         // 16 KB
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;                  // of the epilogue; a producer and an MMA warp follow
 constexpr int kMaxSplit = 8;
 
 template <class P>
@@ -54,14 +54,15 @@ __host__ __device__ constexpr int stages() {
 // four for 16 tokens, the longer code came in 2 us later for one token).
 template <class P>
 __host__ __device__ constexpr int items_ahead() { return P::kN >= 128 ? 4 : P::kN == 64 ? 2 : 1; }
-// Accumulators and the TMEM columns of all of them.
+// Accumulators, used in turn, and the TMEM columns of all of them.
 template <class P>
 __host__ __device__ constexpr int accs() { return P::kPieces == 2 ? 4 : 1; }
+constexpr int kGroup = 1;  // k-blocks of an accumulator with pieces (with two: 8e-6 for 128 x 4096)
 template <class P>
 __host__ __device__ constexpr int columns() { return accs<P>() * P::kN < 32 ? 32 : accs<P>() * P::kN; }
 
 struct alignas(8) Bars {
-    uint64_t full[6], empty[6], done;
+    uint64_t full[6], empty[6], tfull[4], tempty[4], done;
     uint32_t tmem_base;
     int abort;
 };
@@ -96,7 +97,7 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
 }
 
 template <class P>
-__global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ typename P::Args p) {
+__global__ void __launch_bounds__(kThreads + 64) small_gemm(const __grid_constant__ typename P::Args p) {
     constexpr int STAGES = stages<P>(), SB = stage_bytes<P>(), AB = a_bytes<P>(), N = P::kN;
     constexpr int kBBytes = N * kBK * 2, kItems = items_ahead<P>();
     extern __shared__ uint8_t smem_raw[];
@@ -116,9 +117,11 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
         t0 = m * kM;
         f0 = (m + r) * kM;
     }
+    const bool diagonal = P::kMirror && t0 == f0;  // B is A
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kb0 = p.nk * rank / split, kb1 = p.nk * (rank + 1) / split, nk = kb1 - kb0;
-    const int group = (nk + accs<P>() - 1) / accs<P>();  // k-blocks of an accumulator
+    constexpr int ACCS = accs<P>();
+    const int group = P::kPieces == 2 ? kGroup : nk;  // k-blocks of an accumulator
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -126,28 +129,32 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
             mbar_init(smem_u32(&bars->empty[s]), 1);
         }
         mbar_init(smem_u32(&bars->done), 1);
+        for (int a = 0; a < ACCS; ++a) {
+            mbar_init(smem_u32(&bars->tfull[a]), 1);
+            mbar_init(smem_u32(&bars->tempty[a]), kThreads / 32);
+        }
         bars->abort = 0;
         fence_mbar_init();
     }
-    if (threadIdx.x == 64) P::prefetch_maps(p);
+    if (threadIdx.x == 32) P::prefetch_maps(p);
     __syncthreads();
 
     const int first = min(nk, STAGES);
     auto stage_at = [&](int s) { return smem_u32(smem + s * SB); };
     auto issue_a = [&](int i) {
         const uint32_t bar = smem_u32(&bars->full[i % STAGES]);
-        mbar_arrive_expect_tx(bar, SB);
+        mbar_arrive_expect_tx(bar, diagonal ? AB : SB);
 #pragma unroll
         for (int q = 0; q < P::kPieces; ++q)
             P::load_a(p, stage_at(i % STAGES) + q * kABytes, bar, kb0 + i, f0, z, q);
     };
-    if (P::kEarly && threadIdx.x == 0)
+    if (P::kEarly && threadIdx.x == kThreads)
         for (int i = 0; i < first; ++i) issue_a(i);
     // Tensor memory is taken behind the wait, as in pair_gemm.cuh, but behind a grid of
     // ours: two of these take 256 of the 512 columns at most.
-    if (P::kEarly && warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), columns<P>());
+    if (P::kEarly && warp == kThreads / 32 + 1) tmem_alloc(smem_u32(&bars->tmem_base), columns<P>());
     pdl_enter();
-    if (!P::kEarly && warp == 1) tmem_alloc(smem_u32(&bars->tmem_base), columns<P>());
+    if (!P::kEarly && warp == kThreads / 32 + 1) tmem_alloc(smem_u32(&bars->tmem_base), columns<P>());
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -165,9 +172,8 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
             if (i < items) P::fetch(p, row0 + (i >> shift), col0 + item_f(i), z, in[u]);
         }
     };
-    fetch(0, min(N, p.T - t0) * per, t0, f0);
 
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == kThreads) {
         bool ok = true;
         int issued = 0;
         for (int i = 0; i < nk; ++i, ++issued) {
@@ -178,6 +184,7 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
                 break;
             }
             if (!P::kEarly || i >= first) issue_a(i);
+            if (diagonal) continue;
 #pragma unroll
             for (int q = 0; q < P::kPieces; ++q)
                 P::load_b(p, stage_at(s) + AB + q * kBBytes, smem_u32(&bars->full[s]), kb0 + i, t0, z, q);
@@ -188,11 +195,10 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
                 mbar_wait(smem_u32(&bars->full[i % STAGES]), (uint32_t)((i / STAGES) & 1), status, &no_abort);
             }
         }
-    } else if (threadIdx.x == 32) {
+    } else if (threadIdx.x == kThreads + 32) {
         constexpr uint32_t idesc = (1u << 4) | ((uint32_t)P::kFmt << 7) | ((uint32_t)P::kFmt << 10) |
                                    ((uint32_t)P::kAMn << 15) | ((uint32_t)P::kBMn << 16) | ((uint32_t)(N >> 3) << 17) |
                                    ((uint32_t)(kM >> 4) << 24);
-        // MN-major operands of fewer than 128 rows are one 64-element block
         auto mma = [&](uint32_t d, uint32_t sa, uint32_t sb, bool fresh) {
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk)
@@ -200,13 +206,16 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
                             P::kBMn ? pair::mn_desc(sb + kk * 2048) : sw128_kmajor_desc(sb + kk * 32), idesc,
                             fresh && kk == 0 ? 0u : 1u);
         };
-        int acc = 0, left = group;
-        for (int i = 0; i < nk; ++i) {
-            const int s = i % STAGES;
+        int in_group = 0, g = 0, i = 0;
+        for (; i < nk; ++i) {
+            const int s = i % STAGES, acc = g % ACCS;
+            const bool fresh = in_group == 0;
+            if (fresh && g >= ACCS &&
+                !mbar_wait(smem_u32(&bars->tempty[acc]), (uint32_t)((g / ACCS - 1) & 1), status, abort))
+                break;
             if (!mbar_wait(smem_u32(&bars->full[s]), (uint32_t)((i / STAGES) & 1), status, abort)) break;
             tc_fence_after();
-            const uint32_t sa = stage_at(s), sb = sa + AB, d = tmem + acc * N;
-            const bool fresh = left == group;
+            const uint32_t sa = stage_at(s), sb = diagonal ? sa : sa + AB, d = tmem + acc * N;
             if (P::kPieces == 2) {  // the small products first
                 mma(d, sa + kABytes, sb, fresh);
                 mma(d, sa, sb + kBBytes, false);
@@ -215,56 +224,79 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
                 mma(d, sa, sb, fresh);
             }
             tc_commit(smem_u32(&bars->empty[s]));
-            if (--left == 0) {
-                left = group;
-                ++acc;
+            if (++in_group == group || i + 1 == nk) {
+                tc_commit(smem_u32(&bars->tfull[acc]));
+                in_group = 0;
+                ++g;
             }
         }
-        // also after a wait that gave up: what was issued completes here
-        tc_commit(smem_u32(&bars->done));
+        if (i < nk) {  // a wait gave up: what was issued completes before the CTA leaves
+            tc_commit(smem_u32(&bars->done));
+            volatile int no_abort = 0;
+            mbar_wait(smem_u32(&bars->done), 0, status, &no_abort);
+        }
+    } else if (warp < kThreads / 32) {
+        fetch(0, min(N, p.T - t0) * per, t0, f0);
+        // two warps a lane quadrant, each with half of the tokens
+        constexpr int kCols = N == 16 ? 16 : N / 2;
+        const int quad = warp & 3, c0 = (warp >> 2) * kCols;
+        const bool mine = c0 < N;  // 16 tokens: the first four warps
+        const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)c0;
+        float *dst = part + quad * 32 + lane;
+        if constexpr (P::kPieces == 1) {
+            // one accumulator, which goes straight to the place of the stages, all of them
+            // read by then
+            mbar_wait(smem_u32(&bars->tfull[0]), 0, status, abort);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kCols && mine; c += 16) {
+                uint32_t v[16];
+                tmem_ld16(at + c, v);
+                tmem_ld_wait();
+                reg_fence(v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) dst[(c0 + c + i) * kM] = __uint_as_float(v[i]);
+            }
+            tc_fence_before();
+        } else {
+            // the groups' sums in registers, and then in the place of the stages
+            const int groups = (nk + group - 1) / group;
+            float sum[kCols];
+#pragma unroll 1
+            for (int g = 0; g < groups; ++g) {
+                const int acc = g % ACCS;
+                if (!mbar_wait(smem_u32(&bars->tfull[acc]), (uint32_t)((g / ACCS) & 1), status, abort)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < kCols; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(at + acc * N + c, v);
+                    tmem_ld_wait();
+                    reg_fence(v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sum[c + i] = g == 0 ? __uint_as_float(v[i]) : sum[c + i] + __uint_as_float(v[i]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc]));
+            }
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) dst[(c0 + i) * kM] = sum[i];
+            if (P::kMirror) {  // row feature, columns tokens
+                float4 *dt = reinterpret_cast<float4 *>(part + kM * kM + (quad * 32 + lane) * kPitchT + c0);
+#pragma unroll
+                for (int i = 0; i < kCols / 4; ++i)
+                    dt[i] = make_float4(sum[4 * i], sum[4 * i + 1], sum[4 * i + 2], sum[4 * i + 3]);
+            }
+        }
     }
     __syncwarp();
-    // the accumulators to shared memory, token by token: two warps a lane quadrant
-    mbar_wait(smem_u32(&bars->done), 0, status, abort);
-    tc_fence_after();
-    {
-        const int quad = warp & 3, used = accs<P>() > 1 ? (nk + group - 1) / group : 1;
-        constexpr int kHalf = N == 16 ? 16 : N / 2;  // columns of a warp
-        const int c0 = (warp >> 2) * kHalf;
-        const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16);
-        float *dst = part + quad * 32 + lane;
-#pragma unroll 1
-        for (int c = c0; c < c0 + kHalf && c < N; c += 16) {
-            uint32_t v[16];
-            tmem_ld16(at + c, v);
-            tmem_ld_wait();
-            reg_fence(v);
-            if (accs<P>() > 1) {
-#pragma unroll 1
-                for (int a = 1; a < used; ++a) {
-                    uint32_t w[16];
-                    tmem_ld16(at + a * N + c, w);
-                    tmem_ld_wait();
-                    reg_fence(w);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) dst[(c + i) * kM] = __uint_as_float(v[i]);
-            if (P::kMirror) {  // row feature, columns tokens
-                uint4 *dt = reinterpret_cast<uint4 *>(part + kM * kM + (quad * 32 + lane) * kPitchT + c);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dt[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            }
-        }
-        tc_fence_before();
-    }
     if (split > 1) cluster_sync_all();
     else __syncthreads();
 
     // the sums over the cluster, in rank order; the mirrored tile in a second pass
-    const int passes = P::kMirror && t0 != f0 ? 2 : 1;
+    const int passes = warp >= kThreads / 32 ? 0 : P::kMirror && !diagonal ? 2 : 1;
 #pragma unroll 1
     for (int pass = 0; pass < passes; ++pass) {
         const int row0 = pass ? f0 : t0, col0 = pass ? t0 : f0;
@@ -309,7 +341,7 @@ __global__ void __launch_bounds__(kThreads) small_gemm(const __grid_constant__ t
     }
     if (split > 1) cluster_sync_all();  // no CTA leaves while its sums are read
     else __syncthreads();
-    if (warp == 1) {
+    if (warp == kThreads / 32 + 1) {
         tc_fence_after();
         tmem_dealloc(tmem, columns<P>());
     }
@@ -332,7 +364,7 @@ moe_status launch(const typename P::Args &args, int ftiles, int64_t planes, cuda
         return MOE_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)args.split, (unsigned)ftiles, (unsigned)(args.tt * planes));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreads + 64);
     cfg.dynamicSmemBytes = smem_bytes<P>();
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
