@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(kThreads + 64) small_gemm(const __grid_constan
 #pragma unroll 1
     for (int pass = 0; pass < passes; ++pass) {
         const int row0 = pass ? f0 : t0, col0 = pass ? t0 : f0;
-        const uint32_t base = smem_u32(pass ? part + kM * kM : part);
+        const float *const own = pass ? part + kM * kM : part;
+        const uint32_t base = smem_u32(own);
         const int pitch = pass ? kPitchT : kM;
         const int items = min(pass ? kM : N, p.T - row0) * per;
 #pragma unroll 1
@@ -310,11 +311,21 @@ __global__ void __launch_bounds__(kThreads + 64) small_gemm(const __grid_constan
             const float4 zero = make_float4(0, 0, 0, 0);
 #pragma unroll
             for (int u = 0; u < kItems; ++u) a[u] = b[u] = zero;
+            if (split == 1) {
+#pragma unroll
+                for (int u = 0; u < kItems; ++u) {
+                    const int i = i0 + u * kThreads + (int)threadIdx.x;
+                    if (i >= items) continue;
+                    const float4 *at = reinterpret_cast<const float4 *>(own + (i >> shift) * pitch + item_f(i));
+                    a[u] = at[0];
+                    if (P::kPairs) b[u] = at[kM / 2 / 4];
+                }
+            }
 #pragma unroll 4
-            for (int r = 0; r < split; ++r) {
+            for (int r = 0; r < split && split > 1; ++r) {
                 // all items' loads of up to four ranks at once: one by one they take the
                 // distributed memory's latency each
-                const uint32_t from = split > 1 ? cluster_map(base, r) : base;
+                const uint32_t from = cluster_map(base, r);
                 float4 q[kItems], w[kItems];
 #pragma unroll
                 for (int u = 0; u < kItems; ++u) {
