@@ -150,11 +150,10 @@ __global__ void __launch_bounds__(kThreads + 64) small_gemm(const __grid_constan
     };
     if (P::kEarly && threadIdx.x == kThreads)
         for (int i = 0; i < first; ++i) issue_a(i);
-    // Tensor memory is taken behind the wait, as in pair_gemm.cuh, but behind a grid of
-    // ours: two of these take 256 of the 512 columns at most.
-    if (P::kEarly && warp == kThreads / 32 + 1) tmem_alloc(smem_u32(&bars->tmem_base), columns<P>());
     pdl_enter();
-    if (!P::kEarly && warp == kThreads / 32 + 1) tmem_alloc(smem_u32(&bars->tmem_base), columns<P>());
+    // tensor memory behind the wait, as in pair_gemm.cuh: nothing that holds it waits for
+    // another grid
+    if (warp == kThreads / 32 + 1) tmem_alloc(smem_u32(&bars->tmem_base), columns<P>());
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
