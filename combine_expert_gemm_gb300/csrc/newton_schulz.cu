@@ -66,15 +66,43 @@ __device__ __forceinline__ float load_elem(const uint16_t *p, int64_t i) {
 
 // ---------------------------------------------------------- first passes --
 
+// A thread's sum of squares.  Groups of values whose squares stay in fp32 are added there,
+// with the part that each addition cuts carried to the next (a chain of 4096 equal values
+// is off by 6e-5 without it, and a matrix may have 2^32); the others in 64 bits, where
+// nothing vanishes or overflows.  All of it in 64 bits took 4 us more for three
+// matrices 1001 x 717: 16 cycles a warp for each addition.
+struct Squares {
+    float s = 0.0f, cut = 0.0f;
+    double far = 0.0;
+    template <int N>
+    __device__ __forceinline__ void add(const float (&v)[N]) {
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(v[i]));  // drops NaNs, which either sum keeps
+        if (top == 0.0f || (top >= 0x1p-50f && top <= 0x1p45f)) {
+            float t = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) t = fmaf(v[i], v[i], t);
+            t -= cut;
+            const float sum = s + t;
+            cut = (sum - s) - t;
+            s = sum;
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < N; ++i) far = fma((double)v[i], (double)v[i], far);
+        }
+    }
+};
+
 // Sums of squares of matrix blockIdx.y: part[y][x] over a strided share of it.
 // With MUON the values are the update direction and the momentum is advanced.
 template <bool MUON, typename TIN>
 __global__ void __launch_bounds__(kNormThreads)
 ns_norm(int64_t elems, const TIN *__restrict__ x, float *__restrict__ momentum, float mu, int nesterov,
-        float *__restrict__ part) {
+        double *__restrict__ part) {
     pdl_enter();
     const int64_t base = (int64_t)blockIdx.y * elems;
-    float s = 0.0f;
+    Squares sq;
     constexpr int U = 8;  // elements of a thread in flight
     const int64_t step = (int64_t)gridDim.x * kNormThreads;
     for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < elems; i += U * step) {
@@ -92,16 +120,24 @@ ns_norm(int64_t elems, const TIN *__restrict__ x, float *__restrict__ momentum, 
                 if (i + u * step < elems) momentum[base + i + u * step] = m[u];
                 v[u] = nesterov ? fmaf(mu, m[u], v[u]) : m[u];
             }
-            s = fmaf(v[u], v[u], s);
         }
+        sq.add(v);
     }
-    __shared__ float red[kNormThreads / 32];
+    __shared__ double red[kNormThreads / 32];
+    if (__syncthreads_or(sq.far != 0.0)) {
+        double t = sq.far + sq.s;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+        for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = t;
+    } else {
+        float t = sq.s;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = t;
+    }
     __syncthreads();
     if (threadIdx.x == 0) {
-        float t = 0.0f;
+        double t = 0.0;
         for (int i = 0; i < kNormThreads / 32; ++i) t += red[i];
         part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = t;
     }
@@ -114,11 +150,11 @@ constexpr int kSplitTile = 64;
 template <bool MUON, typename TIN>
 __global__ void __launch_bounds__(256)
 ns_split(int rows, int cols, int tall, int64_t ld, const TIN *__restrict__ x, const float *__restrict__ momentum,
-         float mu, int nesterov, float eps, const float *__restrict__ part, int parts, uint16_t *__restrict__ hi,
+         float mu, int nesterov, float eps, const double *__restrict__ part, int parts, uint16_t *__restrict__ hi,
          uint16_t *__restrict__ lo) {
     pdl_enter();
     __shared__ float tile[kSplitTile][kSplitTile + 1];
-    __shared__ float inv_s;
+    __shared__ float inv_s, pre_s;
     const int64_t b = blockIdx.z;
     const int r0 = blockIdx.y * kSplitTile, c0 = blockIdx.x * kSplitTile;
     const int64_t base = b * rows * cols;
@@ -137,13 +173,21 @@ ns_split(int rows, int cols, int tall, int64_t ld, const TIN *__restrict__ x, co
         for (int i = threadIdx.x; i < parts; i += 32) s += part[b * parts + i];
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        if (threadIdx.x == 0) inv_s = 1.0f / ((float)sqrt(s) + eps);
+        if (threadIdx.x == 0) {
+            // v / (|M| + eps) as (v pre) inv, with a power of two that brings a sum of squares
+            // outside fp32 into it (a 64-bit root and division took 3 us more)
+            const bool large = s > 0x1p100, small = s < 0x1p-100;
+            const float pre = large ? 0x1p-100f : 1.0f, up = small ? 0x1p80f : pre;
+            const float root = sqrtf((float)(s * ((double)up * up)));
+            inv_s = 1.0f / ((small ? root * 0x1p-80f : root) + eps * pre);
+            pre_s = pre;
+        }
     }
     __syncthreads();
-    const float inv = inv_s;
+    const float inv = inv_s, pre = pre_s;
     const int64_t out = b * (tall ? cols : rows) * ld;
 #pragma unroll
-    for (int r = 0; r < kSplitTile / 4; ++r) tile[4 * r + ty][tx] = v[r] * inv * kScale;
+    for (int r = 0; r < kSplitTile / 4; ++r) tile[4 * r + ty][tx] = v[r] * pre * inv * kScale;
     __syncthreads();
     // rows of the iterate: of M, or its columns
     const int orow0 = tall ? c0 : r0, ocol0 = tall ? r0 : c0;
@@ -600,7 +644,7 @@ __global__ void __launch_bounds__(kFuseThreads, 1) ns_fused(const __grid_constan
     __shared__ uint64_t bar;
     __shared__ uint32_t tmem_base;
     __shared__ int abort;
-    __shared__ float red[kFuseThreads / 32];
+    __shared__ float red[2][kFuseThreads / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&bar), 1);
@@ -621,7 +665,7 @@ __global__ void __launch_bounds__(kFuseThreads, 1) ns_fused(const __grid_constan
         const int np = 32 * p.nb;  // pairs of a row, padded
         const int next = p.tall ? p.cols : 1;
         float a[kPairs], b[kPairs];
-        float s = 0.0f;
+        float top = 0.0f;
         auto place = [&](int u, int &r, int &c) {
             const int i = u * kFuseThreads + (int)threadIdx.x;
             r = p.tall ? i & (kFuseM - 1) : i / np;
@@ -658,18 +702,37 @@ __global__ void __launch_bounds__(kFuseThreads, 1) ns_fused(const __grid_constan
                     va = p.nesterov ? fmaf(p.mu, ma[u], va) : ma[u];
                     vb = p.nesterov ? fmaf(p.mu, mb[u], vb) : mb[u];
                 }
-                s = fmaf(a[u0 + u], a[u0 + u], s);
-                s = fmaf(b[u0 + u], b[u0 + u], s);
+                top = fmaxf(top, fmaxf(fabsf(a[u0 + u]), fabsf(b[u0 + u])));
             }
         }
 #pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        if (lane == 0) red[0][warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kFuseThreads / 32; ++i) top = fmaxf(top, red[0][i]);
+        // the largest entry's size is taken out first (a power of two, so no bit changes):
+        // squares neither vanish nor overflow.  Below 2^-100, where eps is all that counts,
+        // and from 2^126 on the power stays.
+        const uint32_t size = min(max(__float_as_uint(top) >> 23, 27u), 253u);
+        const float pre = __uint_as_float((254u - size) << 23);
+        float s = 0.0f;
+#pragma unroll
+        for (int u = 0; u < kPairs; ++u) {
+            if (u * kFuseThreads >= kFuseM * np) break;
+            a[u] *= pre;
+            b[u] *= pre;
+            s = fmaf(a[u], a[u], s);
+            s = fmaf(b[u], b[u], s);
+        }
+#pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        if (lane == 0) red[warp] = s;
+        if (lane == 0) red[1][warp] = s;
         __syncthreads();
         float inv = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kFuseThreads / 32; ++i) inv += red[i];
-        inv = 1.0f / (sqrtf(inv) + p.eps);
+        for (int i = 0; i < kFuseThreads / 32; ++i) inv += red[1][i];
+        inv = 1.0f / (sqrtf(inv) + p.eps * pre);
 #pragma unroll
         for (int u = 0; u < kPairs; ++u) {
             if (u * kFuseThreads >= kFuseM * np) break;
@@ -844,7 +907,7 @@ struct Layout {
         lds = (m + 7) / 8 * 8;
         const size_t xb = align256((size_t)(2 * B * m * ldx * 2)), sb = align256((size_t)(2 * B * m * lds * 2));
         part = 256;
-        x[0] = part + align256((size_t)(B * kParts * 4));
+        x[0] = part + align256((size_t)(B * kParts * 8));
         x[1] = x[0] + xb;
         s = x[1] + xb;
         c = s + sb;
@@ -1049,7 +1112,7 @@ moe_status run(int B, int rows, int cols, const TIN *x, float *momentum, float m
     const int64_t elems = (int64_t)rows * cols;
     const int want = std::max(1, 8 * num_sms() / B);
     const int parts = (int)std::min<int64_t>(std::min(want, kParts), (elems + kNormThreads * 8 - 1) / (kNormThreads * 8));
-    float *part = reinterpret_cast<float *>(ws + at.part);
+    double *part = reinterpret_cast<double *>(ws + at.part);
     launch_pdl(ns_norm<MUON, TIN>, dim3(parts, B), kNormThreads, 0, st, elems, x, momentum, mu, nesterov, part);
     moe_status r = launch_status();
     if (r != MOE_OK) return r;

@@ -111,7 +111,9 @@ size_t moe_newton_schulz_workspace_bytes(int32_t B, int32_t rows, int32_t cols);
  * coefficients that can take a singular value in [0, 1] past 7.5, or the factor
  * a + b s^2 + c s^4 past 60, are refused (MOE_ERR_UNSUPPORTED).  A matrix with an
  * infinity or a NaN gives NaNs, in its own entries only.
- * |M|_F is summed in fp32: above 1.8e19 it is infinite there and out is 0.
+ * |M|_F is right for entries of any size, however small or large their squares.  An
+ * entry of X is held to 2^-22 of itself or to 2^-35, whichever is more, so a matrix far
+ * below eps, whose X is about M / eps, keeps fewer bits than one above it.
  * rows and cols are at most 65536, eps is finite and >= 1e-30.  B = 0 does nothing.
  */
 moe_status moe_newton_schulz(int32_t B, int32_t rows, int32_t cols, int32_t x_dtype, const void *x,
