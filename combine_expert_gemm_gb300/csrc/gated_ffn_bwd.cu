@@ -188,7 +188,15 @@ struct SmallFactor {
 // the 2 h columns of dG and dU.  Alone, 96 weight tiles of an 8192-token step on 76
 // pairs take two rounds and 256 tiles of dx four, 127 us where the products take 90;
 // together the pairs get equal shares: first the kind with the longer tiles, in
-// turn, then of the other kind as many as even the shares out (Share).
+// turn, then of the other kind as many as even the shares out (share).
+//
+// The weights' sums run over all tokens, dx's over 2 h.  In one accumulator the gradients
+// of a million tokens came out 0.7% short, as the tensor core cuts where an fp32 addition
+// rounds (pair_gemm.cuh).  Past kMostBlocks an accumulator holds that many, 8192
+// tokens, and they are added in registers: a sum of terms of one sign is at most 2^-14
+// short, whatever its length.  Sums that fit one accumulator stay there: tiles of 96
+// tokens are all epilogue, and took 77 us for 69 through registers.
+constexpr int kMostBlocks = 128;
 struct GradArgs {
     CUtensorMap wa[3];     // dy, dG, dU: rows of a weight gradient
     CUtensorMap wb[2];     // Hs, x: its columns
@@ -208,13 +216,14 @@ struct GradArgs {
     int *status;
 };
 
-template <bool DX32, bool DW32, int N>
+template <bool DX32, bool DW32, int N, bool LONG>
 struct Grad {
     using Args = GradArgs;
     struct Regs {};
     static constexpr int kN = N, kStages = N == 256 ? 6 : 8;
     static constexpr int kStageBytes = OPERAND + b_bytes(N);
-    static constexpr int kGroup = 0;
+    static constexpr int kGroup = LONG ? kMostBlocks : 0;
+    static constexpr int COLS = N / 2;
     static __device__ __forceinline__ int longs(const Args &p, int unit) { return p.q + (unit < p.r ? 1 : 0); }
     static __device__ __forceinline__ int count(const Args &p, int unit, int) {
         const int v = unit - p.r;
@@ -262,6 +271,15 @@ struct Grad {
     }
     static __device__ __forceinline__ void before(const Args &, const Tile &, const Epi &, int, Regs &) {}
     static __device__ __forceinline__ void epilogue(const Args &p, const Tile &t, Epi &e, int wrow, Regs &) {
+        store(p, t, e, wrow, [&](int c, float (&v)[32]) { read32(e.taddr + 32 * c, v); });
+    }
+    static __device__ __forceinline__ void finish(const Args &p, const Tile &t, Epi &e, int wrow,
+                                                  const float (&sum)[COLS]) {
+        store(p, t, e, wrow, [&](int c, float (&v)[32]) { pick32(sum, c, v); });
+    }
+    // The tile's sums, 32 columns of a lane's row at a time from get.
+    template <typename Get>
+    static __device__ __forceinline__ void store(const Args &p, const Tile &t, Epi &e, int wrow, Get &&get) {
         const bool x = t.z == 3;
         const int row0 = t.m + wrow, row = row0 + e.lane;
         const int rows = x ? p.T : t.z ? p.h : p.d, cols = t.z ? p.d : p.h;
@@ -272,14 +290,14 @@ struct Grad {
         // tile has to have left both blocks
         if (DX32 != DW32 && e.lane == 0) bulk_wait_read<0>();
 #pragma unroll 1
-        for (int c = 0; c < N / 2; c += 32) {
-            const int col = t.n + e.col + c;
+        for (int c = 0; c < COLS / 32; ++c) {
+            const int col = t.n + e.col + 32 * c;
             if (col >= cols) break;
             float add[32];
             const bool more = x && p.dx_in;
             if (more) fetch_dx(p, row, col, add);
             float v[32];
-            read32(e.taddr + c, v);
+            get(c, v);
             if (more) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] += add[i];
@@ -352,10 +370,11 @@ inline void share(GradArgs &p, int units, int64_t nl, int64_t cl, int64_t ns, in
     p.se = (int)(rest % (units - p.r));
 }
 
-template <int N>
+template <int N, bool LONG>
 moe_status launch_grad(const GradArgs &g, bool dx32, bool dw32, int64_t tiles, cudaStream_t st) {
-    if (dx32) return dw32 ? launch<Grad<true, true, N>>(g, tiles, st) : launch<Grad<true, false, N>>(g, tiles, st);
-    return dw32 ? launch<Grad<false, true, N>>(g, tiles, st) : launch<Grad<false, false, N>>(g, tiles, st);
+    if (dx32)
+        return dw32 ? launch<Grad<true, true, N, LONG>>(g, tiles, st) : launch<Grad<true, false, N, LONG>>(g, tiles, st);
+    return dw32 ? launch<Grad<false, true, N, LONG>>(g, tiles, st) : launch<Grad<false, false, N, LONG>>(g, tiles, st);
 }
 
 // out[t] = the sum of part[0..n)[t], in order.
@@ -546,5 +565,9 @@ MOE_API moe_status moe_gated_ffn_backward(int32_t T, int32_t d, int32_t h, const
     g.long_x = cx > cw;
     if (g.long_x) share(g, units, xt, cx, wt, cw);
     else share(g, units, wt, cw, xt, cx);
-    return wide ? launch_grad<256>(g, dx32, dw32, tiles, stream) : launch_grad<128>(g, dx32, dw32, tiles, stream);
+    if (std::max(cx, cw) > kMostBlocks)
+        return wide ? launch_grad<256, true>(g, dx32, dw32, tiles, stream)
+                    : launch_grad<128, true>(g, dx32, dw32, tiles, stream);
+    return wide ? launch_grad<256, false>(g, dx32, dw32, tiles, stream)
+                : launch_grad<128, false>(g, dx32, dw32, tiles, stream);
 }

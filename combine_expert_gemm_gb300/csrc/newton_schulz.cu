@@ -315,14 +315,7 @@ struct Ns {
             const int col = col0 + 32 * c;
             if (col >= p.n) break;
             float v[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                v[i] = c & 1 ? sum[32 + i] : sum[i];
-                if constexpr (COLS > 64) {
-                    const float b = c & 1 ? sum[96 + i] : sum[64 + i];
-                    v[i] = c & 2 ? b : v[i];
-                }
-            }
+            pick32(sum, c, v);
             if constexpr (MODE == NS_LAST) {
                 last(p, t, e, row0, col, c + 1 < COLS / 32, v, ahead);
                 continue;

@@ -44,7 +44,7 @@ constexpr int kTmemCols = 512;
 constexpr int kEpiWarps = 8;
 constexpr int kEpiBlock = 4096;      // shared memory of an epilogue warp
 
-// With kGroup > 0 an epilogue thread keeps 128 sums, more than 168 registers hold
+// With kGroup > 0 an epilogue thread keeps up to 128 sums, more than 168 registers hold
 // beside what it works with (2-3 KB of spills): two idle warps fill the
 // first warpgroup, which gives up its registers: 128 x 40 + 256 x 232 = 384 x 168.
 template <class P>
@@ -188,6 +188,20 @@ __device__ __forceinline__ void read32(uint32_t taddr, float (&v)[32]) {
     for (int i = 0; i < 16; ++i) {
         v[i] = __uint_as_float(a[i]);
         v[16 + i] = __uint_as_float(b[i]);
+    }
+}
+
+// Columns 32 c .. 32 c + 31 of a row's 64 or 128 sums, by selections: registers have no
+// index, and a loop over c is short where its unrolled code is not.
+template <int COLS>
+__device__ __forceinline__ void pick32(const float (&sum)[COLS], int c, float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        v[i] = c & 1 ? sum[32 + i] : sum[i];
+        if constexpr (COLS > 64) {
+            const float b = c & 1 ? sum[96 + i] : sum[64 + i];
+            v[i] = c & 2 ? b : v[i];
+        }
     }
 }
 

@@ -46,7 +46,9 @@ size_t moe_gated_ffn_backward_workspace_bytes(int32_t T, int32_t d, int32_t h);
  * and, for the backward, the two factors that it multiplies by:
  *   p_save = bf16(act(G)),  q_save = bf16(U * act'(G))     (relu'(0) = 0)
  * Products and activations are fp32; h_act, p_save, q_save and y are each
- * rounded once.
+ * rounded once.  The tensor core cuts an fp32 sum, towards zero, by up to 2^-23 of its
+ * size for every 16 products: terms of one sign lose up to 2^-16 at widths of 2048, 2^-11
+ * at 65536 (R of the backward too), where half a step of bf16 is up to 2^-8.
  *   x [T, d], w_gate, w_up [h, d], w_down [d, h] bf16; add [T, d] bf16 or NULL
  *   (0), may be y itself; token_scale [T] fp32 or NULL (1); y out [T, d] bf16;
  *   h_act out [T, h] bf16; p_save, q_save out [T, h] bf16, both or neither NULL.
@@ -71,7 +73,9 @@ moe_status moe_gated_ffn(int32_t T, int32_t d, int32_t h, int32_t act, const moe
  *   dtoken_scale out [T], all of dw_dtype (moe_dtype); dtoken_scale may be NULL and
  *   needs token_scale.
  * fp32 sums, each output rounded once (what is below fp32 in an fp32 output is
- * the rounding of h_act, p_save, q_save, dG, dU to bf16).  The gradient of add is
+ * the rounding of h_act, p_save, q_save, dG, dU and, with a token scale, s h_act to
+ * bf16; a sum of dx and of the weights' gradients is cut by up to 2^-14 of its size,
+ * however many tokens it runs over).  The gradient of add is
  * dy.  T = 0 writes zeros to the weights' gradients.
  */
 moe_status moe_gated_ffn_backward(int32_t T, int32_t d, int32_t h, const moe_bf16 *x,
