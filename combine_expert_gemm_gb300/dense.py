@@ -3,8 +3,10 @@
 the Newton-Schulz orthogonalisation with the Muon step that updates weight
 matrices.
 
-Argument marshalling only, as in the package's ``__init__``; like the operators of
-a training block these calls compare every tensor's size with the shape.
+Argument marshalling only, as in the package's ``__init__``.  Weights, their gradients
+and the matrices of Newton-Schulz and Muon have exactly the shape that the call
+states (a transposed one has as many elements); of the tokens' buffers, which may go on
+behind the last row, the number of elements is compared, as in a training block.
 """
 import ctypes
 
@@ -46,15 +48,40 @@ def gated_ffn_backward_workspace_bytes(T, d, h):
     return int(_lib.moe_gated_ffn_backward_workspace_bytes(T, d, h))
 
 
-def _ffn_sizes(x, w_gate):
+def _ffn_sizes(x, w_gate, w_up, w_down):
+    """T, d, h of x [T, d], w_gate and w_up [h, d], w_down [d, h]."""
+    try:
+        (T, d), (h, dg) = x.shape, w_gate.shape
+        if dg == d and w_up.shape == w_gate.shape and w_down.shape == (d, h):
+            return T, d, h
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x: expected [T, d]")
+    d = x.shape[1]
     if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
-        raise ValueError("w_gate: expected [h, d]")
-    (T, d), (h, d2) = x.shape, w_gate.shape
-    if d != d2:
-        raise ValueError(f"w_gate: expected [h, {d}], got [{h}, {d2}]")
-    return T, d, h
+        raise ValueError(f"w_gate: expected [h, {d}]")
+    h, dg = w_gate.shape
+    if dg != d:
+        raise ValueError(f"w_gate: expected [h, {d}], got [{h}, {dg}]")
+    _shape(w_up, "w_up", (h, d))
+    _shape(w_down, "w_down", (d, h))
+
+
+def _ptr(t, dtype, name, dev):
+    """_arg of a tensor whose shape has been compared: its elements are not counted again
+    (one token's call is bound by the host, which each question costs 0.1 to 0.2 us)."""
+    if t is not None and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _arg(t, dtype, name, 0, dev)
+
+
+def _shape(t, name, want):
+    """Refuses a t that has not the shape want."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.shape != want:
+        raise ValueError(f"{name}: expected {list(want)}, got {list(t.shape)}")
 
 
 def gated_ffn(x, w_gate, w_up, w_down, add, token_scale, y, h_act, p_save, q_save, ws, act="silu",
@@ -62,14 +89,14 @@ def gated_ffn(x, w_gate, w_up, w_down, add, token_scale, y, h_act, p_save, q_sav
     """y = add + token_scale * (act(x Wg^T) * (x Wu^T)) Wd^T (include/moe_dense.h).  x [T, d],
     w_gate, w_up [h, d], w_down [d, h]; add, token_scale, and p_save with q_save may be None;
     act is "silu", "gelu" (the tanh form) or "relu"."""
-    T, d, h = _ffn_sizes(x, w_gate)
+    T, d, h = _ffn_sizes(x, w_gate, w_up, w_down)
     if act not in _ACT:
         raise ValueError(f"act: expected one of {', '.join(_ACT)}, got {act!r}")
-    dev, n, nh, nw = torch.cuda.current_device(), T * d, T * h, d * h
+    dev, n, nh = torch.cuda.current_device(), T * d, T * h
     wp, wn = _ws(ws, dev)
     _check(_lib.moe_gated_ffn(
-        T, d, h, _ACT[act], _arg(x, _bf16, "x", n, dev), _arg(w_gate, _bf16, "w_gate", nw, dev),
-        _arg(w_up, _bf16, "w_up", nw, dev), _arg(w_down, _bf16, "w_down", nw, dev),
+        T, d, h, _ACT[act], _arg(x, _bf16, "x", n, dev), _ptr(w_gate, _bf16, "w_gate", dev),
+        _ptr(w_up, _bf16, "w_up", dev), _ptr(w_down, _bf16, "w_down", dev),
         _arg(add, _bf16, "add", n, dev), _arg(token_scale, _f32, "token_scale", T, dev),
         _arg(y, _bf16, "y", n, dev), _arg(h_act, _bf16, "h_act", nh, dev),
         _arg(p_save, _bf16, "p_save", nh, dev), _arg(q_save, _bf16, "q_save", nh, dev), wp, wn,
@@ -81,18 +108,21 @@ def gated_ffn_backward(x, w_gate, w_up, w_down, token_scale, h_act, p_save, q_sa
     """The backward of gated_ffn (include/moe_dense.h): dx = dx_in + the block's input gradient
     (bf16 or fp32, dx_in of dx's type or None), the weights' gradients and dtoken_scale (or
     None), all four bf16 or fp32."""
-    T, d, h = _ffn_sizes(x, w_gate)
+    T, d, h = _ffn_sizes(x, w_gate, w_up, w_down)
     xt, wt = _float_type(dx, "dx"), _float_type(dw_gate, "dw_gate")
-    dev, n, nh, nw = torch.cuda.current_device(), T * d, T * h, d * h
+    _shape(dw_gate, "dw_gate", (h, d))
+    _shape(dw_up, "dw_up", (h, d))
+    _shape(dw_down, "dw_down", (d, h))
+    dev, n, nh = torch.cuda.current_device(), T * d, T * h
     wp, wn = _ws(ws, dev)
     _check(_lib.moe_gated_ffn_backward(
-        T, d, h, _arg(x, _bf16, "x", n, dev), _arg(w_gate, _bf16, "w_gate", nw, dev),
-        _arg(w_up, _bf16, "w_up", nw, dev), _arg(w_down, _bf16, "w_down", nw, dev),
+        T, d, h, _arg(x, _bf16, "x", n, dev), _ptr(w_gate, _bf16, "w_gate", dev),
+        _ptr(w_up, _bf16, "w_up", dev), _ptr(w_down, _bf16, "w_down", dev),
         _arg(token_scale, _f32, "token_scale", T, dev), _arg(h_act, _bf16, "h_act", nh, dev),
         _arg(p_save, _bf16, "p_save", nh, dev), _arg(q_save, _bf16, "q_save", nh, dev),
         _arg(dy, _bf16, "dy", n, dev), _DTYPE[xt], _arg(dx_in, xt, "dx_in", n, dev),
-        _arg(dx, xt, "dx", n, dev), _DTYPE[wt], _arg(dw_gate, wt, "dw_gate", nw, dev),
-        _arg(dw_up, wt, "dw_up", nw, dev), _arg(dw_down, wt, "dw_down", nw, dev),
+        _arg(dx, xt, "dx", n, dev), _DTYPE[wt], _ptr(dw_gate, wt, "dw_gate", dev),
+        _ptr(dw_up, wt, "dw_up", dev), _ptr(dw_down, wt, "dw_down", dev),
         _arg(dtoken_scale, wt, "dtoken_scale", T, dev), wp, wn, _on(stream, dev)),
         "moe_gated_ffn_backward")
 
@@ -107,6 +137,16 @@ def _matrices(t, name):
     if not isinstance(t, torch.Tensor) or t.dim() not in (2, 3):
         raise ValueError(f"{name}: expected [B, rows, cols] or [rows, cols]")
     return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
+
+
+def _same_matrices(t, name, want):
+    """Refuses a t of other matrices than want's (None: left out)."""
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.shape != want.shape and _matrices(t, name) != _matrices(want, name):
+        raise ValueError(f"{name}: expected {list(want.shape)}, got {list(t.shape)}")
 
 
 def _coefficients(c, steps):
@@ -129,10 +169,11 @@ def newton_schulz(x, out, ws, steps=5, coefficients=None, eps=1e-7, stream=None)
     types are one); coefficients: one (a, b, c) for all steps, one for each, or None."""
     B, rows, cols = _matrices(x, "x")
     xt, ot = _float_type(x, "x"), _float_type(out, "out")
-    dev, n = torch.cuda.current_device(), B * rows * cols
+    _same_matrices(out, "out", x)
+    dev = torch.cuda.current_device()
     wp, wn = _ws(ws, dev)
-    _check(_lib.moe_newton_schulz(B, rows, cols, _DTYPE[xt], _arg(x, xt, "x", n, dev), _DTYPE[ot],
-                                  _arg(out, ot, "out", n, dev), steps, _coefficients(coefficients, steps),
+    _check(_lib.moe_newton_schulz(B, rows, cols, _DTYPE[xt], _ptr(x, xt, "x", dev), _DTYPE[ot],
+                                  _ptr(out, ot, "out", dev), steps, _coefficients(coefficients, steps),
                                   eps, wp, wn, _on(stream, dev)), "moe_newton_schulz")
 
 
@@ -141,11 +182,13 @@ def muon_step(w, w_copy, momentum, grad, lr, mu, weight_decay, scale, ws, nester
     """One Muon step of w [B, rows, cols] or [rows, cols] (include/moe_dense.h): momentum and w
     fp32 in place, w_copy (or None) its bf16 copy, lr a [1] fp32 tensor on the device."""
     B, rows, cols = _matrices(w, "w")
-    dev, n = torch.cuda.current_device(), B * rows * cols
+    for t, name in ((w_copy, "w_copy"), (momentum, "momentum"), (grad, "grad")):
+        _same_matrices(t, name, w)
+    dev = torch.cuda.current_device()
     wp, wn = _ws(ws, dev)
     _check(_lib.moe_muon_step(
-        B, rows, cols, _arg(w, _f32, "w", n, dev), _arg(w_copy, _bf16, "w_copy", n, dev),
-        _arg(momentum, _f32, "momentum", n, dev), _arg(grad, _f32, "grad", n, dev),
+        B, rows, cols, _ptr(w, _f32, "w", dev), _ptr(w_copy, _bf16, "w_copy", dev),
+        _ptr(momentum, _f32, "momentum", dev), _ptr(grad, _f32, "grad", dev),
         _arg(lr, _f32, "lr", 1, dev), mu, weight_decay, scale, 1 if nesterov else 0, steps,
         _coefficients(coefficients, steps), eps, wp, wn, _on(stream, dev)), "moe_muon_step")
 
@@ -227,6 +270,8 @@ class Muon:
         grads = list(grads)
         if len(grads) != len(self.weights):
             raise ValueError(f"grads: {len(grads)} tensors, {len(self.weights)} weights")
+        for i, ((w, _), g) in enumerate(zip(self.weights, grads)):  # before any weight moves
+            _same_matrices(g, f"grads[{i}]", w)
         for (w, copy), v, g in zip(self.weights, self.momentum, grads):
             rows, cols = w.shape[-2:]
             scale = max(1.0, rows / cols) ** 0.5 if self.scale is None else self.scale
