@@ -200,7 +200,7 @@ class SharedExpert:
     weights w_gate, w_up [h, d] and w_down [d, h], what its forward keeps for the backward
     (three [T, h] bf16 buffers and the token scale), and the gradients, which hold the last
     backward's results: dw_gate, dw_up, dw_down and, with a token scale, dtoken_scale,
-    all fp32."""
+    all fp32.  The next forward overwrites what it keeps."""
 
     def __init__(self, T, w_gate, w_up, w_down, act="silu"):
         h, d = w_gate.shape
@@ -222,14 +222,20 @@ class SharedExpert:
         is copied for the backward."""
         if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[0] != self.T:
             raise ValueError(f"x: expected [{self.T}, d]")
+        self.refuse_scale(token_scale)
+        # from here on what the forward before kept is gone
+        self.saved = False
+        self.token_scale = None
         if token_scale is not None:
-            _arg(token_scale, _f32, "token_scale", self.T, torch.cuda.current_device())
             self.token_scale = _keep(self.scale, token_scale.view(-1)[:self.T], stream)
-        else:
-            self.token_scale = None
         gated_ffn(x, self.w_gate, self.w_up, self.w_down, add, self.token_scale, y, self.h_act,
                   self.p_save, self.q_save, self.ws, self.act, stream)
         self.saved = True
+
+    def refuse_scale(self, token_scale):
+        """Raises if token_scale is not None nor T fp32 values on the current device."""
+        if token_scale is not None:
+            _arg(token_scale, _f32, "token_scale", self.T, torch.cuda.current_device())
 
     def backward(self, x, dy, dx_in, dx, stream=None):
         """dx = dx_in + the gradient of the forward's x (which x is), and the weights'."""
