@@ -267,6 +267,8 @@ class BlockState:
         self.g_scale, self.u_scale = (torch.empty((R, h // 32), dtype=_u8, **e) for _ in range(2))
         self.y_q = torch.empty((R, d), dtype=_i8, **e)
         self.y_scale = torch.empty((R, d // 32), dtype=_u8, **e)
+        self.shared = None                             # the last forward's shared expert, and which
+        self.shared_forward = 0                        # of that expert's forwards it was
 
 
 class BlockScratch:
@@ -304,13 +306,22 @@ def block_forward(st, sc, x, add, gamma, beta, w_router, bias, w_gate, w_up, w_d
     own output of n, times shared_scale [T] fp32 where that is given.  st keeps what block_backward needs,
     the experts' buffers in 8 bits, and st.losses the balance and z loss over the tokens
     that token_mask [T] uint8 (or None: all) counts.  x, add and token_mask are copied
-    where the backward needs them and may be overwritten once these calls have run."""
+    where the backward needs them and may be overwritten once these calls have run.
+    block_backward takes the same shared, before that runs another forward."""
     s, f = st.shape, sc.fwd
     _, rows, d = _rows(x, "x")
     if (rows, d) != (s.T, s.d):
         raise ValueError(f"x: expected [{s.T}, {s.d}], got [{rows}, {d}]")
+    if shared is None:
+        if shared_scale is not None:
+            raise ValueError("shared_scale: given without shared")
+    elif (shared.T, shared.w_gate.shape[1]) != (s.T, s.d):
+        raise ValueError(f"shared: an expert of [{shared.T}, {shared.w_gate.shape[1]}], [{s.T}, {s.d}] expected")
+    else:
+        shared.refuse_scale(shared_scale)
     layer_norm(x, add, gamma, beta, eps, None if add is None else st.x_sum, st.n, st.mean, st.rstd,
                stream)
+    st.shared = None
     if add is not None:
         st.h = st.x_sum
     elif x.dtype is _f32:
@@ -332,6 +343,7 @@ def block_forward(st, sc, x, add, gamma, beta, w_router, bias, w_gate, w_up, w_d
     combine(s, f.y_disp, st.route_row, st.topk_gate, f.y, stream)
     if shared is not None:
         shared.forward(st.n, f.y, f.y, shared_scale, stream)
+        st.shared, st.shared_forward = shared, shared.forwards
     return f.y
 
 
@@ -341,7 +353,13 @@ def block_backward(st, sc, dh, dx, dlosses, gamma, beta, w_router, bias, w_gate,
     block's dx): it reaches h directly and through the layer.  dx [T, d] bf16 (dh itself
     is allowed) gets the gradient of h; dlosses [2] fp32 on the device are the gradients
     of st.losses.  sc.bwd.dw_gate, dw_up, dw_down, dw_router (and dbias), sc.dgamma and
-    sc.dbeta hold the weights' gradients until the next call."""
+    sc.dbeta hold the weights' gradients until the next call.  shared is the forward's; it
+    holds its own weights' gradients."""
+    if shared is not st.shared:
+        raise ValueError("shared: this state's forward ran without one" if st.shared is None else
+                         "shared: not the shared expert of this state's forward")
+    if shared is not None and shared.forwards != st.shared_forward:
+        raise RuntimeError("shared: another forward of this expert has run since this state's")
     s, f, b = st.shape, sc.fwd, sc.bwd
     combine_backward_checkpoint(s, dh, st.y_q, st.y_scale, st.route_row, st.topk_gate, b.dy_disp,
                                 b.dgate, b.dlogit, stream)

@@ -200,7 +200,8 @@ class SharedExpert:
     weights w_gate, w_up [h, d] and w_down [d, h], what its forward keeps for the backward
     (three [T, h] bf16 buffers and the token scale), and the gradients, which hold the last
     backward's results: dw_gate, dw_up, dw_down and, with a token scale, dtoken_scale,
-    all fp32.  The next forward overwrites what it keeps."""
+    all fp32.  The next forward overwrites what it keeps: an expert that several blocks
+    share runs each block's backward before the next block's forward."""
 
     def __init__(self, T, w_gate, w_up, w_down, act="silu"):
         h, d = w_gate.shape
@@ -209,6 +210,7 @@ class SharedExpert:
         self.w_gate, self.w_up, self.w_down = w_gate, w_up, w_down
         self.h_act, self.p_save, self.q_save = (torch.empty((T, h), dtype=_bf16, **e) for _ in range(3))
         self.saved = False                             # whether a forward has run
+        self.forwards = 0                              # forwards begun, for the blocks that use it
         self.token_scale = None                        # scale, or None where every token's is 1
         self.scale = torch.empty(T, **e)
         self.dw_gate, self.dw_up = (torch.empty((h, d), **e) for _ in range(2))
@@ -225,6 +227,7 @@ class SharedExpert:
         self.refuse_scale(token_scale)
         # from here on what the forward before kept is gone
         self.saved = False
+        self.forwards += 1
         self.token_scale = None
         if token_scale is not None:
             self.token_scale = _keep(self.scale, token_scale.view(-1)[:self.T], stream)
