@@ -109,3 +109,52 @@ def test_muon_step_forms(moe, B, rows, cols, copy):
     assert bool((err <= bound).all()), float((err / bound).max())
     if copy:
         assert torch.equal(wc, wt.to(BF))
+
+
+@pytest.mark.parametrize("a,b", [((300, 40, 50), (300, 60, 30)), ((8, 128, 256), (12, 300, 400)),
+                                 ((20, 70, 400), (4, 900, 1000)), ((3, 1001, 717), (2, 1303, 1000))])
+def test_newton_schulz_on_two_streams(moe, a, b):
+    """Two calls at once, each with its workspace, beside a few tokens' feed-forward on a
+    third stream; and the same captured into one graph."""
+    calls = []
+    for s in (a, b):
+        m = _mats(*s).to(DEV)
+        calls.append((m, torch.empty_like(m), _ws(moe.newton_schulz_workspace_bytes(*s))))
+    t = _ffn_inputs(20, 512, 256, True, True)
+    w = [t[k].to(DEV) for k in ("x", "wg", "wu", "wd", "add", "scale")]
+    y, hb = torch.empty(20, 512, dtype=BF, device=DEV), torch.empty(20, 256, dtype=BF, device=DEV)
+    ws = _ws(moe.gated_ffn_workspace_bytes(20, 512, 256))
+
+    def run(streams):
+        for c, s in zip(calls, streams):
+            moe.newton_schulz(*c, stream=s)
+        moe.gated_ffn(*w, y, hb, None, None, ws, stream=streams[2])
+
+    run([None] * 3)
+    torch.cuda.synchronize()
+    want = [c[1].clone() for c in calls] + [y.clone()]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+
+    def check():
+        torch.cuda.synchronize()
+        for got, q in zip([c[1] for c in calls] + [y], want):
+            assert torch.equal(got, q)
+            got.zero_()
+        torch.cuda.synchronize()
+        assert all(moe.read_device_error(q) == 0 for q in (calls[0][2], calls[1][2], ws))
+
+    for _ in range(3):
+        for _ in range(4):
+            run(streams)
+        check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        now = torch.cuda.current_stream()
+        for s in streams:
+            s.wait_stream(now)
+        run(streams)
+        for s in streams:
+            now.wait_stream(s)
+    for _ in range(2):
+        graph.replay()
+        check()
